@@ -60,8 +60,8 @@ typedef enum pa_status {
 typedef enum pa_dtype {
   PA_FP16 = 0,    /* IEEE binary16 */
   PA_BF16 = 1,    /* bfloat16 (the upper half of an IEEE binary32) */
-  PA_FP8_E4M3 = 2 /* a cache of OCP E4M3 codes (pa_*_fp8 entry points and
-                     pa_copy_blocks only) */
+  PA_FP8_E4M3 = 2 /* a cache of OCP E4M3 codes (pa_*_fp8 and pa_*_fp8_block entry
+                     points, pa_copy_blocks and pa_decode_sparse only) */
 } pa_dtype;
 
 /*
@@ -500,6 +500,225 @@ int pa_decode_splitk_fp8(void* out, const void* q, const void* k_cache, const vo
                          float scale, int dtype, float k_scale, float v_scale, int partition_size,
                          int max_num_partitions, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/*
+ * Block-scaled E4M3 caches.  The pools hold E4M3 codes as above, but the scale
+ * is one float32 per (physical block, KV head), kept beside each pool:
+ *
+ *   k_scales, v_scales  [num_blocks][num_kv_heads] float32
+ *   value of an element = value(code) * scale[its block][its KV head]
+ *
+ * ("PagedAttention: when the KV cache meets OS paging", section 6, puts the
+ * compression inside the block; the block is what a scale can follow without
+ * knowing the data in advance.)  head_dim is 64, 128 or 256.
+ *
+ * A block's scales belong to its contents: whoever copies a block (copy-on-
+ * write) copies its scale rows too.  pa_copy_blocks moves them when num_kv_heads
+ * is a multiple of 4: pass the two scale tables as one-byte pools with
+ * block_size 1 and head_dim 4.
+ */
+
+/*
+ * pa_reshape_and_cache_fp8_block -- write new tokens into block-scaled pools,
+ * with scales taken from the data.
+ *
+ * Per pool and for every block b that slot_mapping names, KV head h:
+ *
+ *   need  = the smallest 2^e, e >= -64, with max|x| <= 448 * 2^e over the
+ *           finite elements x that this call brings to (b, h)
+ *   old   = 0 if this call writes offset 0 of b (the block starts: whatever it
+ *           held is forgotten), else scale[b][h] (read as 0 unless it is finite
+ *           and positive)
+ *   scale[b][h] = s = max(old, need)
+ *   if 0 < old < s, the block's codes that this call does not write become
+ *           E4M3(value(code) * (old / s))
+ *   every new element becomes E4M3_satfinite(x / s)
+ *
+ * So a block starts with the scale that its first tokens need and its scale
+ * only grows while it fills.  The scales are powers of two as long as old is:
+ * x / s is then exact, and moving a code to a larger scale is exact unless it
+ * becomes subnormal.  E4M3 is a floating-point format, so a scale that is a
+ * power of two costs range (less than a factor of 2 of 448) and no precision.
+ * Infinite elements saturate to +-448 * s, NaN stays NaN.
+ *
+ *   key, value        [num_tokens][num_kv_heads][head_dim] of dtype
+ *                     (PA_FP16 or PA_BF16), read only
+ *   k_cache, v_cache  [num_blocks][block_size][num_kv_heads][head_dim]
+ *                     uint8 E4M3 codes
+ *   k_scales,
+ *   v_scales          as above; the rows of the named blocks are updated
+ *   slot_mapping      as pa_reshape_and_cache, and: the tokens of one block
+ *                     stand next to each other (as they do when each
+ *                     sequence's new tokens stand in position order).  The
+ *                     contents and scale of a block named in two separate runs
+ *                     are undefined; nothing else is affected.
+ *
+ * Device-value outcomes as pa_reshape_and_cache.
+ */
+int pa_reshape_and_cache_fp8_block(const void* key, const void* value, void* k_cache, void* v_cache,
+                                   float* k_scales, float* v_scales, const int64_t* slot_mapping,
+                                   int num_tokens, int num_blocks, int block_size, int num_kv_heads,
+                                   int head_dim, int dtype, void* stream);
+
+/*
+ * pa_decode_fp8_block -- pa_decode over block-scaled pools: the same attention
+ * with K_i = value(k code) * k_scales[block][h] and V_i = value(v code) *
+ * v_scales[block][h].
+ *
+ *   q, out   [num_seqs][num_heads][head_dim] of dtype, PA_FP16 or PA_BF16
+ *
+ * The scales may be any finite numbers >= 0 (a v scale below 2^-64 reads as
+ * 0).  The codes are widened exactly to fp16; bf16 queries are brought into
+ * fp16's range by a power of two per row, undone in float32.  Scores, softmax
+ * and accumulation are float32; the attention weights enter the P.V product
+ * as fp16.  The value scale moves into the exponent of the weight, so blocks
+ * of very different scales meet without loss.
+ *
+ * Other arguments, supported shapes and device-value outcomes as pa_decode; in
+ * addition a negative, infinite or NaN scale of a block in the context, or a
+ * NaN code in a valid slot, gives NaN in out for the affected (sequence,
+ * KV-head group).
+ */
+int pa_decode_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                        int num_heads, int num_kv_heads, int head_dim, int block_size,
+                        int num_blocks, float scale, int dtype, void* stream);
+
+/*
+ * pa_decode_splitk_fp8_block -- pa_decode_splitk over block-scaled pools.  The
+ * workspace holds the scaled float32 partials, so pa_splitk_reduce (dtype of
+ * out) finishes the call unchanged.
+ */
+int pa_decode_splitk_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scales, const float* v_scales,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* context_lens, int num_seqs, int num_heads,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                               float scale, int dtype, int partition_size, int max_num_partitions,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_prefill_fp8_block -- pa_prefill over block-scaled pools, K_i and V_i as
+ * pa_decode_fp8_block.  Arguments, supported shapes (head_dim 64 or 128) and
+ * device-value outcomes as pa_prefill; in addition a negative, infinite or NaN
+ * scale gives NaN in the rows that an id outside the pool in its place would.
+ */
+int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                         const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         const int32_t* query_start_loc, int num_seqs, int num_rows,
+                         int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, float scale, int dtype, void* stream);
+
+/*
+ * Block-sparse decode.  Of a long context, each new token attends to a bounded
+ * number of blocks per KV head: the first ones, the last ones and those whose
+ * keys can score highest.  What can score highest is read from bounds of each
+ * block's keys, kept in 8 bits beside the pool (of any element type):
+ *
+ *   key_bounds  [num_blocks][num_kv_heads][2][head_dim] int8: per channel c the
+ *               codes lo_c, hi_c in [-127, 127]
+ *   bound_exps  [num_blocks][num_kv_heads] int32: e
+ *   lo_c * 2^e <= k_c <= hi_c * 2^e  for every (finite) key k of the block
+ *
+ * A step calls pa_update_key_bounds beside the cache write, then
+ * pa_select_blocks, then pa_decode_sparse.  A copied block takes its bounds
+ * along.
+ */
+
+/*
+ * pa_update_key_bounds -- fold new tokens' keys into their blocks' bounds.
+ *
+ * For every block b that slot_mapping names, KV head h: e is the smallest
+ * number >= -100 with max|k| <= 127 * 2^e over the finite elements of the keys
+ * that this call brings, and not below the block's e unless this call writes
+ * offset 0 of b (the block starts and its old bounds are forgotten).
+ * lo = floor(min k / 2^e), hi = ceil(max k / 2^e), folded with the old codes moved
+ * to the new e (floor and ceil again).  Moving by a power of two and rounding
+ * outwards commute, so the bounds do not depend on how the tokens were spread
+ * over calls.  A non-finite element bounds its channel by +-127 at the time of
+ * its write (NaN on both sides).
+ *
+ *   key           [num_tokens][num_kv_heads][head_dim] of dtype, read only
+ *   bound_exps    a named block that does not start must hold an exponent in
+ *                 [-100, 121], as this call leaves it
+ *   slot_mapping  as pa_reshape_and_cache_fp8_block
+ */
+int pa_update_key_bounds(const void* key, int8_t* key_bounds, int32_t* bound_exps,
+                         const int64_t* slot_mapping, int num_tokens, int num_blocks,
+                         int block_size, int num_kv_heads, int head_dim, int dtype, void* stream);
+
+/*
+ * pa_select_workspace_bytes -- size of pa_select_blocks' workspace: one float32
+ * per (sequence, KV head, table entry), rows padded to 4.  Returns 0 for
+ * non-positive arguments.
+ */
+size_t pa_select_workspace_bytes(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+
+/*
+ * pa_select_blocks -- choose the blocks that each (sequence, KV head) reads.
+ *
+ * The score of block b of sequence s for KV head h, a bound of the largest
+ * score that one of its keys can reach:
+ *
+ *   qi_c  = rint(q_c / 2^f), f the smallest number >= -100 with max|q| <= 255 * 2^f
+ *           over the finite elements of the query head's row (an infinite
+ *           element counts as +-255, NaN as 0)
+ *   I     = sum_c max(qi_c * lo_c, qi_c * hi_c)
+ *   score = max over the query heads of the group of I * 2^(f + e), the exponent
+ *           held to [-100, 100]
+ *
+ * I is a whole number below 2^23, so scores are exact and the choice does not
+ * depend on the order of any sum.  Kept, of the n = ceil(context_lens[s] /
+ * block_size) blocks, are k = min(n, max_selected): the first num_first, the
+ * last num_last, then the best by score, the earlier block first among equals.
+ *
+ *   sel_tables      [num_seqs][num_kv_heads][max_selected] int32, written: the
+ *                   physical ids of the kept blocks in position order, then -1
+ *   sel_lens        [num_seqs][num_kv_heads] int32, written: the tokens in them,
+ *                   context_lens[s] - (n - k) * block_size (the last block of
+ *                   the context, the only partial one, is always kept)
+ *   q               [num_seqs][num_heads][head_dim] of dtype
+ *   num_first >= 0, num_last >= 1, num_first + num_last <= max_selected
+ *   workspace       device buffer of workspace_bytes >=
+ *                   pa_select_workspace_bytes(...), 16-byte aligned; scratch,
+ *                   contents on entry ignored
+ *
+ * Other arguments as pa_decode (block tables and context lengths of the whole
+ * sequences).  Device-value outcomes: an id outside the pool scores above every
+ * number, so it is kept and the decode that reads it gives NaN; a context length
+ * outside the table's capacity gives sel_lens = -1 and a row of -1; 0 gives 0
+ * and a row of -1.
+ */
+int pa_select_blocks(int32_t* sel_tables, int32_t* sel_lens, const void* q,
+                     const int8_t* key_bounds, const int32_t* bound_exps,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                     int head_dim, int block_size, int num_blocks, int max_selected, int num_first,
+                     int num_last, int dtype, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * pa_decode_sparse -- decode attention with a block table per (sequence, KV
+ * head): query head j of sequence s attends to the first sel_lens[s][h] tokens
+ * of the blocks sel_tables[s][h][...], h = j / G.
+ *
+ *   sel_tables  [num_seqs][num_kv_heads][max_selected] int32 physical ids; only
+ *               the first ceil(sel_lens / block_size) entries of a row are read
+ *   sel_lens    [num_seqs][num_kv_heads] int32
+ *   kv_dtype    dtype: 16-bit pools of the query type (k_scales and v_scales
+ *               ignored), or PA_FP8_E4M3: block-scaled pools
+ *
+ * Usually the output of pa_select_blocks; any tables do.  Other arguments and
+ * device-value outcomes as pa_decode and pa_decode_fp8_block, per (sequence,
+ * KV head).
+ */
+int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const float* k_scales, const float* v_scales, const int32_t* sel_tables,
+                     int max_selected, const int32_t* sel_lens, int num_seqs, int num_heads,
+                     int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                     int dtype, int kv_dtype, void* stream);
 
 /*
  * pa_selftest_wait -- checks, on the device, the bounded wait that every

@@ -47,6 +47,16 @@ SIGNATURES = {
     "pa_append_and_decode_splitk": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _F,
                                          _F, _I, _I, _P, _SZ, _P]),
     "pa_prefill": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "pa_reshape_and_cache_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pa_decode_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "pa_decode_splitk_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _I,
+                                        _P, _SZ, _P]),
+    "pa_prefill_fp8_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                                  _P]),
+    "pa_update_key_bounds": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "pa_select_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "pa_select_blocks": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pa_decode_sparse": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
     "pa_selftest_wait": (_I, [_P, ctypes.c_uint, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_last_error": (ctypes.c_char_p, []),

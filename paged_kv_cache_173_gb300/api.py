@@ -325,6 +325,193 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     _lib.check("pa_prefill", st)
 
 
+def _need_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, num_blocks: int, num_kv_heads: int,
+                 device: torch.device):
+    """Pointers of the scale tables [N, Hk] (float32) beside a pair of block-scaled pools."""
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if not isinstance(t, torch.Tensor) or t.shape != (num_blocks, num_kv_heads):
+            raise ValueError(f"{name} must be [N, Hk] = [{num_blocks}, {num_kv_heads}], one scale per block and KV head")
+    return (_need(k_scales, "k_scales", torch.float32, device), _need(v_scales, "v_scales", torch.float32, device))
+
+
+def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                                   v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                   slot_mapping: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise key/value [T, Hk, d] (float16 or bfloat16) into the E4M3 pools [N, B, Hk, d]
+    at slot_mapping [T], with one scale per (block, KV head) in k_scales / v_scales [N, Hk]
+    (float32) taken from the data and grown as a block fills.  The tokens of one block
+    stand next to each other in slot_mapping."""
+    dev = _cuda_device(k_cache)
+    N, B, Hk, d = k_cache.shape
+    T = key.shape[0]
+    if key.shape != (T, Hk, d) or value.shape != (T, Hk, d) or v_cache.shape != k_cache.shape:
+        raise ValueError("key/value must be [T, Hk, d] matching the pools [N, B, Hk, d]")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    dt = key.dtype
+    st = _lib.lib().pa_reshape_and_cache_fp8_block(
+        _need(key, "key", dt, dev), _need(value, "value", dt, dev),
+        _need_codes(k_cache, "k_cache", dev), _need_codes(v_cache, "v_cache", dev), pks, pvs,
+        _need(slot_mapping, "slot_mapping", torch.int64, dev), T, N, B, Hk, d, _dtype_code(key),
+        _stream_ptr(k_cache, stream))
+    _lib.check("pa_reshape_and_cache_fp8_block", st)
+
+
+def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, scale: float,
+                        stream: Optional[torch.cuda.Stream] = None) -> None:
+    """pa_decode over block-scaled E4M3 pools: values are code * k_scales[block, head] (K) and
+    code * v_scales[block, head] (V); q and out are float16 or bfloat16."""
+    dev, S, H, d, N, B, Hk, M, (po, pq, pk, pv, pbt), pcl = _decode_common(
+        out, q, k_cache, v_cache, block_tables, context_lens, codes=True)
+    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    st = _lib.lib().pa_decode_fp8_block(po, pq, pk, pv, pks, pvs, pbt, M, pcl, S, H, Hk, d, B, N, float(scale),
+                                        _dtype_code(q), _stream_ptr(q, stream))
+    _lib.check("pa_decode_fp8_block", st)
+
+
+def pa_decode_splitk_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                               context_lens: torch.Tensor, scale: float, partition_size: int,
+                               workspace: torch.Tensor, max_num_partitions: Optional[int] = None,
+                               stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Split-K decode over block-scaled pools; follow with pa_splitk_reduce on the same stream."""
+    dev, S, H, d, N, B, Hk, M, (po, pq, pk, pv, pbt), pcl = _decode_common(
+        out, q, k_cache, v_cache, block_tables, context_lens, codes=True)
+    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    P = max_num_partitions or max_num_partitions_for(M, B, partition_size)
+    ws = _need(workspace, "workspace", workspace.dtype, dev)
+    st = _lib.lib().pa_decode_splitk_fp8_block(
+        po, pq, pk, pv, pks, pvs, pbt, M, pcl, S, H, Hk, d, B, N, float(scale), _dtype_code(q), int(partition_size),
+        int(P), ws, workspace.numel() * workspace.element_size(), _stream_ptr(q, stream))
+    _lib.check("pa_decode_splitk_fp8_block", st)
+
+
+def pa_prefill_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,
+                         scale: float, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """pa_prefill over block-scaled E4M3 pools (k_scales / v_scales [N, Hk])."""
+    dev = _cuda_device(q)
+    R, H, d = q.shape
+    N, B, Hk, d2 = k_cache.shape
+    S = int(context_lens.shape[0])
+    if d2 != d or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("q/out [rows, H, d] must match the pools [N, B, Hk, d]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start_loc.shape != (S + 1,):
+        raise ValueError("block_tables must be [S, M] and query_start_loc [S + 1]")
+    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    dt = q.dtype
+    st = _lib.lib().pa_prefill_fp8_block(
+        _need(out, "out", dt, dev), _need(q, "q", dt, dev), _need_codes(k_cache, "k_cache", dev),
+        _need_codes(v_cache, "v_cache", dev), pks, pvs, _need(block_tables, "block_tables", torch.int32, dev),
+        int(block_tables.shape[1]), _need(context_lens, "context_lens", torch.int32, dev),
+        _need(query_start_loc, "query_start_loc", torch.int32, dev), S, R, int(max_query_len), H, Hk, d, B, N,
+        float(scale), _dtype_code(q), _stream_ptr(q, stream))
+    _lib.check("pa_prefill_fp8_block", st)
+
+
+def _need_bounds(key_bounds: torch.Tensor, bound_exps: torch.Tensor, num_kv_heads: int, head_dim: int,
+                 device: torch.device):
+    if key_bounds.dim() != 4 or key_bounds.shape[1:] != (num_kv_heads, 2, head_dim):
+        raise ValueError(f"key_bounds must be [N, Hk, 2, d] with Hk = {num_kv_heads}, d = {head_dim}")
+    N = int(key_bounds.shape[0])
+    if bound_exps.shape != (N, num_kv_heads):
+        raise ValueError("bound_exps must be [N, Hk]")
+    return (N, _need(key_bounds, "key_bounds", torch.int8, device),
+            _need(bound_exps, "bound_exps", torch.int32, device))
+
+
+def pa_update_key_bounds(key: torch.Tensor, key_bounds: torch.Tensor, bound_exps: torch.Tensor,
+                         slot_mapping: torch.Tensor, block_size: int,
+                         stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Fold key [T, Hk, d] into the bounds of the blocks named by slot_mapping [T]: key_bounds
+    [N, Hk, 2, d] (int8 lo, hi) and bound_exps [N, Hk] (int32), lo * 2^e <= k <= hi * 2^e.
+    The tokens of one block stand next to each other in slot_mapping."""
+    dev = _cuda_device(key_bounds)
+    T, Hk, d = key.shape
+    N, pb, pe = _need_bounds(key_bounds, bound_exps, Hk, d, dev)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    st = _lib.lib().pa_update_key_bounds(
+        _need(key, "key", key.dtype, dev), pb, pe, _need(slot_mapping, "slot_mapping", torch.int64, dev), T, N,
+        int(block_size), Hk, d, _dtype_code(key), _stream_ptr(key_bounds, stream))
+    _lib.check("pa_update_key_bounds", st)
+
+
+def pa_select_workspace_bytes(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int) -> int:
+    return int(_lib.lib().pa_select_workspace_bytes(num_seqs, num_kv_heads, max_blocks_per_seq))
+
+
+def alloc_select_workspace(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int, device) -> torch.Tensor:
+    """A float32 device buffer of the size pa_select_workspace_bytes states."""
+    nbytes = pa_select_workspace_bytes(num_seqs, num_kv_heads, max_blocks_per_seq)
+    return torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=device)
+
+
+def pa_select_blocks(sel_tables: torch.Tensor, sel_lens: torch.Tensor, q: torch.Tensor, key_bounds: torch.Tensor,
+                     bound_exps: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     block_size: int, num_first: int, num_last: int, workspace: torch.Tensor,
+                     stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Choose the blocks that each (sequence, KV head) reads: the first num_first, the last
+    num_last and the best by the bounds of their keys, max_selected in all.  Writes
+    sel_tables [S, Hk, max_selected] (physical ids in position order, then -1) and
+    sel_lens [S, Hk] (tokens), both int32."""
+    dev = _cuda_device(q)
+    S, H, d = q.shape
+    if sel_tables.dim() != 3 or sel_tables.shape[0] != S:
+        raise ValueError("sel_tables must be [S, Hk, max_selected]")
+    Hk, K = int(sel_tables.shape[1]), int(sel_tables.shape[2])
+    if sel_lens.shape != (S, Hk):
+        raise ValueError("sel_lens must be [S, Hk]")
+    N, pb, pe = _need_bounds(key_bounds, bound_exps, Hk, d, dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, M] and context_lens [S]")
+    st = _lib.lib().pa_select_blocks(
+        _need(sel_tables, "sel_tables", torch.int32, dev), _need(sel_lens, "sel_lens", torch.int32, dev),
+        _need(q, "q", q.dtype, dev), pb, pe, _need(block_tables, "block_tables", torch.int32, dev),
+        int(block_tables.shape[1]), _need(context_lens, "context_lens", torch.int32, dev), S, H, Hk, d,
+        int(block_size), N, K, int(num_first), int(num_last), _dtype_code(q),
+        _need(workspace, "workspace", workspace.dtype, dev), workspace.numel() * workspace.element_size(),
+        _stream_ptr(q, stream))
+    _lib.check("pa_select_blocks", st)
+
+
+def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     sel_tables: torch.Tensor, sel_lens: torch.Tensor, scale: float,
+                     k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Decode with a block table per (sequence, KV head): sel_tables [S, Hk, max_selected] and
+    sel_lens [S, Hk] (pa_select_blocks writes them).  16-bit pools of the query type, or
+    block-scaled E4M3 pools with k_scales and v_scales [N, Hk]."""
+    dev = _cuda_device(q)
+    S, H, d = q.shape
+    N, B, Hk, d2 = k_cache.shape
+    if d2 != d or v_cache.shape != k_cache.shape or out.shape != q.shape:
+        raise ValueError("q/out [S, H, d] must match the pools [N, B, Hk, d]")
+    if sel_tables.dim() != 3 or sel_tables.shape[:2] != (S, Hk) or sel_lens.shape != (S, Hk):
+        raise ValueError("sel_tables must be [S, Hk, max_selected] and sel_lens [S, Hk]")
+    dt = _dtype_code(q)
+    if k_cache.dtype in _CODE_DTYPES:
+        if k_scales is None or v_scales is None:
+            raise ValueError("E4M3 pools need k_scales and v_scales [N, Hk]")
+        pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+        pk, pv, kv = _need_codes(k_cache, "k_cache", dev), _need_codes(v_cache, "v_cache", dev), PA_FP8_E4M3
+    else:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("16-bit pools take no scales")
+        pks = pvs = None
+        pk, pv, kv = _need(k_cache, "k_cache", q.dtype, dev), _need(v_cache, "v_cache", q.dtype, dev), dt
+    st = _lib.lib().pa_decode_sparse(
+        _need(out, "out", q.dtype, dev), _need(q, "q", q.dtype, dev), pk, pv, pks, pvs,
+        _need(sel_tables, "sel_tables", torch.int32, dev), int(sel_tables.shape[2]),
+        _need(sel_lens, "sel_lens", torch.int32, dev), S, H, Hk, d, B, N, float(scale), dt, kv,
+        _stream_ptr(q, stream))
+    _lib.check("pa_decode_sparse", st)
+
+
 def pa_selftest_wait(device=None, limit_us: int = 20000,
                      stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Run the library's bounded-wait self-test on `device` (default: the current CUDA

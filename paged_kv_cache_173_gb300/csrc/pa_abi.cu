@@ -281,6 +281,104 @@ int check_reshape(const void* key, const void* value, const void* k_cache, const
   return PA_OK;
 }
 
+// The checks shared by both prefills.
+int check_prefill(const void* out, const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                  const int32_t* query_start_loc, int num_seqs, int num_rows, int max_query_len, int num_heads,
+                  int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale, int dtype) {
+  const int st = check_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                              num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "prefill supports head_dim 64 or 128 (got %d)", head_dim);
+  const int G = num_heads / num_kv_heads;
+  if (128 % G != 0)
+    return fail(PA_ERR_UNSUPPORTED, "prefill needs a query group size dividing 128 (got %d)", G);
+  if (max_query_len < 0 || num_rows < 0)
+    return fail(PA_ERR_INVALID_ARG, "max_query_len (%d) and num_rows (%d) must be >= 0", max_query_len, num_rows);
+  if (num_seqs == 0 || max_query_len == 0 || num_rows == 0) return PA_OK;
+  if (!query_start_loc) return fail(PA_ERR_INVALID_ARG, "query_start_loc is NULL");
+  if (!aligned(query_start_loc, 4)) return fail(PA_ERR_INVALID_ARG, "query_start_loc must be 4-byte aligned");
+  return PA_OK;
+}
+
+// A pair of tables beside the pools (scales; bounds and exponents).
+int check_side(const void* a, const void* b, const char* what) {
+  if (!a || !b) return fail(PA_ERR_INVALID_ARG, "%s must not be NULL", what);
+  if (!aligned(a, 4) || !aligned(b, 4)) return fail(PA_ERR_INVALID_ARG, "%s must be 4-byte aligned", what);
+  return PA_OK;
+}
+
+// Shapes that the writers of per-block side data share with the decode.
+int check_block_shape(int block_size, int num_blocks, int num_kv_heads, int head_dim) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(PA_ERR_UNSUPPORTED, "head_dim %d is not supported (64, 128 or 256)", head_dim);
+  if (!block_size_supported(block_size))
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d is not supported (16, 32, 64, 128 or 256)", block_size);
+  if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size exceeds 2^31 - 1 token slots");
+  return PA_OK;
+}
+
+pa::BlockDecodeArgs block_args(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scales, const float* v_scales, const int32_t* tables, int max_blocks,
+                               const int32_t* lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, float scale, int dtype, int kv_dtype) {
+  pa::BlockDecodeArgs a{};
+  a.dtype = dtype;
+  a.kv_dtype = kv_dtype;
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = tables;
+  a.context_lens = lens;
+  a.max_blocks_per_seq = max_blocks;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.scale = scale;
+  a.partition_size = max_blocks * block_size;
+  a.max_num_partitions = 1;
+  return a;
+}
+
+// pa_decode_fp8_block / pa_decode_splitk_fp8_block.
+int block_decode_impl(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                      const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, float scale, int dtype, bool splitk, int partition_size,
+                      int max_num_partitions, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                        num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  if (splitk) {
+    st = check_splitk(max_blocks_per_seq, block_size, partition_size, max_num_partitions, workspace,
+                      workspace_bytes, num_seqs, num_heads, head_dim);
+    if (st != PA_OK) return st;
+  }
+  if (num_seqs == 0) return ok();
+  st = check_side(k_scales, v_scales, "k_scales and v_scales");
+  if (st != PA_OK) return st;
+  pa::BlockDecodeArgs a = block_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks_per_seq,
+                                     context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                     num_blocks, scale, dtype, PA_FP8_E4M3);
+  if (splitk) {
+    a.ws = static_cast<float*>(workspace);
+    a.partition_size = partition_size;
+    a.max_num_partitions = max_num_partitions;
+  }
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return cuda_status(dtype == PA_BF16 ? pa::launch_block_decode_bf16(a, cs) : pa::launch_block_decode_f16(a, cs),
+                     splitk ? "block-scaled split-K decode launch" : "block-scaled decode launch");
+}
+
 }  // namespace
 
 namespace pa {
@@ -504,24 +602,152 @@ int pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cach
                const int32_t* query_start_loc, int num_seqs, int num_rows, int max_query_len,
                int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
                float scale, int dtype, void* stream) {
-  int st = check_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-                        num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-                        dtype);
+  const int st = check_prefill(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                               query_start_loc, num_seqs, num_rows, max_query_len, num_heads, num_kv_heads,
+                               head_dim, block_size, num_blocks, scale, dtype);
   if (st != PA_OK) return st;
-  if (head_dim != 64 && head_dim != 128)
-    return fail(PA_ERR_UNSUPPORTED, "prefill supports head_dim 64 or 128 (got %d)", head_dim);
-  const int G = num_heads / num_kv_heads;
-  if (128 % G != 0)
-    return fail(PA_ERR_UNSUPPORTED, "prefill needs a query group size dividing 128 (got %d)", G);
-  if (max_query_len < 0 || num_rows < 0)
-    return fail(PA_ERR_INVALID_ARG, "max_query_len (%d) and num_rows (%d) must be >= 0", max_query_len, num_rows);
   if (num_seqs == 0 || max_query_len == 0 || num_rows == 0) return ok();
-  if (!query_start_loc) return fail(PA_ERR_INVALID_ARG, "query_start_loc is NULL");
-  if (!aligned(query_start_loc, 4)) return fail(PA_ERR_INVALID_ARG, "query_start_loc must be 4-byte aligned");
   pa::PrefillArgs a{dtype,      out,       q,           k_cache,      v_cache,      block_tables,
                     context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_rows,
                     max_query_len, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale};
   return cuda_status(pa::launch_prefill(a, static_cast<cudaStream_t>(stream)), "prefill launch");
+}
+
+int pa_reshape_and_cache_fp8_block(const void* key, const void* value, void* k_cache, void* v_cache,
+                                   float* k_scales, float* v_scales, const int64_t* slot_mapping,
+                                   int num_tokens, int num_blocks, int block_size, int num_kv_heads,
+                                   int head_dim, int dtype, void* stream) {
+  int st = check_reshape(key, value, k_cache, v_cache, slot_mapping, num_tokens, num_blocks, block_size,
+                         num_kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  st = check_block_shape(block_size, num_blocks, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (num_tokens == 0) return ok();
+  st = check_side(k_scales, v_scales, "k_scales and v_scales");
+  if (st != PA_OK) return st;
+  pa::BlockWriteArgs a{key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, num_tokens,
+                       num_blocks, block_size, num_kv_heads, head_dim, dtype};
+  return cuda_status(pa::launch_block_write(a, static_cast<cudaStream_t>(stream)),
+                     "reshape_and_cache_fp8_block launch");
+}
+
+int pa_decode_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                        int block_size, int num_blocks, float scale, int dtype, void* stream) {
+  return block_decode_impl(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks_per_seq,
+                           context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                           dtype, false, 0, 1, nullptr, 0, stream);
+}
+
+int pa_decode_splitk_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_heads,
+                               int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                               int dtype, int partition_size, int max_num_partitions, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return block_decode_impl(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks_per_seq,
+                           context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                           dtype, true, partition_size, max_num_partitions, workspace, workspace_bytes, stream);
+}
+
+int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                         const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int num_rows,
+                         int max_query_len, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                         int num_blocks, float scale, int dtype, void* stream) {
+  int st = check_prefill(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
+                         num_seqs, num_rows, max_query_len, num_heads, num_kv_heads, head_dim, block_size,
+                         num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0 || max_query_len == 0 || num_rows == 0) return ok();
+  st = check_side(k_scales, v_scales, "k_scales and v_scales");
+  if (st != PA_OK) return st;
+  pa::BlockPrefillArgs b{{dtype, out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                          max_blocks_per_seq, num_seqs, num_rows, max_query_len, num_heads, num_kv_heads, head_dim,
+                          block_size, num_blocks, scale},
+                         k_scales,
+                         v_scales};
+  return cuda_status(pa::launch_block_prefill(b, static_cast<cudaStream_t>(stream)), "block-scaled prefill launch");
+}
+
+int pa_update_key_bounds(const void* key, int8_t* key_bounds, int32_t* bound_exps, const int64_t* slot_mapping,
+                         int num_tokens, int num_blocks, int block_size, int num_kv_heads, int head_dim, int dtype,
+                         void* stream) {
+  // the checks of a cache write, with the bounds in the place of the pools
+  int st = check_reshape(key, key, key_bounds, key_bounds, slot_mapping, num_tokens, num_blocks, block_size,
+                         num_kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  st = check_block_shape(block_size, num_blocks, num_kv_heads, head_dim);
+  if (st != PA_OK) return st;
+  if (num_tokens == 0) return ok();
+  st = check_side(key_bounds, bound_exps, "key_bounds and bound_exps");
+  if (st != PA_OK) return st;
+  pa::KeyBoundsArgs a{key, key_bounds, bound_exps, slot_mapping, num_tokens, num_blocks, block_size,
+                      num_kv_heads, head_dim, dtype};
+  return cuda_status(pa::launch_key_bounds(a, static_cast<cudaStream_t>(stream)), "key bounds launch");
+}
+
+size_t pa_select_workspace_bytes(int num_seqs, int num_kv_heads, int max_blocks_per_seq) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0) return 0;
+  return static_cast<size_t>(num_seqs) * num_kv_heads * pa::select_pitch(max_blocks_per_seq) * sizeof(float);
+}
+
+int pa_select_blocks(int32_t* sel_tables, int32_t* sel_lens, const void* q, const int8_t* key_bounds,
+                     const int32_t* bound_exps, const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                     int block_size, int num_blocks, int max_selected, int num_first, int num_last, int dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  // the checks of a decode, with the bounds in the place of the pools
+  int st = check_decode(q, q, key_bounds, key_bounds, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                        num_heads, num_kv_heads, head_dim, block_size, num_blocks, 1.f, dtype);
+  if (st != PA_OK) return st;
+  if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
+  if (num_first < 0 || num_last < 1)
+    return fail(PA_ERR_INVALID_ARG, "num_first (%d) must be >= 0 and num_last (%d) >= 1", num_first, num_last);
+  if (static_cast<int64_t>(num_first) + num_last > max_selected)
+    return fail(PA_ERR_INVALID_ARG, "num_first (%d) + num_last (%d) exceed max_selected (%d)", num_first, num_last,
+                max_selected);
+  if (static_cast<int64_t>(max_selected) * block_size > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "max_selected * block_size exceeds 2^31 - 1");
+  if (num_seqs == 0) return ok();
+  if (!sel_tables || !sel_lens) return fail(PA_ERR_INVALID_ARG, "sel_tables and sel_lens must not be NULL");
+  if (!aligned(sel_tables, 4) || !aligned(sel_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "sel_tables and sel_lens must be 4-byte aligned");
+  st = check_side(key_bounds, bound_exps, "key_bounds and bound_exps");
+  if (st != PA_OK) return st;
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned(workspace, 16)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const size_t need = pa_select_workspace_bytes(num_seqs, num_kv_heads, max_blocks_per_seq);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID_ARG, "workspace_bytes %zu < %zu required", workspace_bytes, need);
+  pa::SelectArgs a{sel_tables, sel_lens, q, key_bounds, bound_exps, block_tables, context_lens,
+                   static_cast<float*>(workspace), max_blocks_per_seq, num_seqs, num_heads, num_kv_heads, head_dim,
+                   block_size, num_blocks, max_selected, num_first, num_last, dtype};
+  return cuda_status(pa::launch_select_blocks(a, static_cast<cudaStream_t>(stream)), "block selection launch");
+}
+
+int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                     const float* v_scales, const int32_t* sel_tables, int max_selected, const int32_t* sel_lens,
+                     int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                     float scale, int dtype, int kv_dtype, void* stream) {
+  if (kv_dtype != PA_FP8_E4M3 && kv_dtype != dtype)
+    return fail(PA_ERR_UNSUPPORTED, "kv_dtype %d must equal dtype %d or be PA_FP8_E4M3", kv_dtype, dtype);
+  int st = check_decode(out, q, k_cache, v_cache, sel_tables, max_selected, sel_lens, num_seqs, num_heads,
+                        num_kv_heads, head_dim, block_size, num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0) return ok();
+  const bool fp8 = kv_dtype == PA_FP8_E4M3;
+  if (fp8) {
+    st = check_side(k_scales, v_scales, "k_scales and v_scales");
+    if (st != PA_OK) return st;
+  }
+  const pa::BlockDecodeArgs a = block_args(out, q, k_cache, v_cache, fp8 ? k_scales : nullptr, fp8 ? v_scales : nullptr,
+                                           sel_tables, max_selected, sel_lens, num_seqs, num_heads, num_kv_heads,
+                                           head_dim, block_size, num_blocks, scale, dtype, kv_dtype);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return cuda_status(dtype == PA_BF16 ? pa::launch_sparse_decode_bf16(a, cs) : pa::launch_sparse_decode_f16(a, cs),
+                     "sparse decode launch");
 }
 
 int pa_splitk_reduce(void* out, const void* workspace, size_t workspace_bytes,

@@ -1,0 +1,665 @@
+// pa_block_decode.cuh -- decode attention with side data per (block, KV head):
+// E4M3 pools whose scale is one float per (block, KV head), and tables of
+// blocks per (sequence, KV head) (block-sparse decode, over those pools or over
+// 16-bit ones).  Included by one translation unit per query type and use.
+//
+//  block_decode_kernel   the pipeline of paged_decode_kernel (pa_decode.cuh):
+//                        one CTA per (KV head, partition, sequence), each warp
+//                        streams 16-token chunks through a private ring of TMA
+//                        stages; clusters split a sequence when the pairs do
+//                        not fill the GPU.
+//
+// The mathematics of the scales.  Block b of a sequence holds the keys
+// ks_b * code and the values vs_b * code.  With s_i the base-2 score of token
+// i (scale * log2(e) * ks_b * q . code_i) and vs_b = m_b * 2^e_b, 1 <= m_b < 2,
+//
+//   out = sum_i 2^s_i vs_b code_i / sum_i 2^s_i
+//       = sum_i w_i m_b code_i / sum_i w_i 2^-e_b,   w_i = 2^(s_i + e_b - M),
+//
+// with M the running maximum of s_i + e_b.  So the value scale moves into the
+// exponent of the one exponential that each score needs anyway: the weights
+// that meet the codes lie in [0, 2) whatever the scales are, the accumulators
+// change scale only when M moves, and the sum of weights takes one multiply
+// by the power of two 2^-e_b.  Nothing is lost when a block of large values
+// stands next to one of tiny values: the dominant products set M.  m_b is 1
+// for the power-of-two scales that pa_reshape_and_cache_fp8_block makes.
+//
+// Queries enter the MMAs as float16 beside the widened codes (exact in
+// float16).  A bfloat16 query row is first scaled by the power of two that
+// brings its largest element to [2^14, 2^15): exact for every element within
+// 2^-28 of the largest, and within 2^-39 of the largest's size below that; the
+// inverse multiplies the scores in float32.
+#pragma once
+
+#include "pa_block.cuh"
+#include "pa_decode.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr float kMinValueScale = 5.421010862427522e-20f;  // 2^-64: smaller value scales read as 0
+
+struct BlockDecodeParams {
+  CUtensorMap tmap_k;  // as DecodeParams: [N*B rows][Hk][d], 16-row boxes
+  CUtensorMap tmap_v;
+  void* out;
+  const void* q;
+  const float* k_scales;  // [N][Hk]; null for 16-bit pools
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* ws_o;
+  float* ws_m;
+  float* ws_l;
+  int max_blocks_per_seq;
+  int num_heads;
+  int num_kv_heads;
+  int group;
+  int block_size;
+  int chunks_per_block_log2;
+  int num_blocks;
+  int partition_chunks;
+  int max_num_partitions;
+  int num_seqs;
+  float scale_log2;  // scale * log2(e)
+};
+
+// Query fragments for E4M3 keys (the order of load_q_frags_e4m3) as float16,
+// and inv[nt] = the factor that undoes row nt * 8 + lane / 4's scaling.
+template <typename T, int HEAD_DIM, int NT>
+__device__ __forceinline__ void load_q_frags_scaled(uint32_t (&qf)[HEAD_DIM / 16][NT][2], float (&inv)[NT],
+                                                    const void* q, int s, int H, int kvh, int G, int lane) {
+  load_q_frags_e4m3<HEAD_DIM, NT>(qf, q, s, H, kvh, G, G, lane);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    inv[nt] = 1.f;
+    if constexpr (!std::is_same<T, __half>::value) {
+      float amax = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < HEAD_DIM / 16; ++ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f = unpack_bf162(qf[ks][nt][j]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 2));
+      const int x = (__float_as_int(amax) >> 23) - 127;  // -127 for zeros and subnormals
+      const int e = min(14 - x, 126);
+      const float f = pow2f(e);
+      inv[nt] = pow2f(-e);
+#pragma unroll
+      for (int ks = 0; ks < HEAD_DIM / 16; ++ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 v = unpack_bf162(qf[ks][nt][j]);
+          qf[ks][nt][j] = pack_half2(v.x * f, v.y * f);
+        }
+    }
+  }
+}
+
+// The scale of one chunk's keys, and of its values as m * 2^e.
+struct ChunkScale {
+  float ks;
+  float vm;    // mantissa in [1, 2), or 0 for values that read as zero
+  float ve;    // exponent
+  float vinv;  // 2^-e
+  bool bad;    // a scale that is negative, infinite or NaN
+
+  __device__ __forceinline__ void set(float k, float v) {
+    bad = !(k >= 0.f && k <= kFloatMax && v >= 0.f && v <= kFloatMax);
+    ks = k;
+    const bool zero = !(v >= kMinValueScale);
+    const int bits = __float_as_int(zero ? kMinValueScale : v);
+    const int e = (bits >> 23) - 127;
+    vm = zero ? 0.f : __int_as_float((bits & 0x7fffff) | 0x3f800000);
+    ve = static_cast<float>(e);
+    vinv = __int_as_float((127 - min(e, 126)) << 23);
+    if (e > 126) vinv = 0.5f * vinv;  // 2^-127, a subnormal
+  }
+};
+
+// softmax_step (pa_decode.cuh) with a scale per chunk: sl[nt][j] is the
+// base-2 factor of query nt * 8 + 2c + j without the key scale.  P^T enters
+// as float16(w * m); the running sum adds w * 2^-e unrounded.
+template <int HEAD_DIM, int NT, int NSUB>
+__device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, const float (&sacc)[NSUB][NT][4],
+                                                    const int (&valid)[NSUB], const float (&sl)[NT][2],
+                                                    const ChunkScale (&cs)[NSUB], int lane,
+                                                    uint32_t (&pb)[NSUB][NT][2]) {
+  constexpr int KSTEPS = HEAD_DIM / 16;
+  const int g = lane >> 2;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float x[NSUB][4];
+#pragma unroll
+    for (int sb = 0; sb < NSUB; ++sb) {
+      const bool v0 = g < valid[sb];
+      const bool v1 = g + 8 < valid[sb];
+      const float f0 = sl[nt][0] * cs[sb].ks, f1 = sl[nt][1] * cs[sb].ks;
+      x[sb][0] = v0 ? fmaf(sacc[sb][nt][0], f0, cs[sb].ve) : -INFINITY;
+      x[sb][1] = v0 ? fmaf(sacc[sb][nt][1], f1, cs[sb].ve) : -INFINITY;
+      x[sb][2] = v1 ? fmaf(sacc[sb][nt][2], f0, cs[sb].ve) : -INFINITY;
+      x[sb][3] = v1 ? fmaf(sacc[sb][nt][3], f1, cs[sb].ve) : -INFINITY;
+    }
+    float mx0 = fmaxf(x[0][0], x[0][2]);
+    float mx1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+    for (int sb = 1; sb < NSUB; ++sb) {
+      mx0 = fmaxf(mx0, fmaxf(x[sb][0], x[sb][2]));
+      mx1 = fmaxf(mx1, fmaxf(x[sb][1], x[sb][3]));
+    }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, off));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, off));
+    }
+    const float mn0 = fmaxf(acc.m[nt][0], mx0);
+    const float mn1 = fmaxf(acc.m[nt][1], mx1);
+    const float cr0 = ex2(acc.m[nt][0] - mn0);
+    const float cr1 = ex2(acc.m[nt][1] - mn1);
+    const bool grew = __any_sync(FULL_MASK, (mn0 != acc.m[nt][0]) | (mn1 != acc.m[nt][1]));
+    acc.m[nt][0] = mn0;
+    acc.m[nt][1] = mn1;
+    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+    for (int sb = 0; sb < NSUB; ++sb) {
+      const float p0 = ex2(x[sb][0] - mn0), p1 = ex2(x[sb][1] - mn1);  // token g
+      const float p2 = ex2(x[sb][2] - mn0), p3 = ex2(x[sb][3] - mn1);  // token g + 8
+      sum0 = fmaf(p0 + p2, cs[sb].vinv, sum0);
+      sum1 = fmaf(p1 + p3, cs[sb].vinv, sum1);
+      const float m = cs[sb].vm;
+      pb[sb][nt][0] = movmatrix_trans(pack_half2(p0 * m, p1 * m));  // P^T tokens 0-7 as the B fragment
+      pb[sb][nt][1] = movmatrix_trans(pack_half2(p2 * m, p3 * m));  // P^T tokens 8-15
+    }
+    acc.l[nt][0] = fmaf(acc.l[nt][0], cr0, sum0);
+    acc.l[nt][1] = fmaf(acc.l[nt][1], cr1, sum1);
+    if (grew) {  // a running maximum moved: rescale the accumulators
+#pragma unroll
+      for (int dm = 0; dm < KSTEPS; ++dm) {
+        acc.o[dm][nt][0] *= cr0;
+        acc.o[dm][nt][1] *= cr1;
+        acc.o[dm][nt][2] *= cr0;
+        acc.o[dm][nt][3] *= cr1;
+      }
+    }
+  }
+}
+
+// One or two chunks of a stage (NSUB): scores, softmax step, P V.  Chunks
+// before the last are full.
+template <int HEAD_DIM, int NT, int ROW_BYTES, int NSUB>
+__device__ __forceinline__ void attend_scaled(WarpAcc<HEAD_DIM, NT>& acc, const uint32_t (&qf)[HEAD_DIM / 16][NT][2],
+                                              uint32_t kb, uint32_t chunk_bytes, uint32_t half_bytes, int valid_last,
+                                              const float (&sl)[NT][2], const ChunkScale (&cs)[NSUB], int lane) {
+  const uint32_t tok = e4m3_tok(lane), uo = e4m3_uo(lane);
+  float sacc[NSUB][NT][4];
+  int valid[NSUB];
+#pragma unroll
+  for (int sb = 0; sb < NSUB; ++sb) {
+    qk_e4m3<HEAD_DIM, NT, ROW_BYTES>(sacc[sb], qf, kb + sb * chunk_bytes, tok, uo);
+    valid[sb] = sb == NSUB - 1 ? valid_last : CHUNK;
+  }
+  uint32_t pb[NSUB][NT][2];
+  softmax_step_scaled<HEAD_DIM, NT, NSUB>(acc, sacc, valid, sl, cs, lane, pb);
+  uint32_t mlo, mhi;
+  v_masks(valid_last, lane, mlo, mhi);
+#pragma unroll
+  for (int sb = 0; sb < NSUB - 1; ++sb)
+    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[sb], kb + sb * chunk_bytes + half_bytes, tok, uo, mlo, mhi);
+  const uint32_t vb = kb + (NSUB - 1) * chunk_bytes + half_bytes;
+  if (valid_last == CHUNK) {
+    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi);
+  } else {  // the last chunk of the sequence
+    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, true>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi);
+  }
+}
+
+// KV: E4M3 (block scales), or T (16-bit pools; PER_HEAD only).  PER_HEAD: the
+// table row and the context length belong to (sequence, KV head).  MODE as
+// decode_cta: MODE_GRID, MODE_CLUSTER or MODE_LONGEST_FIRST.
+template <typename T, typename KV, int HEAD_DIM, int NT, int WARPS, int STAGES, int MODE, bool PER_HEAD>
+__global__ void __launch_bounds__(WARPS * 32) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+  constexpr bool CLUSTER = MODE == MODE_CLUSTER;
+  constexpr bool LONGEST = MODE == MODE_LONGEST_FIRST;
+  static_assert(!(LONGEST && PER_HEAD), "sparse batches are not ranked");
+  constexpr bool FP8 = kIsFp8<KV>;
+  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, kElemBytes<KV>>;
+  constexpr int KSTEPS = HEAD_DIM / 16;
+  constexpr int GMAX = Cfg::GMAX;
+  constexpr int CPS = Cfg::CPS;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+  uint8_t* ring = smem + Cfg::BAR_BYTES;
+
+  const int kvh = blockIdx.x;
+  const int part = blockIdx.y;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = p.group;
+  const int H = p.num_heads;
+
+  grid_dependency_wait();
+
+  const int cap = p.max_blocks_per_seq * p.block_size;
+  int s = static_cast<int>(blockIdx.z);
+  int ctx;
+  if constexpr (LONGEST) {  // as decode_cta: CTA z takes the sequence of rank z
+    int* lens = reinterpret_cast<int*>(ring);
+    int* pick = lens + kLongestFirstMax;
+    const int S = p.num_seqs;
+    for (int t = threadIdx.x; t < S; t += WARPS * 32) lens[t] = __ldg(p.context_lens + t);
+    __syncthreads();
+    for (int t = threadIdx.x; t < S; t += WARPS * 32) {
+      const int ct = lens[t];
+      int rank = 0;
+      for (int j = 0; j < S; ++j) {
+        const int cj = lens[j];
+        rank += (cj > ct) | ((cj == ct) & (j < t));
+      }
+      if (rank == s) *pick = t;
+    }
+    __syncthreads();
+    s = *pick;
+    ctx = lens[s];
+    __syncthreads();
+  } else {
+    ctx = __ldg(p.context_lens + (PER_HEAD ? static_cast<size_t>(s) * p.num_kv_heads + kvh : static_cast<size_t>(s)));
+  }
+  const int cpb_log2 = p.chunks_per_block_log2;
+  const int table_chunks = p.max_blocks_per_seq << cpb_log2;
+  const bool ctx_bad = ctx < 0 || ctx > cap;
+  const int nchunks = ctx_bad ? 0 : (ctx + CHUNK - 1) / CHUNK;
+  const int nclu = CLUSTER ? static_cast<int>(gridDim.y) : 1;
+  const int c0 = CLUSTER ? static_cast<int>((static_cast<int64_t>(part) * nchunks) / nclu) : part * p.partition_chunks;
+  const int cmax = CLUSTER ? static_cast<int>((static_cast<int64_t>(part + 1) * nchunks) / nclu)
+                           : min(c0 + p.partition_chunks, table_chunks);
+  const int first = c0 + warp;
+  const int nk_cap = first < cmax ? (cmax - first + WARPS - 1) / WARPS : 0;
+
+  uint32_t qf[KSTEPS][NT][2];
+  float sl[NT][2];  // base-2 score factor of queries nt * 8 + 2c, + 1
+  if constexpr (FP8) {
+    float inv[NT];
+    load_q_frags_scaled<T, HEAD_DIM, NT>(qf, inv, p.q, s, H, kvh, G, lane);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        sl[nt][j] = std::is_same<T, __half>::value
+                        ? p.scale_log2
+                        : p.scale_log2 * __shfl_sync(FULL_MASK, inv[nt], (2 * (lane & 3) + j) << 2);
+  } else {
+    load_q_frags<HEAD_DIM, NT>(qf, p.q, s, H, kvh, G, G, lane);
+  }
+
+  // ---- block-table window, as decode_cta; beside it the window's scales.
+  //      Stages are consumed at most STAGES * CPS <= 32 chunks after they are
+  //      issued, so a consumed chunk lies in the current or the last window.
+  const int32_t* bt =
+      p.block_tables +
+      (PER_HEAD ? static_cast<size_t>(s) * p.num_kv_heads + kvh : static_cast<size_t>(s)) * p.max_blocks_per_seq;
+  auto win_load = [&](int kbase) -> int {
+    const int k = kbase + lane;
+    if (k >= nk_cap) return 0;
+    return __ldg(bt + ((first + k * WARPS) >> cpb_log2));
+  };
+  static_assert(STAGES * CPS <= 32, "the scale windows cover the chunks in flight");
+  int win_cur = win_load(0);
+  int win_nxt = win_load(32);
+  float ks_cur = 0.f, vs_cur = 0.f, ks_last = 0.f, vs_last = 0.f;
+  int win_index = 0;
+  auto scales_load = [&]() {  // the current window's; entries past the context may be any number
+    if constexpr (FP8) {
+      const bool in = static_cast<unsigned>(win_cur) < static_cast<unsigned>(p.num_blocks);
+      const size_t at = static_cast<size_t>(in ? win_cur : 0) * p.num_kv_heads + kvh;
+      ks_cur = __ldg(p.k_scales + at);
+      vs_cur = __ldg(p.v_scales + at);
+    }
+  };
+
+  uint64_t* wbar = bars + warp * STAGES;
+  uint8_t* wring = ring + warp * STAGES * Cfg::STAGE_BYTES;
+  if (lane == 0) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&wbar[i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  const int nparts = CLUSTER ? nclu : (nchunks + p.partition_chunks - 1) / p.partition_chunks;
+  if (nchunks == 0) {  // empty: zeros; impossible length: NaN.  Written once.
+    if (part == 0) {
+      const T v = to_elem<T>(ctx_bad ? NAN : 0.f);
+      T* o = static_cast<T*>(p.out) + (static_cast<size_t>(s) * H + kvh * G) * HEAD_DIM;
+      for (int i = threadIdx.x; i < G * HEAD_DIM; i += WARPS * 32) o[i] = v;
+    }
+    allow_dependent_launch();
+    return;  // in a cluster every CTA takes this exit together
+  }
+  if (!CLUSTER && part >= nparts) {
+    allow_dependent_launch();
+    return;
+  }
+  const bool single = !CLUSTER && nparts == 1;
+  const int c1 = CLUSTER ? cmax : min(c0 + p.partition_chunks, nchunks);
+  const int nk = first < c1 ? (c1 - first + WARPS - 1) / WARPS : 0;
+  const bool empty = CLUSTER && c1 <= c0;  // a short sequence: nothing for this CTA
+
+  const int nst = (nk + CPS - 1) / CPS;
+  int issued = 0;
+  bool bad = false;
+
+  auto issue_next = [&]() {
+    const int it = issued;
+    const int slot = it % STAGES;
+    const int nload = min(CPS, nk - it * CPS);
+    uint8_t* dst = wring + slot * Cfg::STAGE_BYTES;
+    if (lane == 0) mbar_arrive_expect_tx(&wbar[slot], nload * Cfg::CHUNK_BYTES);
+#pragma unroll
+    for (int j = 0; j < CPS; ++j) {
+      const int k = it * CPS + j;
+      if (j > 0 && k >= nk) break;  // warp-uniform
+      if (k > 0 && (k & 31) == 0) {
+        win_cur = win_nxt;
+        win_nxt = win_load(k + 32);
+        ks_last = ks_cur;
+        vs_last = vs_cur;
+        scales_load();
+        ++win_index;
+      }
+      int phys = __shfl_sync(FULL_MASK, win_cur, k & 31);
+      if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
+        bad = true;  // never read outside the pool; the result becomes NaN
+        phys = 0;
+      }
+      const int ch = first + k * WARPS;
+      const int row0 = (ch & ((1 << cpb_log2) - 1)) * CHUNK;
+      if (lane == 0) {
+        uint8_t* cd = dst + j * Cfg::CHUNK_BYTES;
+        const int y = phys * p.block_size + row0;
+#pragma unroll
+        for (int b = 0; b < Cfg::DBOX; ++b) {
+          tma_load_3d(cd + b * Cfg::BOX_B, &p.tmap_k, b * Cfg::BOX_ELEMS, kvh, y, &wbar[slot]);
+          tma_load_3d(cd + Cfg::HALF_BYTES + b * Cfg::BOX_B, &p.tmap_v, b * Cfg::BOX_ELEMS, kvh, y, &wbar[slot]);
+        }
+      }
+    }
+    ++issued;
+  };
+
+#pragma unroll 1
+  for (int i = 0; i < STAGES && i < nst; ++i) issue_next();
+  if (nst > 0) scales_load();  // the first window's, behind its copies (no window moves before)
+
+  WarpAcc<HEAD_DIM, NT> acc;
+  acc.reset();
+
+  auto chunk_scale = [&](int k) {
+    ChunkScale c;
+    const bool cur = (k >> 5) == win_index;
+    c.set(__shfl_sync(FULL_MASK, cur ? ks_cur : ks_last, k & 31), __shfl_sync(FULL_MASK, cur ? vs_cur : vs_last, k & 31));
+    bad |= c.bad;
+    return c;
+  };
+
+  int consumed = 0;
+  bool timed_out = false;
+#pragma unroll 1
+  for (; consumed < nst; ++consumed) {
+    const int it = consumed;
+    const int slot = it % STAGES;
+    const bool ok = mbar_wait_bounded(&wbar[slot], (it / STAGES) & 1, WAIT_LIMIT_NS);
+    if (!__all_sync(FULL_MASK, ok)) {  // a warp-uniform decision
+      timed_out = true;
+      break;
+    }
+    const int k0 = it * CPS;
+    const int ch = first + k0 * WARPS;
+    const int valid = min(CHUNK, ctx - ch * CHUNK);
+    const uint32_t stage = smem_addr(wring + slot * Cfg::STAGE_BYTES);
+    if constexpr (FP8) {
+      if (CPS == 2 && k0 + 1 < nk) {
+        const int valid2 = min(CHUNK, ctx - (ch + WARPS) * CHUNK);
+        const ChunkScale cs[2] = {chunk_scale(k0), chunk_scale(k0 + 1)};
+        attend_scaled<HEAD_DIM, NT, Cfg::ROW_BYTES, 2>(acc, qf, stage, Cfg::CHUNK_BYTES, Cfg::HALF_BYTES, valid2, sl,
+                                                       cs, lane);
+      } else {
+        const ChunkScale cs[1] = {chunk_scale(k0)};
+        attend_scaled<HEAD_DIM, NT, Cfg::ROW_BYTES, 1>(acc, qf, stage, Cfg::CHUNK_BYTES, Cfg::HALF_BYTES, valid, sl,
+                                                       cs, lane);
+      }
+    } else {
+      attend_chunk<T, HEAD_DIM, NT>(acc, qf, stage, Cfg::HALF_BYTES, valid, p.scale_log2, lane);
+    }
+    fence_proxy_async_smem();  // this lane's reads of the slot precede the refill's writes
+    __syncwarp();
+    if (issued < nst) issue_next();
+  }
+
+  if (timed_out) {
+    bad = true;
+    for (int k = consumed; k < issued; ++k)
+      (void)mbar_wait_bounded(&wbar[k % STAGES], (k / STAGES) & 1, WAIT_LIMIT_NS);
+  }
+
+  reduce_warp_sums<HEAD_DIM, NT>(acc);
+
+  __syncthreads();  // every warp is done with its ring: reuse it for the merge
+  float* mo = reinterpret_cast<float*>(ring);
+  float* mm = mo + WARPS * GMAX * Cfg::MO_PITCH;
+  float* ml = mm + WARPS * GMAX;
+  int* mbad = reinterpret_cast<int*>(ml + WARPS * GMAX);
+  store_warp_state<HEAD_DIM, NT, FP8>(acc, mo + warp * GMAX * Cfg::MO_PITCH, mm + warp * GMAX, ml + warp * GMAX,
+                                      Cfg::MO_PITCH, lane);
+  if (lane == 0) mbad[warp] = bad ? 1 : 0;
+  __syncthreads();
+
+  bool any_bad = false;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) any_bad |= mbad[w] != 0;
+
+  for (int idx = threadIdx.x; idx < G * HEAD_DIM; idx += WARPS * 32) {
+    const int head = idx / HEAD_DIM;
+    const int d = idx - head * HEAD_DIM;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mm[w * GMAX + head]);
+    float L = 0.f, O = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ex2(mm[w * GMAX + head] - M);  // warps without chunks: 2^-inf = 0
+        L += ml[w * GMAX + head] * f;
+        O += mo[(w * GMAX + head) * Cfg::MO_PITCH + d] * f;
+      }
+    }
+    // no positive sum: a cluster CTA without chunks (weight 0), or NaN scores
+    const bool none = !(L > 0.f) && !empty;
+    const float r = any_bad || none ? NAN : (empty ? 0.f : O / L);
+    const size_t qrow = static_cast<size_t>(s) * H + kvh * G + head;
+    if (CLUSTER) {
+      float* cta = reinterpret_cast<float*>(ring + Cfg::CTA_OFFSET);
+      cta[head * HEAD_DIM + d] = r;
+      if (d == 0) {
+        cta[GMAX * HEAD_DIM + head] = any_bad || none ? 0.f : M;
+        cta[GMAX * HEAD_DIM + GMAX + head] = any_bad || none ? 1.f : L;
+      }
+    } else if (single) {
+      static_cast<T*>(p.out)[qrow * HEAD_DIM + d] = to_elem<T>(r);
+    } else {
+      const size_t row = qrow * p.max_num_partitions + part;
+      p.ws_o[row * HEAD_DIM + d] = r;
+      if (d == 0) {
+        p.ws_m[row] = any_bad || none ? 0.f : M;
+        p.ws_l[row] = any_bad || none ? 1.f : L;
+      }
+    }
+  }
+
+  if constexpr (CLUSTER) {  // as decode_cta: merge the cluster's results through distributed shared memory
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    float* cta = reinterpret_cast<float*>(ring + Cfg::CTA_OFFSET);
+    const int rank = static_cast<int>(cluster.block_rank());
+    for (int idx = rank * (WARPS * 32) + threadIdx.x; idx < G * HEAD_DIM; idx += nclu * WARPS * 32) {
+      const int head = idx / HEAD_DIM;
+      const int d = idx - head * HEAD_DIM;
+      float M = -INFINITY;
+      for (int r = 0; r < nclu; ++r) {
+        const float* peer = cluster.map_shared_rank(cta, r);
+        M = fmaxf(M, peer[GMAX * HEAD_DIM + head]);
+      }
+      float L = 0.f, O = 0.f;
+      for (int r = 0; r < nclu; ++r) {
+        const float* peer = cluster.map_shared_rank(cta, r);
+        const float w = peer[GMAX * HEAD_DIM + GMAX + head] * ex2(peer[GMAX * HEAD_DIM + head] - M);
+        L += w;
+        O += w * peer[head * HEAD_DIM + d];
+      }
+      static_cast<T*>(p.out)[(static_cast<size_t>(s) * H + kvh * G + head) * HEAD_DIM + d] = to_elem<T>(O / L);
+    }
+    cluster.sync();  // no CTA leaves while the others still read its shared memory
+  }
+  allow_dependent_launch();
+}
+
+// ================================================================ launchers
+template <typename T, typename KV, int HEAD_DIM, int NT, int MODE, int KIND, bool PER_HEAD>
+cudaError_t launch_block_decode_t(const BlockDecodeArgs& a, cudaStream_t stream) {
+  constexpr bool CLUSTER = MODE == MODE_CLUSTER;
+  constexpr int ELEM = kElemBytes<KV>;
+  constexpr int WARPS = DecodeShape<HEAD_DIM, ELEM, KIND>::WARPS;
+  constexpr int STAGES = DecodeShape<HEAD_DIM, ELEM, KIND>::STAGES;
+  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, ELEM>;
+  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, WARPS, STAGES, MODE, PER_HEAD>;
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = ensure_smem(kern, Cfg::SMEM_BYTES, smem_set);
+  if (e != cudaSuccess) return e;
+  BlockDecodeParams p;
+  const int64_t pool_rows = static_cast<int64_t>(a.num_blocks) * a.block_size;
+  e = make_pool_map<KV, HEAD_DIM>(&p.tmap_k, a.k_cache, a.num_kv_heads, pool_rows);
+  if (e != cudaSuccess) return e;
+  e = make_pool_map<KV, HEAD_DIM>(&p.tmap_v, a.v_cache, a.num_kv_heads, pool_rows);
+  if (e != cudaSuccess) return e;
+  p.out = a.out;
+  p.q = a.q;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  const size_t rows = ws_rows(a.num_seqs, a.num_heads, a.max_num_partitions);
+  p.ws_o = a.ws;
+  p.ws_m = a.ws ? a.ws + rows * HEAD_DIM : nullptr;
+  p.ws_l = a.ws ? a.ws + rows * HEAD_DIM + rows : nullptr;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = a.num_heads / a.num_kv_heads;
+  p.block_size = a.block_size;
+  p.chunks_per_block_log2 = __builtin_ctz(static_cast<unsigned>(a.block_size / CHUNK));
+  p.num_blocks = a.num_blocks;
+  p.partition_chunks = a.partition_size / CHUNK;
+  p.max_num_partitions = a.max_num_partitions;
+  p.num_seqs = a.num_seqs;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.num_kv_heads, CLUSTER ? a.cluster_size : a.max_num_partitions, a.num_seqs);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if constexpr (CLUSTER) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = a.cluster_size;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Resident CTAs of the single launch on the device (SMs x CTAs per SM), cached
+// per device.
+template <typename T, typename KV, int HEAD_DIM, int NT, bool PER_HEAD>
+cudaError_t block_decode_slots(int* slots) {
+  constexpr int ELEM = kElemBytes<KV>;
+  constexpr int WARPS = DecodeShape<HEAD_DIM, ELEM>::WARPS;
+  constexpr int STAGES = DecodeShape<HEAD_DIM, ELEM>::STAGES;
+  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, ELEM>;
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64) {
+    const int c = cache[dev].load(std::memory_order_acquire);
+    if (c > 0) {
+      *slots = c;
+      return cudaSuccess;
+    }
+  }
+  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, WARPS, STAGES, MODE_GRID, PER_HEAD>;
+  static std::atomic<uint64_t> smem_set{0};
+  e = ensure_smem(kern, Cfg::SMEM_BYTES, smem_set);
+  if (e != cudaSuccess) return e;
+  int sms = 0, per_sm = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, WARPS * 32, Cfg::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  *slots = sms * (per_sm > 0 ? per_sm : 1);
+  if (dev < 64) cache[dev].store(*slots, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// As launch_decode_auto: one CTA per (sequence, KV head) when those fill the
+// resident slots (longest first when they need one second wave), else
+// clusters of up to 8 CTAs per pair.  Split-K (a workspace): the plain grid.
+template <typename T, typename KV, int HEAD_DIM, int NT, bool PER_HEAD>
+cudaError_t launch_block_decode_auto(const BlockDecodeArgs& a, cudaStream_t stream) {
+  if constexpr (!PER_HEAD) {
+    if (a.ws != nullptr) return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_GRID, KIND_SPLITK, false>(a, stream);
+  }
+  int slots = 0;
+  cudaError_t e = block_decode_slots<T, KV, HEAD_DIM, NT, PER_HEAD>(&slots);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
+  const int64_t k = std::min<int64_t>(slots / pairs, (cap + 511) / 512);
+  BlockDecodeArgs b = a;
+  b.cluster_size = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, k)));
+  if (b.cluster_size > 1) return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_CLUSTER, KIND_SINGLE, PER_HEAD>(b, stream);
+  if constexpr (!PER_HEAD) {
+    if (pairs > slots && pairs <= 2 * static_cast<int64_t>(slots) && a.num_seqs <= kLongestFirstMax)
+      return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_LONGEST_FIRST, KIND_SINGLE, false>(b, stream);
+  }
+  return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_GRID, KIND_SINGLE, PER_HEAD>(b, stream);
+}
+
+template <typename T, typename KV, bool PER_HEAD>
+cudaError_t launch_block_decode_typed(const BlockDecodeArgs& a, cudaStream_t stream) {
+  const bool two = a.num_heads / a.num_kv_heads > 8;
+  switch (a.head_dim) {
+    case 64:
+      return two ? launch_block_decode_auto<T, KV, 64, 2, PER_HEAD>(a, stream)
+                 : launch_block_decode_auto<T, KV, 64, 1, PER_HEAD>(a, stream);
+    case 128:
+      return two ? launch_block_decode_auto<T, KV, 128, 2, PER_HEAD>(a, stream)
+                 : launch_block_decode_auto<T, KV, 128, 1, PER_HEAD>(a, stream);
+    case 256: return two ? cudaErrorInvalidValue : launch_block_decode_auto<T, KV, 256, 1, PER_HEAD>(a, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+}  // namespace pa

@@ -101,6 +101,94 @@ struct PrefillArgs {
   float scale;
 };
 
+// E4M3 pools with one float32 scale per (block, KV head): [num_blocks][num_kv_heads].
+struct BlockWriteArgs {
+  const void* key;
+  const void* value;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;
+  float* v_scales;
+  const int64_t* slot_mapping;
+  int num_tokens;
+  int num_blocks;
+  int block_size;
+  int num_kv_heads;
+  int head_dim;
+  int dtype;  // key / value: PA_FP16 or PA_BF16
+};
+
+struct KeyBoundsArgs {
+  const void* key;
+  int8_t* key_bounds;   // [num_blocks][num_kv_heads][2][head_dim]
+  int32_t* bound_exps;  // [num_blocks][num_kv_heads]
+  const int64_t* slot_mapping;
+  int num_tokens;
+  int num_blocks;
+  int block_size;
+  int num_kv_heads;
+  int head_dim;
+  int dtype;
+};
+
+struct SelectArgs {
+  int32_t* sel_tables;  // [num_seqs][num_kv_heads][max_selected]
+  int32_t* sel_lens;    // [num_seqs][num_kv_heads]
+  const void* q;
+  const int8_t* key_bounds;
+  const int32_t* bound_exps;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* scores;  // workspace [num_seqs][num_kv_heads][select_pitch]
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_heads;
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  int num_blocks;
+  int max_selected;
+  int num_first;
+  int num_last;
+  int dtype;
+};
+
+// Blocks per (sequence, KV head) in the selection workspace: the table width
+// rounded up so that every row starts on 16 bytes.
+inline int64_t select_pitch(int max_blocks_per_seq) { return (static_cast<int64_t>(max_blocks_per_seq) + 3) / 4 * 4; }
+
+// Decode over block-scaled pools, or over per-KV-head tables (sparse).
+struct BlockDecodeArgs {
+  int dtype;     // q and out
+  int kv_dtype;  // the pools: dtype (sparse only) or PA_FP8_E4M3 with block scales
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;  // [num_blocks][num_kv_heads], PA_FP8_E4M3 pools only
+  const float* v_scales;
+  const int32_t* block_tables;  // [S][M], or per head: [S][Hk][M]
+  const int32_t* context_lens;  // [S], or per head: [S][Hk]
+  float* ws;                    // split-K workspace (nullptr: single launch)
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_heads;
+  int num_kv_heads;
+  int head_dim;
+  int block_size;
+  int num_blocks;
+  float scale;
+  int partition_size;
+  int max_num_partitions;
+  int cluster_size;  // set by the launcher
+};
+
+struct BlockPrefillArgs {
+  PrefillArgs a;
+  const float* k_scales;
+  const float* v_scales;
+};
+
 // Record a formatted message as the calling thread's last error; returns status.
 int set_last_error(int status, const char* fmt, ...);
 
@@ -130,6 +218,19 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 // shared-prefix split-K (pa_decode_prefix.cu): the shared pass, then the
 // per-sequence pass
 cudaError_t launch_decode_prefix(const DecodeArgs& a, cudaStream_t stream);
+
+// the block-scaled E4M3 cache and the block selection (pa_block_cache.cu)
+cudaError_t launch_block_write(const BlockWriteArgs& a, cudaStream_t stream);
+cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t stream);
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream);
+// decode over block-scaled pools (pa_block_decode_{f16,bf16}.cu)
+cudaError_t launch_block_decode_f16(const BlockDecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_block_decode_bf16(const BlockDecodeArgs& a, cudaStream_t stream);
+// decode over per-KV-head tables (pa_sparse_decode_{f16,bf16}.cu)
+cudaError_t launch_sparse_decode_f16(const BlockDecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_sparse_decode_bf16(const BlockDecodeArgs& a, cudaStream_t stream);
+// prefill over block-scaled pools (pa_block_prefill.cu)
+cudaError_t launch_block_prefill(const BlockPrefillArgs& a, cudaStream_t stream);
 
 // Workspace geometry shared by the partition kernel and the reduce kernel:
 // o [S][H][P][d], then m [S][H][P], then l [S][H][P], float32.
