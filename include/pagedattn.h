@@ -665,7 +665,7 @@ size_t pa_select_workspace_bytes(int num_seqs, int num_kv_heads, int max_blocks_
  *   qi_c  = rint(q_c / 2^f), f the smallest number >= -100 with max|q| <= 255 * 2^f
  *           over the finite elements of the query head's row (an infinite
  *           element counts as +-255, NaN as 0)
- *   I     = sum_c max(qi_c * lo_c, qi_c * hi_c)
+ *   I     = sum_c qi_c * (qi_c >= 0 ? hi_c : lo_c)
  *   score = max over the query heads of the group of I * 2^(f + e), the exponent
  *           held to [-100, 100]
  *

@@ -121,7 +121,7 @@ def scores(q: np.ndarray, codes: np.ndarray, exps: np.ndarray, ids) -> np.ndarra
             if not 0 <= b < N:
                 out[i] = np.inf
                 continue
-            dot = np.maximum(qi * codes[b, 0], qi * codes[b, 1]).sum()
+            dot = (qi * np.where(qi >= 0, codes[b, 1], codes[b, 0])).sum()
             out[i] = max(out[i], math.ldexp(dot, min(max(f + int(exps[b]), -100), 100)))
     return out
 

@@ -2,9 +2,9 @@
 // into E4M3 pools with one scale per (block, KV head), the key bounds of the
 // block selection, and the selection itself.
 //
-//  block_write_kernel   one warp per (run of new tokens in a block, KV head, K or V)
-//  key_bounds_kernel    one warp per (run of new tokens in a block, KV head)
-//  block_score_kernel   one warp per (block of a sequence, KV head)
+//  block_write_kernel   block_size / 16 warps per (run of new tokens in a block, KV head, K or V)
+//  key_bounds_kernel    the same per (run of new tokens in a block, KV head)
+//  block_score_kernel   one warp per (64 blocks of a sequence, KV head)
 //  select_kernel        one CTA per (sequence, KV head)
 //
 // "PagedAttention: when the KV cache meets OS paging", section 6, stacks
@@ -29,138 +29,245 @@ __device__ __forceinline__ int64_t slot_block(int64_t slot, int64_t num_slots, i
   return slot < 0 || slot >= num_slots ? -1 : slot >> log2_b;
 }
 
-// The run of token t: [t, returned end), the tokens from t on that go to t's
-// block; empty when t continues the run of t - 1 or goes nowhere.
-__device__ __forceinline__ int run_end(const int64_t* sm, int t, int num_tokens, int64_t num_slots, int log2_b,
-                                       int64_t* blk) {
-  *blk = slot_block(__ldg(sm + t), num_slots, log2_b);
-  if (*blk < 0) return t;
-  if (t > 0 && slot_block(__ldg(sm + t - 1), num_slots, log2_b) == *blk) return t;
-  int e = t + 1;
-  while (e < num_tokens && slot_block(__ldg(sm + e), num_slots, log2_b) == *blk) ++e;
-  return e;
+// ---------------------------------------------------------- runs of new tokens
+// The new tokens of one block stand next to each other in slot_mapping: a run.
+// A CTA looks at a stretch of tokens for one KV head and hands each run that
+// begins there to a group of block_size / 16 warps; warp g of the group holds
+// the run's tokens 16 g .. 16 g + 15 in registers, so every element is read
+// once, whatever the block size.  (One warp per run that walked its tokens twice
+// took 153 us for the write and 135 us for the bounds of 8 prompts of 2048
+// tokens, 8 KV heads of 128; this split: see the kernels.)
+constexpr int kRunRows = 16;      // tokens a warp holds
+constexpr int kMaxStretch = 128;  // tokens a CTA looks at, at most
+constexpr int kMaxGroup = 16;     // warps per group at most: 256-token blocks
+
+struct RunParams {
+  const int64_t* slot_mapping;
+  int64_t num_slots;  // num_blocks * block_size
+  int num_tokens;
+  int num_kv_heads;
+  int block_size;
+  int log2_b;
+  int stretch;  // tokens per CTA
+};
+
+// Bit l of mask[i]: a run begins at token t0 + 32 i + l.  Every warp computes it.
+__device__ __forceinline__ int find_runs(const RunParams& p, int t0, unsigned (&mask)[kMaxStretch / 32], int lane) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxStretch / 32; ++i) {
+    mask[i] = 0u;
+    if (32 * i >= p.stretch) continue;  // uniform
+    const int t = t0 + 32 * i + lane;
+    const bool in = 32 * i + lane < p.stretch && t < p.num_tokens;
+    const int64_t blk = in ? slot_block(__ldg(p.slot_mapping + t), p.num_slots, p.log2_b) : -1;
+    const int64_t prev = in && t > 0 ? slot_block(__ldg(p.slot_mapping + t - 1), p.num_slots, p.log2_b) : -1;
+    mask[i] = __ballot_sync(kFull, blk >= 0 && blk != prev);
+    n += __popc(mask[i]);
+  }
+  return n;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// The first token of run k of the stretch, k < the number of runs.
+__device__ __forceinline__ int run_start(const unsigned (&mask)[kMaxStretch / 32], int t0, int k) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
-  return v;
+  for (int i = 0; i < kMaxStretch / 32; ++i) {
+    const int c = __popc(mask[i]);
+    if (k < c) {
+      unsigned m = mask[i];
+      for (; k > 0; --k) m &= m - 1;
+      return t0 + 32 * i + __ffs(m) - 1;
+    }
+    k -= c;
+  }
+  return t0;  // not reached
 }
+
+// Lane r < 16: the offset in the block of the run's token (first + r), -1 if it
+// belongs to another block.  `first`: the warp's first token, `blk` the run's block.
+__device__ __forceinline__ int row_offset(const RunParams& p, int first, int64_t blk, int lane) {
+  const int t = first + lane;
+  if (lane >= kRunRows || t >= p.num_tokens) return -1;
+  const int64_t slot = __ldg(p.slot_mapping + t);
+  return slot_block(slot, p.num_slots, p.log2_b) == blk ? static_cast<int>(slot & (p.block_size - 1)) : -1;
+}
+
+// A warp's 16 rows of one KV head: lane i holds 16-byte unit i % U of row (32 / U) j + i / U.
+template <int HEAD_DIM>
+struct RowTile {
+  static constexpr int U = HEAD_DIM / 8;              // units per row
+  static constexpr int RPI = 32 / U;                  // rows per load
+  static constexpr int N = kRunRows / RPI;            // loads
+  uint4 v[N];
+  int off[N];  // the row's offset in the block, -1: none
+
+  // `rows`: the tensor as units, `first`: the warp's first token, off16: row_offset of each lane.
+  __device__ __forceinline__ void load(const uint4* rows, int first, int num_kv_heads, int h, int off16, int lane) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int r = j * RPI + lane / U;
+      off[j] = __shfl_sync(kFull, off16, r);
+      v[j] = off[j] >= 0 ? __ldg(rows + (static_cast<int64_t>(first + r) * num_kv_heads + h) * U + lane % U)
+                         : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  // The largest |element| over finite elements.  16-bit floats order like their
+  // bits, so the maximum runs on packed pairs; a non-finite element, the only
+  // case that needs a look at each, shows in it.
+  template <typename T>
+  __device__ __forceinline__ float finite_amax(bool* all_finite) const {
+    constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      m = __vmaxu2(m, v[j].x & 0x7fff7fffu);
+      m = __vmaxu2(m, v[j].y & 0x7fff7fffu);
+      m = __vmaxu2(m, v[j].z & 0x7fff7fffu);
+      m = __vmaxu2(m, v[j].w & 0x7fff7fffu);
+    }
+    uint32_t top = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+    *all_finite = top < kInf;
+    if (top >= kInf) {  // warp-uniform
+      m = 0u;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+          m = max(m, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+        }
+      }
+      top = __reduce_max_sync(kFull, m);
+    }
+    return unpack2<T>(top).x;
+  }
+};
 
 struct BlockWriteParams {
-  const uint4* key;  // 8 elements per vector
+  RunParams r;
+  const uint4* key;
   const uint4* value;
-  uint2* k_cache;  // 8 codes per vector
+  uint2* k_cache;  // 8 codes per unit
   uint2* v_cache;
   float* k_scales;
   float* v_scales;
-  const int64_t* slot_mapping;
-  int64_t num_slots;
-  int num_tokens;
-  int num_kv_heads;
-  int block_size;
-  int log2_b;
-  int row_vecs;  // head_dim / 8
 };
 
+// 8 elements times inv (or, with division, over s) as 8 codes.
 template <typename T>
-__global__ void __launch_bounds__(64) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
+__device__ __forceinline__ uint2 to_codes8(const uint4& v, float inv, float s, bool pow2) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 f = unpack2<T>(w[i]);
+    f = pow2 ? make_float2(f.x * inv, f.y * inv) : make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    c[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// 8 codes moved to another scale: value(code) * ratio, rounded to float32, then to a code.
+__device__ __forceinline__ uint2 move_codes8(const uint2& v, float ratio) {
+  const uint32_t in[2] = {v.x, v.y};
+  uint32_t out[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t lo, hi;
+    e4m3x4_to_half2x2(in[j], lo, hi);
+    const float2 a = unpack_half2(lo), b = unpack_half2(hi);
+    const uint32_t c0 = __nv_cvt_float2_to_fp8x2(make_float2(a.x * ratio, a.y * ratio), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(b.x * ratio, b.y * ratio), __NV_SATFINITE, __NV_E4M3);
+    out[j] = c0 | (c1 << 16);
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// Grid (stretch, KV head, K or V).  The write is a copy that shrinks: 3 bytes
+// moved per element, so HBM bounds prompts and latency bounds single tokens.
+template <typename T, int HEAD_DIM>
+__global__ void __launch_bounds__(kMaxGroup * 32) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
+  using Tile = RowTile<HEAD_DIM>;
+  __shared__ float sh_amax[kMaxGroup];
+  __shared__ int sh_starts[kMaxGroup];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int t = blockIdx.x;
-  const int h = blockIdx.y;
-  const bool is_v = threadIdx.x >= 32;
+  const RunParams& rp = p.r;
   const int lane = threadIdx.x & 31;
-  int64_t blk;
-  const int end = run_end(p.slot_mapping, t, p.num_tokens, p.num_slots, p.log2_b, &blk);
-  if (end == t) return;
+  const int warp = threadIdx.x >> 5;
+  const int gw = rp.block_size / kRunRows;  // warps per group
+  const int groups = (blockDim.x >> 5) / gw;
+  const int g = warp / gw;
+  const int wg = warp - g * gw;
+  const int h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int t0 = blockIdx.x * rp.stretch;
+  unsigned mask[kMaxStretch / 32];
+  const int nruns = find_runs(rp, t0, mask, lane);
   const uint4* src = is_v ? p.value : p.key;
-  uint2* pool = (is_v ? p.v_cache : p.k_cache) + blk * p.block_size * p.num_kv_heads * p.row_vecs;
-  float* scale = (is_v ? p.v_scales : p.k_scales) + blk * p.num_kv_heads + h;
-  const int rv = p.row_vecs;
-
-  float amax = 0.f;
-  bool starts = false;
-  for (int i = t; i < end; ++i) {
-    starts |= (__ldg(p.slot_mapping + i) & (p.block_size - 1)) == 0;
-    const uint4* row = src + (static_cast<int64_t>(i) * p.num_kv_heads + h) * rv;
-    for (int x = lane; x < rv; x += 32) {
-      const uint4 v = __ldg(row + x);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(w[j]);
-        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+  uint2* cache = is_v ? p.v_cache : p.k_cache;
+  float* scales = is_v ? p.v_scales : p.k_scales;
+  for (int k0 = 0; k0 < nruns; k0 += groups) {  // the same trips for every warp
+    const int k = k0 + g;
+    const bool on = k < nruns;
+    const int t = on ? run_start(mask, t0, k) : 0;
+    const int64_t blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : -2;
+    const int first = t + wg * kRunRows;
+    const int off16 = on ? row_offset(rp, first, blk, lane) : -1;
+    float* scale = scales + (on ? blk * rp.num_kv_heads + h : 0);
+    Tile tile;
+    tile.load(src, first, rp.num_kv_heads, h, off16, lane);
+    const float was = on ? *scale : 0.f;
+    bool finite;
+    float amax = tile.template finite_amax<T>(&finite);
+    int starts = __any_sync(kFull, off16 == 0);
+    if (gw > 1) {
+      if (lane == 0) {
+        sh_amax[warp] = amax;
+        sh_starts[warp] = starts;
+      }
+      __syncthreads();
+      for (int i = g * gw; i < (g + 1) * gw; ++i) {
+        amax = fmaxf(amax, sh_amax[i]);
+        starts |= sh_starts[i];
       }
     }
-  }
-  amax = warp_max(amax);
-  const float need = pow2f(scale_exp(amax));
-  float old = starts ? 0.f : *scale;
-  if (!(old > 0.f && old <= kFloatMax)) old = 0.f;  // no scale to keep
-  const float s = fmaxf(old, need);
-  if (old > 0.f && s > old) {  // the block's other codes move to the new scale
-    const float ratio = __fdiv_rn(old, s);
-    for (int o = 0; o < p.block_size; ++o) {
-      uint2* row = pool + (static_cast<int64_t>(o) * p.num_kv_heads + h) * rv;
-      for (int x = lane; x < rv; x += 32) {
-        const uint2 c = row[x];
-        const uint32_t in[2] = {c.x, c.y};
-        uint32_t out[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t lo, hi;
-          e4m3x4_to_half2x2(in[j], lo, hi);
-          const float2 a = unpack_half2(lo), b = unpack_half2(hi);
-          out[j] = float_to_e4m3_sat(a.x * ratio) | (float_to_e4m3_sat(a.y * ratio) << 8) |
-                   (float_to_e4m3_sat(b.x * ratio) << 16) | (static_cast<uint32_t>(float_to_e4m3_sat(b.y * ratio)) << 24);
-        }
-        row[x] = make_uint2(out[0], out[1]);
-      }
+    const float need = pow2f(scale_exp(amax));
+    const float old = !starts && was > 0.f && was <= kFloatMax ? was : 0.f;
+    const float s = fmaxf(old, need);
+    uint2* rows = cache + on * ((blk * rp.block_size * rp.num_kv_heads + h) * Tile::U + lane % Tile::U);
+    const int64_t pitch = static_cast<int64_t>(rp.num_kv_heads) * Tile::U;
+    if (on && old > 0.f && s > old) {  // the block's other codes move to the new scale
+      const float ratio = __fdiv_rn(old, s);
+#pragma unroll 4
+      for (int o = wg * kRunRows + lane / Tile::U; o < (wg + 1) * kRunRows; o += Tile::RPI)
+        rows[o * pitch] = move_codes8(rows[o * pitch], ratio);
     }
-  }
-  __syncwarp();  // the moved codes before the new ones, which may share their rows
-  for (int i = t; i < end; ++i) {
-    const int o = static_cast<int>(__ldg(p.slot_mapping + i) & (p.block_size - 1));
-    const uint4* row = src + (static_cast<int64_t>(i) * p.num_kv_heads + h) * rv;
-    uint2* dst = pool + (static_cast<int64_t>(o) * p.num_kv_heads + h) * rv;
-    for (int x = lane; x < rv; x += 32) {
-      const uint4 v = __ldg(row + x);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t c[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<T>(w[j]);
-        const uint32_t c0 = float_to_e4m3_sat(__fdiv_rn(f.x, s));
-        const uint32_t c1 = float_to_e4m3_sat(__fdiv_rn(f.y, s));
-        c[j >> 1] |= (c0 | (c1 << 8)) << ((j & 1) * 16);
-      }
-      dst[x] = make_uint2(c[0], c[1]);
+    // the moved codes before the new ones (which may share rows with them), every
+    // read of the scale before its write
+    if (gw > 1) {
+      __syncthreads();
+    } else {
+      __syncwarp();
     }
+    const int bits = __float_as_int(s);
+    const bool pow2 = (bits & 0x7fffff) == 0 && bits <= (126 + 127) << 23 && bits >= 1 << 23;
+    const float inv = pow2 ? pow2f(127 - (bits >> 23)) : 1.f;
+#pragma unroll
+    for (int j = 0; j < Tile::N; ++j)
+      if (tile.off[j] >= 0) rows[tile.off[j] * pitch] = to_codes8<T>(tile.v[j], inv, s, pow2);
+    if (on && wg == 0 && lane == 0) *scale = s;
   }
-  if (lane == 0) *scale = s;
 }
 
 struct KeyBoundsParams {
-  const void* key;
+  RunParams r;
+  const uint4* key;
   int8_t* bounds;
   int32_t* exps;
-  const int64_t* slot_mapping;
-  int64_t num_slots;
-  int num_tokens;
-  int num_kv_heads;
-  int block_size;
-  int log2_b;
 };
-
-template <typename T>
-__device__ __forceinline__ float elem_to_float(T x) {
-  if constexpr (std::is_same<T, __half>::value) {
-    return __half2float(x);
-  } else {
-    return __bfloat162float(x);
-  }
-}
 
 // lo (up = false): floor(v / 2^e); hi: ceil.  Codes stay in [-127, 127].
 __device__ __forceinline__ int bound_code(float v, float inv, bool up) {
@@ -169,56 +276,165 @@ __device__ __forceinline__ int bound_code(float v, float inv, bool up) {
   return static_cast<int>(fminf(fmaxf(r, -127.f), 127.f));
 }
 
+// Packed minimum and maximum of 16-bit floats without NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// NaN halves of a packed pair replaced by `with` (both halves of it).
+template <typename T>
+__device__ __forceinline__ uint32_t nan2(uint32_t w, uint32_t with) {
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  uint32_t r = w;
+  if ((w & 0x7fffu) > kInf) r = (r & 0xffff0000u) | (with & 0xffffu);
+  if (((w >> 16) & 0x7fffu) > kInf) r = (r & 0xffffu) | (with & 0xffff0000u);
+  return r;
+}
+
+// Grid (stretch, KV head).  Reads 2 bytes per element and writes 2 per channel
+// and block: HBM bounds prompts, latency single tokens.
 template <typename T, int HEAD_DIM>
-__global__ void __launch_bounds__(32) key_bounds_kernel(const __grid_constant__ KeyBoundsParams p) {
-  constexpr int N = HEAD_DIM / 32;
+__global__ void __launch_bounds__(kMaxGroup * 32) key_bounds_kernel(const __grid_constant__ KeyBoundsParams p) {
+  using Tile = RowTile<HEAD_DIM>;
+  constexpr int U = Tile::U;
+  constexpr uint32_t kPosInf = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t kNegInf = kPosInf | 0x80008000u;
+  __shared__ float sh_amax[kMaxGroup];
+  __shared__ int sh_starts[kMaxGroup];
+  __shared__ uint4 sh_lo[kMaxGroup][U], sh_hi[kMaxGroup][U];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int t = blockIdx.x;
+  const RunParams& rp = p.r;
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int gw = rp.block_size / kRunRows;
+  const int groups = (blockDim.x >> 5) / gw;
+  const int g = warp / gw;
+  const int wg = warp - g * gw;
   const int h = blockIdx.y;
-  const int lane = threadIdx.x;
-  int64_t blk;
-  const int end = run_end(p.slot_mapping, t, p.num_tokens, p.num_slots, p.log2_b, &blk);
-  if (end == t) return;
-  float lo[N], hi[N], amax = 0.f;
+  const int t0 = blockIdx.x * rp.stretch;
+  unsigned mask[kMaxStretch / 32];
+  const int nruns = find_runs(rp, t0, mask, lane);
+  for (int k0 = 0; k0 < nruns; k0 += groups) {  // the same trips for every warp
+    const int k = k0 + g;
+    const bool on = k < nruns;
+    const int t = on ? run_start(mask, t0, k) : 0;
+    const int64_t blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : -2;
+    const int first = t + wg * kRunRows;
+    const int off16 = on ? row_offset(rp, first, blk, lane) : -1;
+    const int64_t at = on ? blk * rp.num_kv_heads + h : 0;
+    Tile tile;
+    tile.load(p.key, first, rp.num_kv_heads, h, off16, lane);
+    // the block's bounds as they are, on the lanes that will write them
+    const bool writer = on && wg == 0 && lane < U;
+    uint2* lo_at = reinterpret_cast<uint2*>(p.bounds + at * 2 * HEAD_DIM) + lane % U;
+    uint2* hi_at = lo_at + HEAD_DIM / 8;
+    uint2 old_lo = make_uint2(0u, 0u), old_hi = make_uint2(0u, 0u);
+    int was = kMinBoundExp;
+    if (writer) {
+      old_lo = *lo_at;
+      old_hi = *hi_at;
+      was = p.exps[at];
+    }
+    bool finite;
+    float amax = tile.template finite_amax<T>(&finite);
+    int starts = __any_sync(kFull, off16 == 0);
+    uint32_t lo[4], hi[4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    lo[i] = INFINITY;
-    hi[i] = -INFINITY;
-  }
-  bool starts = false;
-  for (int i = t; i < end; ++i) {
-    starts |= (__ldg(p.slot_mapping + i) & (p.block_size - 1)) == 0;
-    const T* row = static_cast<const T*>(p.key) + (static_cast<int64_t>(i) * p.num_kv_heads + h) * HEAD_DIM;
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = kPosInf;
+      hi[i] = kNegInf;
+    }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float f = elem_to_float(row[lane + 32 * j]);
-      amax = fmaxf(amax, finite_abs(f));
-      lo[j] = f == f ? fminf(lo[j], f) : -INFINITY;  // NaN: the widest bound
-      hi[j] = f == f ? fmaxf(hi[j], f) : INFINITY;
+    for (int j = 0; j < Tile::N; ++j) {
+      if (tile.off[j] < 0) continue;
+      const uint32_t w[4] = {tile.v[j].x, tile.v[j].y, tile.v[j].z, tile.v[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = min2<T>(lo[i], finite ? w[i] : nan2<T>(w[i], kNegInf));  // NaN: the widest bound
+        hi[i] = max2<T>(hi[i], finite ? w[i] : nan2<T>(w[i], kPosInf));
+      }
+    }
+#pragma unroll
+    for (int o = U; o < 32; o <<= 1)  // over the lanes that hold the same channels
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = min2<T>(lo[i], __shfl_xor_sync(kFull, lo[i], o));
+        hi[i] = max2<T>(hi[i], __shfl_xor_sync(kFull, hi[i], o));
+      }
+    if (gw > 1) {
+      if (lane == 0) {
+        sh_amax[warp] = amax;
+        sh_starts[warp] = starts;
+      }
+      if (lane < U) {
+        sh_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        sh_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      }
+      __syncthreads();
+      if (wg == 0) {
+        for (int i = g * gw + 1; i < (g + 1) * gw; ++i) {
+          amax = fmaxf(amax, sh_amax[i]);
+          starts |= sh_starts[i];
+          const uint4 l = sh_lo[i][lane % U], u = sh_hi[i][lane % U];
+          const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            lo[x] = min2<T>(lo[x], lw[x]);
+            hi[x] = max2<T>(hi[x], uw[x]);
+          }
+        }
+      }
+      __syncthreads();  // the shared rows are read before the next trip writes them
+    }
+    if (writer) {
+      const int old_e = starts ? kMinBoundExp : was;
+      const int e = max(bound_exp(amax), old_e);
+      const int shift = min(e - old_e, 31);
+      const float inv = pow2f(-e);
+      uint32_t cl[2] = {0u, 0u}, ch[2] = {0u, 0u};
+      const uint32_t ol[2] = {old_lo.x, old_lo.y}, oh[2] = {old_hi.x, old_hi.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 l = unpack2<T>(lo[i]), u = unpack2<T>(hi[i]);
+        const float lf[2] = {l.x, l.y}, uf[2] = {u.x, u.y};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int c = 2 * i + x;  // the lane's channel
+          int a = bound_code(lf[x], inv, false);
+          int b = bound_code(uf[x], inv, true);
+          if (!starts) {  // nested floors: moving a bound to a larger step is a shift
+            const int la = static_cast<int8_t>(ol[c >> 2] >> ((c & 3) * 8));
+            const int lb = static_cast<int8_t>(oh[c >> 2] >> ((c & 3) * 8));
+            a = min(a, la >> shift);
+            b = max(b, -((-lb) >> shift));
+          }
+          cl[c >> 2] |= (static_cast<uint32_t>(a) & 0xffu) << ((c & 3) * 8);
+          ch[c >> 2] |= (static_cast<uint32_t>(b) & 0xffu) << ((c & 3) * 8);
+        }
+      }
+      *lo_at = make_uint2(cl[0], cl[1]);
+      *hi_at = make_uint2(ch[0], ch[1]);
+      if (lane == 0) p.exps[at] = e;
     }
   }
-  amax = warp_max(amax);
-  int8_t* b = p.bounds + (blk * p.num_kv_heads + h) * 2 * HEAD_DIM;
-  int32_t* ex = p.exps + blk * p.num_kv_heads + h;
-  const int old_e = starts ? kMinBoundExp : *ex;
-  const int e = max(bound_exp(amax), old_e);
-  const int shift = min(e - old_e, 31);
-  const float inv = pow2f(-e);
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int c = lane + 32 * j;
-    int l = bound_code(lo[j], inv, false);
-    int u = bound_code(hi[j], inv, true);
-    if (!starts) {  // nested floors: moving a bound to a larger step is a shift
-      l = min(l, static_cast<int>(b[c]) >> shift);
-      u = max(u, -((-static_cast<int>(b[HEAD_DIM + c])) >> shift));
-    }
-    b[c] = static_cast<int8_t>(l);
-    b[HEAD_DIM + c] = static_cast<int8_t>(u);
-  }
-  __syncwarp();
-  if (lane == 0) *ex = e;
 }
 
 // ================================================================ selection
@@ -243,70 +459,205 @@ struct SelectParams {
   int num_last;
 };
 
-template <typename T, int HEAD_DIM>
-__global__ void __launch_bounds__(32) block_score_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int N = HEAD_DIM / 32;
-  grid_dependency_wait();
-  const int b = blockIdx.x;
-  const int kvh = blockIdx.y;
-  const int s = blockIdx.z;
-  const int lane = threadIdx.x;
-  const int ctx = __ldg(p.context_lens + s);
-  if (ctx <= 0 || static_cast<int64_t>(b) * p.block_size >= ctx) return;
-  const int phys = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks + b);
-  float best = -INFINITY;
-  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-    best = INFINITY;  // selected, so that the decode meets it and gives NaN
-  } else {
-    const int8_t* bd = p.bounds + (static_cast<int64_t>(phys) * p.num_kv_heads + kvh) * 2 * HEAD_DIM;
-    const int e = __ldg(p.exps + static_cast<int64_t>(phys) * p.num_kv_heads + kvh);
-    for (int g = 0; g < p.group; ++g) {
-      const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(s) * p.num_heads + kvh * p.group + g) * HEAD_DIM;
-      float f[N], amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        f[j] = elem_to_float(q[lane + 32 * j]);
-        amax = fmaxf(amax, finite_abs(f[j]));
-      }
-      const int fe = query_exp(warp_max(amax));
-      int sum = 0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float x = rintf(f[j] * pow2f(-fe));
-        const int qi = x == x ? static_cast<int>(fminf(fmaxf(x, -255.f), 255.f)) : 0;
-        const int c = lane + 32 * j;
-        sum += max(qi * bd[c], qi * bd[HEAD_DIM + c]);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-      const int x = min(max(fe + e, -100), 100);
-      best = fmaxf(best, static_cast<float>(sum) * pow2f(x));
-    }
-  }
-  if (lane == 0) p.scores[(static_cast<int64_t>(s) * p.num_kv_heads + kvh) * p.pitch + b] = best;
+// ---------------------------------------------------------------- scores
+// With lo <= hi, max(qi lo, qi hi) is qi hi for qi >= 0 and qi lo otherwise, so
+// the scores of 16 blocks for up to 8 query heads are one matrix product of
+// depth 2 d: [lo | hi] (16 x 2d) times [min(qi, 0) | max(qi, 0)]^T (2d x heads).
+// The codes and the whole-number queries are exact in float16, every product is
+// below 2^15 and every partial sum below 2^23, so float16 MMAs with float32
+// accumulators give the integer I exactly, in whatever order they add.
+// (One warp per block on integer units took 189 us for selection and sparse
+// decode of 4 sequences of 43 K to 115 K tokens, 8 KV heads of 128.)
+//
+// HBM bounds it: 2 d bytes per (block, KV head) against about 220 warp
+// instructions per 4 KB.  A warp holds 16 blocks of one KV head, straight from
+// global memory in the MMA's layout (lane (g, c) reads 16-byte units c, c + 4,
+// ... of rows g and g + 8; a unit's four words are four k-steps); neighbouring
+// warps take neighbouring heads, whose rows of a block are neighbours in memory.
+constexpr int kScoreTiles = 4;  // tiles of 16 blocks per warp, behind one preparation of the queries
+constexpr int kScoreWarps = 8;
+
+// Four codes of one word as two pairs of float16: code + 128 + 1024 by bytes, minus 1152.
+__device__ __forceinline__ void codes4_to_half(uint32_t w, uint32_t& a, uint32_t& b) {
+  const uint32_t x = w ^ 0x80808080u;
+  const uint32_t lo = __byte_perm(x, 0x64646464u, 0x4140), hi = __byte_perm(x, 0x64646464u, 0x4342);
+  const uint32_t k = 0x64806480u;  // 1152
+  const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&k));
+  const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&hi), *reinterpret_cast<const __half2*>(&k));
+  a = *reinterpret_cast<const uint32_t*>(&ra);
+  b = *reinterpret_cast<const uint32_t*>(&rb);
 }
 
+// x / 2^f as a whole number in [-255, 255]; NaN counts as 0.
+__device__ __forceinline__ float whole(float x, float inv) {
+  return fminf(fmaxf(rintf(x == x ? x * inv : 0.f), -255.f), 255.f);
+}
+
+template <typename T, int HEAD_DIM, int NT>
+__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int UH = HEAD_DIM / 64;  // 16-byte units per lane and half (lo or hi) of a row
+  constexpr int STEPS = UH * 4;      // k-steps per half
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2;
+  const int c = lane & 3;
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kScoreWarps + (threadIdx.x >> 5);
+  const int s = blockIdx.y;
+  const int kvh = static_cast<int>(wid % p.num_kv_heads);
+  const int64_t b0 = wid / p.num_kv_heads * (16 * kScoreTiles);
+  const int ctx = __ldg(p.context_lens + s);
+  if (ctx <= 0 || ctx > static_cast<int64_t>(p.max_blocks) * p.block_size) return;
+  const int n = (ctx + p.block_size - 1) / p.block_size;
+  if (n <= p.max_selected || b0 >= n) return;  // every block is kept, or none is here
+  const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
+
+  // tile t's rows g and g + 8: physical blocks (-1: outside the pool), codes, exponents
+  uint4 code[2][2 * UH];
+  int phys[2], ex[2];
+  auto table = [&](int t, int (&ph)[2]) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t b = b0 + 16 * t + 8 * r + g;
+      ph[r] = b < n ? __ldg(bt + b) : 0;
+    }
+  };
+  auto load = [&](const int (&ph)[2]) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool in = static_cast<unsigned>(ph[r]) < static_cast<unsigned>(p.num_blocks);
+      const int64_t at = static_cast<int64_t>(in ? ph[r] : 0) * p.num_kv_heads + kvh;
+      const uint4* row = reinterpret_cast<const uint4*>(p.bounds + at * 2 * HEAD_DIM);
+#pragma unroll
+      for (int i = 0; i < 2 * UH; ++i) code[r][i] = __ldg(row + (i / UH) * (HEAD_DIM / 16) + (i % UH) * 4 + c);
+      ex[r] = __ldg(p.exps + at);
+      phys[r] = in ? 0 : -1;
+    }
+  };
+  int ph_next[2];
+  table(0, ph_next);
+  load(ph_next);
+  table(1, ph_next);
+
+  // the queries: column g of tile nt is head kvh * G + nt * 8 + g; k-step (i, w) holds
+  // channels 16 (c + 4 i) + 4 w .. + 3
+  uint32_t qn[STEPS][NT][2], qp[STEPS][NT][2];
+  int fe[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int j = nt * 8 + g;
+    const bool on = j < p.group;
+    const uint4* q = reinterpret_cast<const uint4*>(
+        static_cast<const T*>(p.q) + (static_cast<int64_t>(s) * p.num_heads + kvh * p.group + (on ? j : 0)) * HEAD_DIM);
+    uint32_t w[STEPS][2];
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < UH; ++i) {
+      const uint4 u0 = __ldg(q + (c + 4 * i) * 2), u1 = __ldg(q + (c + 4 * i) * 2 + 1);
+      const uint32_t e[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        w[4 * i + k / 2][k & 1] = on ? e[k] : 0u;
+        const float2 f = unpack2<T>(w[4 * i + k / 2][k & 1]);
+        amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+    fe[nt] = query_exp(amax);
+    const float inv = pow2f(-fe[nt]);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float2 f = unpack2<T>(w[k][x]);
+        const float a = whole(f.x, inv), b = whole(f.y, inv);
+        qn[k][nt][x] = pack_half2(fminf(a, 0.f), fminf(b, 0.f));
+        qp[k][nt][x] = pack_half2(fmaxf(a, 0.f), fmaxf(b, 0.f));
+      }
+  }
+
+  float* out = p.scores + (static_cast<int64_t>(s) * p.num_kv_heads + kvh) * p.pitch;
+#pragma unroll 1
+  for (int t = 0; t < kScoreTiles && b0 + 16 * t < n; ++t) {
+    float acc[2][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][nt][i] = acc[1][nt][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * UH; ++i) {
+      const uint32_t w0[4] = {code[0][i].x, code[0][i].y, code[0][i].z, code[0][i].w};
+      const uint32_t w1[4] = {code[1][i].x, code[1][i].y, code[1][i].z, code[1][i].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a[4];
+        codes4_to_half(w0[w], a[0], a[2]);
+        codes4_to_half(w1[w], a[1], a[3]);
+        const int k = (i % UH) * 4 + w;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t* q = i < UH ? qn[k][nt] : qp[k][nt];
+          mma_f16_16816(acc[i & 1][nt], a, q[0], q[1]);
+        }
+      }
+    }
+    const int bad[2] = {phys[0], phys[1]}, e2[2] = {ex[0], ex[1]};
+    if (t + 1 < kScoreTiles && b0 + 16 * (t + 1) < n) {
+      load(ph_next);
+      table(t + 2, ph_next);
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {  // accumulators 0, 1: row g, heads 2c, 2c + 1; 2, 3: row g + 8
+        const int f = __shfl_sync(kFull, fe[nt], (2 * c + j) << 2);
+        if (nt * 8 + 2 * c + j < p.group) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float v = acc[0][nt][2 * r + j] + acc[1][nt][2 * r + j];
+            best[r] = fmaxf(best[r], v * pow2f(min(max(f + e2[r], -100), 100)));
+          }
+        }
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
+      best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
+      const int64_t b = b0 + 16 * t + 8 * r + g;
+      // a block outside the pool is selected, so that the decode meets it and gives NaN
+      if (c == 0 && b < n) out[b] = bad[r] < 0 ? INFINITY : best[r];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the k best
 // A float's bits as an unsigned number of the same order.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 counts as +0
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 256;
-
-__device__ __forceinline__ int block_sum(int v, int* sh) {
-  __syncthreads();
-  const int w = __reduce_add_sync(kFull, v);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = w;
-  __syncthreads();
-  int t = 0;
-  for (int i = 0; i < kSelThreads / 32; ++i) t += sh[i];
-  return t;
-}
+// One CTA per (sequence, KV head).  The k-th largest key is found two bits at a
+// time: each pass counts the keys at or above three trial values and keeps the
+// largest that still has k (a pass that finds one with exactly k ends the
+// search: no tie is left to break).  Keys sit in registers, 8 per thread, when
+// the sequence has at most 8192 blocks; longer tables are read again per pass.
+// No atomics, and a histogram would not do: the scores of one row share their
+// leading bits.  Latency bounds it (a few us; the scores are 32 KB).
+constexpr int kSelThreads = 1024;
+constexpr int kSelKeys = 8;
+constexpr int kSelChunk = kSelThreads * kSelKeys;
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ int sh[kSelThreads / 32];
+  constexpr int WARPS = kSelThreads / 32;
+  __shared__ int sh[2][3][WARPS];
+  __shared__ int sh_scan[WARPS];
   grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int kvh = blockIdx.x;
   const int s = blockIdx.y;
   const int64_t row = static_cast<int64_t>(s) * p.num_kv_heads + kvh;
@@ -323,52 +674,108 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     return;
   }
   const float* sc = p.scores + row * p.pitch;
-  auto key = [&](int i) -> uint32_t {
-    if (i < p.num_first || i >= n - p.num_last) return 0xffffffffu;
-    return order_key(sc[i]);
+  uint32_t key[kSelKeys];
+  auto load = [&](int chunk) {  // the thread's keys of chunk `chunk`, in index order; 0 past the end
+    const int i0 = chunk * kSelChunk + threadIdx.x * kSelKeys;
+#pragma unroll
+    for (int h = 0; h < kSelKeys / 4; ++h) {
+      const int i = i0 + 4 * h;
+      // rows are padded to 4, so the vector stays in the row; scores are at least -inf, whose key is above 0
+      const float4 v = i < n ? *reinterpret_cast<const float4*>(sc + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        key[4 * h + x] = i + x >= n ? 0u
+                         : (i + x < p.num_first || i + x >= n - p.num_last) ? 0xffffffffu : order_key(f[x]);
+    }
   };
-  // the k-th largest key, bit by bit
-  uint32_t kth = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t trial = kth | (1u << bit);
-    int c = 0;
-    for (int i = threadIdx.x; i < n; i += kSelThreads) c += key(i) >= trial;
-    if (block_sum(c, sh) >= k) kth = trial;
+  const int chunks = (n + kSelChunk - 1) / kSelChunk;
+  load(0);
+  uint32_t kth = 0;  // the largest value found so far that at least k keys reach
+  int reach = n;     // the number of keys that reach it
+  int buf = 0;
+  for (int bit = 30; bit >= 0 && reach != k; bit -= 2, buf ^= 1) {
+    int cnt[3] = {0, 0, 0};
+    for (int ch = 0; ch < chunks; ++ch) {
+      if (chunks > 1) load(ch);
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i)
+#pragma unroll
+        for (int t = 0; t < 3; ++t) cnt[t] += key[i] >= (kth | (static_cast<uint32_t>(t + 1) << bit));
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      cnt[t] = __reduce_add_sync(kFull, cnt[t]);
+      if (lane == 0) sh[buf][t][warp] = cnt[t];
+    }
+    __syncthreads();  // two buffers: the next pass writes the other one
+    uint32_t best = kth;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const int total = __reduce_add_sync(kFull, sh[buf][t][lane]);
+      if (total >= k) {
+        best = kth | (static_cast<uint32_t>(t + 1) << bit);
+        reach = total;
+      }
+    }
+    kth = best;
   }
-  int above = 0;
-  for (int i = threadIdx.x; i < n; i += kSelThreads) above += key(i) > kth;
-  above = block_sum(above, sh);
-  const int ties = k - above;  // of the keys equal to kth, the first ones
-  int done = 0, tied = 0;
-  for (int base = 0; base < n; base += kSelThreads) {
-    const int i = base + threadIdx.x;
-    const uint32_t x = i < n ? key(i) : 0u;
-    const int gt = i < n && x > kth;
-    const int eq = i < n && x == kth;
-    const unsigned meq = __ballot_sync(kFull, eq);
-    const unsigned below = (1u << (threadIdx.x & 31)) - 1u;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = __popc(meq);
-    __syncthreads();
-    int beq = tied, all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < (threadIdx.x >> 5)) beq += sh[w];
-      all += sh[w];
+  // taken: keys above kth, and of the keys equal to it the first `ties`.  When exactly k
+  // keys reach kth every equal key is taken.
+  int ties = n;
+  if (reach != k) {  // kth is itself a key, held by more than are left
+    int above = 0;
+    for (int ch = 0; ch < chunks; ++ch) {
+      if (chunks > 1) load(ch);
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) above += key[i] > kth;
     }
-    const int take = gt || (eq && beq + __popc(meq & below) < ties);
-    tied += all;
-    const unsigned mt = __ballot_sync(kFull, take);
+    above = __reduce_add_sync(kFull, above);
+    if (lane == 0) sh[buf][0][warp] = above;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = __popc(mt);
-    __syncthreads();
-    int at = done;
-    all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < (threadIdx.x >> 5)) at += sh[w];
-      all += sh[w];
+    ties = k - __reduce_add_sync(kFull, sh[buf][0][lane]);
+  }
+  int done = 0, tied = 0;  // keys taken and equal keys met in earlier chunks
+  for (int ch = 0; ch < chunks; ++ch) {
+    if (chunks > 1) load(ch);
+    const int i0 = ch * kSelChunk + threadIdx.x * kSelKeys;
+    int eq = 0, gt = 0;
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      eq += i0 + i < n && key[i] == kth;
+      gt += i0 + i < n && key[i] > kth;
     }
-    if (take) out[at + __popc(mt & below)] = __ldg(bt + i);
-    done += all;
+    // exclusive prefix sums of (equal, greater) over the threads, 16 bits each (a chunk has 8192 keys)
+    int v = eq | (gt << 16);
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += u;
+    }
+    __syncthreads();  // sh_scan of the previous chunk has been read
+    if (lane == 31) sh_scan[warp] = inc;
+    __syncthreads();
+    int w = sh_scan[lane];
+    int winc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, winc, o);
+      if (lane >= o) winc += u;
+    }
+    const int total = __shfl_sync(kFull, winc, 31);
+    const int before = __shfl_sync(kFull, winc - w, warp) + inc - v;
+    int eqs = tied + (before & 0xffff);  // equal keys before this thread's
+    int at = done + (before >> 16) + min(before & 0xffff, max(ties - tied, 0));
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      if (i0 + i >= n) break;
+      const bool same = key[i] == kth;
+      if (key[i] > kth || (same && eqs < ties)) out[at++] = __ldg(bt + i0 + i);
+      eqs += same;
+    }
+    done += (total >> 16) + min(total & 0xffff, max(ties - tied, 0));
+    tied += total & 0xffff;
   }
 }
 
@@ -384,27 +791,75 @@ cudaLaunchConfig_t pdl_config(dim3 grid, dim3 block, cudaStream_t stream, cudaLa
   return cfg;
 }
 
-template <typename T>
-cudaError_t key_bounds_typed(const KeyBoundsArgs& a, const KeyBoundsParams& p, cudaStream_t stream) {
+// Tokens per CTA: enough CTAs to fill the GPU (1024 of them: 152 SMs, several
+// each) before a CTA takes more than one token per group of warps, and at most
+// kMaxStretch, which in a prompt holds one run per group.
+RunParams run_params(const int64_t* slot_mapping, int num_tokens, int num_blocks, int block_size, int num_kv_heads,
+                     int parts, int* threads) {
+  RunParams r;
+  r.slot_mapping = slot_mapping;
+  r.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  r.num_tokens = num_tokens;
+  r.num_kv_heads = num_kv_heads;
+  r.block_size = block_size;
+  r.log2_b = __builtin_ctz(static_cast<unsigned>(block_size));
+  const int gw = block_size / kRunRows;
+  const int warps = gw > 8 ? gw : 8;
+  *threads = warps * 32;
+  const int64_t per_cta = static_cast<int64_t>(num_tokens) * num_kv_heads * parts / 1024;
+  r.stretch = warps / gw;
+  while (r.stretch < kMaxStretch && r.stretch < per_cta) r.stretch *= 2;
+  return r;
+}
+
+template <typename P, typename K>
+cudaError_t launch_runs(K kernel, const P& p, int num_kv_heads, int parts, int threads, cudaStream_t stream) {
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(a.num_tokens, a.num_kv_heads), dim3(32), stream, &attr);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((p.r.num_tokens + p.r.stretch - 1) / p.r.stretch, num_kv_heads, parts),
+                                            dim3(threads), stream, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t block_write_typed(const BlockWriteArgs& a, const BlockWriteParams& p, int threads, cudaStream_t stream) {
   switch (a.head_dim) {
-    case 64: return cudaLaunchKernelEx(&cfg, key_bounds_kernel<T, 64>, p);
-    case 128: return cudaLaunchKernelEx(&cfg, key_bounds_kernel<T, 128>, p);
-    case 256: return cudaLaunchKernelEx(&cfg, key_bounds_kernel<T, 256>, p);
+    case 64: return launch_runs(block_write_kernel<T, 64>, p, a.num_kv_heads, 2, threads, stream);
+    case 128: return launch_runs(block_write_kernel<T, 128>, p, a.num_kv_heads, 2, threads, stream);
+    case 256: return launch_runs(block_write_kernel<T, 256>, p, a.num_kv_heads, 2, threads, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 template <typename T>
-cudaError_t block_score_typed(const SelectArgs& a, const SelectParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg =
-      pdl_config(dim3(a.max_blocks_per_seq, a.num_kv_heads, a.num_seqs), dim3(32), stream, &attr);
+cudaError_t key_bounds_typed(const KeyBoundsArgs& a, const KeyBoundsParams& p, int threads, cudaStream_t stream) {
   switch (a.head_dim) {
-    case 64: return cudaLaunchKernelEx(&cfg, block_score_kernel<T, 64>, p);
-    case 128: return cudaLaunchKernelEx(&cfg, block_score_kernel<T, 128>, p);
-    case 256: return cudaLaunchKernelEx(&cfg, block_score_kernel<T, 256>, p);
+    case 64: return launch_runs(key_bounds_kernel<T, 64>, p, a.num_kv_heads, 1, threads, stream);
+    case 128: return launch_runs(key_bounds_kernel<T, 128>, p, a.num_kv_heads, 1, threads, stream);
+    case 256: return launch_runs(key_bounds_kernel<T, 256>, p, a.num_kv_heads, 1, threads, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <typename T, int HEAD_DIM, int NT>
+cudaError_t block_score_t(const SelectArgs& a, const SelectParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr;
+  const int64_t stretches = (a.max_blocks_per_seq + 16 * kScoreTiles - 1) / (16 * kScoreTiles);
+  const int64_t ctas = (stretches * a.num_kv_heads + kScoreWarps - 1) / kScoreWarps;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  const cudaLaunchConfig_t cfg =
+      pdl_config(dim3(static_cast<unsigned>(ctas), a.num_seqs), dim3(kScoreWarps * 32), stream, &attr);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, block_score_kernel<T, HEAD_DIM, NT>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t block_score_typed(const SelectArgs& a, const SelectParams& p, cudaStream_t stream) {
+  const bool two = p.group > 8;
+  switch (a.head_dim) {
+    case 64: return two ? block_score_t<T, 64, 2>(a, p, stream) : block_score_t<T, 64, 1>(a, p, stream);
+    case 128: return two ? block_score_t<T, 128, 2>(a, p, stream) : block_score_t<T, 128, 1>(a, p, stream);
+    case 256: return two ? cudaErrorInvalidValue : block_score_t<T, 256, 1>(a, p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -413,40 +868,27 @@ cudaError_t block_score_typed(const SelectArgs& a, const SelectParams& p, cudaSt
 
 cudaError_t launch_block_write(const BlockWriteArgs& a, cudaStream_t stream) {
   BlockWriteParams p;
+  int threads;
+  p.r = run_params(a.slot_mapping, a.num_tokens, a.num_blocks, a.block_size, a.num_kv_heads, 2, &threads);
   p.key = static_cast<const uint4*>(a.key);
   p.value = static_cast<const uint4*>(a.value);
   p.k_cache = static_cast<uint2*>(a.k_cache);
   p.v_cache = static_cast<uint2*>(a.v_cache);
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;
-  p.slot_mapping = a.slot_mapping;
-  p.num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
-  p.num_tokens = a.num_tokens;
-  p.num_kv_heads = a.num_kv_heads;
-  p.block_size = a.block_size;
-  p.log2_b = __builtin_ctz(static_cast<unsigned>(a.block_size));
-  p.row_vecs = a.head_dim / 8;
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(a.num_tokens, a.num_kv_heads), dim3(64), stream, &attr);
-  const cudaError_t e = a.dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, block_write_kernel<__nv_bfloat16>, p)
-                                           : cudaLaunchKernelEx(&cfg, block_write_kernel<__half>, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return a.dtype == PA_BF16 ? block_write_typed<__nv_bfloat16>(a, p, threads, stream)
+                            : block_write_typed<__half>(a, p, threads, stream);
 }
 
 cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t stream) {
   KeyBoundsParams p;
-  p.key = a.key;
+  int threads;
+  p.r = run_params(a.slot_mapping, a.num_tokens, a.num_blocks, a.block_size, a.num_kv_heads, 1, &threads);
+  p.key = static_cast<const uint4*>(a.key);
   p.bounds = a.key_bounds;
   p.exps = a.bound_exps;
-  p.slot_mapping = a.slot_mapping;
-  p.num_slots = static_cast<int64_t>(a.num_blocks) * a.block_size;
-  p.num_tokens = a.num_tokens;
-  p.num_kv_heads = a.num_kv_heads;
-  p.block_size = a.block_size;
-  p.log2_b = __builtin_ctz(static_cast<unsigned>(a.block_size));
-  const cudaError_t e = a.dtype == PA_BF16 ? key_bounds_typed<__nv_bfloat16>(a, p, stream)
-                                           : key_bounds_typed<__half>(a, p, stream);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return a.dtype == PA_BF16 ? key_bounds_typed<__nv_bfloat16>(a, p, threads, stream)
+                            : key_bounds_typed<__half>(a, p, threads, stream);
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream) {
