@@ -24,9 +24,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// The block of a slot, -1 for padding and slots outside the pool.
-__device__ __forceinline__ int64_t slot_block(int64_t slot, int64_t num_slots, int log2_b) {
-  return slot < 0 || slot >= num_slots ? -1 : slot >> log2_b;
+// The block of a slot, -1 for padding and slots outside the pool (num_slots < 2^31).
+__device__ __forceinline__ int slot_block(int64_t slot, int num_slots, int log2_b) {
+  return static_cast<uint64_t>(slot) < static_cast<uint64_t>(num_slots) ? static_cast<int>(slot) >> log2_b : -1;
 }
 
 // ---------------------------------------------------------- runs of new tokens
@@ -43,7 +43,7 @@ constexpr int kMaxGroup = 16;     // warps per group at most: 256-token blocks
 
 struct RunParams {
   const int64_t* slot_mapping;
-  int64_t num_slots;  // num_blocks * block_size
+  int num_slots;  // num_blocks * block_size
   int num_tokens;
   int num_kv_heads;
   int block_size;
@@ -51,45 +51,59 @@ struct RunParams {
   int stretch;  // tokens per CTA
 };
 
-// Bit l of mask[i]: a run begins at token t0 + 32 i + l.  Every warp computes it.
-__device__ __forceinline__ int find_runs(const RunParams& p, int t0, unsigned (&mask)[kMaxStretch / 32], int lane) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxStretch / 32; ++i) {
-    mask[i] = 0u;
-    if (32 * i >= p.stretch) continue;  // uniform
-    const int t = t0 + 32 * i + lane;
-    const bool in = 32 * i + lane < p.stretch && t < p.num_tokens;
-    const int64_t blk = in ? slot_block(__ldg(p.slot_mapping + t), p.num_slots, p.log2_b) : -1;
-    const int64_t prev = in && t > 0 ? slot_block(__ldg(p.slot_mapping + t - 1), p.num_slots, p.log2_b) : -1;
-    mask[i] = __ballot_sync(kFull, blk >= 0 && blk != prev);
-    n += __popc(mask[i]);
-  }
-  return n;
-}
+// The first tokens of the runs that begin in a CTA's stretch, by 32 tokens: one
+// warp looks at each 32.
+struct RunList {
+  int count[kMaxStretch / 32];
+  int start[kMaxStretch / 32][32];
 
-// The first token of run k of the stretch, k < the number of runs.
-__device__ __forceinline__ int run_start(const unsigned (&mask)[kMaxStretch / 32], int t0, int k) {
-#pragma unroll
-  for (int i = 0; i < kMaxStretch / 32; ++i) {
-    const int c = __popc(mask[i]);
-    if (k < c) {
-      unsigned m = mask[i];
-      for (; k > 0; --k) m &= m - 1;
-      return t0 + 32 * i + __ffs(m) - 1;
+  __device__ __forceinline__ void find(const RunParams& p, int t0) {
+    const int lane = threadIdx.x & 31;
+    const int i = threadIdx.x >> 5;
+    if (i < kMaxStretch / 32) {
+      const int x = 32 * i + lane;
+      const int t = t0 + x;
+      const bool in = x < p.stretch && t < p.num_tokens;
+      const int blk = in ? slot_block(__ldg(p.slot_mapping + t), p.num_slots, p.log2_b) : -1;
+      const int prev = in && t > 0 ? slot_block(__ldg(p.slot_mapping + t - 1), p.num_slots, p.log2_b) : -1;
+      const bool first = blk >= 0 && blk != prev;
+      const unsigned mask = __ballot_sync(kFull, first);
+      if (first) start[i][__popc(mask & ((1u << lane) - 1u))] = t;
+      if (lane == 0) count[i] = __popc(mask);
     }
-    k -= c;
+    __syncthreads();
   }
-  return t0;  // not reached
-}
+  // The first token of run k, -1 past the last.
+  __device__ __forceinline__ int get(int k) const {
+#pragma unroll
+    for (int i = 0; i < kMaxStretch / 32; ++i) {
+      const int c = count[i];
+      if (k < c) return start[i][k];
+      k -= c;
+    }
+    return -1;
+  }
+  __device__ __forceinline__ int total() const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxStretch / 32; ++i) n += count[i];
+    return n;
+  }
+};
 
 // Lane r < 16: the offset in the block of the run's token (first + r), -1 if it
 // belongs to another block.  `first`: the warp's first token, `blk` the run's block.
-__device__ __forceinline__ int row_offset(const RunParams& p, int first, int64_t blk, int lane) {
+__device__ __forceinline__ int row_offset(const RunParams& p, int first, int blk, int lane) {
   const int t = first + lane;
   if (lane >= kRunRows || t >= p.num_tokens) return -1;
   const int64_t slot = __ldg(p.slot_mapping + t);
   return slot_block(slot, p.num_slots, p.log2_b) == blk ? static_cast<int>(slot & (p.block_size - 1)) : -1;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // A warp's 16 rows of one KV head: lane i holds 16-byte unit i % U of row (32 / U) j + i / U.
@@ -98,17 +112,23 @@ struct RowTile {
   static constexpr int U = HEAD_DIM / 8;              // units per row
   static constexpr int RPI = 32 / U;                  // rows per load
   static constexpr int N = kRunRows / RPI;            // loads
-  uint4 v[N];
-  int off[N];  // the row's offset in the block, -1: none
+  uint4 v[N];  // zeros in rows that hold no token of the run
 
-  // `rows`: the tensor as units, `first`: the warp's first token, off16: row_offset of each lane.
-  __device__ __forceinline__ void load(const uint4* rows, int first, int num_kv_heads, int h, int off16, int lane) {
+  // `rows`: the tensor as units, `first`: the warp's first token, off16: row_offset of each
+  // lane, `whole`: every row holds a token.
+  __device__ __forceinline__ void load(const uint4* rows, int first, int num_kv_heads, int h, int off16, bool whole,
+                                       int lane) {
+    const int64_t pitch = static_cast<int64_t>(num_kv_heads) * U;
+    const uint4* at = rows + (first + lane / U) * pitch + static_cast<int64_t>(h) * U + lane % U;
+    if (whole) {  // warp-uniform
+#pragma unroll
+      for (int j = 0; j < N; ++j, at += RPI * pitch) v[j] = __ldg(at);
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int r = j * RPI + lane / U;
-      off[j] = __shfl_sync(kFull, off16, r);
-      v[j] = off[j] >= 0 ? __ldg(rows + (static_cast<int64_t>(first + r) * num_kv_heads + h) * U + lane % U)
-                         : make_uint4(0u, 0u, 0u, 0u);
+      v[j] = __shfl_sync(kFull, off16, r) >= 0 ? __ldg(at + static_cast<int64_t>(j) * RPI * pitch) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
 
@@ -121,10 +141,10 @@ struct RowTile {
     uint32_t m = 0u;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      m = __vmaxu2(m, v[j].x & 0x7fff7fffu);
-      m = __vmaxu2(m, v[j].y & 0x7fff7fffu);
-      m = __vmaxu2(m, v[j].z & 0x7fff7fffu);
-      m = __vmaxu2(m, v[j].w & 0x7fff7fffu);
+      m = max_u16x2(m, v[j].x & 0x7fff7fffu);
+      m = max_u16x2(m, v[j].y & 0x7fff7fffu);
+      m = max_u16x2(m, v[j].z & 0x7fff7fffu);
+      m = max_u16x2(m, v[j].w & 0x7fff7fffu);
     }
     uint32_t top = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
     *all_finite = top < kInf;
@@ -145,6 +165,10 @@ struct RowTile {
   }
 };
 
+// 256 threads for blocks of up to 128 tokens (8 groups of one warp ... one of 8), 512
+// for 256.  A warp's rows take 32 registers at d = 128, so 64 in all let 32 warps share an SM.
+constexpr int run_min_ctas(int head_dim, int threads) { return (head_dim > 128 ? 512 : 1024) / threads; }
+
 struct BlockWriteParams {
   RunParams r;
   const uint4* key;
@@ -155,15 +179,15 @@ struct BlockWriteParams {
   float* v_scales;
 };
 
-// 8 elements times inv (or, with division, over s) as 8 codes.
-template <typename T>
-__device__ __forceinline__ uint2 to_codes8(const uint4& v, float inv, float s, bool pow2) {
+// 8 elements times k (DIVIDE: over k) as 8 codes.
+template <typename T, bool DIVIDE>
+__device__ __forceinline__ uint2 to_codes8(const uint4& v, float k) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 f = unpack2<T>(w[i]);
-    f = pow2 ? make_float2(f.x * inv, f.y * inv) : make_float2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    f = DIVIDE ? make_float2(__fdiv_rn(f.x, k), __fdiv_rn(f.y, k)) : make_float2(f.x * k, f.y * k);
     c[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
@@ -187,9 +211,10 @@ __device__ __forceinline__ uint2 move_codes8(const uint2& v, float ratio) {
 
 // Grid (stretch, KV head, K or V).  The write is a copy that shrinks: 3 bytes
 // moved per element, so HBM bounds prompts and latency bounds single tokens.
-template <typename T, int HEAD_DIM>
-__global__ void __launch_bounds__(kMaxGroup * 32) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
+template <typename T, int HEAD_DIM, int THREADS>
+__global__ void __launch_bounds__(THREADS, run_min_ctas(HEAD_DIM, THREADS)) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
   using Tile = RowTile<HEAD_DIM>;
+  __shared__ RunList runs;
   __shared__ float sh_amax[kMaxGroup];
   __shared__ int sh_starts[kMaxGroup];
   grid_dependency_wait();
@@ -197,28 +222,31 @@ __global__ void __launch_bounds__(kMaxGroup * 32) block_write_kernel(const __gri
   const RunParams& rp = p.r;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const int gw = rp.block_size / kRunRows;  // warps per group
-  const int groups = (blockDim.x >> 5) / gw;
-  const int g = warp / gw;
-  const int wg = warp - g * gw;
+  const int gw_log2 = rp.log2_b - 4;  // 2^gw_log2 = block_size / kRunRows warps per group
+  const int gw = 1 << gw_log2;
+  const int groups = (THREADS / 32) >> gw_log2;
+  const int g = warp >> gw_log2;
+  const int wg = warp & (gw - 1);
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int t0 = blockIdx.x * rp.stretch;
-  unsigned mask[kMaxStretch / 32];
-  const int nruns = find_runs(rp, t0, mask, lane);
+  runs.find(rp, t0);
+  const int nruns = runs.total();
   const uint4* src = is_v ? p.value : p.key;
   uint2* cache = is_v ? p.v_cache : p.k_cache;
   float* scales = is_v ? p.v_scales : p.k_scales;
   for (int k0 = 0; k0 < nruns; k0 += groups) {  // the same trips for every warp
-    const int k = k0 + g;
-    const bool on = k < nruns;
-    const int t = on ? run_start(mask, t0, k) : 0;
-    const int64_t blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : -2;
+    const int t = runs.get(k0 + g);
+    const bool on = t >= 0;
+    const int blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : 0;
     const int first = t + wg * kRunRows;
     const int off16 = on ? row_offset(rp, first, blk, lane) : -1;
-    float* scale = scales + (on ? blk * rp.num_kv_heads + h : 0);
+    float* scale = scales + (static_cast<int64_t>(blk) * rp.num_kv_heads + h);
+    // 16 tokens in consecutive slots
+    const int off0 = __shfl_sync(kFull, off16, 0);
+    const bool whole = __all_sync(kFull, lane >= kRunRows || (off0 >= 0 && off16 == off0 + lane));
     Tile tile;
-    tile.load(src, first, rp.num_kv_heads, h, off16, lane);
+    tile.load(src, first, rp.num_kv_heads, h, off16, whole, lane);
     const float was = on ? *scale : 0.f;
     bool finite;
     float amax = tile.template finite_amax<T>(&finite);
@@ -237,13 +265,13 @@ __global__ void __launch_bounds__(kMaxGroup * 32) block_write_kernel(const __gri
     const float need = pow2f(scale_exp(amax));
     const float old = !starts && was > 0.f && was <= kFloatMax ? was : 0.f;
     const float s = fmaxf(old, need);
-    uint2* rows = cache + on * ((blk * rp.block_size * rp.num_kv_heads + h) * Tile::U + lane % Tile::U);
-    const int64_t pitch = static_cast<int64_t>(rp.num_kv_heads) * Tile::U;
+    const int pitch = rp.num_kv_heads * Tile::U;  // units between slots
+    uint2* rows = cache + static_cast<int64_t>(blk << rp.log2_b) * pitch + h * Tile::U + lane % Tile::U;
     if (on && old > 0.f && s > old) {  // the block's other codes move to the new scale
       const float ratio = __fdiv_rn(old, s);
 #pragma unroll 4
       for (int o = wg * kRunRows + lane / Tile::U; o < (wg + 1) * kRunRows; o += Tile::RPI)
-        rows[o * pitch] = move_codes8(rows[o * pitch], ratio);
+        rows[static_cast<int64_t>(o) * pitch] = move_codes8(rows[static_cast<int64_t>(o) * pitch], ratio);
     }
     // the moved codes before the new ones (which may share rows with them), every
     // read of the scale before its write
@@ -254,10 +282,30 @@ __global__ void __launch_bounds__(kMaxGroup * 32) block_write_kernel(const __gri
     }
     const int bits = __float_as_int(s);
     const bool pow2 = (bits & 0x7fffff) == 0 && bits <= (126 + 127) << 23 && bits >= 1 << 23;
-    const float inv = pow2 ? pow2f(127 - (bits >> 23)) : 1.f;
+    if (pow2) {  // uniform over the group: a multiplication by the exact inverse
+      const float inv = pow2f(127 - (bits >> 23));
+      if (whole) {
+        uint2* at = rows + static_cast<int64_t>(off0 + lane / Tile::U) * pitch;
+        const int64_t step = static_cast<int64_t>(Tile::RPI) * pitch;
 #pragma unroll
-    for (int j = 0; j < Tile::N; ++j)
-      if (tile.off[j] >= 0) rows[tile.off[j] * pitch] = to_codes8<T>(tile.v[j], inv, s, pow2);
+        for (int j = 0; j < Tile::N; ++j, at += step) *at = to_codes8<T, false>(tile.v[j], inv);
+      } else {
+#pragma unroll
+        for (int j = 0; j < Tile::N; ++j) {
+          const int off = __shfl_sync(kFull, off16, j * Tile::RPI + lane / Tile::U);
+          if (off >= 0) rows[static_cast<int64_t>(off) * pitch] = to_codes8<T, false>(tile.v[j], inv);
+        }
+      }
+    } else {  // a scale from elsewhere
+#pragma unroll 1
+      for (int j = 0; j < kRunRows; j += Tile::RPI) {
+        const int r = j + lane / Tile::U;
+        const int off = __shfl_sync(kFull, off16, r);
+        if (off >= 0)
+          rows[static_cast<int64_t>(off) * pitch] =
+              to_codes8<T, true>(__ldg(src + (static_cast<int64_t>(first + r) * rp.num_kv_heads + h) * Tile::U + lane % Tile::U), s);
+      }
+    }
     if (on && wg == 0 && lane == 0) *scale = s;
   }
 }
@@ -310,12 +358,13 @@ __device__ __forceinline__ uint32_t nan2(uint32_t w, uint32_t with) {
 
 // Grid (stretch, KV head).  Reads 2 bytes per element and writes 2 per channel
 // and block: HBM bounds prompts, latency single tokens.
-template <typename T, int HEAD_DIM>
-__global__ void __launch_bounds__(kMaxGroup * 32) key_bounds_kernel(const __grid_constant__ KeyBoundsParams p) {
+template <typename T, int HEAD_DIM, int THREADS>
+__global__ void __launch_bounds__(THREADS, run_min_ctas(HEAD_DIM, THREADS)) key_bounds_kernel(const __grid_constant__ KeyBoundsParams p) {
   using Tile = RowTile<HEAD_DIM>;
   constexpr int U = Tile::U;
   constexpr uint32_t kPosInf = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
   constexpr uint32_t kNegInf = kPosInf | 0x80008000u;
+  __shared__ RunList runs;
   __shared__ float sh_amax[kMaxGroup];
   __shared__ int sh_starts[kMaxGroup];
   __shared__ uint4 sh_lo[kMaxGroup][U], sh_hi[kMaxGroup][U];
@@ -324,24 +373,25 @@ __global__ void __launch_bounds__(kMaxGroup * 32) key_bounds_kernel(const __grid
   const RunParams& rp = p.r;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const int gw = rp.block_size / kRunRows;
-  const int groups = (blockDim.x >> 5) / gw;
-  const int g = warp / gw;
-  const int wg = warp - g * gw;
+  const int gw_log2 = rp.log2_b - 4;  // 2^gw_log2 = block_size / kRunRows warps per group
+  const int gw = 1 << gw_log2;
+  const int groups = (THREADS / 32) >> gw_log2;
+  const int g = warp >> gw_log2;
+  const int wg = warp & (gw - 1);
   const int h = blockIdx.y;
   const int t0 = blockIdx.x * rp.stretch;
-  unsigned mask[kMaxStretch / 32];
-  const int nruns = find_runs(rp, t0, mask, lane);
+  runs.find(rp, t0);
+  const int nruns = runs.total();
   for (int k0 = 0; k0 < nruns; k0 += groups) {  // the same trips for every warp
-    const int k = k0 + g;
-    const bool on = k < nruns;
-    const int t = on ? run_start(mask, t0, k) : 0;
-    const int64_t blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : -2;
+    const int t = runs.get(k0 + g);
+    const bool on = t >= 0;
+    const int blk = on ? slot_block(__ldg(rp.slot_mapping + t), rp.num_slots, rp.log2_b) : 0;
     const int first = t + wg * kRunRows;
     const int off16 = on ? row_offset(rp, first, blk, lane) : -1;
-    const int64_t at = on ? blk * rp.num_kv_heads + h : 0;
+    const int64_t at = static_cast<int64_t>(blk) * rp.num_kv_heads + h;
+    const bool whole = __all_sync(kFull, off16 >= 0 || lane >= kRunRows);  // 16 tokens of the run
     Tile tile;
-    tile.load(p.key, first, rp.num_kv_heads, h, off16, lane);
+    tile.load(p.key, first, rp.num_kv_heads, h, off16, whole, lane);
     // the block's bounds as they are, on the lanes that will write them
     const bool writer = on && wg == 0 && lane < U;
     uint2* lo_at = reinterpret_cast<uint2*>(p.bounds + at * 2 * HEAD_DIM) + lane % U;
@@ -362,14 +412,26 @@ __global__ void __launch_bounds__(kMaxGroup * 32) key_bounds_kernel(const __grid
       lo[i] = kPosInf;
       hi[i] = kNegInf;
     }
+    if (finite && whole) {
 #pragma unroll
-    for (int j = 0; j < Tile::N; ++j) {
-      if (tile.off[j] < 0) continue;
-      const uint32_t w[4] = {tile.v[j].x, tile.v[j].y, tile.v[j].z, tile.v[j].w};
+      for (int j = 0; j < Tile::N; ++j) {
+        const uint32_t w[4] = {tile.v[j].x, tile.v[j].y, tile.v[j].z, tile.v[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = min2<T>(lo[i], finite ? w[i] : nan2<T>(w[i], kNegInf));  // NaN: the widest bound
-        hi[i] = max2<T>(hi[i], finite ? w[i] : nan2<T>(w[i], kPosInf));
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = min2<T>(lo[i], w[i]);
+          hi[i] = max2<T>(hi[i], w[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < Tile::N; ++j) {
+        if (__shfl_sync(kFull, off16, j * Tile::RPI + lane / U) < 0) continue;
+        const uint32_t w[4] = {tile.v[j].x, tile.v[j].y, tile.v[j].z, tile.v[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo[i] = min2<T>(lo[i], nan2<T>(w[i], kNegInf));  // NaN: the widest bound
+          hi[i] = max2<T>(hi[i], nan2<T>(w[i], kPosInf));
+        }
       }
     }
 #pragma unroll
@@ -494,7 +556,7 @@ __device__ __forceinline__ float whole(float x, float inv) {
 }
 
 template <typename T, int HEAD_DIM, int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_score_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? 3 : 1) block_score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int UH = HEAD_DIM / 64;  // 16-byte units per lane and half (lo or hi) of a row
   constexpr int STEPS = UH * 4;      // k-steps per half
   grid_dependency_wait();
@@ -639,21 +701,46 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head).  The k-th largest key is found two bits at a
-// time: each pass counts the keys at or above three trial values and keeps the
-// largest that still has k (a pass that finds one with exactly k ends the
-// search: no tie is left to break).  Keys sit in registers, 8 per thread, when
-// the sequence has at most 8192 blocks; longer tables are read again per pass.
-// No atomics, and a histogram would not do: the scores of one row share their
-// leading bits.  Latency bounds it (a few us; the scores are 32 KB).
+// One CTA per (sequence, KV head).  The smallest kept key is found by counting:
+// the range of the keys is cut into 1024 buckets, the keys in each are counted
+// (integer atomics in shared memory: the counts, and so the result, do not
+// depend on their order), and the bucket that holds the last kept key becomes
+// the next range, until its keys are all kept or all equal.  The range starts at
+// the row's own minimum and maximum, because the scores of one row share their
+// leading bits: counting by leading bits would put most keys in one bucket, and
+// comparing all keys with three trial values per two bits took 16 us.  Ten bits
+// a round: at most four rounds, usually two.
+// Latency bounds it: the scores of 8192 blocks are 32 KB.
 constexpr int kSelThreads = 1024;
-constexpr int kSelKeys = 8;
+constexpr int kSelKeys = 8;  // per thread; rows of more than 8192 blocks are read again in each round
 constexpr int kSelChunk = kSelThreads * kSelKeys;
+
+// Inclusive sums over the CTA's threads in order; `sh` has one entry per warp and
+// is free again after the next __syncthreads.
+__device__ __forceinline__ int cta_scan(int v, int* sh, int* total) {
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  const int w = sh[lane];
+  const int before = __reduce_add_sync(kFull, lane < warp ? w : 0);
+  *total = __reduce_add_sync(kFull, w);
+  return before + inc;
+}
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p) {
   constexpr int WARPS = kSelThreads / 32;
-  __shared__ int sh[2][3][WARPS];
-  __shared__ int sh_scan[WARPS];
+  static_assert(WARPS == 32, "one scan entry per lane");
+  __shared__ int hist[kSelThreads];
+  __shared__ int sh_scan[2][WARPS];
+  __shared__ uint32_t sh_lo[WARPS], sh_hi[WARPS];
+  __shared__ int sh_pick[3];
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
@@ -673,105 +760,105 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     for (int i = threadIdx.x; i < n; i += kSelThreads) out[i] = __ldg(bt + i);
     return;
   }
+  // the blocks that compete are [num_first, n - num_last) (not empty: n > max_selected)
+  const int c0 = p.num_first, c1 = n - p.num_last;
   const float* sc = p.scores + row * p.pitch;
   uint32_t key[kSelKeys];
-  auto load = [&](int chunk) {  // the thread's keys of chunk `chunk`, in index order; 0 past the end
+  auto load = [&](int chunk) {  // the thread's keys of chunk `chunk`, in index order
     const int i0 = chunk * kSelChunk + threadIdx.x * kSelKeys;
 #pragma unroll
     for (int h = 0; h < kSelKeys / 4; ++h) {
-      const int i = i0 + 4 * h;
-      // rows are padded to 4, so the vector stays in the row; scores are at least -inf, whose key is above 0
+      const int i = i0 + 4 * h;  // rows are padded to 4, so the vector stays in the row
       const float4 v = i < n ? *reinterpret_cast<const float4*>(sc + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        key[4 * h + x] = i + x >= n ? 0u
-                         : (i + x < p.num_first || i + x >= n - p.num_last) ? 0xffffffffu : order_key(f[x]);
+      key[4 * h] = order_key(v.x);
+      key[4 * h + 1] = order_key(v.y);
+      key[4 * h + 2] = order_key(v.z);
+      key[4 * h + 3] = order_key(v.w);
     }
   };
   const int chunks = (n + kSelChunk - 1) / kSelChunk;
   load(0);
-  uint32_t kth = 0;  // the largest value found so far that at least k keys reach
-  int reach = n;     // the number of keys that reach it
-  int buf = 0;
-  for (int bit = 30; bit >= 0 && reach != k; bit -= 2, buf ^= 1) {
-    int cnt[3] = {0, 0, 0};
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  for (int ch = 0; ch < chunks; ++ch) {
+    if (ch > 0) load(ch);
+    const int i0 = ch * kSelChunk + threadIdx.x * kSelKeys;
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i)
+      if (i0 + i >= c0 && i0 + i < c1) {
+        lo = min(lo, key[i]);
+        hi = max(hi, key[i]);
+      }
+  }
+  lo = __reduce_min_sync(kFull, lo);
+  hi = __reduce_max_sync(kFull, hi);
+  if (lane == 0) {
+    sh_lo[warp] = lo;
+    sh_hi[warp] = hi;
+  }
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  lo = __reduce_min_sync(kFull, sh_lo[lane]);
+  hi = __reduce_max_sync(kFull, sh_hi[lane]);
+  int need = k - p.num_first - p.num_last;  // competing blocks still to be kept among the keys in [lo, hi]
+  int ties = n;                             // of the keys equal to lo in the end, how many are kept
+  for (int round = 0; need > 0; ++round) {
+    const int shift = max(0, 32 - __clz(hi - lo) - 10);
     for (int ch = 0; ch < chunks; ++ch) {
       if (chunks > 1) load(ch);
+      const int i0 = ch * kSelChunk + threadIdx.x * kSelKeys;
 #pragma unroll
       for (int i = 0; i < kSelKeys; ++i)
-#pragma unroll
-        for (int t = 0; t < 3; ++t) cnt[t] += key[i] >= (kth | (static_cast<uint32_t>(t + 1) << bit));
+        if (i0 + i >= c0 && i0 + i < c1 && key[i] >= lo && key[i] <= hi) atomicAdd(&hist[(key[i] - lo) >> shift], 1);
     }
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      cnt[t] = __reduce_add_sync(kFull, cnt[t]);
-      if (lane == 0) sh[buf][t][warp] = cnt[t];
-    }
-    __syncthreads();  // two buffers: the next pass writes the other one
-    uint32_t best = kth;
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      const int total = __reduce_add_sync(kFull, sh[buf][t][lane]);
-      if (total >= k) {
-        best = kth | (static_cast<uint32_t>(t + 1) << bit);
-        reach = total;
-      }
-    }
-    kth = best;
-  }
-  // taken: keys above kth, and of the keys equal to it the first `ties`.  When exactly k
-  // keys reach kth every equal key is taken.
-  int ties = n;
-  if (reach != k) {  // kth is itself a key, held by more than are left
-    int above = 0;
-    for (int ch = 0; ch < chunks; ++ch) {
-      if (chunks > 1) load(ch);
-#pragma unroll
-      for (int i = 0; i < kSelKeys; ++i) above += key[i] > kth;
-    }
-    above = __reduce_add_sync(kFull, above);
-    if (lane == 0) sh[buf][0][warp] = above;
     __syncthreads();
-    ties = k - __reduce_add_sync(kFull, sh[buf][0][lane]);
+    const int b = kSelThreads - 1 - threadIdx.x;  // the threads walk the buckets from the top
+    const int count = hist[b];
+    int total;
+    const int upto = cta_scan(count, sh_scan[round & 1], &total);  // (its barrier: the buckets are read)
+    hist[b] = 0;
+    if (upto >= need && upto - count < need) {
+      sh_pick[0] = b;
+      sh_pick[1] = need - (upto - count);
+      sh_pick[2] = count;
+    }
+    __syncthreads();
+    need = sh_pick[1];
+    lo += static_cast<uint32_t>(sh_pick[0]) << shift;
+    hi = lo + ((1u << shift) - 1u);
+    if (sh_pick[2] == need) break;  // every key from lo on is kept
+    if (shift == 0) {               // equal keys: the first `need` of them
+      ties = need;
+      break;
+    }
   }
-  int done = 0, tied = 0;  // keys taken and equal keys met in earlier chunks
+  const bool any = k > p.num_first + p.num_last;  // otherwise the forced blocks fill the row
+  // kept in index order: forced blocks, keys above lo, and of those equal to lo the first `ties`
+  int done = 0, tied = 0;
   for (int ch = 0; ch < chunks; ++ch) {
     if (chunks > 1) load(ch);
     const int i0 = ch * kSelChunk + threadIdx.x * kSelKeys;
     int eq = 0, gt = 0;
 #pragma unroll
     for (int i = 0; i < kSelKeys; ++i) {
-      eq += i0 + i < n && key[i] == kth;
-      gt += i0 + i < n && key[i] > kth;
+      const int at = i0 + i;
+      const bool rival = at >= c0 && at < c1;
+      eq += any && rival && key[i] == lo;
+      gt += at < n && (!rival || (any && key[i] > lo));
     }
-    // exclusive prefix sums of (equal, greater) over the threads, 16 bits each (a chunk has 8192 keys)
-    int v = eq | (gt << 16);
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += u;
-    }
-    __syncthreads();  // sh_scan of the previous chunk has been read
-    if (lane == 31) sh_scan[warp] = inc;
-    __syncthreads();
-    int w = sh_scan[lane];
-    int winc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(kFull, winc, o);
-      if (lane >= o) winc += u;
-    }
-    const int total = __shfl_sync(kFull, winc, 31);
-    const int before = __shfl_sync(kFull, winc - w, warp) + inc - v;
+    // prefix sums of (equal, others kept), 16 bits each: a chunk has 8192 keys
+    const int v = eq | (gt << 16);
+    int total;
+    __syncthreads();  // the previous use of the scan entries is over
+    const int before = cta_scan(v, sh_scan[0], &total) - v;
     int eqs = tied + (before & 0xffff);  // equal keys before this thread's
     int at = done + (before >> 16) + min(before & 0xffff, max(ties - tied, 0));
 #pragma unroll
     for (int i = 0; i < kSelKeys; ++i) {
-      if (i0 + i >= n) break;
-      const bool same = key[i] == kth;
-      if (key[i] > kth || (same && eqs < ties)) out[at++] = __ldg(bt + i0 + i);
+      const int x = i0 + i;
+      if (x >= n) break;
+      const bool rival = x >= c0 && x < c1;
+      const bool same = any && rival && key[i] == lo;
+      if (!rival || (any && key[i] > lo) || (same && eqs < ties)) out[at++] = __ldg(bt + x);
       eqs += same;
     }
     done += (total >> 16) + min(total & 0xffff, max(ties - tied, 0));
@@ -798,7 +885,7 @@ RunParams run_params(const int64_t* slot_mapping, int num_tokens, int num_blocks
                      int parts, int* threads) {
   RunParams r;
   r.slot_mapping = slot_mapping;
-  r.num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  r.num_slots = num_blocks * block_size;
   r.num_tokens = num_tokens;
   r.num_kv_heads = num_kv_heads;
   r.block_size = block_size;
@@ -821,22 +908,22 @@ cudaError_t launch_runs(K kernel, const P& p, int num_kv_heads, int parts, int t
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t block_write_typed(const BlockWriteArgs& a, const BlockWriteParams& p, int threads, cudaStream_t stream) {
+template <typename T, int THREADS>
+cudaError_t block_write_typed(const BlockWriteArgs& a, const BlockWriteParams& p, cudaStream_t stream) {
   switch (a.head_dim) {
-    case 64: return launch_runs(block_write_kernel<T, 64>, p, a.num_kv_heads, 2, threads, stream);
-    case 128: return launch_runs(block_write_kernel<T, 128>, p, a.num_kv_heads, 2, threads, stream);
-    case 256: return launch_runs(block_write_kernel<T, 256>, p, a.num_kv_heads, 2, threads, stream);
+    case 64: return launch_runs(block_write_kernel<T, 64, THREADS>, p, a.num_kv_heads, 2, THREADS, stream);
+    case 128: return launch_runs(block_write_kernel<T, 128, THREADS>, p, a.num_kv_heads, 2, THREADS, stream);
+    case 256: return launch_runs(block_write_kernel<T, 256, THREADS>, p, a.num_kv_heads, 2, THREADS, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
-template <typename T>
-cudaError_t key_bounds_typed(const KeyBoundsArgs& a, const KeyBoundsParams& p, int threads, cudaStream_t stream) {
+template <typename T, int THREADS>
+cudaError_t key_bounds_typed(const KeyBoundsArgs& a, const KeyBoundsParams& p, cudaStream_t stream) {
   switch (a.head_dim) {
-    case 64: return launch_runs(key_bounds_kernel<T, 64>, p, a.num_kv_heads, 1, threads, stream);
-    case 128: return launch_runs(key_bounds_kernel<T, 128>, p, a.num_kv_heads, 1, threads, stream);
-    case 256: return launch_runs(key_bounds_kernel<T, 256>, p, a.num_kv_heads, 1, threads, stream);
+    case 64: return launch_runs(key_bounds_kernel<T, 64, THREADS>, p, a.num_kv_heads, 1, THREADS, stream);
+    case 128: return launch_runs(key_bounds_kernel<T, 128, THREADS>, p, a.num_kv_heads, 1, THREADS, stream);
+    case 256: return launch_runs(key_bounds_kernel<T, 256, THREADS>, p, a.num_kv_heads, 1, THREADS, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -876,8 +963,11 @@ cudaError_t launch_block_write(const BlockWriteArgs& a, cudaStream_t stream) {
   p.v_cache = static_cast<uint2*>(a.v_cache);
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;
-  return a.dtype == PA_BF16 ? block_write_typed<__nv_bfloat16>(a, p, threads, stream)
-                            : block_write_typed<__half>(a, p, threads, stream);
+  if (threads == 512)
+    return a.dtype == PA_BF16 ? block_write_typed<__nv_bfloat16, 512>(a, p, stream)
+                              : block_write_typed<__half, 512>(a, p, stream);
+  return a.dtype == PA_BF16 ? block_write_typed<__nv_bfloat16, 256>(a, p, stream)
+                            : block_write_typed<__half, 256>(a, p, stream);
 }
 
 cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t stream) {
@@ -887,8 +977,11 @@ cudaError_t launch_key_bounds(const KeyBoundsArgs& a, cudaStream_t stream) {
   p.key = static_cast<const uint4*>(a.key);
   p.bounds = a.key_bounds;
   p.exps = a.bound_exps;
-  return a.dtype == PA_BF16 ? key_bounds_typed<__nv_bfloat16>(a, p, threads, stream)
-                            : key_bounds_typed<__half>(a, p, threads, stream);
+  if (threads == 512)
+    return a.dtype == PA_BF16 ? key_bounds_typed<__nv_bfloat16, 512>(a, p, stream)
+                              : key_bounds_typed<__half, 512>(a, p, stream);
+  return a.dtype == PA_BF16 ? key_bounds_typed<__nv_bfloat16, 256>(a, p, stream)
+                            : key_bounds_typed<__half, 256>(a, p, stream);
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t stream) {
