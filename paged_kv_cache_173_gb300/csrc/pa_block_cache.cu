@@ -536,8 +536,13 @@ struct SelectParams {
 // global memory in the MMA's layout (lane (g, c) reads 16-byte units c, c + 4,
 // ... of rows g and g + 8; a unit's four words are four k-steps); neighbouring
 // warps take neighbouring heads, whose rows of a block are neighbours in memory.
-constexpr int kScoreTiles = 4;  // tiles of 16 blocks per warp, behind one preparation of the queries
-constexpr int kScoreWarps = 8;
+#ifndef SC_T
+#define SC_T 4
+#define SC_W 8
+#define SC_M 3
+#endif
+constexpr int kScoreTiles = SC_T;  // tiles of 16 blocks per warp, behind one preparation of the queries
+constexpr int kScoreWarps = SC_W;
 
 // Four codes of one word as two pairs of float16: code + 128 + 1024 by bytes, minus 1152.
 __device__ __forceinline__ void codes4_to_half(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -556,7 +561,7 @@ __device__ __forceinline__ float whole(float x, float inv) {
 }
 
 template <typename T, int HEAD_DIM, int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? 3 : 1) block_score_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? SC_M : 1) block_score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int UH = HEAD_DIM / 64;  // 16-byte units per lane and half (lo or hi) of a row
   constexpr int STEPS = UH * 4;      // k-steps per half
   grid_dependency_wait();

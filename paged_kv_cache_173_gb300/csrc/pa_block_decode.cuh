@@ -10,19 +10,20 @@
 //                        not fill the GPU.
 //
 // The mathematics of the scales.  Block b of a sequence holds the keys
-// ks_b * code and the values vs_b * code.  With s_i the base-2 score of token
-// i (scale * log2(e) * ks_b * q . code_i) and vs_b = m_b * 2^e_b, 1 <= m_b < 2,
+// ks_b * code and the values v_b * code.  With s_i the base-2 score of token i
+// (scale * log2(e) * ks_b * q . code_i),
 //
-//   out = sum_i 2^s_i vs_b code_i / sum_i 2^s_i
-//       = sum_i w_i m_b code_i / sum_i w_i 2^-e_b,   w_i = 2^(s_i + e_b - M),
+//   out = sum_i 2^s_i v_b code_i / sum_i 2^s_i
+//       = sum_i w_i code_i / sum_i w_i / v_b,   w_i = 2^(s_i + log2 v_b - M),
 //
-// with M the running maximum of s_i + e_b.  So the value scale moves into the
-// exponent of the one exponential that each score needs anyway: the weights
-// that meet the codes lie in [0, 2) whatever the scales are, the accumulators
-// change scale only when M moves, and the sum of weights takes one multiply
-// by the power of two 2^-e_b.  Nothing is lost when a block of large values
-// stands next to one of tiny values: the dominant products set M.  m_b is 1
-// for the power-of-two scales that pa_reshape_and_cache_fp8_block makes.
+// with M the running maximum of s_i + log2 v_b.  So the value scale moves into
+// the exponent of the one exponential that each score needs anyway: the weights
+// that meet the codes lie in [0, 1] whatever the scales are, the accumulators
+// change scale only when M moves, and the sum takes one multiply per chunk.
+// Nothing is lost when a block of large values stands next to one of tiny
+// values: the dominant products set M.  The rounding of log2 v_b (below 2^-17)
+// is the same in w_i above and below the line, so it weighs a block by 1 + 2^-17
+// at most.
 //
 // Queries enter the MMAs as float16 beside the widened codes (exact in
 // float16).  A bfloat16 query row is first scaled by the power of two that
@@ -38,7 +39,7 @@ namespace pa {
 
 namespace {
 
-constexpr float kMinValueScale = 5.421010862427522e-20f;  // 2^-64: smaller value scales read as 0
+constexpr float kMinValueScale = 5.421010862427522e-20f;  // 2^-64: smaller value scales read as this
 
 struct BlockDecodeParams {
   CUtensorMap tmap_k;  // as DecodeParams: [N*B rows][Hk][d], 16-row boxes
@@ -100,30 +101,25 @@ __device__ __forceinline__ void load_q_frags_scaled(uint32_t (&qf)[HEAD_DIM / 16
   }
 }
 
-// The scale of one chunk's keys, and of its values as m * 2^e.
+// The scale of one chunk's keys, and of its values v as log2 v and 1 / v.
 struct ChunkScale {
   float ks;
-  float vm;    // mantissa in [1, 2), or 0 for values that read as zero
-  float ve;    // exponent
-  float vinv;  // 2^-e
-  bool bad;    // a scale that is negative, infinite or NaN
+  float lv;
+  float vinv;
+  bool bad;  // a scale that is negative, infinite or NaN
 
   __device__ __forceinline__ void set(float k, float v) {
     bad = !(k >= 0.f && k <= kFloatMax && v >= 0.f && v <= kFloatMax);
     ks = k;
-    const bool zero = !(v >= kMinValueScale);
-    const int bits = __float_as_int(zero ? kMinValueScale : v);
-    const int e = (bits >> 23) - 127;
-    vm = zero ? 0.f : __int_as_float((bits & 0x7fffff) | 0x3f800000);
-    ve = static_cast<float>(e);
-    vinv = __int_as_float((127 - min(e, 126)) << 23);
-    if (e > 126) vinv = 0.5f * vinv;  // 2^-127, a subnormal
+    v = fmaxf(v, kMinValueScale);
+    lv = __log2f(v);
+    vinv = __frcp_rn(v);
   }
 };
 
 // softmax_step (pa_decode.cuh) with a scale per chunk: sl[nt][j] is the
 // base-2 factor of query nt * 8 + 2c + j without the key scale.  P^T enters
-// as float16(w * m); the running sum adds w * 2^-e unrounded.
+// as float16(w); the running sum adds w / v unrounded.
 template <int HEAD_DIM, int NT, int NSUB>
 __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, const float (&sacc)[NSUB][NT][4],
                                                     const int (&valid)[NSUB], const float (&sl)[NT][2],
@@ -139,10 +135,10 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
       const bool v0 = g < valid[sb];
       const bool v1 = g + 8 < valid[sb];
       const float f0 = sl[nt][0] * cs[sb].ks, f1 = sl[nt][1] * cs[sb].ks;
-      x[sb][0] = v0 ? fmaf(sacc[sb][nt][0], f0, cs[sb].ve) : -INFINITY;
-      x[sb][1] = v0 ? fmaf(sacc[sb][nt][1], f1, cs[sb].ve) : -INFINITY;
-      x[sb][2] = v1 ? fmaf(sacc[sb][nt][2], f0, cs[sb].ve) : -INFINITY;
-      x[sb][3] = v1 ? fmaf(sacc[sb][nt][3], f1, cs[sb].ve) : -INFINITY;
+      x[sb][0] = v0 ? fmaf(sacc[sb][nt][0], f0, cs[sb].lv) : -INFINITY;
+      x[sb][1] = v0 ? fmaf(sacc[sb][nt][1], f1, cs[sb].lv) : -INFINITY;
+      x[sb][2] = v1 ? fmaf(sacc[sb][nt][2], f0, cs[sb].lv) : -INFINITY;
+      x[sb][3] = v1 ? fmaf(sacc[sb][nt][3], f1, cs[sb].lv) : -INFINITY;
     }
     float mx0 = fmaxf(x[0][0], x[0][2]);
     float mx1 = fmaxf(x[0][1], x[0][3]);
@@ -170,9 +166,8 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
       const float p2 = ex2(x[sb][2] - mn0), p3 = ex2(x[sb][3] - mn1);  // token g + 8
       sum0 = fmaf(p0 + p2, cs[sb].vinv, sum0);
       sum1 = fmaf(p1 + p3, cs[sb].vinv, sum1);
-      const float m = cs[sb].vm;
-      pb[sb][nt][0] = movmatrix_trans(pack_half2(p0 * m, p1 * m));  // P^T tokens 0-7 as the B fragment
-      pb[sb][nt][1] = movmatrix_trans(pack_half2(p2 * m, p3 * m));  // P^T tokens 8-15
+      pb[sb][nt][0] = movmatrix_trans(pack_half2(p0, p1));  // P^T tokens 0-7 as the B fragment
+      pb[sb][nt][1] = movmatrix_trans(pack_half2(p2, p3));  // P^T tokens 8-15
     }
     acc.l[nt][0] = fmaf(acc.l[nt][0], cr0, sum0);
     acc.l[nt][1] = fmaf(acc.l[nt][1], cr1, sum1);
@@ -217,16 +212,73 @@ __device__ __forceinline__ void attend_scaled(WarpAcc<HEAD_DIM, NT>& acc, const 
   }
 }
 
+// CTA shapes: warps, stages per warp, 16-token chunks per stage, and the CTAs
+// per SM that the registers are bounded for (0: unbounded).  Measured on one GPU
+// through graph replays, E4M3 pools, beside the shapes of the pool-scaled decode
+// (DecodeShape: 4 warps x 2 stages x 2 chunks up to d = 128):
+//  - single launch, d = 128, groups up to 8: 8 x 2 x 1.  A CTA that walks a long
+//    sequence alone is paced by its warps' chains, and eight of them halve its
+//    share of each (64 sequences of 128 to 2048 tokens, 32/8 heads: 31.2 -> 29.3
+//    us; 32 x 8192, 64/8 heads: 91.1 -> 83.5 us; 8 x 1 x 2: 30.5 and 88.3 us).
+//    d = 64: 8 x 2 x 2 (64 x 128 to 4096 tokens: 44.1 -> 29.7 us).  At d = 256 and for
+//    groups of 16 the accumulators leave no room for more warps (36.5 us against
+//    38.2 to 50.9; 104.5 us against 110 to 134).
+//  - split-K, whose CTAs cover a partition: many small CTAs overlap their
+//    beginnings and ends.  d = 128: 2 x 2 x 2, six per SM (32 K to 131 K tokens, 512
+//    per partition: 139.8 -> 129.4 us); groups of 16: 2 x 2 x 1 (227 -> 175 us);
+//    d = 256: 2 x 2 x 1 (82.5 -> 80.0 us).
+template <int HEAD_DIM, int NT, int ELEM, int KIND, bool PER_HEAD>
+struct BlockShape {
+  using Base = DecodeShape<HEAD_DIM, ELEM, KIND>;
+  static constexpr bool FP8 = ELEM == 1;
+  static constexpr bool WIDE = FP8 && KIND == KIND_SINGLE && NT == 1 && HEAD_DIM <= 128;
+  static constexpr bool SMALL = FP8 && KIND == KIND_SPLITK && HEAD_DIM >= 128;
+#ifdef SW_W
+  static constexpr bool ON = ELEM == SW_E && HEAD_DIM == SW_D && NT == SW_NT && KIND == SW_K;
+  static constexpr int WARPS = ON ? SW_W : WIDE ? 8 : SMALL ? 2 : Base::WARPS;
+  static constexpr int STAGES = ON ? SW_S : WIDE || SMALL ? 2 : Base::STAGES;
+  static constexpr int CPS = ON ? SW_C : FP8 && (HEAD_DIM == 64 || (HEAD_DIM == 128 && !WIDE && (!SMALL || NT == 1))) ? 2 : 1;
+  static constexpr int MIN_CTAS = ON ? SW_M : WIDE ? 2 : SMALL ? (NT == 1 ? 6 : 5) : 0;
+#else
+  static constexpr int WARPS = WIDE ? 8 : SMALL ? 2 : Base::WARPS;
+  static constexpr int STAGES = WIDE || SMALL ? 2 : Base::STAGES;
+  static constexpr int CPS = FP8 && (HEAD_DIM == 64 || (HEAD_DIM == 128 && !WIDE && (!SMALL || NT == 1))) ? 2 : 1;
+  static constexpr int MIN_CTAS = WIDE ? 2 : SMALL ? (NT == 1 ? 6 : 5) : 0;
+#endif
+};
+// Tokens of table capacity per CTA of a cluster, at least (a context of 485: 6.0 us
+// with 512, 4.9 us with 128).
+#ifndef SW_CT
+#define SW_CT 128
+#endif
+
+// DecodeCfg with the shape's chunks per stage.
+template <typename Shape, int HEAD_DIM, int NT, int ELEM>
+struct BlockCfg : DecodeCfg<HEAD_DIM, NT, Shape::WARPS, Shape::STAGES, ELEM> {
+  using Base = DecodeCfg<HEAD_DIM, NT, Shape::WARPS, Shape::STAGES, ELEM>;
+  static constexpr int CPS = Shape::CPS;
+  static constexpr int STAGE_BYTES = CPS * Base::CHUNK_BYTES;
+  static constexpr int RING_BYTES = Shape::WARPS * Shape::STAGES * STAGE_BYTES;
+  static_assert(RING_BYTES >= (kLongestFirstMax + 1) * 4, "the longest-first ranking fits in the ring");
+  static constexpr int SMEM_BYTES =
+      1024 + Base::BAR_BYTES + (RING_BYTES > Base::TAIL_BYTES ? RING_BYTES : Base::TAIL_BYTES);
+};
+
 // KV: E4M3 (block scales), or T (16-bit pools; PER_HEAD only).  PER_HEAD: the
 // table row and the context length belong to (sequence, KV head).  MODE as
 // decode_cta: MODE_GRID, MODE_CLUSTER or MODE_LONGEST_FIRST.
-template <typename T, typename KV, int HEAD_DIM, int NT, int WARPS, int STAGES, int MODE, bool PER_HEAD>
-__global__ void __launch_bounds__(WARPS * 32) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+template <typename T, typename KV, int HEAD_DIM, int NT, int KIND, int MODE, bool PER_HEAD>
+__global__ void __launch_bounds__(BlockShape<HEAD_DIM, NT, kElemBytes<KV>, KIND, PER_HEAD>::WARPS * 32,
+                                  BlockShape<HEAD_DIM, NT, kElemBytes<KV>, KIND, PER_HEAD>::MIN_CTAS)
+    block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+  using Shape = BlockShape<HEAD_DIM, NT, kElemBytes<KV>, KIND, PER_HEAD>;
+  constexpr int WARPS = Shape::WARPS;
+  constexpr int STAGES = Shape::STAGES;
   constexpr bool CLUSTER = MODE == MODE_CLUSTER;
   constexpr bool LONGEST = MODE == MODE_LONGEST_FIRST;
   static_assert(!(LONGEST && PER_HEAD), "sparse batches are not ranked");
   constexpr bool FP8 = kIsFp8<KV>;
-  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, kElemBytes<KV>>;
+  using Cfg = BlockCfg<Shape, HEAD_DIM, NT, kElemBytes<KV>>;
   constexpr int KSTEPS = HEAD_DIM / 16;
   constexpr int GMAX = Cfg::GMAX;
   constexpr int CPS = Cfg::CPS;
@@ -529,22 +581,74 @@ __global__ void __launch_bounds__(WARPS * 32) block_decode_kernel(const __grid_c
 }
 
 // ================================================================ launchers
+// Tensor maps over the pools.  Dense launches use make_pool_map, whose copies ask
+// L2 for 256 bytes around each row: the neighbouring head's row, which a
+// neighbouring CTA reads.  With a table per KV head the neighbour usually wants
+// another block, so one-byte rows of 128 bytes ask for 128 (16 sequences, 96 of
+// 125 to 1024 blocks of 32 tokens each: 138 -> 104 MB read).  Maps of recent pools
+// are kept as in make_pool_map: a map depends on nothing but its arguments.
+template <typename KV, int HEAD_DIM, bool PER_HEAD>
+struct PoolMaps {
+  static cudaError_t make(CUtensorMap* map, const void* pool, int num_kv_heads, int64_t rows) {
+    if constexpr (!PER_HEAD || HEAD_DIM * kElemBytes<KV> >= 256) {
+      return make_pool_map<KV, HEAD_DIM>(map, pool, num_kv_heads, rows);
+    } else {
+      struct Entry {
+        CUtensorMap map;
+        const void* pool;
+        int64_t rows;
+        int heads;
+      };
+      constexpr int kEntries = 16;
+      thread_local Entry cache[kEntries];
+      thread_local int next = 0;
+      for (const Entry& e : cache)
+        if (e.pool != nullptr && e.pool == pool && e.rows == rows && e.heads == num_kv_heads) {
+          *map = e.map;
+          return cudaSuccess;
+        }
+      EncodeTiledFn enc = nullptr;
+      const cudaError_t err = encode_fn(&enc);
+      if (err != cudaSuccess) return err;
+      using Cfg = DecodeCfg<HEAD_DIM, 1, 1, 1, kElemBytes<KV>>;
+      constexpr int ELEM = kElemBytes<KV>;
+      const cuuint64_t dims[3] = {static_cast<cuuint64_t>(HEAD_DIM), static_cast<cuuint64_t>(num_kv_heads),
+                                  static_cast<cuuint64_t>(rows)};
+      const cuuint64_t strides[2] = {static_cast<cuuint64_t>(HEAD_DIM) * ELEM,
+                                     static_cast<cuuint64_t>(num_kv_heads) * HEAD_DIM * ELEM};
+      const cuuint32_t box[3] = {Cfg::BOX_ELEMS, 1, CHUNK};
+      const cuuint32_t estride[3] = {1, 1, 1};
+      const CUresult r =
+          enc(map, tma_dtype<KV>(), 3, const_cast<void*>(pool), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              Cfg::ROW_BYTES == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              HEAD_DIM * ELEM >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+      cache[next] = Entry{*map, pool, rows, num_kv_heads};
+      next = (next + 1) % kEntries;
+      return cudaSuccess;
+    }
+  }
+};
+
 template <typename T, typename KV, int HEAD_DIM, int NT, int MODE, int KIND, bool PER_HEAD>
 cudaError_t launch_block_decode_t(const BlockDecodeArgs& a, cudaStream_t stream) {
   constexpr bool CLUSTER = MODE == MODE_CLUSTER;
   constexpr int ELEM = kElemBytes<KV>;
-  constexpr int WARPS = DecodeShape<HEAD_DIM, ELEM, KIND>::WARPS;
-  constexpr int STAGES = DecodeShape<HEAD_DIM, ELEM, KIND>::STAGES;
-  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, ELEM>;
-  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, WARPS, STAGES, MODE, PER_HEAD>;
+  using Shape = BlockShape<HEAD_DIM, NT, ELEM, KIND, PER_HEAD>;
+  constexpr int WARPS = Shape::WARPS;
+  using Cfg = BlockCfg<Shape, HEAD_DIM, NT, ELEM>;
+  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, KIND, MODE, PER_HEAD>;
   static std::atomic<uint64_t> smem_set{0};
   cudaError_t e = ensure_smem(kern, Cfg::SMEM_BYTES, smem_set);
   if (e != cudaSuccess) return e;
   BlockDecodeParams p;
   const int64_t pool_rows = static_cast<int64_t>(a.num_blocks) * a.block_size;
-  e = make_pool_map<KV, HEAD_DIM>(&p.tmap_k, a.k_cache, a.num_kv_heads, pool_rows);
+  using Maps = PoolMaps<KV, HEAD_DIM, PER_HEAD>;
+  e = Maps::make(&p.tmap_k, a.k_cache, a.num_kv_heads, pool_rows);
   if (e != cudaSuccess) return e;
-  e = make_pool_map<KV, HEAD_DIM>(&p.tmap_v, a.v_cache, a.num_kv_heads, pool_rows);
+  e = Maps::make(&p.tmap_v, a.v_cache, a.num_kv_heads, pool_rows);
   if (e != cudaSuccess) return e;
   p.out = a.out;
   p.q = a.q;
@@ -593,9 +697,9 @@ cudaError_t launch_block_decode_t(const BlockDecodeArgs& a, cudaStream_t stream)
 template <typename T, typename KV, int HEAD_DIM, int NT, bool PER_HEAD>
 cudaError_t block_decode_slots(int* slots) {
   constexpr int ELEM = kElemBytes<KV>;
-  constexpr int WARPS = DecodeShape<HEAD_DIM, ELEM>::WARPS;
-  constexpr int STAGES = DecodeShape<HEAD_DIM, ELEM>::STAGES;
-  using Cfg = DecodeCfg<HEAD_DIM, NT, WARPS, STAGES, ELEM>;
+  using Shape = BlockShape<HEAD_DIM, NT, ELEM, KIND_SINGLE, PER_HEAD>;
+  constexpr int WARPS = Shape::WARPS;
+  using Cfg = BlockCfg<Shape, HEAD_DIM, NT, ELEM>;
   static std::atomic<int> cache[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -607,7 +711,7 @@ cudaError_t block_decode_slots(int* slots) {
       return cudaSuccess;
     }
   }
-  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, WARPS, STAGES, MODE_GRID, PER_HEAD>;
+  auto kern = block_decode_kernel<T, KV, HEAD_DIM, NT, KIND_SINGLE, MODE_GRID, PER_HEAD>;
   static std::atomic<uint64_t> smem_set{0};
   e = ensure_smem(kern, Cfg::SMEM_BYTES, smem_set);
   if (e != cudaSuccess) return e;
@@ -634,7 +738,7 @@ cudaError_t launch_block_decode_auto(const BlockDecodeArgs& a, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
-  const int64_t k = std::min<int64_t>(slots / pairs, (cap + 511) / 512);
+  const int64_t k = std::min<int64_t>(slots / pairs, (cap + SW_CT - 1) / SW_CT);
   BlockDecodeArgs b = a;
   b.cluster_size = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, k)));
   if (b.cluster_size > 1) return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_CLUSTER, KIND_SINGLE, PER_HEAD>(b, stream);
