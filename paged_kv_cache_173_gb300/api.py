@@ -26,8 +26,9 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _stream_ptr(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(t.device)
-    return int(s.cuda_stream)
+    if stream is None:  # the raw handle: building a Stream object costs 2 us a call
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return int(stream.cuda_stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) -> int:
@@ -325,13 +326,53 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     _lib.check("pa_prefill", st)
 
 
-def _need_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, num_blocks: int, num_kv_heads: int,
-                 device: torch.device):
-    """Pointers of the scale tables [N, Hk] (float32) beside a pair of block-scaled pools."""
-    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        if not isinstance(t, torch.Tensor) or t.shape != (num_blocks, num_kv_heads):
-            raise ValueError(f"{name} must be [N, Hk] = [{num_blocks}, {num_kv_heads}], one scale per block and KV head")
-    return (_need(k_scales, "k_scales", torch.float32, device), _need(v_scales, "v_scales", torch.float32, device))
+# ---------------------------------------------------------------------------
+# Block-scaled E4M3 pools and block-sparse decode.  A small decode step is paced
+# by the host, so these calls check each tensor once, on its type, device and
+# contiguity together, and build the message only when a check fails (a decode
+# call: 16 us -> 9 us on the host).
+# ---------------------------------------------------------------------------
+def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> int:
+    """Pointer of a contiguous tensor of `dtype` on CUDA device `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _need(t, name, dtype, torch.device("cuda", index))  # raises, with the reason
+
+
+def _ptr_codes(t: torch.Tensor, name: str, index: int) -> int:
+    if t.dtype not in _CODE_DTYPES:
+        raise TypeError(f"{name} must be a uint8 or float8_e4m3fn tensor of E4M3 codes")
+    return _ptr(t, name, t.dtype, index)
+
+
+def _cuda_index(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("paged attention tensors must live on a CUDA device")
+    return t.get_device()
+
+
+def _run(fn, name: str, index: int, stream: Optional[torch.cuda.Stream], args: tuple) -> None:
+    """Call a launching entry point with its arguments and the stream, the tensors' device current."""
+    sp = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream.cuda_stream)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, sp)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, sp)
+    if st:
+        _lib.check(name, st)
+
+
+def _check_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, N: int, Hk: int) -> None:
+    if k_scales.shape != (N, Hk) or v_scales.shape != (N, Hk):
+        raise ValueError(f"k_scales and v_scales must be [N, Hk] = [{N}, {Hk}], one scale per block and KV head")
+
+
+def _check_bounds(key_bounds: torch.Tensor, bound_exps: torch.Tensor, Hk: int, d: int) -> int:
+    N = key_bounds.shape[0]
+    if key_bounds.shape != (N, Hk, 2, d) or bound_exps.shape != (N, Hk):
+        raise ValueError(f"key_bounds must be [N, Hk, 2, d] and bound_exps [N, Hk] with Hk = {Hk}, d = {d}")
+    return N
 
 
 def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -341,21 +382,40 @@ def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cac
     at slot_mapping [T], with one scale per (block, KV head) in k_scales / v_scales [N, Hk]
     (float32) taken from the data and grown as a block fills.  The tokens of one block
     stand next to each other in slot_mapping."""
-    dev = _cuda_device(k_cache)
-    N, B, Hk, d = k_cache.shape
+    i = _cuda_index(k_cache)
+    shape = k_cache.shape
+    N, B, Hk, d = shape
     T = key.shape[0]
-    if key.shape != (T, Hk, d) or value.shape != (T, Hk, d) or v_cache.shape != k_cache.shape:
+    if key.shape != (T, Hk, d) or value.shape != (T, Hk, d) or v_cache.shape != shape:
         raise ValueError("key/value must be [T, Hk, d] matching the pools [N, B, Hk, d]")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    _check_scales(k_scales, v_scales, N, Hk)
     dt = key.dtype
-    st = _lib.lib().pa_reshape_and_cache_fp8_block(
-        _need(key, "key", dt, dev), _need(value, "value", dt, dev),
-        _need_codes(k_cache, "k_cache", dev), _need_codes(v_cache, "v_cache", dev), pks, pvs,
-        _need(slot_mapping, "slot_mapping", torch.int64, dev), T, N, B, Hk, d, _dtype_code(key),
-        _stream_ptr(k_cache, stream))
-    _lib.check("pa_reshape_and_cache_fp8_block", st)
+    _run(_lib.lib().pa_reshape_and_cache_fp8_block, "pa_reshape_and_cache_fp8_block", i, stream,
+         (_ptr(key, "key", dt, i), _ptr(value, "value", dt, i), _ptr_codes(k_cache, "k_cache", i),
+          _ptr_codes(v_cache, "v_cache", i), _ptr(k_scales, "k_scales", torch.float32, i),
+          _ptr(v_scales, "v_scales", torch.float32, i), _ptr(slot_mapping, "slot_mapping", torch.int64, i), T, N, B,
+          Hk, d, _dtype_code(key)))
+
+
+def _block_decode_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale):
+    i = _cuda_index(q)
+    qs, ks = q.shape, k_cache.shape
+    S, H, d = qs
+    N, B, Hk, d2 = ks
+    if d2 != d or v_cache.shape != ks or out.shape != qs:
+        raise ValueError("q/out [S, H, d] must match the pools [N, B, Hk, d]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S, M] and context_lens [S]")
+    _check_scales(k_scales, v_scales, N, Hk)
+    dt = q.dtype
+    return i, S, H, d, B, block_tables.shape[1], (
+        _ptr(out, "out", dt, i), _ptr(q, "q", dt, i), _ptr_codes(k_cache, "k_cache", i),
+        _ptr_codes(v_cache, "v_cache", i), _ptr(k_scales, "k_scales", torch.float32, i),
+        _ptr(v_scales, "v_scales", torch.float32, i), _ptr(block_tables, "block_tables", torch.int32, i),
+        block_tables.shape[1], _ptr(context_lens, "context_lens", torch.int32, i), S, H, Hk, d, B, N, float(scale),
+        _dtype_code(q))
 
 
 def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -364,12 +424,9 @@ def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tenso
                         stream: Optional[torch.cuda.Stream] = None) -> None:
     """pa_decode over block-scaled E4M3 pools: values are code * k_scales[block, head] (K) and
     code * v_scales[block, head] (V); q and out are float16 or bfloat16."""
-    dev, S, H, d, N, B, Hk, M, (po, pq, pk, pv, pbt), pcl = _decode_common(
-        out, q, k_cache, v_cache, block_tables, context_lens, codes=True)
-    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
-    st = _lib.lib().pa_decode_fp8_block(po, pq, pk, pv, pks, pvs, pbt, M, pcl, S, H, Hk, d, B, N, float(scale),
-                                        _dtype_code(q), _stream_ptr(q, stream))
-    _lib.check("pa_decode_fp8_block", st)
+    i, _, _, _, _, _, args = _block_decode_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                                scale)
+    _run(_lib.lib().pa_decode_fp8_block, "pa_decode_fp8_block", i, stream, args)
 
 
 def pa_decode_splitk_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -378,15 +435,12 @@ def pa_decode_splitk_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torc
                                workspace: torch.Tensor, max_num_partitions: Optional[int] = None,
                                stream: Optional[torch.cuda.Stream] = None) -> None:
     """Split-K decode over block-scaled pools; follow with pa_splitk_reduce on the same stream."""
-    dev, S, H, d, N, B, Hk, M, (po, pq, pk, pv, pbt), pcl = _decode_common(
-        out, q, k_cache, v_cache, block_tables, context_lens, codes=True)
-    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    i, _, _, _, B, M, args = _block_decode_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                                scale)
     P = max_num_partitions or max_num_partitions_for(M, B, partition_size)
-    ws = _need(workspace, "workspace", workspace.dtype, dev)
-    st = _lib.lib().pa_decode_splitk_fp8_block(
-        po, pq, pk, pv, pks, pvs, pbt, M, pcl, S, H, Hk, d, B, N, float(scale), _dtype_code(q), int(partition_size),
-        int(P), ws, workspace.numel() * workspace.element_size(), _stream_ptr(q, stream))
-    _lib.check("pa_decode_splitk_fp8_block", st)
+    _run(_lib.lib().pa_decode_splitk_fp8_block, "pa_decode_splitk_fp8_block", i, stream,
+         args + (int(partition_size), int(P), _ptr(workspace, "workspace", workspace.dtype, i),
+                 workspace.numel() * workspace.element_size()))
 
 
 def pa_prefill_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -394,34 +448,24 @@ def pa_prefill_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
                          context_lens: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,
                          scale: float, stream: Optional[torch.cuda.Stream] = None) -> None:
     """pa_prefill over block-scaled E4M3 pools (k_scales / v_scales [N, Hk])."""
-    dev = _cuda_device(q)
-    R, H, d = q.shape
-    N, B, Hk, d2 = k_cache.shape
-    S = int(context_lens.shape[0])
-    if d2 != d or v_cache.shape != k_cache.shape or out.shape != q.shape:
+    i = _cuda_index(q)
+    qs, ks = q.shape, k_cache.shape
+    R, H, d = qs
+    N, B, Hk, d2 = ks
+    S = context_lens.shape[0]
+    if d2 != d or v_cache.shape != ks or out.shape != qs:
         raise ValueError("q/out [rows, H, d] must match the pools [N, B, Hk, d]")
     if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start_loc.shape != (S + 1,):
         raise ValueError("block_tables must be [S, M] and query_start_loc [S + 1]")
-    pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
+    _check_scales(k_scales, v_scales, N, Hk)
     dt = q.dtype
-    st = _lib.lib().pa_prefill_fp8_block(
-        _need(out, "out", dt, dev), _need(q, "q", dt, dev), _need_codes(k_cache, "k_cache", dev),
-        _need_codes(v_cache, "v_cache", dev), pks, pvs, _need(block_tables, "block_tables", torch.int32, dev),
-        int(block_tables.shape[1]), _need(context_lens, "context_lens", torch.int32, dev),
-        _need(query_start_loc, "query_start_loc", torch.int32, dev), S, R, int(max_query_len), H, Hk, d, B, N,
-        float(scale), _dtype_code(q), _stream_ptr(q, stream))
-    _lib.check("pa_prefill_fp8_block", st)
-
-
-def _need_bounds(key_bounds: torch.Tensor, bound_exps: torch.Tensor, num_kv_heads: int, head_dim: int,
-                 device: torch.device):
-    if key_bounds.dim() != 4 or key_bounds.shape[1:] != (num_kv_heads, 2, head_dim):
-        raise ValueError(f"key_bounds must be [N, Hk, 2, d] with Hk = {num_kv_heads}, d = {head_dim}")
-    N = int(key_bounds.shape[0])
-    if bound_exps.shape != (N, num_kv_heads):
-        raise ValueError("bound_exps must be [N, Hk]")
-    return (N, _need(key_bounds, "key_bounds", torch.int8, device),
-            _need(bound_exps, "bound_exps", torch.int32, device))
+    _run(_lib.lib().pa_prefill_fp8_block, "pa_prefill_fp8_block", i, stream,
+         (_ptr(out, "out", dt, i), _ptr(q, "q", dt, i), _ptr_codes(k_cache, "k_cache", i),
+          _ptr_codes(v_cache, "v_cache", i), _ptr(k_scales, "k_scales", torch.float32, i),
+          _ptr(v_scales, "v_scales", torch.float32, i), _ptr(block_tables, "block_tables", torch.int32, i),
+          block_tables.shape[1], _ptr(context_lens, "context_lens", torch.int32, i),
+          _ptr(query_start_loc, "query_start_loc", torch.int32, i), S, R, int(max_query_len), H, Hk, d, B, N,
+          float(scale), _dtype_code(q)))
 
 
 def pa_update_key_bounds(key: torch.Tensor, key_bounds: torch.Tensor, bound_exps: torch.Tensor,
@@ -430,15 +474,15 @@ def pa_update_key_bounds(key: torch.Tensor, key_bounds: torch.Tensor, bound_exps
     """Fold key [T, Hk, d] into the bounds of the blocks named by slot_mapping [T]: key_bounds
     [N, Hk, 2, d] (int8 lo, hi) and bound_exps [N, Hk] (int32), lo * 2^e <= k <= hi * 2^e.
     The tokens of one block stand next to each other in slot_mapping."""
-    dev = _cuda_device(key_bounds)
+    i = _cuda_index(key_bounds)
     T, Hk, d = key.shape
-    N, pb, pe = _need_bounds(key_bounds, bound_exps, Hk, d, dev)
+    N = _check_bounds(key_bounds, bound_exps, Hk, d)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    st = _lib.lib().pa_update_key_bounds(
-        _need(key, "key", key.dtype, dev), pb, pe, _need(slot_mapping, "slot_mapping", torch.int64, dev), T, N,
-        int(block_size), Hk, d, _dtype_code(key), _stream_ptr(key_bounds, stream))
-    _lib.check("pa_update_key_bounds", st)
+    _run(_lib.lib().pa_update_key_bounds, "pa_update_key_bounds", i, stream,
+         (_ptr(key, "key", key.dtype, i), _ptr(key_bounds, "key_bounds", torch.int8, i),
+          _ptr(bound_exps, "bound_exps", torch.int32, i), _ptr(slot_mapping, "slot_mapping", torch.int64, i), T, N,
+          int(block_size), Hk, d, _dtype_code(key)))
 
 
 def pa_select_workspace_bytes(num_seqs: int, num_kv_heads: int, max_blocks_per_seq: int) -> int:
@@ -459,24 +503,23 @@ def pa_select_blocks(sel_tables: torch.Tensor, sel_lens: torch.Tensor, q: torch.
     num_last and the best by the bounds of their keys, max_selected in all.  Writes
     sel_tables [S, Hk, max_selected] (physical ids in position order, then -1) and
     sel_lens [S, Hk] (tokens), both int32."""
-    dev = _cuda_device(q)
+    i = _cuda_index(q)
     S, H, d = q.shape
     if sel_tables.dim() != 3 or sel_tables.shape[0] != S:
         raise ValueError("sel_tables must be [S, Hk, max_selected]")
-    Hk, K = int(sel_tables.shape[1]), int(sel_tables.shape[2])
+    _, Hk, K = sel_tables.shape
     if sel_lens.shape != (S, Hk):
         raise ValueError("sel_lens must be [S, Hk]")
-    N, pb, pe = _need_bounds(key_bounds, bound_exps, Hk, d, dev)
+    N = _check_bounds(key_bounds, bound_exps, Hk, d)
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [S, M] and context_lens [S]")
-    st = _lib.lib().pa_select_blocks(
-        _need(sel_tables, "sel_tables", torch.int32, dev), _need(sel_lens, "sel_lens", torch.int32, dev),
-        _need(q, "q", q.dtype, dev), pb, pe, _need(block_tables, "block_tables", torch.int32, dev),
-        int(block_tables.shape[1]), _need(context_lens, "context_lens", torch.int32, dev), S, H, Hk, d,
-        int(block_size), N, K, int(num_first), int(num_last), _dtype_code(q),
-        _need(workspace, "workspace", workspace.dtype, dev), workspace.numel() * workspace.element_size(),
-        _stream_ptr(q, stream))
-    _lib.check("pa_select_blocks", st)
+    _run(_lib.lib().pa_select_blocks, "pa_select_blocks", i, stream,
+         (_ptr(sel_tables, "sel_tables", torch.int32, i), _ptr(sel_lens, "sel_lens", torch.int32, i),
+          _ptr(q, "q", q.dtype, i), _ptr(key_bounds, "key_bounds", torch.int8, i),
+          _ptr(bound_exps, "bound_exps", torch.int32, i), _ptr(block_tables, "block_tables", torch.int32, i),
+          block_tables.shape[1], _ptr(context_lens, "context_lens", torch.int32, i), S, H, Hk, d, int(block_size), N, K,
+          int(num_first), int(num_last), _dtype_code(q), _ptr(workspace, "workspace", workspace.dtype, i),
+          workspace.numel() * workspace.element_size()))
 
 
 def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -486,30 +529,32 @@ def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, 
     """Decode with a block table per (sequence, KV head): sel_tables [S, Hk, max_selected] and
     sel_lens [S, Hk] (pa_select_blocks writes them).  16-bit pools of the query type, or
     block-scaled E4M3 pools with k_scales and v_scales [N, Hk]."""
-    dev = _cuda_device(q)
-    S, H, d = q.shape
-    N, B, Hk, d2 = k_cache.shape
-    if d2 != d or v_cache.shape != k_cache.shape or out.shape != q.shape:
+    i = _cuda_index(q)
+    qs, ks = q.shape, k_cache.shape
+    S, H, d = qs
+    N, B, Hk, d2 = ks
+    if d2 != d or v_cache.shape != ks or out.shape != qs:
         raise ValueError("q/out [S, H, d] must match the pools [N, B, Hk, d]")
     if sel_tables.dim() != 3 or sel_tables.shape[:2] != (S, Hk) or sel_lens.shape != (S, Hk):
         raise ValueError("sel_tables must be [S, Hk, max_selected] and sel_lens [S, Hk]")
-    dt = _dtype_code(q)
+    dt = q.dtype
+    code = _dtype_code(q)
     if k_cache.dtype in _CODE_DTYPES:
         if k_scales is None or v_scales is None:
             raise ValueError("E4M3 pools need k_scales and v_scales [N, Hk]")
-        pks, pvs = _need_scales(k_scales, v_scales, N, Hk, dev)
-        pk, pv, kv = _need_codes(k_cache, "k_cache", dev), _need_codes(v_cache, "v_cache", dev), PA_FP8_E4M3
+        _check_scales(k_scales, v_scales, N, Hk)
+        pools = (_ptr_codes(k_cache, "k_cache", i), _ptr_codes(v_cache, "v_cache", i),
+                 _ptr(k_scales, "k_scales", torch.float32, i), _ptr(v_scales, "v_scales", torch.float32, i))
+        kv = PA_FP8_E4M3
     else:
         if k_scales is not None or v_scales is not None:
             raise ValueError("16-bit pools take no scales")
-        pks = pvs = None
-        pk, pv, kv = _need(k_cache, "k_cache", q.dtype, dev), _need(v_cache, "v_cache", q.dtype, dev), dt
-    st = _lib.lib().pa_decode_sparse(
-        _need(out, "out", q.dtype, dev), _need(q, "q", q.dtype, dev), pk, pv, pks, pvs,
-        _need(sel_tables, "sel_tables", torch.int32, dev), int(sel_tables.shape[2]),
-        _need(sel_lens, "sel_lens", torch.int32, dev), S, H, Hk, d, B, N, float(scale), dt, kv,
-        _stream_ptr(q, stream))
-    _lib.check("pa_decode_sparse", st)
+        pools = (_ptr(k_cache, "k_cache", dt, i), _ptr(v_cache, "v_cache", dt, i), None, None)
+        kv = code
+    _run(_lib.lib().pa_decode_sparse, "pa_decode_sparse", i, stream,
+         (_ptr(out, "out", dt, i), _ptr(q, "q", dt, i)) + pools +
+         (_ptr(sel_tables, "sel_tables", torch.int32, i), sel_tables.shape[2],
+          _ptr(sel_lens, "sel_lens", torch.int32, i), S, H, Hk, d, B, N, float(scale), code, kv))
 
 
 def pa_selftest_wait(device=None, limit_us: int = 20000,

@@ -536,13 +536,12 @@ struct SelectParams {
 // global memory in the MMA's layout (lane (g, c) reads 16-byte units c, c + 4,
 // ... of rows g and g + 8; a unit's four words are four k-steps); neighbouring
 // warps take neighbouring heads, whose rows of a block are neighbours in memory.
-#ifndef SC_T
-#define SC_T 4
-#define SC_W 8
-#define SC_M 3
-#endif
-constexpr int kScoreTiles = SC_T;  // tiles of 16 blocks per warp, behind one preparation of the queries
-constexpr int kScoreWarps = SC_W;
+// Tiles of 16 blocks per warp, behind one preparation of the queries, and warps per CTA
+// (five CTAs per SM by registers).  2 x 4 beside 4 x 8 at three CTAs: selection 22.2 ->
+// 20.2 us (4 sequences of 43 K to 115 K tokens, blocks of 16) and 20.3 -> 14.6 us (16 of
+// 4 K to 32 K, blocks of 32); 4 x 4: 19.5 and 17.4 us.
+constexpr int kScoreTiles = 2;
+constexpr int kScoreWarps = 4;
 
 // Four codes of one word as two pairs of float16: code + 128 + 1024 by bytes, minus 1152.
 __device__ __forceinline__ void codes4_to_half(uint32_t w, uint32_t& a, uint32_t& b) {
@@ -561,7 +560,7 @@ __device__ __forceinline__ float whole(float x, float inv) {
 }
 
 template <typename T, int HEAD_DIM, int NT>
-__global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? SC_M : 1) block_score_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? 5 : 1) block_score_kernel(const __grid_constant__ SelectParams p) {
   constexpr int UH = HEAD_DIM / 64;  // 16-byte units per lane and half (lo or hi) of a row
   constexpr int STEPS = UH * 4;      // k-steps per half
   grid_dependency_wait();
@@ -573,10 +572,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? SC_M 
   const int s = blockIdx.y;
   const int kvh = static_cast<int>(wid % p.num_kv_heads);
   const int64_t b0 = wid / p.num_kv_heads * (16 * kScoreTiles);
+  if (b0 >= p.max_blocks) return;
   const int ctx = __ldg(p.context_lens + s);
-  if (ctx <= 0 || ctx > static_cast<int64_t>(p.max_blocks) * p.block_size) return;
-  const int n = (ctx + p.block_size - 1) / p.block_size;
-  if (n <= p.max_selected || b0 >= n) return;  // every block is kept, or none is here
   const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
 
   // tile t's rows g and g + 8: physical blocks (-1: outside the pool), codes, exponents
@@ -585,8 +582,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? SC_M 
   auto table = [&](int t, int (&ph)[2]) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int64_t b = b0 + 16 * t + 8 * r + g;
-      ph[r] = b < n ? __ldg(bt + b) : 0;
+      const int64_t b = b0 + 16 * t + 8 * r + g;  // entries past the context may be any number
+      ph[r] = t < kScoreTiles && b < p.max_blocks ? __ldg(bt + b) : 0;
     }
   };
   auto load = [&](const int (&ph)[2]) {
@@ -601,10 +598,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32, HEAD_DIM * NT <= 128 ? SC_M 
       phys[r] = in ? 0 : -1;
     }
   };
-  int ph_next[2];
+  // the table's entries, which do not depend on the context length, before it is looked at
+  int ph_next[2], ph_last[2];
   table(0, ph_next);
+  table(1, ph_last);
+  if (ctx <= 0 || ctx > static_cast<int64_t>(p.max_blocks) * p.block_size) return;
+  const int n = (ctx + p.block_size - 1) / p.block_size;
+  if (n <= p.max_selected || b0 >= n) return;  // every block is kept, or none is here
   load(ph_next);
-  table(1, ph_next);
+  ph_next[0] = ph_last[0];
+  ph_next[1] = ph_last[1];
 
   // the queries: column g of tile nt is head kvh * G + nt * 8 + g; k-step (i, w) holds
   // channels 16 (c + 4 i) + 4 w .. + 3

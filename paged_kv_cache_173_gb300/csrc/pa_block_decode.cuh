@@ -233,24 +233,14 @@ struct BlockShape {
   static constexpr bool FP8 = ELEM == 1;
   static constexpr bool WIDE = FP8 && KIND == KIND_SINGLE && NT == 1 && HEAD_DIM <= 128;
   static constexpr bool SMALL = FP8 && KIND == KIND_SPLITK && HEAD_DIM >= 128;
-#ifdef SW_W
-  static constexpr bool ON = ELEM == SW_E && HEAD_DIM == SW_D && NT == SW_NT && KIND == SW_K;
-  static constexpr int WARPS = ON ? SW_W : WIDE ? 8 : SMALL ? 2 : Base::WARPS;
-  static constexpr int STAGES = ON ? SW_S : WIDE || SMALL ? 2 : Base::STAGES;
-  static constexpr int CPS = ON ? SW_C : FP8 && (HEAD_DIM == 64 || (HEAD_DIM == 128 && !WIDE && (!SMALL || NT == 1))) ? 2 : 1;
-  static constexpr int MIN_CTAS = ON ? SW_M : WIDE ? 2 : SMALL ? (NT == 1 ? 6 : 5) : 0;
-#else
   static constexpr int WARPS = WIDE ? 8 : SMALL ? 2 : Base::WARPS;
   static constexpr int STAGES = WIDE || SMALL ? 2 : Base::STAGES;
   static constexpr int CPS = FP8 && (HEAD_DIM == 64 || (HEAD_DIM == 128 && !WIDE && (!SMALL || NT == 1))) ? 2 : 1;
   static constexpr int MIN_CTAS = WIDE ? 2 : SMALL ? (NT == 1 ? 6 : 5) : 0;
-#endif
 };
 // Tokens of table capacity per CTA of a cluster, at least (a context of 485: 6.0 us
 // with 512, 4.9 us with 128).
-#ifndef SW_CT
-#define SW_CT 128
-#endif
+constexpr int kClusterTokens = 128;
 
 // DecodeCfg with the shape's chunks per stage.
 template <typename Shape, int HEAD_DIM, int NT, int ELEM>
@@ -738,7 +728,7 @@ cudaError_t launch_block_decode_auto(const BlockDecodeArgs& a, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
-  const int64_t k = std::min<int64_t>(slots / pairs, (cap + SW_CT - 1) / SW_CT);
+  const int64_t k = std::min<int64_t>(slots / pairs, (cap + kClusterTokens - 1) / kClusterTokens);
   BlockDecodeArgs b = a;
   b.cluster_size = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, k)));
   if (b.cluster_size > 1) return launch_block_decode_t<T, KV, HEAD_DIM, NT, MODE_CLUSTER, KIND_SINGLE, PER_HEAD>(b, stream);

@@ -63,9 +63,10 @@ template <int HEAD_DIM>
 struct BpCfg {
   static constexpr int SOFT = TC_TILES * TC_ROWS;  // softmax threads
   static constexpr int MMA_WARP = SOFT / 32;
-  static constexpr int PROD_WARP = MMA_WARP + 1;  // K: two warps, then V: two
-  static constexpr int PROD = 64;                 // producer threads of K, and of V
-  static constexpr int THREADS = SOFT + 32 + 2 * PROD;
+  static constexpr int PROD_WARP = MMA_WARP + 1;
+  static constexpr int PROD_WARPS = 3;  // twelve warps in all: three per scheduler, 168 registers a thread
+  static constexpr int PROD = PROD_WARPS * 32;
+  static constexpr int THREADS = SOFT + 32 + PROD;
   static constexpr int DBOX = HEAD_DIM / BOX_DIMS;
   static constexpr int QATOM = TC_ROWS * 128;
   static constexpr int QBYTES = DBOX * QATOM;
@@ -82,7 +83,7 @@ struct BpCfg {
   static constexpr int V_OFF = K_OFF + KSTAGES * KBYTES;
   static constexpr int SC_OFF = V_OFF + VSTAGES * KBYTES;  // [VSTAGES][CHUNKS] float4
   static constexpr int BAR_OFF = SC_OFF + VSTAGES * CHUNKS * 16;
-  static constexpr int NBARS = 2 * KSTAGES + 3 * VSTAGES + 3 * TC_TILES + 3;
+  static constexpr int NBARS = 2 * KSTAGES + 3 * VSTAGES + 4 * TC_TILES + 3;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
   static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
@@ -102,6 +103,29 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
   e4m3x4_to_half2x2(c.w, b.z, b.w);
 }
 
+// Pairs of float32 in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float x) { return pack_f32x2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <typename T, int HEAD_DIM>
 __global__ void __launch_bounds__(BpCfg<HEAD_DIM>::THREADS, 1)
 block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
@@ -115,14 +139,14 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float4* scales = reinterpret_cast<float4*>(sm + C::SC_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
-  uint64_t* kfull = bars;                  // [KS] K of a block is widened (64 arrivals)
+  uint64_t* kfull = bars;                  // [KS] K of a block is widened (96 arrivals)
   uint64_t* kempty = kfull + KS;           // [KS] that block's Q K^T (both tiles) is done
-  uint64_t* vfull = kempty + KS;           // [VS] V of a block is widened (64 arrivals)
+  uint64_t* vfull = kempty + KS;           // [VS] V of a block is widened (96 arrivals)
   uint64_t* vempty = vfull + VS;           // [VS] that block's P V (both tiles) is done
   uint64_t* scfull = vempty + VS;          // [VS] the scales of the block are in `scales`
   uint64_t* sfull = scfull + VS;           // [tile] S of the tile's next block is in TMEM
-  uint64_t* pfull = sfull + TC_TILES;      // [tile] P of that block is written (128 arrivals)
-  uint64_t* pvdone = pfull + TC_TILES;     // [tile] the tile's P V of that block has completed
+  uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
+  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the tile's P V of that block has completed
   uint64_t* qbar = pvdone + TC_TILES;      // Q of both tiles landed
   uint64_t* qready = qbar + 1;             // bfloat16: Q is float16 now (256 arrivals)
   uint64_t* drain = qready + 1;            // every MMA issued has completed
@@ -169,7 +193,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     }
     for (int i = 0; i < TC_TILES; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], TC_ROWS);
+      mbar_init(&pfull[2 * i], TC_ROWS);
+      mbar_init(&pfull[2 * i + 1], TC_ROWS);
       mbar_init(&pvdone[i], 1);
     }
     mbar_init(qbar, 1);
@@ -192,32 +217,32 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   const uint32_t tmem = *tslot;
 
   if (warp >= C::PROD_WARP) {
-    // ------------------------------------------------ producers: K, then V
-    const bool is_v = warp >= C::PROD_WARP + 2;
-    const int w2 = (warp - C::PROD_WARP) & 1;
-    const int ns = is_v ? VS : KS;
-    uint64_t* fullb = is_v ? vfull : kfull;
-    uint64_t* emptyb = is_v ? vempty : kempty;
-    const uint8_t* pool = is_v ? p.v_cache : p.k_cache;
-    uint8_t* ring = sm + (is_v ? C::V_OFF : C::K_OFF);
+    // ------------------------------------------------ producers: K, then V of each block
+    const int pw = warp - C::PROD_WARP;
     if (nblk > 0) {
-      constexpr int RG = 8;                   // groups of 8 rows per warp and block
-      constexpr int HALVES = HEAD_DIM / 64;   // 64-code halves of a row
+      constexpr int RG = 16;                              // groups of 8 rows per block
+      constexpr int NG = (RG + C::PROD_WARPS - 1) / C::PROD_WARPS;  // a warp's, at most
+      constexpr int HALVES = HEAD_DIM / 64;               // 64-code halves of a row
       const int32_t* bt = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
       const int r8 = lane >> 2;  // four lanes per row: 64 codes of it per load
       const int c = lane & 3;
       const size_t row_bytes = static_cast<size_t>(p.num_kv_heads) * HEAD_DIM;
-      const uint8_t* head = pool + static_cast<size_t>(kvh) * HEAD_DIM + c * 16;
+      const uint8_t* khead = p.k_cache + static_cast<size_t>(kvh) * HEAD_DIM + c * 16;
+      const uint8_t* vhead = p.v_cache + static_cast<size_t>(kvh) * HEAD_DIM + c * 16;
       const int bmask = (1 << p.log2_b) - 1;
-      int ph[RG];  // physical block of each row group of a block of keys (8 rows lie in one pool block)
+      // the warp's groups of K and of V: 6 + 5, 5 + 5 and 5 + 6
+      auto kg = [&](int i) { return pw + C::PROD_WARPS * i; };
+      auto vg = [&](int i) { return C::PROD_WARPS - 1 - pw + C::PROD_WARPS * i; };
+      int kph[NG], vph[NG];  // physical block of each row group (8 rows lie in one pool block)
       auto fetch = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < RG; ++i) ph[i] = __ldg(bt + (min(j * TC_KEYS + (i * 2 + w2) * 8, kend - 1) >> p.log2_b));
+        for (int i = 0; i < NG; ++i) {  // (a group past the last one is clamped, and not used)
+          kph[i] = __ldg(bt + (min(j * TC_KEYS + kg(i) * 8, kend - 1) >> p.log2_b));
+          vph[i] = __ldg(bt + (min(j * TC_KEYS + vg(i) * 8, kend - 1) >> p.log2_b));
+        }
       };
-      uint4 data[RG][HALVES];
-      auto load = [&](int j, int i) {
-        int phys = ph[i];
-        const int key = j * TC_KEYS + (i * 2 + w2) * 8 + r8;
+      uint4 kd[NG][HALVES], vd[NG][HALVES];
+      auto load = [&](uint4 (&d)[HALVES], const uint8_t* head, int phys, int key) {
         if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
           flags[0] = 1;  // never read outside the pool; the tiles' outputs become NaN
           phys = 0;
@@ -225,10 +250,21 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         const uint8_t* src = head + ((static_cast<size_t>(phys) << p.log2_b) + (key & bmask)) * row_bytes;
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)  // rows past the stream's last key are zeros: 0 x NaN must not occur
-          data[i][h] = key < kend ? ldg128(src + h * 64) : make_uint4(0u, 0u, 0u, 0u);
+          d[h] = key < kend ? ldg128(src + h * 64) : make_uint4(0u, 0u, 0u, 0u);
       };
-      // scales of the block's 16-key chunks: lanes 0-7 of the first V warp
-      const bool side = is_v && w2 == 0;
+      auto store = [&](const uint4 (&d)[HALVES], uint8_t* stage, int r) {
+        uint8_t* drow = stage + r * 128;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+          uint4 a, b;
+          widen16(d[h], a, b);
+          // unit u of row r sits at u ^ (r % 8): the eight lanes of two rows write eight different units
+          *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c) ^ (r & 7)) << 4)) = a;
+          *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
+        }
+      };
+      // scales of the block's 16-key chunks: lanes 0-7 of the second warp
+      const bool side = pw == 1;
       float sk = 0.f, sv = 0.f;
       auto side_load = [&](int j) {
         if (side && lane < C::CHUNKS) {
@@ -246,13 +282,20 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
       };
       fetch(0);
-#pragma unroll
-      for (int i = 0; i < RG; ++i) load(0, i);
       side_load(0);
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        if (kg(i) < RG) load(kd[i], khead, kph[i], kg(i) * 8 + r8);
+        if (vg(i) < RG) load(vd[i], vhead, vph[i], vg(i) * 8 + r8);
+      }
       fetch(min(1, nblk - 1));
       for (int j = 0; j < nblk; ++j) {
-        const int slot = j % ns;
-        if (j >= ns && !__all_sync(FULL_MASK, tc_wait(&emptyb[slot], ((j / ns) - 1) & 1))) {
+        const int kslot = j % KS;
+        const int vslot = j % VS;
+        // V first: its stage (and the scales' row) falls free with P V of block j - VS, before K's
+        const bool vok = j < VS || __all_sync(FULL_MASK, tc_wait(&vempty[vslot], ((j / VS) - 1) & 1));
+        const bool ok = vok && (j < KS || __all_sync(FULL_MASK, tc_wait(&kempty[kslot], ((j / KS) - 1) & 1)));
+        if (!ok) {
           flags[1] = 1;
           break;
         }
@@ -260,32 +303,34 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           if (lane < C::CHUNKS) {
             if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax)) flags[0] = 1;
             const float v = fmaxf(sv, 5.421010862427522e-20f);  // 2^-64
-            scales[slot * C::CHUNKS + lane] = make_float4(sk * p.scale_log2, __log2f(v), __frcp_rn(v), 0.f);
+            // a factor of 0 would turn a masked score (-inf) into NaN: 2^-120 makes 0 of every score
+            float a = sk * p.scale_log2;
+            a = fabsf(a) >= 7.52316384526264e-37f ? a : copysignf(7.52316384526264e-37f, p.scale_log2);
+            scales[vslot * C::CHUNKS + lane] = make_float4(a, __log2f(v), __frcp_rn(v), 0.f);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&scfull[slot]);
+          if (lane == 0) mbar_arrive(&scfull[vslot]);
+          if (j + 1 < nblk) side_load(j + 1);
         }
-        uint8_t* dst = ring + slot * C::KBYTES;
+        uint8_t* kdst = sm + C::K_OFF + kslot * C::KBYTES;
+        uint8_t* vdst = sm + C::V_OFF + vslot * C::KBYTES;
 #pragma unroll
-        for (int i = 0; i < RG; ++i) {
-          const int r = (i * 2 + w2) * 8 + r8;
-          uint8_t* drow = dst + r * 128;
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h) {
-            uint4 a, b;
-            widen16(data[i][h], a, b);
-            // unit u of row r sits at u ^ (r % 8): the eight lanes of two rows write eight different units
-            *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c) ^ (r & 7)) << 4)) = a;
-            *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
-          }
-          if (j + 1 < nblk) load(j + 1, i);
-        }
-        if (j + 1 < nblk) {
-          side_load(j + 1);
-          fetch(min(j + 2, nblk - 1));
+        for (int i = 0; i < NG; ++i) {
+          if (kg(i) >= RG) continue;
+          store(kd[i], kdst, kg(i) * 8 + r8);
+          if (j + 1 < nblk) load(kd[i], khead, kph[i], (j + 1) * TC_KEYS + kg(i) * 8 + r8);
         }
         fence_proxy_async_smem();  // the widened rows become visible to the tensor core
-        mbar_arrive(&fullb[slot]);
+        mbar_arrive(&kfull[kslot]);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          if (vg(i) >= RG) continue;
+          store(vd[i], vdst, vg(i) * 8 + r8);
+          if (j + 1 < nblk) load(vd[i], vhead, vph[i], (j + 1) * TC_KEYS + vg(i) * 8 + r8);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&vfull[vslot]);
+        fetch(min(j + 2, nblk - 1));
       }
     }
   } else if (warp == C::MMA_WARP) {
@@ -325,7 +370,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         bool have_v = false;
         for (int u = 0; u < ntiles; ++u) {
           if (j >= nbt[u]) continue;
-          if (!tc_wait(&pfull[u], j & 1)) {
+          if (!tc_wait(&pfull[2 * u], j & 1)) {
             ok = false;
             break;
           }
@@ -340,9 +385,18 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
           const uint32_t tP = tmem + 256 * u;
           const uint32_t tO = tP + 128;
+          // the first 64 keys while the softmax writes the weights of the others
 #pragma unroll
-          for (int kk = 0; kk < TC_KEYS / 16; ++kk)  // 16 keys = 8 columns of P
-            umma_f16_ts(tO, tP + 64 * (kk >> 2) + 8 * (kk & 3), umma_desc_add(vj, kk * 2048), C::ID_PV, j > 0 || kk > 0);
+          for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
+            umma_f16_ts(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, j > 0 || kk > 0);
+          if (!tc_wait(&pfull[2 * u + 1], j & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
+            umma_f16_ts(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
           umma_commit(&pvdone[u]);
           if (j + 1 < nbt[u]) {
             if (!wait_k(j + 1)) {
@@ -417,65 +471,41 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         mbar_arrive(qready);
       }
     }
-    float x[TC_HALF];  // base-2 scores of one half of the block's keys, value exponent added; masked ones -inf
-    auto load_half = [&](int j, int h) {
-      uint32_t v[TC_HALF / 16][16];
-#pragma unroll
-      for (int c = 0; c < TC_HALF / 16; ++c) tmem_ld16(tS + TC_HALF * h + 16 * c, v[c]);
-      tmem_wait_ld();
-      const float4* sc = scales + (j % VS) * C::CHUNKS + 4 * h;
-#pragma unroll
-      for (int c = 0; c < TC_HALF / 16; ++c) {
-        const float4 f = sc[c];
-        const float a = BF16 ? f.x * qinv : f.x;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[16 * c + i] = fmaf(__uint_as_float(v[c][i]), a, f.y);
-      }
-      const int k0 = j * TC_KEYS + TC_HALF * h;
-      if (k0 + TC_HALF - 1 > base + t0) {  // a key here may lie past some row of the tile
-#pragma unroll
-        for (int c = 0; c < TC_HALF; ++c)
-          if (k0 + c > pos) x[c] = -INFINITY;
-      }
-    };
-    auto half_max = [&]() {
-      float mq[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mq[i] = x[i];
-#pragma unroll
-      for (int c = 4; c < TC_HALF; ++c) mq[c & 3] = fmaxf(mq[c & 3], x[c]);
-      return fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-    };
-    // the weights of the half in x, written as P over the half's first 32 columns; returns
-    // their sum, each chunk's divided by its value scale
-    auto half_weights = [&](int j, int h, float bias) {
-      uint32_t w[TC_HALF / 2];
-      const float4* sc = scales + (j % VS) * C::CHUNKS + 4 * h;
-      float sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < TC_HALF / 16; ++c) {
-        float ls[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p0 = ex2(x[16 * c + 2 * i] + bias);
-          const float p1 = ex2(x[16 * c + 2 * i + 1] + bias);
-          ls[i & 1] += p0 + p1;
-          w[8 * c + i] = pack_half2(p0, p1);
-        }
-        sum = fmaf(ls[0] + ls[1], sc[c].z, sum);
-      }
-      tmem_st16(tS + TC_HALF * h, w);
-      tmem_st16(tS + TC_HALF * h + 16, w + 16);
-      return sum;
-    };
+    // A negative `scale` turns the order of the scores around: the largest product is then
+    // the smallest score times the (negative) factor.
+    const bool neg = p.scale_log2 < 0.f;
+    const float hidden = neg ? INFINITY : -INFINITY;
+    uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
     for (int j = 0; j < nb; ++j) {
       wait(&scfull[j % VS], (j / VS) & 1);
       wait(&sfull[u], j & 1);
       tc_fence_after_sync();
-      load_half(j, 0);
-      float mx = half_max();
-      load_half(j, 1);  // half 1 stays in x for its weights
-      mx = fmaxf(mx, half_max());
+#pragma unroll
+      for (int c = 0; c < TC_KEYS / 16; ++c) tmem_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
+      tmem_wait_ld();
+      const int k0 = j * TC_KEYS;
+      if (k0 + TC_KEYS - 1 > base + t0) {  // a key here may lie past some row of the tile
+#pragma unroll
+        for (int c = 0; c < TC_KEYS; ++c)
+          if (k0 + c > pos) x[c] = __float_as_uint(hidden);
+      }
+      // the row's maximum: per chunk of raw scores (the factor is the same), then one fma each
+      const float4* sc = scales + (j % VS) * C::CHUNKS;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C::CHUNKS; ++c) {
+        float e = __uint_as_float(x[16 * c]);
+        if (!neg) {
+#pragma unroll
+          for (int i = 1; i < 15; i += 2)
+            e = fmaxf(fmaxf(e, __uint_as_float(x[16 * c + i])), __uint_as_float(x[16 * c + i + 1]));
+          e = fmaxf(e, __uint_as_float(x[16 * c + 15]));
+        } else {
+#pragma unroll
+          for (int i = 1; i < 16; ++i) e = fminf(e, __uint_as_float(x[16 * c + i]));
+        }
+        mx = fmaxf(mx, fmaf(e, BF16 ? sc[c].x * qinv : sc[c].x, sc[c].y));
+      }
       const float m_new = fmaxf(m_used, mx);
       // The exponent's offset moves at the first block and when the row maximum has grown
       // by more than 2^8; O and l then scale by f.
@@ -494,13 +524,33 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           tmem_st16(tO + c, o16);
         }
       }
-      float lsum = half_weights(j, 1, bias);
-      load_half(j, 0);
-      lsum += half_weights(j, 0, bias);
-      l = l * f + lsum;
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(&pfull[u]);
+      l *= f;
+      // the weights, half of the keys at a time: P in the half's first 32 columns; l takes each
+      // chunk's sum divided by its value scale
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 4 * h; c < 4 * h + 4; ++c) {
+          const float4 s4 = sc[c];
+          const uint64_t a2 = pack_f32x2(BF16 ? s4.x * qinv : s4.x);
+          const uint64_t b2 = pack_f32x2(s4.y + bias);
+          uint64_t sum2 = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(x[16 * c + 2 * i], x[16 * c + 2 * i + 1]), a2, b2));
+            const float p0 = ex2(t.x), p1 = ex2(t.y);
+            sum2 = add_f32x2(sum2, pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+            x[8 * c + i] = pack_half2(p0, p1);  // (its place was consumed: 8 c + i <= 16 c + 2 i)
+          }
+          const float2 s2 = unpack_f32x2(sum2);
+          l = fmaf(s2.x + s2.y, s4.z, l);
+        }
+        tmem_st16(tS + 32 * h, &x[32 * h]);
+        tmem_st16(tS + 32 * h + 16, &x[32 * h + 16]);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&pfull[2 * u + h]);
+      }
     }
     // ------------------------------------------------ O / l
     if (nb > 0) wait(&pvdone[u], (nb - 1) & 1);
