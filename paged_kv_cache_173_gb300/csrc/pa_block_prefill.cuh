@@ -83,7 +83,8 @@ struct BpCfg {
   static constexpr int V_OFF = K_OFF + KSTAGES * KBYTES;
   static constexpr int SC_OFF = V_OFF + VSTAGES * KBYTES;  // [VSTAGES][CHUNKS] float4
   static constexpr int BAR_OFF = SC_OFF + VSTAGES * CHUNKS * 16;
-  static constexpr int NBARS = 2 * KSTAGES + 3 * VSTAGES + 4 * TC_TILES + 3;
+  static constexpr int DONE = KSTAGES > VSTAGES ? KSTAGES : VSTAGES;  // ring of completed steps
+  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 4 * TC_TILES + 3;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
   static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
@@ -126,6 +127,29 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The MMAs and the commit of pa_ptx.cuh issued by one elected lane of a warp that
+// runs them together.
+__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+__device__ __forceinline__ void umma_f16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                  bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+__device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
+}
+
 template <typename T, int HEAD_DIM>
 __global__ void __launch_bounds__(BpCfg<HEAD_DIM>::THREADS, 1)
 block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
@@ -140,13 +164,14 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   float4* scales = reinterpret_cast<float4*>(sm + C::SC_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
   uint64_t* kfull = bars;                  // [KS] K of a block is widened (96 arrivals)
-  uint64_t* kempty = kfull + KS;           // [KS] that block's Q K^T (both tiles) is done
-  uint64_t* vfull = kempty + KS;           // [VS] V of a block is widened (96 arrivals)
-  uint64_t* vempty = vfull + VS;           // [VS] that block's P V (both tiles) is done
-  uint64_t* scfull = vempty + VS;          // [VS] the scales of the block are in `scales`
-  uint64_t* sfull = scfull + VS;           // [tile] S of the tile's next block is in TMEM
+  uint64_t* vfull = kfull + KS;            // [VS] V of a block is widened (96 arrivals)
+  uint64_t* scfull = vfull + VS;           // [VS] the scales of the block are in `scales`
+  // step i of the MMA warp: P V of block i - 1, then Q K^T of block i, of both tiles.  One
+  // commit per step frees K of block i and V of block i - 1.
+  uint64_t* done = scfull + VS;            // [DONE] the MMAs of a step have completed
+  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
-  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the tile's P V of that block has completed
+  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the tile's last P V has completed
   uint64_t* qbar = pvdone + TC_TILES;      // Q of both tiles landed
   uint64_t* qready = qbar + 1;             // bfloat16: Q is float16 now (256 arrivals)
   uint64_t* drain = qready + 1;            // every MMA issued has completed
@@ -184,13 +209,12 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   if (warp == C::MMA_WARP && lane == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(&kfull[i], C::PROD);
-      mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
       mbar_init(&vfull[i], C::PROD);
-      mbar_init(&vempty[i], 1);
       mbar_init(&scfull[i], 1);
     }
+    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < TC_TILES; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[2 * i], TC_ROWS);
@@ -234,12 +258,14 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       auto kg = [&](int i) { return pw + C::PROD_WARPS * i; };
       auto vg = [&](int i) { return C::PROD_WARPS - 1 - pw + C::PROD_WARPS * i; };
       int kph[NG], vph[NG];  // physical block of each row group (8 rows lie in one pool block)
-      auto fetch = [&](int j) {
+      // (a group past the last one is clamped, and not used)
+      auto fetch_k = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {  // (a group past the last one is clamped, and not used)
-          kph[i] = __ldg(bt + (min(j * TC_KEYS + kg(i) * 8, kend - 1) >> p.log2_b));
-          vph[i] = __ldg(bt + (min(j * TC_KEYS + vg(i) * 8, kend - 1) >> p.log2_b));
-        }
+        for (int i = 0; i < NG; ++i) kph[i] = __ldg(bt + (min(j * TC_KEYS + kg(i) * 8, kend - 1) >> p.log2_b));
+      };
+      auto fetch_v = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) vph[i] = __ldg(bt + (min(j * TC_KEYS + vg(i) * 8, kend - 1) >> p.log2_b));
       };
       uint4 kd[NG][HALVES], vd[NG][HALVES];
       auto load = [&](uint4 (&d)[HALVES], const uint8_t* head, int phys, int key) {
@@ -263,54 +289,23 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
         }
       };
-      // scales of the block's 16-key chunks: lanes 0-7 of the second warp
-      const bool side = pw == 1;
-      float sk = 0.f, sv = 0.f;
-      auto side_load = [&](int j) {
-        if (side && lane < C::CHUNKS) {
-          const int key = j * TC_KEYS + lane * CHUNK;
-          sk = 0.f;
-          sv = 1.f;
-          if (key < kend) {
-            const int phys = __ldg(bt + (key >> p.log2_b));
-            if (static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_blocks)) {
-              const size_t at = static_cast<size_t>(phys) * p.num_kv_heads + kvh;
-              sk = __ldg(p.k_scales + at);
-              sv = __ldg(p.v_scales + at);
-            }
-          }
-        }
-      };
-      fetch(0);
-      side_load(0);
+      fetch_k(0);
+      fetch_v(0);
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
         if (kg(i) < RG) load(kd[i], khead, kph[i], kg(i) * 8 + r8);
         if (vg(i) < RG) load(vd[i], vhead, vph[i], vg(i) * 8 + r8);
       }
-      fetch(min(1, nblk - 1));
+      fetch_k(min(1, nblk - 1));
+      fetch_v(min(1, nblk - 1));
       for (int j = 0; j < nblk; ++j) {
         const int kslot = j % KS;
         const int vslot = j % VS;
-        // V first: its stage (and the scales' row) falls free with P V of block j - VS, before K's
-        const bool vok = j < VS || __all_sync(FULL_MASK, tc_wait(&vempty[vslot], ((j / VS) - 1) & 1));
-        const bool ok = vok && (j < KS || __all_sync(FULL_MASK, tc_wait(&kempty[kslot], ((j / KS) - 1) & 1)));
-        if (!ok) {
+        // K's stage is free after step j - KS, V's after step j - VS + 1
+        const int step = max(j - KS, j - VS + 1);
+        if (step >= 0 && !__all_sync(FULL_MASK, tc_wait(&done[step % C::DONE], (step / C::DONE) & 1))) {
           flags[1] = 1;
           break;
-        }
-        if (side) {
-          if (lane < C::CHUNKS) {
-            if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax)) flags[0] = 1;
-            const float v = fmaxf(sv, 5.421010862427522e-20f);  // 2^-64
-            // a factor of 0 would turn a masked score (-inf) into NaN: 2^-120 makes 0 of every score
-            float a = sk * p.scale_log2;
-            a = fabsf(a) >= 7.52316384526264e-37f ? a : copysignf(7.52316384526264e-37f, p.scale_log2);
-            scales[vslot * C::CHUNKS + lane] = make_float4(a, __log2f(v), __frcp_rn(v), 0.f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&scfull[vslot]);
-          if (j + 1 < nblk) side_load(j + 1);
         }
         uint8_t* kdst = sm + C::K_OFF + kslot * C::KBYTES;
         uint8_t* vdst = sm + C::V_OFF + vslot * C::KBYTES;
@@ -322,6 +317,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
         fence_proxy_async_smem();  // the widened rows become visible to the tensor core
         mbar_arrive(&kfull[kslot]);
+        fetch_k(min(j + 2, nblk - 1));  // a whole block before their use
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
           if (vg(i) >= RG) continue;
@@ -330,18 +326,22 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
         fence_proxy_async_smem();
         mbar_arrive(&vfull[vslot]);
-        fetch(min(j + 2, nblk - 1));
+        fetch_v(min(j + 2, nblk - 1));
       }
     }
   } else if (warp == C::MMA_WARP) {
-    // ------------------------------------------------ MMA issue (lane 0), as paged_prefill_tc_kernel
-    if (lane == 0 && nblk > 0) {
+    // ------------------------------------------------ MMA issue
+    // The whole warp runs this loop and one elected lane issues: every value stays uniform, so
+    // descriptors sit in uniform registers (with one lane in a branch of its own each MMA paid
+    // for moving its operands there, and the 16 MMAs of a tile and block took 2000 cycles to issue).
+    if (nblk > 0) {
       int nbt[TC_TILES];
       for (int u = 0; u < TC_TILES; ++u) nbt[u] = u < ntiles ? tile_blocks(u) : 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL_MASK, tc_wait(bar, parity)) != 0; };
       int k_seen = -1;
       auto wait_k = [&](int j) -> bool {
         if (j <= k_seen) return true;
-        if (!tc_wait(&kfull[j % KS], (j / KS) & 1)) return false;
+        if (!wait(&kfull[j % KS], (j / KS) & 1)) return false;
         k_seen = j;
         tc_fence_after_sync();
         return true;
@@ -356,31 +356,63 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
           const uint32_t off = (ks >> 2) * C::QATOM + ((ks & 3) << 5);
           const uint32_t koff = (ks >> 2) * C::KATOM + ((ks & 3) << 5);
-          umma_f16(tmem + 256 * u, umma_desc_add(qu, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
+          umma_f16_elect(tmem + 256 * u, umma_desc_add(qu, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
         }
-        umma_commit(&sfull[u]);
+        umma_commit_elect(&sfull[u]);
       };
-      bool ok = tc_wait(BF16 ? qready : qbar, 0) && wait_k(0);
+      // Scales of each block's 16-key chunks, lanes 0-7: read two blocks before their use, their
+      // physical block's id three before.  Row b % VS is free for block b once the softmax of
+      // block b - VS is over, which this warp has waited for.  (A producer warp that carried the
+      // scales too waited for its latest row loads at each, 900 cycles a block.)
+      const int32_t* bt = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
+      float sk = 0.f, sv = 0.f;
+      int sph = 0;
+      auto scale_fetch = [&](int j) {
+        if (lane < C::CHUNKS) sph = __ldg(bt + (min(j * TC_KEYS + lane * CHUNK, kend - 1) >> p.log2_b));
+      };
+      auto scale_load = [&]() {  // (chunks past the stream repeat its last one: their keys are masked)
+        if (lane < C::CHUNKS) {
+          const bool in = static_cast<unsigned>(sph) < static_cast<unsigned>(p.num_blocks);
+          const size_t at = static_cast<size_t>(in ? sph : 0) * p.num_kv_heads + kvh;
+          sk = __ldg(p.k_scales + at);
+          sv = __ldg(p.v_scales + at);
+        }
+      };
+      auto scale_store = [&](int j) {
+        if (lane < C::CHUNKS) {
+          if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax)) flags[0] = 1;
+          // a factor of 0 would turn a masked score (-inf) into NaN: 2^-120 makes 0 of every score
+          float a = sk * p.scale_log2;
+          a = fabsf(a) >= 7.52316384526264e-37f ? a : copysignf(7.52316384526264e-37f, p.scale_log2);
+          const float lv = __log2f(fmaxf(sv, 5.421010862427522e-20f));  // at least 2^-64
+          scales[(j % VS) * C::CHUNKS + lane] = make_float4(a, lv, ex2(-lv), 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scfull[j % VS]);
+      };
+      static_assert(VS >= 3, "two blocks' scales ahead");
+      scale_fetch(0);
+      scale_load();
+      scale_fetch(1);
+      scale_store(0);
+      scale_load();
+      scale_fetch(2);
+      bool ok = wait(BF16 ? qready : qbar, 0) && wait_k(0);
       if (ok) {
         for (int u = 0; u < ntiles; ++u) qk(u, 0);
-        umma_commit(&kempty[0]);
+        umma_commit_elect(&done[0]);
       }
+      if (nblk > 1) scale_store(1);
+      scale_load();
+      scale_fetch(3);
       for (int j = 0; ok && j < nblk; ++j) {
         const int vslot = j % VS;
         bool have_v = false;
         for (int u = 0; u < ntiles; ++u) {
           if (j >= nbt[u]) continue;
-          if (!tc_wait(&pfull[2 * u], j & 1)) {
-            ok = false;
-            break;
-          }
-          if (!have_v) {
-            if (!tc_wait(&vfull[vslot], (j / VS) & 1)) {
-              ok = false;
-              break;
-            }
-            have_v = true;
-          }
+          ok = wait(&pfull[2 * u], j & 1) && (have_v || wait(&vfull[vslot], (j / VS) & 1));
+          if (!ok) break;
+          have_v = true;
           tc_fence_after_sync();
           const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
           const uint32_t tP = tmem + 256 * u;
@@ -388,31 +420,32 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           // the first 64 keys while the softmax writes the weights of the others
 #pragma unroll
           for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
-            umma_f16_ts(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, j > 0 || kk > 0);
-          if (!tc_wait(&pfull[2 * u + 1], j & 1)) {
-            ok = false;
-            break;
-          }
+            umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, j > 0 || kk > 0);
+          ok = wait(&pfull[2 * u + 1], j & 1);
+          if (!ok) break;
           tc_fence_after_sync();
 #pragma unroll
           for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
-            umma_f16_ts(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
-          umma_commit(&pvdone[u]);
+            umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
           if (j + 1 < nbt[u]) {
-            if (!wait_k(j + 1)) {
-              ok = false;
-              break;
-            }
+            ok = wait_k(j + 1);
+            if (!ok) break;
             qk(u, j + 1);
+          } else {
+            umma_commit_elect(&pvdone[u]);
           }
         }
         if (!ok) break;
-        umma_commit(&vempty[vslot]);
-        if (j + 1 < nblk) umma_commit(&kempty[(j + 1) % KS]);
+        umma_commit_elect(&done[(j + 1) % C::DONE]);
+        if (j + 2 < nblk) {
+          scale_store(j + 2);
+          scale_load();
+          scale_fetch(j + 4);
+        }
       }
       if (!ok) flags[1] = 1;
-      umma_commit(drain);  // every MMA finishes before the TMEM is released
-      if (!tc_wait(drain, 0)) flags[1] = 1;
+      umma_commit_elect(drain);  // every MMA finishes before the TMEM is released
+      if (!wait(drain, 0)) flags[1] = 1;
     }
   } else {
     // ------------------------------------------------ softmax: warps 4 u .. 4 u + 3 run tile u
@@ -553,7 +586,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       }
     }
     // ------------------------------------------------ O / l
-    if (nb > 0) wait(&pvdone[u], (nb - 1) & 1);
+    if (nb > 0) wait(&pvdone[u], 0);
     const bool have = ok && nb > 0;
     if (!ok) flags[1] = 1;
     __syncthreads();  // the other warps' flags are visible past this point
