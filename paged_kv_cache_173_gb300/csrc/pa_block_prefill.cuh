@@ -50,10 +50,12 @@ struct BlockPrefillParams {
   int num_heads;
   int num_kv_heads;
   int group;
+  int log2_g;  // group = 1 << log2_g: it divides 128
   int log2_b;  // block_size = 1 << log2_b
   int num_blocks;
   int pairs;
   int tile_tokens;
+  int by_length;  // grid order: 1: (KV head, sequence, pair), 0: (pair, KV head, sequence)
   float scale_log2;
 };
 
@@ -95,6 +97,12 @@ struct BpCfg {
 };
 
 __device__ __forceinline__ uint4 ldg128(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// What is computed from x is computed after this point.  A value loaded an
+// iteration ahead would otherwise be turned into an address right behind its
+// load, and the warp would wait there.
+__device__ __forceinline__ void use_here(int& x) { asm volatile("" : "+r"(x)); }
+__device__ __forceinline__ void use_here(float& x) { asm volatile("" : "+f"(x)); }
 
 // 16 codes widened to float16: two 16-byte units.
 __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
@@ -178,9 +186,10 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::SLOT_OFF);
   volatile int* flags = reinterpret_cast<volatile int*>(sm + C::SLOT_OFF + 4);  // [0] bad block or scale, [1] timeout
 
-  const int pair = p.pairs - 1 - static_cast<int>(blockIdx.x);  // the longest pairs start first
-  const int kvh = blockIdx.y;
-  const int s = blockIdx.z;
+  // the longest pairs start first
+  const int pair = p.pairs - 1 - static_cast<int>(p.by_length ? blockIdx.z : blockIdx.x);
+  const int kvh = p.by_length ? blockIdx.x : blockIdx.y;
+  const int s = p.by_length ? blockIdx.y : blockIdx.z;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = p.group;
@@ -234,16 +243,12 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           tma_load_3d(sm + u * C::QBYTES + db * C::QATOM, &p.tmap_q, db * BOX_DIMS, kvh * G, q0 + ta + u * tt, qbar);
     }
   }
-  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = *tslot;
-
   if (warp >= C::PROD_WARP) {
     // ------------------------------------------------ producers: K, then V of each block
     const int pw = warp - C::PROD_WARP;
-    if (nblk > 0) {
+    if (nblk == 0) {
+      __syncthreads();
+    } else {
       constexpr int RG = 16;                              // groups of 8 rows per block
       constexpr int NG = (RG + C::PROD_WARPS - 1) / C::PROD_WARPS;  // a warp's, at most
       constexpr int HALVES = HEAD_DIM / 64;               // 64-code halves of a row
@@ -268,9 +273,11 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         for (int i = 0; i < NG; ++i) vph[i] = __ldg(bt + (min(j * TC_KEYS + vg(i) * 8, kend - 1) >> p.log2_b));
       };
       uint4 kd[NG][HALVES], vd[NG][HALVES];
+      bool bad = false;
       auto load = [&](uint4 (&d)[HALVES], const uint8_t* head, int phys, int key) {
+        use_here(phys);
         if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-          flags[0] = 1;  // never read outside the pool; the tiles' outputs become NaN
+          bad = true;  // never read outside the pool; the tiles' outputs become NaN
           phys = 0;
         }
         const uint8_t* src = head + ((static_cast<size_t>(phys) << p.log2_b) + (key & bmask)) * row_bytes;
@@ -298,6 +305,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       }
       fetch_k(min(1, nblk - 1));
       fetch_v(min(1, nblk - 1));
+      // (the first block's rows are on their way while the barriers and the tensor memory are set up)
+      __syncthreads();
       for (int j = 0; j < nblk; ++j) {
         const int kslot = j % KS;
         const int vslot = j % VS;
@@ -328,8 +337,21 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         mbar_arrive(&vfull[vslot]);
         fetch_v(min(j + 2, nblk - 1));
       }
+      if (bad) flags[0] = 1;  // read after the barrier below
     }
-  } else if (warp == C::MMA_WARP) {
+    // the producers meet the softmax warps at their two barriers
+    __syncthreads();
+    __syncthreads();
+    allow_dependent_launch();
+    return;
+  }
+  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tslot;
+
+  if (warp == C::MMA_WARP) {
     // ------------------------------------------------ MMA issue
     // The whole warp runs this loop and one elected lane issues: every value stays uniform, so
     // descriptors sit in uniform registers (with one lane in a branch of its own each MMA paid
@@ -371,6 +393,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         if (lane < C::CHUNKS) sph = __ldg(bt + (min(j * TC_KEYS + lane * CHUNK, kend - 1) >> p.log2_b));
       };
       auto scale_load = [&]() {  // (chunks past the stream repeat its last one: their keys are masked)
+        use_here(sph);
         if (lane < C::CHUNKS) {
           const bool in = static_cast<unsigned>(sph) < static_cast<unsigned>(p.num_blocks);
           const size_t at = static_cast<size_t>(in ? sph : 0) * p.num_kv_heads + kvh;
@@ -379,6 +402,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
       };
       auto scale_store = [&](int j) {
+        use_here(sk);
+        use_here(sv);
         if (lane < C::CHUNKS) {
           if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax)) flags[0] = 1;
           // a factor of 0 would turn a masked score (-inf) into NaN: 2^-120 makes 0 of every score
@@ -409,6 +434,13 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         const int vslot = j % VS;
         bool have_v = false;
         for (int u = 0; u < ntiles; ++u) {
+          // while the last tile's weights are awaited, and while the producers are quiet: behind
+          // the commit below their loads crowd the queue, and this warp's waited 900 cycles
+          if (u == ntiles - 1 && j + 2 < nblk) {
+            scale_store(j + 2);
+            scale_load();
+            scale_fetch(j + 4);
+          }
           if (j >= nbt[u]) continue;
           ok = wait(&pfull[2 * u], j & 1) && (have_v || wait(&vfull[vslot], (j / VS) & 1));
           if (!ok) break;
@@ -437,11 +469,6 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
         if (!ok) break;
         umma_commit_elect(&done[(j + 1) % C::DONE]);
-        if (j + 2 < nblk) {
-          scale_store(j + 2);
-          scale_load();
-          scale_fetch(j + 4);
-        }
       }
       if (!ok) flags[1] = 1;
       umma_commit_elect(drain);  // every MMA finishes before the TMEM is released
@@ -453,7 +480,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     const int r = 32 * (warp & 3) + lane;
     const bool tile_on = u < ntiles;
     const int t0 = ta + u * tt;
-    const int t = t0 + r / G;
+    const int t = t0 + (r >> p.log2_g);
     const bool rv = tile_on && t < tile_end(u);
     const int pos = rv ? base + t : -1;
     const int nb = tile_on ? tile_blocks(u) : 0;
@@ -591,23 +618,49 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     if (!ok) flags[1] = 1;
     __syncthreads();  // the other warps' flags are visible past this point
     tc_fence_after_sync();
+    // O / l through the tile's Q rows in shared memory (its MMAs are over): a thread holds one
+    // row, and rows of different tokens are far apart in `out`, so writing them from here
+    // would touch 32 lines per store.  A warp turns its own 32 rows (6300 -> 1900 cycles per CTA).
     const float inv = (!have || ctx_bad || flags[0] || flags[1]) ? NAN : 1.f / l;
-    T* dst = static_cast<T*>(p.out) + (static_cast<size_t>(q0 + t) * H + kvh * G + r % G) * HEAD_DIM;
+    if (nb > 0) {
+      uint8_t* qrow = sm + u * C::QBYTES + r * 128;
+#pragma unroll 1
+      for (int h = 0; h < DO / 64; ++h) {  // one 64-dim atom at a time
+        uint32_t o[64];
+        if (have) {
 #pragma unroll
-    for (int c = 0; c < DO; c += 16) {
-      uint32_t o16[16];
-      if (have) {  // warp-uniform
-        tmem_ld16(tO + c, o16);
-        tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) tmem_ld16(tO + 64 * h + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w4[i] = have ? pack2<T>(__uint_as_float(o[8 * c + 2 * i]) * inv, __uint_as_float(o[8 * c + 2 * i + 1]) * inv)
+                         : pack2<T>(NAN, NAN);
+          *reinterpret_cast<uint4*>(qrow + h * C::QATOM + ((c ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
       }
-      if (rv) {
-        uint32_t w8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          w8[i] = have ? pack2<T>(__uint_as_float(o16[2 * i]) * inv, __uint_as_float(o16[2 * i + 1]) * inv)
-                       : pack2<T>(NAN, NAN);
-        *reinterpret_cast<uint4*>(dst + c) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+      __syncwarp();
+    }
+    if (tile_on) {  // rows in order, DO / 8 lanes of 16 bytes each
+      constexpr int U = DO / 8;
+      constexpr int RPI = 32 / U;
+      const int unit = lane % U;
+      const int rw = 32 * (warp & 3);
+      const int t_end = tile_end(u);
+#pragma unroll 4
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int rr = rw + i * RPI + lane / U;
+        const int tr = t0 + (rr >> p.log2_g);
+        if (tr < t_end) {
+          const uint4 v = nb > 0 ? *reinterpret_cast<const uint4*>(sm + u * C::QBYTES + rr * 128 + (unit >> 3) * C::QATOM +
+                                                                   (((unit & 7) ^ (rr & 7)) << 4))
+                                 : make_uint4(pack2<T>(NAN, NAN), pack2<T>(NAN, NAN), pack2<T>(NAN, NAN), pack2<T>(NAN, NAN));
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                    (static_cast<size_t>(q0 + tr) * H + kvh * G + (rr & (G - 1))) * HEAD_DIM + unit * 8) = v;
+        }
       }
     }
     tc_fence_before_sync();
@@ -616,7 +669,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     allow_dependent_launch();
     return;
   }
-  // the MMA and producer warps meet the softmax warps at their two barriers
+  // the MMA warp meets the softmax warps at their two barriers
   tc_fence_before_sync();
   __syncthreads();
   __syncthreads();
@@ -647,6 +700,7 @@ cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t strea
   p.num_heads = a.num_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.group = group;
+  p.log2_g = __builtin_ctz(static_cast<unsigned>(group));
   p.log2_b = __builtin_ctz(static_cast<unsigned>(a.block_size));
   p.num_blocks = a.num_blocks;
   p.tile_tokens = TC_ROWS / group;
@@ -655,7 +709,13 @@ cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t strea
   p.scale_log2 = a.scale * 1.4426950408889634f;
   if (p.pairs == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.pairs, a.num_kv_heads, a.num_seqs);
+  // Over all sequences and heads longest first leaves the shortest CTAs for the end (8 prompts
+  // of 2048: 339 -> 295 us; 16 chunks of 509 on 1536: 245 -> 230 us; 2 prompts of 16384: 3147 ->
+  // 3098 us).  Where most of the context is cached the pairs are nearly equal, and pairs of one
+  // head that run together share its K and V in L2 (16 x 512 on 16384: 1574 us against 1673).
+  const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
+  p.by_length = cap <= 8 * static_cast<int64_t>(a.max_query_len) && p.pairs <= 65535;
+  cfg.gridDim = p.by_length ? dim3(a.num_kv_heads, a.num_seqs, p.pairs) : dim3(p.pairs, a.num_kv_heads, a.num_seqs);
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
