@@ -656,9 +656,11 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const vo
                          const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs, int num_rows,
                          int max_query_len, int num_heads, int num_kv_heads, int head_dim, int block_size,
                          int num_blocks, float scale, int dtype, void* stream) {
+  // a batch without new rows has no queries to point at: it is checked like an empty one
+  const bool none = num_rows == 0 || max_query_len == 0;
   int st = check_prefill(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
-                         num_seqs, num_rows, max_query_len, num_heads, num_kv_heads, head_dim, block_size,
-                         num_blocks, scale, dtype);
+                         none && num_seqs > 0 ? 0 : num_seqs, num_rows, max_query_len, num_heads, num_kv_heads,
+                         head_dim, block_size, num_blocks, scale, dtype);
   if (st != PA_OK) return st;
   if (num_seqs == 0 || max_query_len == 0 || num_rows == 0) return ok();
   st = check_side(k_scales, v_scales, "k_scales and v_scales");

@@ -86,7 +86,7 @@ struct BpCfg {
   static constexpr int SC_OFF = V_OFF + VSTAGES * KBYTES;  // [VSTAGES][CHUNKS] float4
   static constexpr int BAR_OFF = SC_OFF + VSTAGES * CHUNKS * 16;
   static constexpr int DONE = KSTAGES > VSTAGES ? KSTAGES : VSTAGES;  // ring of completed steps
-  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 4 * TC_TILES + 3;
+  static constexpr int NBARS = KSTAGES + VSTAGES + DONE + 4 * TC_TILES + 3;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
   static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
@@ -173,11 +173,10 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
   uint64_t* kfull = bars;                  // [KS] K of a block is widened (96 arrivals)
   uint64_t* vfull = kfull + KS;            // [VS] V of a block is widened (96 arrivals)
-  uint64_t* scfull = vfull + VS;           // [VS] the scales of the block are in `scales`
   // step i of the MMA warp: P V of block i - 1, then Q K^T of block i, of both tiles.  One
   // commit per step frees K of block i and V of block i - 1.
-  uint64_t* done = scfull + VS;            // [DONE] the MMAs of a step have completed
-  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
+  uint64_t* done = vfull + VS;             // [DONE] the MMAs of a step have completed
+  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM, its scales in `scales`
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
   uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the tile's last P V has completed
   uint64_t* qbar = pvdone + TC_TILES;      // Q of both tiles landed
@@ -221,11 +220,10 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     }
     for (int i = 0; i < VS; ++i) {
       mbar_init(&vfull[i], C::PROD);
-      mbar_init(&scfull[i], 1);
     }
     for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], 1);
     for (int i = 0; i < TC_TILES; ++i) {
-      mbar_init(&sfull[i], 1);
+      mbar_init(&sfull[i], 2);
       mbar_init(&pfull[2 * i], TC_ROWS);
       mbar_init(&pfull[2 * i + 1], TC_ROWS);
       mbar_init(&pvdone[i], 1);
@@ -380,6 +378,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           const uint32_t koff = (ks >> 2) * C::KATOM + ((ks & 3) << 5);
           umma_f16_elect(tmem + 256 * u, umma_desc_add(qu, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
         }
+        if (lane == 0) mbar_arrive(&sfull[u]);
         umma_commit_elect(&sfull[u]);
       };
       // Scales of each block's 16-key chunks, lanes 0-7: read two blocks before their use, their
@@ -412,8 +411,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           const float lv = __log2f(fmaxf(sv, 5.421010862427522e-20f));  // at least 2^-64
           scales[(j % VS) * C::CHUNKS + lane] = make_float4(a, lv, ex2(-lv), 0.f);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&scfull[j % VS]);
+        __syncwarp();  // lane 0's next arrival on sfull releases them
       };
       static_assert(VS >= 3, "two blocks' scales ahead");
       scale_fetch(0);
@@ -537,7 +535,6 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     const float hidden = neg ? INFINITY : -INFINITY;
     uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
     for (int j = 0; j < nb; ++j) {
-      wait(&scfull[j % VS], (j / VS) & 1);
       wait(&sfull[u], j & 1);
       tc_fence_after_sync();
 #pragma unroll
