@@ -62,7 +62,12 @@ SIGNATURES = {
     "pa_last_error": (ctypes.c_char_p, []),
 }
 
+# The entry points that _fast.so (csrc/py_fast.cpp) calls, in the order its bind() takes.
+FAST_ENTRIES = ("pa_reshape_and_cache_fp8_block", "pa_update_key_bounds", "pa_decode_fp8_block",
+                "pa_decode_splitk_fp8_block", "pa_prefill_fp8_block", "pa_select_blocks", "pa_decode_sparse")
+
 _lib: Optional[ctypes.CDLL] = None
+_fast = None
 _lock = threading.Lock()
 
 
@@ -88,6 +93,23 @@ def lib() -> ctypes.CDLL:
                     f.argtypes = args
                 _lib = L
     return _lib
+
+
+def fast():
+    """The C++ half of the binding, bound to the loaded library."""
+    global _fast
+    if _fast is None:
+        L = lib()
+        with _lock:
+            if _fast is None:
+                try:
+                    from . import _fast as m
+                except ImportError as e:
+                    raise RuntimeError("the binding's C++ half (_fast.so) is missing or does not load: build it first "
+                                       "(python -m paged_kv_cache_173_gb300.build)") from e
+                m.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in FAST_ENTRIES])
+                _fast = m
+    return _fast
 
 
 def status_name(status: int) -> str:

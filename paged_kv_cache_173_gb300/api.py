@@ -328,10 +328,15 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cach
 
 # ---------------------------------------------------------------------------
 # Block-scaled E4M3 pools and block-sparse decode.  A small decode step is paced
-# by the host, so these calls check each tensor once, on its type, device and
-# contiguity together, and build the message only when a check fails (a decode
-# call: 16 us -> 9 us on the host).
+# by the host, so each call first goes the short way through csrc/py_fast.cpp,
+# which reads the tensors in C++ and launches when everything is as wanted.  When
+# it is not (or the tensors' device is not current), nothing has been launched and
+# the call goes on below, where each check has its message.
 # ---------------------------------------------------------------------------
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _ptr(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> int:
     """Pointer of a contiguous tensor of `dtype` on CUDA device `index`."""
     if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
@@ -382,6 +387,11 @@ def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cac
     at slot_mapping [T], with one scale per (block, KV head) in k_scales / v_scales [N, Hk]
     (float32) taken from the data and grown as a block fills.  The tokens of one block
     stand next to each other in slot_mapping."""
+    if k_cache.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().write(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, dev, sp):
+            return
     i = _cuda_index(k_cache)
     shape = k_cache.shape
     N, B, Hk, d = shape
@@ -424,6 +434,12 @@ def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tenso
                         stream: Optional[torch.cuda.Stream] = None) -> None:
     """pa_decode over block-scaled E4M3 pools: values are code * k_scales[block, head] (K) and
     code * v_scales[block, head] (V); q and out are float16 or bfloat16."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().decode(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, dev,
+                              sp):
+            return
     i, _, _, _, _, _, args = _block_decode_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                                 scale)
     _run(_lib.lib().pa_decode_fp8_block, "pa_decode_fp8_block", i, stream, args)
@@ -435,6 +451,13 @@ def pa_decode_splitk_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torc
                                workspace: torch.Tensor, max_num_partitions: Optional[int] = None,
                                stream: Optional[torch.cuda.Stream] = None) -> None:
     """Split-K decode over block-scaled pools; follow with pa_splitk_reduce on the same stream."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        P = max_num_partitions or max_num_partitions_for(block_tables.shape[-1], k_cache.shape[1], partition_size)
+        if _lib.fast().splitk(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale,
+                              partition_size, P, workspace, dev, sp):
+            return
     i, _, _, _, B, M, args = _block_decode_args(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                                 scale)
     P = max_num_partitions or max_num_partitions_for(M, B, partition_size)
@@ -448,6 +471,12 @@ def pa_prefill_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
                          context_lens: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int,
                          scale: float, stream: Optional[torch.cuda.Stream] = None) -> None:
     """pa_prefill over block-scaled E4M3 pools (k_scales / v_scales [N, Hk])."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().prefill(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                               query_start_loc, max_query_len, scale, dev, sp):
+            return
     i = _cuda_index(q)
     qs, ks = q.shape, k_cache.shape
     R, H, d = qs
@@ -474,6 +503,11 @@ def pa_update_key_bounds(key: torch.Tensor, key_bounds: torch.Tensor, bound_exps
     """Fold key [T, Hk, d] into the bounds of the blocks named by slot_mapping [T]: key_bounds
     [N, Hk, 2, d] (int8 lo, hi) and bound_exps [N, Hk] (int32), lo * 2^e <= k <= hi * 2^e.
     The tokens of one block stand next to each other in slot_mapping."""
+    if key_bounds.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().bounds(key, key_bounds, bound_exps, slot_mapping, block_size, dev, sp):
+            return
     i = _cuda_index(key_bounds)
     T, Hk, d = key.shape
     N = _check_bounds(key_bounds, bound_exps, Hk, d)
@@ -503,6 +537,12 @@ def pa_select_blocks(sel_tables: torch.Tensor, sel_lens: torch.Tensor, q: torch.
     num_last and the best by the bounds of their keys, max_selected in all.  Writes
     sel_tables [S, Hk, max_selected] (physical ids in position order, then -1) and
     sel_lens [S, Hk] (tokens), both int32."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().select(sel_tables, sel_lens, q, key_bounds, bound_exps, block_tables, context_lens, block_size,
+                              num_first, num_last, workspace, dev, sp):
+            return
     i = _cuda_index(q)
     S, H, d = q.shape
     if sel_tables.dim() != 3 or sel_tables.shape[0] != S:
@@ -529,6 +569,11 @@ def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, 
     """Decode with a block table per (sequence, KV head): sel_tables [S, Hk, max_selected] and
     sel_lens [S, Hk] (pa_select_blocks writes them).  16-bit pools of the query type, or
     block-scaled E4M3 pools with k_scales and v_scales [N, Hk]."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().sparse(out, q, k_cache, v_cache, sel_tables, sel_lens, scale, k_scales, v_scales, dev, sp):
+            return
     i = _cuda_index(q)
     qs, ks = q.shape, k_cache.shape
     S, H, d = qs

@@ -1,4 +1,5 @@
-"""Build ``libpagedattn.so`` in-tree with nvcc for GB300 (sm_103a).
+"""Build ``libpagedattn.so`` in-tree with nvcc for GB300 (sm_103a), and
+``_fast.so``, the C++ half of the Python binding, with the host compiler.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked into
 one shared library with the CUDA runtime linked statically, so the library
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
+FAST = os.path.join(PKG, "_fast.so")
+FAST_SRC = os.path.join(CSRC, "py_fast.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
@@ -52,15 +55,41 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
     return obj
 
 
+def build_fast(force: bool = False) -> str:
+    """The binding's C++ half (torch's headers, no CUDA): a CPython extension in the package."""
+    deps = [FAST_SRC, os.path.join(INCLUDE, "pagedattn.h")]
+    if not force and os.path.exists(FAST) and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
+        return FAST
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], FAST_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on py_fast.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST)
+    return FAST
+
+
 def build_library(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(p) <= t for p in _deps()):
+            build_fast()
             return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        fast = ex.submit(build_fast, force)
         objs = list(ex.map(lambda s: _compile(s, ptxas_verbose), srcs))
+        fast.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

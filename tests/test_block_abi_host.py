@@ -216,3 +216,21 @@ def test_attention_matches_torch():
     want = torch.nn.functional.scaled_dot_product_attention(q[None], k[None], v[None], scale=0.3)[0]
     assert np.allclose(out, want.numpy(), atol=1e-12)
     assert (np.abs(out) <= A_ + 1e-12).all() and S.shape == (3, 1)
+
+
+def test_the_short_way_declines_what_it_does_not_know(L):
+    """_fast answers False, and launches nothing, for anything but contiguous tensors of the current
+    device with the call's types; the caller then goes through the checks that have messages."""
+    fast = _lib.fast()
+    x = torch.zeros(2, 3, 4, dtype=torch.float16)
+    arity = dict(write=9, bounds=7, decode=11, splitk=14, prefill=13, select=13, sparse=11)
+    for name, n in arity.items():
+        f = getattr(fast, name)
+        assert f() is False and f(*[None] * n) is False and f(*[x] * n) is False
+        assert f(*[x] * (n - 2), 0, 0) is False                 # host tensors
+        assert f(*[x] * (n - 2), -1, 0) is False and f(*[x] * (n - 2), 0, 1 << 70) is False
+        assert f(*[object()] * (n - 2), 1 << 70, 0) is False    # numbers past 64 bits
+    with pytest.raises((TypeError, ValueError)):
+        fast.bind(1, 2)
+    with pytest.raises(ValueError):
+        fast.bind(*[0] * 7)

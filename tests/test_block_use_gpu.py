@@ -9,7 +9,7 @@ import torch
 
 from block_cases import Batch, assert_close, to_np
 from oracle import block_oracle as bo
-from paged_kv_cache_173_gb300 import api
+from paged_kv_cache_173_gb300 import _lib, api
 from paged_kv_cache_173_gb300._lib import PagedAttnError
 
 pytestmark = pytest.mark.gpu
@@ -275,3 +275,33 @@ def test_binding_refuses_what_it_cannot_take():
     with pytest.raises(TypeError):
         api.pa_reshape_and_cache_fp8_block(s.key, s.value, s.kc, s.vc, s.ks, s.vs, s.slots.int())
     torch.cuda.synchronize()
+
+
+def test_short_way_takes_good_calls_and_no_others():
+    """_fast launches a well-formed call itself; anything else it declines with nothing launched."""
+    b = Batch([70, 1, 33], 4, 2, 128, 16, torch.float16, 12)
+    q, kc, vc, ks, vs, bt, cl = b.dev("q", "kc", "vc", "ks", "vs", "tables", "lens")
+    out = torch.full_like(q, 7.0)
+    fast, dev, sp = _lib.fast(), torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+    good = [out, q, kc, vc, ks, vs, bt, cl, float(b.scale)]
+
+    def answer(i=None, x=None, d=dev):
+        a = list(good)
+        if i is not None:
+            a[i] = x
+        return fast.decode(*a, d, sp)
+
+    wide = torch.zeros(q.shape[0], q.shape[1], 2 * q.shape[2], dtype=q.dtype, device="cuda")
+    for i, x in [(0, out.cpu()), (0, out.float()), (0, wide[..., ::2]), (1, q[:2]), (2, kc.to(torch.int8)), (3, vc[:-1]),
+                 (4, ks.double()), (5, vs[:, :1]), (6, bt.long()), (6, bt[:, 0]), (7, cl[:2]), (8, 1), (8, None),
+                 (8, float("nan")), (1, None), (1, q.double())]:
+        assert answer(i, x) is False, (i, x)
+    assert answer(d=dev + 1) is False
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
+    assert answer() is True
+    want = torch.empty_like(q)
+    api.pa_decode_fp8_block(want, q, kc, vc, ks, vs, bt, cl, b.scale)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert answer(2, kc.view(torch.float8_e4m3fn)) is True
