@@ -603,6 +603,8 @@ int pa_decode_splitk_fp8_block(void* out, const void* q, const void* k_cache, co
  * pa_decode_fp8_block.  Arguments, supported shapes (head_dim 64 or 128) and
  * device-value outcomes as pa_prefill; in addition a negative, infinite or NaN
  * scale gives NaN in the rows that an id outside the pool in its place would.
+ * A NaN code gives NaN only in the rows whose causal range holds its token (a
+ * key's in all of the row, a value's in its channel).
  */
 int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scales, const float* v_scales, const int32_t* block_tables,

@@ -1,17 +1,33 @@
 // pa_block_prefill.cuh -- prefill over block-scaled E4M3 pools on the tcgen05
 // tensor cores.
 //
-//  block_prefill_tc_kernel  the pipeline of paged_prefill_tc_kernel
-//                           (pa_prefill_tc.cuh): one CTA per (pair of query
-//                           tiles, KV head, sequence), tiles of 128 rows
-//                           (128 / G new tokens x G heads), Q K^T and P V in
-//                           tensor memory, one softmax thread per row.
+//  block_prefill_tc_kernel  one CTA per SM; an item of work is a pair of query
+//                           tiles of a (KV head, sequence), a tile 128 rows
+//                           (128 / G new tokens x G heads).  Q K^T and P V in
+//                           tensor memory (S 128 and O 128 columns per tile, P
+//                           over S), one softmax thread per row with the block's
+//                           128 scores in registers.
 //
-// What differs is the way in: the codes do not fit a kind::f16 MMA, so four
-// producer warps read them from the pools (16 codes per lane and load, one
-// block of 128 keys ahead, held in registers while the stage is in use), widen
-// them exactly to float16 and store them in the swizzled layout that a TMA box
-// of 16-bit rows would leave.  Two warps carry K, two V.
+// The bound is the tensor cores: 4 x 128 x 128 x d multiply-adds per pair and 128
+// keys, 2050 cycles at d = 128.  What kept them waiting, and what stands against it:
+//  - The codes do not fit a kind::f16 MMA.  Four producer warps read them from the
+//    pools (16 codes per lane and load, one block of 128 keys ahead, held in
+//    registers while the stage is in use), widen them exactly to float16 and store
+//    them in the swizzled layout that a TMA box of 16-bit rows would leave.
+//  - A tile's chain (scores, softmax, weights, P V, next scores) takes longer than
+//    its MMAs.  Two tiles alternate, an MMA warp for each, in turns, so that one
+//    tile's MMAs run under the other's softmax.
+//  - The start and the end of a pair (first loads, last outputs) took as long as
+//    five blocks of keys when each pair had its own CTA.  A CTA goes on to the next
+//    pair that has not started, and its producers, Q loads and first MMAs overlap
+//    the outputs of the last pair.
+//  - 128 scores per softmax thread leave 40 registers for the rest.  The launch's
+//    512 x 128 registers are shared out: 168 a softmax thread, 112 a producer, 64 the
+//    others; nothing spills.
+// Measured (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of 2048 tokens 235 us,
+// 2 of 16384 2973 us (0.78 of the measured peak), 16 x 512 on 16384 cached 1547 us;
+// bf16, 16 chunks of 509 on 1536 cached 206 us.  One CTA per pair, one MMA warp for
+// both tiles: 282, 3005, 1584 and 230 us.
 //
 // The mathematics of the scales is that of pa_block_decode.cuh: with v_b the
 // value scale of the block of key i,
@@ -63,12 +79,18 @@ struct BlockPrefillParams {
 // codes, the scales of the V ring's blocks, the barriers.
 template <int HEAD_DIM>
 struct BpCfg {
+  // Warps: two warpgroups of softmax, one of producers, and one of MMA issue (a warp per tile),
+  // items and scales (one warp) and one idle warp.
   static constexpr int SOFT = TC_TILES * TC_ROWS;  // softmax threads
-  static constexpr int MMA_WARP = SOFT / 32;
-  static constexpr int PROD_WARP = MMA_WARP + 1;
-  static constexpr int PROD_WARPS = 3;  // twelve warps in all: three per scheduler, 168 registers a thread
+  static constexpr int PROD_WARP = SOFT / 32;
+  static constexpr int PROD_WARPS = 4;
   static constexpr int PROD = PROD_WARPS * 32;
-  static constexpr int THREADS = SOFT + 32 + PROD;
+  static constexpr int MMA_WARP = PROD_WARP + PROD_WARPS;
+  static constexpr int ITEM_WARP = MMA_WARP + TC_TILES;
+  static constexpr int THREADS = SOFT + PROD + 128;
+  static constexpr int SOFT_REGS = 168, PROD_REGS = 112, MMA_REGS = 64;
+  // what the warpgroups hold is what the block was launched with
+  static_assert(SOFT * SOFT_REGS + PROD * PROD_REGS + 128 * MMA_REGS <= THREADS * 128, "registers");
   static constexpr int DBOX = HEAD_DIM / BOX_DIMS;
   static constexpr int QATOM = TC_ROWS * 128;
   static constexpr int QBYTES = DBOX * QATOM;
@@ -83,10 +105,16 @@ struct BpCfg {
   static_assert(KSTAGES >= 2 && VSTAGES >= 2, "the rings do not fit");
   static constexpr int K_OFF = TC_TILES * QBYTES;
   static constexpr int V_OFF = K_OFF + KSTAGES * KBYTES;
-  static constexpr int SC_OFF = V_OFF + VSTAGES * KBYTES;  // [VSTAGES][CHUNKS] float4
-  static constexpr int BAR_OFF = SC_OFF + VSTAGES * CHUNKS * 16;
-  static constexpr int DONE = KSTAGES > VSTAGES ? KSTAGES : VSTAGES;  // ring of completed steps
-  static constexpr int NBARS = KSTAGES + VSTAGES + DONE + 4 * TC_TILES + 3;
+  static constexpr int SC_OFF = V_OFF + VSTAGES * KBYTES;  // [2 * GROUP][CHUNKS] float4
+  static constexpr int GROUP = 4;  // blocks whose scales one warp loads together, a lane per 16-key chunk
+  static_assert(GROUP * CHUNKS == 32, "one chunk per lane");
+  static constexpr int INFO_OFF = SC_OFF + 2 * GROUP * CHUNKS * 16;
+  static constexpr int ITEMS = 4;  // ring of published work items
+  static constexpr int RESP_OFF = INFO_OFF + ITEMS * 32;
+  static constexpr int BAR_OFF = RESP_OFF + 16;
+  static constexpr int DONE = VSTAGES;  // ring of completed steps
+  static_assert(KSTAGES <= VSTAGES, "a step's commit is waited for before its place is used again");
+  static constexpr int NBARS = KSTAGES + VSTAGES + DONE + 8 * TC_TILES + ITEMS + 5;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
   static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
@@ -158,6 +186,135 @@ __device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
       : "memory");
 }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// ---------------------------------------------------------------- work items
+// An item is a pair of query tiles of one (sequence, KV head).  A CTA starts with
+// the item of its own grid index and then takes over CTAs that have not started
+// yet, one at a time: cancelling one hands over its index.
+
+// Ask for a CTA of this grid that has not started; the answer lands in `resp`.
+__device__ __forceinline__ void ask_for_cta(void* resp, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_addr(resp)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Whether the answer names a CTA, and its grid index.
+__device__ __forceinline__ bool cta_given(const void* resp, uint3& id) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
+      : "=&r"(got), "=&r"(id.x), "=&r"(id.y), "=&r"(id.z)
+      : "r"(smem_addr(resp))
+      : "memory");
+  return got != 0;
+}
+
+struct PrefillItem {
+  int s, kvh;
+  int ta;    // first new token of tile 0
+  int q0;    // row of the sequence's first new token
+  int qlen;  // its new tokens
+  int base;  // its tokens before them
+
+  __device__ __forceinline__ int tiles(int tt) const { return ta + tt < qlen ? 2 : 1; }
+  // one past tile u's last new token, and the key blocks that it meets
+  __device__ __forceinline__ int tile_end(int u, int tt) const { return min(qlen, ta + (u + 1) * tt); }
+  __device__ __forceinline__ int tile_blocks(int u, int tt) const {
+    return u < tiles(tt) ? (base + tile_end(u, tt) + TC_KEYS - 1) / TC_KEYS : 0;
+  }
+  __device__ __forceinline__ int kend(int tt) const { return base + tile_end(1, tt); }  // the keys' end
+  __device__ __forceinline__ int blocks(int tt) const { return (kend(tt) + TC_KEYS - 1) / TC_KEYS; }
+};
+
+// The item of a grid index: 0 nothing to do, 1 work, -1 a context length that cannot be.
+__device__ __forceinline__ int find_item(const BlockPrefillParams& p, uint3 id, PrefillItem& it) {
+  const int pair = p.pairs - 1 - static_cast<int>(p.by_length ? id.z : id.x);  // the longest pairs start first
+  it.kvh = p.by_length ? id.x : id.y;
+  it.s = p.by_length ? id.y : id.z;
+  it.q0 = __ldg(p.query_start_loc + it.s);
+  it.qlen = __ldg(p.query_start_loc + it.s + 1) - it.q0;
+  const int ctx = __ldg(p.context_lens + it.s);
+  it.base = ctx - it.qlen;
+  it.ta = 2 * pair * p.tile_tokens;
+  if (it.ta >= it.qlen) return 0;
+  return ctx < it.qlen || ctx > (p.max_blocks_per_seq << p.log2_b) ? -1 : 1;
+}
+
+// NaN in the rows of an item, by `n` threads.
+template <typename T, int HEAD_DIM>
+__device__ __forceinline__ void write_nan_rows(const BlockPrefillParams& p, const PrefillItem& it, int i, int n) {
+  constexpr int U = HEAD_DIM / 8;
+  const uint32_t v = pack2<T>(NAN, NAN);
+  const int rows = (it.tile_end(1, p.tile_tokens) - it.ta) << p.log2_g;
+#pragma unroll 1
+  for (; i < rows * U; i += n) {
+    const int r = i / U;
+    T* row = static_cast<T*>(p.out) + (static_cast<size_t>(it.q0 + it.ta + (r >> p.log2_g)) * p.num_heads +
+                                       it.kvh * p.group + (r & (p.group - 1))) * HEAD_DIM;
+    reinterpret_cast<uint4*>(row)[i % U] = make_uint4(v, v, v, v);
+  }
+}
+
+// The bytes of a word of codes that are NaN, as 0x80 each.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// The four lanes 4 i .. 4 i + 3 exchange: lane q's unit a[c] goes to a[q] of lane c.
+__device__ __forceinline__ void transpose4(uint4 (&a)[4], int lane) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = o == 1 ? 2 * i : i;
+      const uint4 x = up ? a[c] : a[c + o];
+      uint4 y;
+      y.x = __shfl_xor_sync(FULL_MASK, x.x, o);
+      y.y = __shfl_xor_sync(FULL_MASK, x.y, o);
+      y.z = __shfl_xor_sync(FULL_MASK, x.z, o);
+      y.w = __shfl_xor_sync(FULL_MASK, x.w, o);
+      if (up) a[c] = y;
+      else a[c + o] = y;
+    }
+  }
+}
+
+// The registers of each thread of the calling warpgroup from here on.
+template <bool UP, int N>
+__device__ __forceinline__ void set_max_regs() {
+  if constexpr (UP) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  }
+}
+
 template <typename T, int HEAD_DIM>
 __global__ void __launch_bounds__(BpCfg<HEAD_DIM>::THREADS, 1)
 block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
@@ -170,175 +327,204 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float4* scales = reinterpret_cast<float4*>(sm + C::SC_OFF);
+  // [ITEMS][8]: the item (s: -1 past the last), [6] a bad block or scale was met, [7] a masked row may meet a NaN value
+  int* infos = reinterpret_cast<int*>(sm + C::INFO_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+  // Phases count over all items of the CTA.
   uint64_t* kfull = bars;                  // [KS] K of a block is widened (96 arrivals)
   uint64_t* vfull = kfull + KS;            // [VS] V of a block is widened (96 arrivals)
-  // step i of the MMA warp: P V of block i - 1, then Q K^T of block i, of both tiles.  One
-  // commit per step frees K of block i and V of block i - 1.
-  uint64_t* done = vfull + VS;             // [DONE] the MMAs of a step have completed
-  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM, its scales in `scales`
+  // step n: P V of block n - 1, then Q K^T of block n.  One commit per step and tile frees K of
+  // block n and V of block n - 1.
+  uint64_t* done = vfull + VS;             // [DONE] both tiles' MMAs of a step have completed
+  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
-  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the tile's last P V has completed
-  uint64_t* qbar = pvdone + TC_TILES;      // Q of both tiles landed
-  uint64_t* qready = qbar + 1;             // bfloat16: Q is float16 now (256 arrivals)
-  uint64_t* drain = qready + 1;            // every MMA issued has completed
+  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the last P V of the tile's item has completed
+  uint64_t* qbar = pvdone + TC_TILES;      // [tile] Q of the tile's next item landed
+  uint64_t* qready = qbar + TC_TILES;      // [tile] bfloat16: it is float16 now (128 arrivals)
+  uint64_t* drain = qready + TC_TILES;     // [tile] every MMA issued has completed
+  uint64_t* turn = drain + TC_TILES;       // [tile] its MMA warp may issue the next step
+  uint64_t* ifull = turn + TC_TILES;      // [ITEMS] an item is published
+  uint64_t* scfull = ifull + C::ITEMS;     // [2] a group of scales is stored
+  uint64_t* scfree = scfull + 2;           // [2] it is read (one arrival per softmax warp)
+  uint64_t* cbar = scfree + 2;             // the answer about another CTA landed
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::SLOT_OFF);
-  volatile int* flags = reinterpret_cast<volatile int*>(sm + C::SLOT_OFF + 4);  // [0] bad block or scale, [1] timeout
 
-  // the longest pairs start first
-  const int pair = p.pairs - 1 - static_cast<int>(p.by_length ? blockIdx.z : blockIdx.x);
-  const int kvh = p.by_length ? blockIdx.x : blockIdx.y;
-  const int s = p.by_length ? blockIdx.y : blockIdx.z;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int G = p.group;
-  const int H = p.num_heads;
   const int tt = p.tile_tokens;
 
   grid_dependency_wait();  // the cache write before this launch has finished
 
-  const int q0 = __ldg(p.query_start_loc + s);
-  const int qlen = __ldg(p.query_start_loc + s + 1) - q0;
-  const int ctx = __ldg(p.context_lens + s);
-  const int cap = p.max_blocks_per_seq << p.log2_b;
-  const int ta = 2 * pair * tt;  // first new token of tile 0
-  if (ta >= qlen) {
+  PrefillItem it;
+  const int found = find_item(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it);
+  if (found <= 0) {
+    if (found < 0) write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
     allow_dependent_launch();
     return;
   }
-  const int ntiles = ta + tt < qlen ? 2 : 1;
-  const bool ctx_bad = ctx < qlen || ctx > cap;
-  const int base = ctx - qlen;
-  auto tile_end = [&](int u) { return min(qlen, ta + (u + 1) * tt); };
-  auto tile_blocks = [&](int u) { return ctx_bad ? 0 : (base + tile_end(u) + TC_KEYS - 1) / TC_KEYS; };
-  const int kend = ctx_bad ? 0 : base + tile_end(ntiles - 1);  // the K/V stream's last key + 1
-  const int nblk = tile_blocks(ntiles - 1);
+  auto load_q = [&](const PrefillItem& i, int u) {  // one thread
+    mbar_arrive_expect_tx(&qbar[u], C::QBYTES);
+    for (int db = 0; db < C::DBOX; ++db)
+      tma_load_3d(sm + u * C::QBYTES + db * C::QATOM, &p.tmap_q, db * BOX_DIMS, i.kvh * G, i.q0 + i.ta + u * tt, &qbar[u]);
+  };
+  auto publish = [&](const PrefillItem& i, int k) {  // one thread
+    int* f = infos + (k % C::ITEMS) * 8;
+    f[0] = i.s, f[1] = i.kvh, f[2] = i.ta, f[3] = i.q0, f[4] = i.qlen, f[5] = i.base, f[6] = 0, f[7] = 0;
+    mbar_arrive(&ifull[k % C::ITEMS]);
+  };
+  // Item k of the CTA, published.
+  auto item = [&](int k) -> PrefillItem {
+    const volatile int* f = infos + (k % C::ITEMS) * 8;
+    PrefillItem i;
+    i.s = f[0], i.kvh = f[1], i.ta = f[2], i.q0 = f[3], i.qlen = f[4], i.base = f[5];
+    return i;
+  };
+  // Waits for it; false past the last (or when the MMA warp gave up).
+  auto has_item = [&](int k) -> bool {
+    return __all_sync(FULL_MASK, tc_wait(&ifull[k % C::ITEMS], (k / C::ITEMS) & 1)) &&
+           *const_cast<const volatile int*>(infos + (k % C::ITEMS) * 8) >= 0;
+  };
+  auto read_item = [&](int k, PrefillItem& i) -> bool {
+    if (!has_item(k)) return false;
+    i = item(k);
+    return true;
+  };
 
   if (warp == C::MMA_WARP && lane == 0) {
-    for (int i = 0; i < KS; ++i) {
-      mbar_init(&kfull[i], C::PROD);
-    }
-    for (int i = 0; i < VS; ++i) {
-      mbar_init(&vfull[i], C::PROD);
-    }
-    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], 1);
+    for (int i = 0; i < KS; ++i) mbar_init(&kfull[i], C::PROD);
+    for (int i = 0; i < VS; ++i) mbar_init(&vfull[i], C::PROD);
+    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], TC_TILES);
     for (int i = 0; i < TC_TILES; ++i) {
-      mbar_init(&sfull[i], 2);
+      mbar_init(&sfull[i], 1);
       mbar_init(&pfull[2 * i], TC_ROWS);
       mbar_init(&pfull[2 * i + 1], TC_ROWS);
-      mbar_init(&pvdone[i], 1);
+      mbar_init(&pvdone[i], 2);
+      mbar_init(&qbar[i], 1);
+      mbar_init(&qready[i], TC_ROWS);
+      mbar_init(&drain[i], 1);
+      mbar_init(&turn[i], 1);
     }
-    mbar_init(qbar, 1);
-    mbar_init(qready, C::SOFT);
-    mbar_init(drain, 1);
-    flags[0] = 0;
-    flags[1] = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&scfull[i], 1);
+      mbar_init(&scfree[i], C::SOFT / 32);
+    }
+    for (int i = 0; i < C::ITEMS; ++i) mbar_init(&ifull[i], 1);
+    mbar_init(cbar, 1);
     fence_mbar_init();
-    if (nblk > 0) {
-      mbar_arrive_expect_tx(qbar, ntiles * C::QBYTES);
-      for (int u = 0; u < ntiles; ++u)
-        for (int db = 0; db < C::DBOX; ++db)
-          tma_load_3d(sm + u * C::QBYTES + db * C::QATOM, &p.tmap_q, db * BOX_DIMS, kvh * G, q0 + ta + u * tt, qbar);
-    }
+    for (int u = 0; u < it.tiles(tt); ++u) load_q(it, u);
+    publish(it, 0);
+    ask_for_cta(sm + C::RESP_OFF, cbar);
   }
-  if (warp >= C::PROD_WARP) {
+  if (warp >= C::PROD_WARP && warp < C::MMA_WARP) {
     // ------------------------------------------------ producers: K, then V of each block
+    set_max_regs<false, C::PROD_REGS>();
     const int pw = warp - C::PROD_WARP;
-    if (nblk == 0) {
-      __syncthreads();
-    } else {
-      constexpr int RG = 16;                              // groups of 8 rows per block
-      constexpr int NG = (RG + C::PROD_WARPS - 1) / C::PROD_WARPS;  // a warp's, at most
-      constexpr int HALVES = HEAD_DIM / 64;               // 64-code halves of a row
-      const int32_t* bt = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-      const int r8 = lane >> 2;  // four lanes per row: 64 codes of it per load
-      const int c = lane & 3;
-      const size_t row_bytes = static_cast<size_t>(p.num_kv_heads) * HEAD_DIM;
-      const uint8_t* khead = p.k_cache + static_cast<size_t>(kvh) * HEAD_DIM + c * 16;
-      const uint8_t* vhead = p.v_cache + static_cast<size_t>(kvh) * HEAD_DIM + c * 16;
-      const int bmask = (1 << p.log2_b) - 1;
-      // the warp's groups of K and of V: 6 + 5, 5 + 5 and 5 + 6
-      auto kg = [&](int i) { return pw + C::PROD_WARPS * i; };
-      auto vg = [&](int i) { return C::PROD_WARPS - 1 - pw + C::PROD_WARPS * i; };
-      int kph[NG], vph[NG];  // physical block of each row group (8 rows lie in one pool block)
-      // (a group past the last one is clamped, and not used)
-      auto fetch_k = [&](int j) {
+    constexpr int NG = 16 / C::PROD_WARPS;  // the warp's groups of 8 rows of a block
+    constexpr int HALVES = HEAD_DIM / 64;               // 64-code halves of a row
+    const int r8 = lane >> 2;  // four lanes per row: 64 codes of it per load
+    const int c = lane & 3;
+    const unsigned row_bytes = p.num_kv_heads * HEAD_DIM;
+    const int bmask = (1 << p.log2_b) - 1;
+    auto rg = [&](int i) { return pw + C::PROD_WARPS * i; };
+    uint4 kd[NG][HALVES], vd[NG][HALVES];
+    auto store = [&](const uint4 (&d)[HALVES], uint8_t* stage, int r) {
+      uint8_t* drow = stage + r * 128;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) kph[i] = __ldg(bt + (min(j * TC_KEYS + kg(i) * 8, kend - 1) >> p.log2_b));
+      for (int h = 0; h < HALVES; ++h) {
+        uint4 a, b;
+        widen16(d[h], a, b);
+        // unit u of row r sits at u ^ (r % 8): the eight lanes of two rows write eight different units
+        *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c) ^ (r & 7)) << 4)) = a;
+        *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
+      }
+    };
+    bool go = true;
+    int n = 0;  // blocks stored, over all items
+#pragma unroll 1
+    for (int k = 0; go; ++k) {
+      const int kend = it.kend(tt);
+      const int nblk = it.blocks(tt);
+      const int full = it.base + it.ta;  // every row of the item sees the keys up to this one
+      const int32_t* bt = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
+      const unsigned head = it.kvh * HEAD_DIM + c * 16;
+      // lane i: the physical block of row group i % 16 (8 rows lie in one pool block)
+      auto fetch = [&](int j) { return __ldg(bt + (min(j * TC_KEYS + (lane & 15) * 8, kend - 1) >> p.log2_b)); };
+      auto flag = [&](int f) { *const_cast<volatile int*>(infos + (k % C::ITEMS) * 8 + f) = 1; };
+      // the ids in hand, checked: never read outside the pool; the tiles' outputs become NaN
+      auto checked = [&](int id) {
+        use_here(id);
+        const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+        if (!in) flag(6);
+        return in ? id : 0;
       };
-      auto fetch_v = [&](int j) {
+      auto load = [&](uint4 (&d)[HALVES], const uint8_t* pool, int phys, int key) {
+        // (slots fit 31 bits)
+        const uint8_t* src = pool + (static_cast<size_t>((static_cast<unsigned>(phys) << p.log2_b) + (key & bmask)) * row_bytes + head);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) vph[i] = __ldg(bt + (min(j * TC_KEYS + vg(i) * 8, kend - 1) >> p.log2_b));
-      };
-      uint4 kd[NG][HALVES], vd[NG][HALVES];
-      bool bad = false;
-      auto load = [&](uint4 (&d)[HALVES], const uint8_t* head, int phys, int key) {
-        use_here(phys);
-        if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) {
-          bad = true;  // never read outside the pool; the tiles' outputs become NaN
-          phys = 0;
-        }
-        const uint8_t* src = head + ((static_cast<size_t>(phys) << p.log2_b) + (key & bmask)) * row_bytes;
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)  // rows past the stream's last key are zeros: 0 x NaN must not occur
+        for (int h = 0; h < HALVES; ++h)  // rows past the item's last key are zeros: 0 x NaN must not occur
           d[h] = key < kend ? ldg128(src + h * 64) : make_uint4(0u, 0u, 0u, 0u);
       };
-      auto store = [&](const uint4 (&d)[HALVES], uint8_t* stage, int r) {
-        uint8_t* drow = stage + r * 128;
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          uint4 a, b;
-          widen16(d[h], a, b);
-          // unit u of row r sits at u ^ (r % 8): the eight lanes of two rows write eight different units
-          *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c) ^ (r & 7)) << 4)) = a;
-          *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
-        }
-      };
-      fetch_k(0);
-      fetch_v(0);
+      int ids = checked(fetch(0));
+      int next = fetch(min(1, nblk - 1));
+      auto phys = [&](int g) { return __shfl_sync(FULL_MASK, ids, g & 15); };
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        if (kg(i) < RG) load(kd[i], khead, kph[i], kg(i) * 8 + r8);
-        if (vg(i) < RG) load(vd[i], vhead, vph[i], vg(i) * 8 + r8);
+        load(kd[i], p.k_cache, phys(rg(i)), rg(i) * 8 + r8);
+        load(vd[i], p.v_cache, phys(rg(i)), rg(i) * 8 + r8);
       }
-      fetch_k(min(1, nblk - 1));
-      fetch_v(min(1, nblk - 1));
       // (the first block's rows are on their way while the barriers and the tensor memory are set up)
-      __syncthreads();
-      for (int j = 0; j < nblk; ++j) {
-        const int kslot = j % KS;
-        const int vslot = j % VS;
-        // K's stage is free after step j - KS, V's after step j - VS + 1
-        const int step = max(j - KS, j - VS + 1);
+      if (k == 0) __syncthreads();
+#pragma unroll 1
+      for (int j = 0; j < nblk; ++j, ++n) {
+        const int kslot = n % KS;
+        const int vslot = n % VS;
+        // K's stage is free after step n - KS, V's after step n - VS + 1
+        const int step = max(n - KS, n - VS + 1);
         if (step >= 0 && !__all_sync(FULL_MASK, tc_wait(&done[step % C::DONE], (step / C::DONE) & 1))) {
-          flags[1] = 1;
+          go = false;
           break;
         }
+        ids = checked(next);
+        next = fetch(min(j + 2, nblk - 1));  // a whole block before their use
         uint8_t* kdst = sm + C::K_OFF + kslot * C::KBYTES;
         uint8_t* vdst = sm + C::V_OFF + vslot * C::KBYTES;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          if (kg(i) >= RG) continue;
-          store(kd[i], kdst, kg(i) * 8 + r8);
-          if (j + 1 < nblk) load(kd[i], khead, kph[i], (j + 1) * TC_KEYS + kg(i) * 8 + r8);
+          store(kd[i], kdst, rg(i) * 8 + r8);
+          if (j + 1 < nblk) load(kd[i], p.k_cache, phys(rg(i)), (j + 1) * TC_KEYS + rg(i) * 8 + r8);
         }
         fence_proxy_async_smem();  // the widened rows become visible to the tensor core
         mbar_arrive(&kfull[kslot]);
-        fetch_k(min(j + 2, nblk - 1));  // a whole block before their use
+        if ((j + 1) * TC_KEYS - 1 > full) {
+          // some row does not see some key here: its weight is 0, and 0 x NaN must not occur.
+          // NaN values enter as 0; the rows that see them get their NaN at the end.
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+  #pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(&vd[i][h]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t m = nan_codes(w[x]);
+                any |= m;
+                w[x] &= ~((m >> 7) * 0xffu);
+              }
+            }
+          }
+          if (any) flag(7);
+        }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          if (vg(i) >= RG) continue;
-          store(vd[i], vdst, vg(i) * 8 + r8);
-          if (j + 1 < nblk) load(vd[i], vhead, vph[i], (j + 1) * TC_KEYS + vg(i) * 8 + r8);
+          store(vd[i], vdst, rg(i) * 8 + r8);
+          if (j + 1 < nblk) load(vd[i], p.v_cache, phys(rg(i)), (j + 1) * TC_KEYS + rg(i) * 8 + r8);
         }
         fence_proxy_async_smem();
         mbar_arrive(&vfull[vslot]);
-        fetch_v(min(j + 2, nblk - 1));
       }
-      if (bad) flags[0] = 1;  // read after the barrier below
+      go = go && read_item(k + 1, it);
     }
-    // the producers meet the softmax warps at their two barriers
-    __syncthreads();
     __syncthreads();
     allow_dependent_launch();
     return;
@@ -349,205 +535,319 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   tc_fence_after_sync();
   const uint32_t tmem = *tslot;
 
-  if (warp == C::MMA_WARP) {
-    // ------------------------------------------------ MMA issue
-    // The whole warp runs this loop and one elected lane issues: every value stays uniform, so
-    // descriptors sit in uniform registers (with one lane in a branch of its own each MMA paid
-    // for moving its operands there, and the 16 MMAs of a tile and block took 2000 cycles to issue).
-    if (nblk > 0) {
-      int nbt[TC_TILES];
-      for (int u = 0; u < TC_TILES; ++u) nbt[u] = u < ntiles ? tile_blocks(u) : 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL_MASK, tc_wait(bar, parity)) != 0; };
-      int k_seen = -1;
-      auto wait_k = [&](int j) -> bool {
-        if (j <= k_seen) return true;
-        if (!wait(&kfull[j % KS], (j / KS) & 1)) return false;
-        k_seen = j;
-        tc_fence_after_sync();
-        return true;
-      };
-      const uint64_t dq = umma_desc_sw128(smem_addr(sm), 16, 1024);                    // Q, K-major
+  if (warp >= C::MMA_WARP) {
+    set_max_regs<false, C::MMA_REGS>();
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(FULL_MASK, tc_wait(bar, parity)) != 0; };
+    if (warp < C::ITEM_WARP) {
+      // ---------------------------------------------- MMA issue: warp u, tile u
+      // A warp per tile: one for both spent 3100 cycles a step in its waits and issues.  The whole warp runs the loop and one elected lane
+      // issues: every value stays uniform, so descriptors sit in uniform registers (with one lane
+      // in a branch of its own the 16 MMAs of a tile and block took 2000 cycles to issue).
+      const int u = __shfl_sync(FULL_MASK, warp - C::MMA_WARP, 0);
+      const uint64_t dq = umma_desc_sw128(smem_addr(sm + u * C::QBYTES), 16, 1024);    // Q, K-major
       const uint64_t dk = umma_desc_sw128(smem_addr(sm + C::K_OFF), 16, 1024);         // K, K-major
       const uint64_t dv = umma_desc_sw128(smem_addr(sm + C::V_OFF), C::KATOM, 1024);   // V, MN-major
-      auto qk = [&](int u, int j) {
-        const uint64_t qu = umma_desc_add(dq, u * C::QBYTES);
-        const uint64_t kj = umma_desc_add(dk, (j % KS) * C::KBYTES);
+      const uint32_t tP = tmem + 256 * u;
+      const uint32_t tO = tP + 128;
+      // stages of the next block's K and of the current one's V, parities of the phases
+      int kslot = 0, vslot = 0, dslot = 0;
+      uint32_t kpar = 0, vpar = 0, spar = 0, ppar = 0, qpar = 0, tpar = u ^ 1;
+      // Three barriers at once, a lane each: the waits cost a hundred cycles together, not each.
+      // (A test, not a wait that suspends: that one sleeps past the completion of one lane's
+      // barrier while another lane's is open.)  The limit is some seconds.
+      auto wait3 = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2) -> bool {
+        uint64_t* b = lane == 0 ? b0 : lane == 1 ? b1 : b2;
+        const uint32_t par = lane == 0 ? p0 : lane == 1 ? p1 : p2;
+#pragma unroll 1
+        for (int i = 0; i < 1 << 26; ++i)
+          if (__all_sync(FULL_MASK, mbar_test(b, par))) return true;
+        return false;
+      };
+      auto qk = [&]() {
+        const uint64_t kj = umma_desc_add(dk, kslot * C::KBYTES);
 #pragma unroll
         for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
           const uint32_t off = (ks >> 2) * C::QATOM + ((ks & 3) << 5);
           const uint32_t koff = (ks >> 2) * C::KATOM + ((ks & 3) << 5);
-          umma_f16_elect(tmem + 256 * u, umma_desc_add(qu, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
+          umma_f16_elect(tP, umma_desc_add(dq, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
         }
-        if (lane == 0) mbar_arrive(&sfull[u]);
+      };
+      auto first_qk = [&]() -> bool {  // of an item
+        uint64_t* q = BF16 ? &qready[u] : &qbar[u];
+        if (!wait3(q, qpar, q, qpar, &kfull[kslot], kpar)) return false;
+        tc_fence_after_sync();
+        qpar ^= 1;
+        qk();
         umma_commit_elect(&sfull[u]);
+        return true;
       };
-      // Scales of each block's 16-key chunks, lanes 0-7: read two blocks before their use, their
-      // physical block's id three before.  Row b % VS is free for block b once the softmax of
-      // block b - VS is over, which this warp has waited for.  (A producer warp that carried the
-      // scales too waited for its latest row loads at each, 900 cycles a block.)
-      const int32_t* bt = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-      float sk = 0.f, sv = 0.f;
-      int sph = 0;
-      auto scale_fetch = [&](int j) {
-        if (lane < C::CHUNKS) sph = __ldg(bt + (min(j * TC_KEYS + lane * CHUNK, kend - 1) >> p.log2_b));
+      auto end_step = [&]() {
+        umma_commit_elect(&done[dslot]);
+        dslot = dslot + 1 == C::DONE ? 0 : dslot + 1;
+        kpar ^= kslot + 1 == KS;
+        kslot = kslot + 1 == KS ? 0 : kslot + 1;
       };
-      auto scale_load = [&]() {  // (chunks past the stream repeat its last one: their keys are masked)
-        use_here(sph);
-        if (lane < C::CHUNKS) {
-          const bool in = static_cast<unsigned>(sph) < static_cast<unsigned>(p.num_blocks);
-          const size_t at = static_cast<size_t>(in ? sph : 0) * p.num_kv_heads + kvh;
-          sk = __ldg(p.k_scales + at);
-          sv = __ldg(p.v_scales + at);
+      // The tiles' MMAs take turns, so that one tile's run under the other's softmax: issued as
+      // they become ready, the two tiles' interleave, end together and leave the tensor cores idle
+      // while both wait for weights (2 x 16384: 3244 us against 2973).
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(&turn[u ^ 1]);
+        __syncwarp();
+      };
+      // P V of the current block in the tile's turn, and Q K^T of the next one; first: the item's
+      // first block, last: the tile's last one
+      auto step = [&](bool first, bool last) -> bool {
+        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &pfull[2 * u], ppar)) return false;
+        tpar ^= 1;
+        tc_fence_after_sync();
+        const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
+        // the first 64 keys while the softmax writes the weights of the others
+#pragma unroll
+        for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
+          umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, !first || kk > 0);
+        uint64_t* p1 = &pfull[2 * u + 1];
+        if (!wait3(p1, ppar, p1, ppar, last ? p1 : &kfull[kslot], last ? ppar : kpar)) return false;
+        ppar ^= 1;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
+          umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
+        if (!last) qk();
+        pass_turn();
+        if (last) {
+          if (lane == 0) mbar_arrive(&pvdone[u]);
+          umma_commit_elect(&pvdone[u]);
+        } else {
+          umma_commit_elect(&sfull[u]);
+          spar ^= 1;
         }
+        return true;
       };
-      auto scale_store = [&](int j) {
-        use_here(sk);
-        use_here(sv);
-        if (lane < C::CHUNKS) {
-          if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax)) flags[0] = 1;
+      // a step of the item in which the tile has no block: at the pace of the other tile
+      auto no_step = [&]() -> bool {
+        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &vfull[vslot], vpar)) return false;
+        tpar ^= 1;
+        pass_turn();
+        return true;
+      };
+      auto next_v = [&]() {
+        vpar ^= vslot + 1 == VS;
+        vslot = vslot + 1 == VS ? 0 : vslot + 1;
+      };
+      int nb, nblk;  // blocks of the tile and of the item
+      auto lengths = [&](const PrefillItem& i) {
+        nb = __shfl_sync(FULL_MASK, i.tile_blocks(u, tt), 0);
+        nblk = __shfl_sync(FULL_MASK, i.blocks(tt), 0);
+      };
+      lengths(it);
+      bool ok = nb == 0 || first_qk();
+      if (ok) end_step();
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        // all blocks but the item's last
+#pragma unroll 1
+        for (int j = 0; j + 1 < nblk; ++j) {
+          ok = j < nb ? step(j == 0, j + 1 == nb) : no_step();
+          if (!ok) break;
+          end_step();
+          next_v();
+        }
+        if (!ok) break;
+        // the last one, and Q K^T of the next item's first
+        const bool more = has_item(k + 1);
+        const int last_nb = nb, last = nblk - 1;
+        if (more) lengths(item(k + 1));
+        if (more && nb > 0) {
+          if (last_nb > 0) ok = wait(&sfull[u], spar);  // the tile's last S is there: its Q has been read
+          if (!ok) break;
+          if (lane == 0) load_q(item(k + 1), u);
+          __syncwarp();
+        }
+        ok = last < last_nb ? step(last == 0, true) : no_step();
+        if (!ok) break;
+        if (last_nb > 0) spar ^= 1;
+        if (!more) break;
+        if (nb > 0) {
+          ok = first_qk();
+          if (!ok) break;
+        }
+        end_step();
+        next_v();
+      }
+      umma_commit_elect(&drain[u]);  // every MMA finishes before the TMEM is released
+      wait(&drain[u], 0);
+      tc_fence_before_sync();
+    } else if (warp == C::ITEM_WARP) {
+      // ---------------------------------------------- items and scales
+      // Items are asked for one ahead of their use, and published at once.
+      int asked = 0, published = 1;
+      bool open = true;  // an answer is on its way
+      auto next_item = [&](PrefillItem& i) -> bool {
+        while (open) {
+          if (!wait(cbar, asked & 1)) {
+            open = false;
+            break;
+          }
+          ++asked;
+          uint3 id;
+          open = cta_given(sm + C::RESP_OFF, id);
+          __syncwarp();  // every lane has read the answer
+          if (!open) break;
+          if (lane == 0) {
+            fence_proxy_async_smem();
+            ask_for_cta(sm + C::RESP_OFF, cbar);
+          }
+          const int f = find_item(p, id, i);
+          if (f < 0) write_nan_rows<T, HEAD_DIM>(p, i, lane, 32);
+          if (f > 0) return true;
+        }
+        return false;
+      };
+      // Scales of the blocks' 16-key chunks, four blocks (a lane per chunk) at a time, one such
+      // group ahead of the softmax.
+      bool ok = true;
+#pragma unroll 1
+      for (int g = 0, n = 0; ok; ++n) {
+        const int32_t* bt = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
+        const int nblk = it.blocks(tt);
+        const int kend = it.kend(tt);
+#pragma unroll 1
+        for (int b = 0; b < nblk; b += C::GROUP, ++g) {
+          // (chunks past the item's last key repeat the last one: their keys are masked)
+          const int phys = __ldg(bt + (min(b * TC_KEYS + lane * CHUNK, kend - 1) >> p.log2_b));
+          const bool in = static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_blocks);
+          const size_t at = static_cast<size_t>(in ? phys : 0) * p.num_kv_heads + it.kvh;
+          const float sk = __ldg(p.k_scales + at);
+          const float sv = __ldg(p.v_scales + at);
+          if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax))
+            *const_cast<volatile int*>(infos + (n % C::ITEMS) * 8 + 6) = 1;
           // a factor of 0 would turn a masked score (-inf) into NaN: 2^-120 makes 0 of every score
           float a = sk * p.scale_log2;
           a = fabsf(a) >= 7.52316384526264e-37f ? a : copysignf(7.52316384526264e-37f, p.scale_log2);
           const float lv = __log2f(fmaxf(sv, 5.421010862427522e-20f));  // at least 2^-64
-          scales[(j % VS) * C::CHUNKS + lane] = make_float4(a, lv, ex2(-lv), 0.f);
-        }
-        __syncwarp();  // lane 0's next arrival on sfull releases them
-      };
-      static_assert(VS >= 3, "two blocks' scales ahead");
-      scale_fetch(0);
-      scale_load();
-      scale_fetch(1);
-      scale_store(0);
-      scale_load();
-      scale_fetch(2);
-      bool ok = wait(BF16 ? qready : qbar, 0) && wait_k(0);
-      if (ok) {
-        for (int u = 0; u < ntiles; ++u) qk(u, 0);
-        umma_commit_elect(&done[0]);
-      }
-      if (nblk > 1) scale_store(1);
-      scale_load();
-      scale_fetch(3);
-      for (int j = 0; ok && j < nblk; ++j) {
-        const int vslot = j % VS;
-        bool have_v = false;
-        for (int u = 0; u < ntiles; ++u) {
-          // while the last tile's weights are awaited, and while the producers are quiet: behind
-          // the commit below their loads crowd the queue, and this warp's waited 900 cycles
-          if (u == ntiles - 1 && j + 2 < nblk) {
-            scale_store(j + 2);
-            scale_load();
-            scale_fetch(j + 4);
-          }
-          if (j >= nbt[u]) continue;
-          ok = wait(&pfull[2 * u], j & 1) && (have_v || wait(&vfull[vslot], (j / VS) & 1));
+          const float4 v = make_float4(a, lv, ex2(-lv), 0.f);
+          ok = g < 2 || wait(&scfree[g & 1], ((g >> 1) - 1) & 1);
           if (!ok) break;
-          have_v = true;
-          tc_fence_after_sync();
-          const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
-          const uint32_t tP = tmem + 256 * u;
-          const uint32_t tO = tP + 128;
-          // the first 64 keys while the softmax writes the weights of the others
-#pragma unroll
-          for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
-            umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, j > 0 || kk > 0);
-          ok = wait(&pfull[2 * u + 1], j & 1);
-          if (!ok) break;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
-            umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
-          if (j + 1 < nbt[u]) {
-            ok = wait_k(j + 1);
-            if (!ok) break;
-            qk(u, j + 1);
-          } else {
-            umma_commit_elect(&pvdone[u]);
-          }
+          scales[(g & 1) * 32 + lane] = v;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scfull[g & 1]);
         }
-        if (!ok) break;
-        umma_commit_elect(&done[(j + 1) % C::DONE]);
+        if (!ok || !next_item(it)) break;
+        if (lane == 0) publish(it, published);
+        __syncwarp();
+        ++published;
       }
-      if (!ok) flags[1] = 1;
-      umma_commit_elect(drain);  // every MMA finishes before the TMEM is released
-      if (!wait(drain, 0)) flags[1] = 1;
+      if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
+        uint3 id;
+        if (cta_given(sm + C::RESP_OFF, id) && find_item(p, id, it) != 0) write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
+      }
+      it.s = -1;
+      if (lane == 0) publish(it, published);
     }
-  } else {
-    // ------------------------------------------------ softmax: warps 4 u .. 4 u + 3 run tile u
-    const int u = warp >> 2;
-    const int r = 32 * (warp & 3) + lane;
-    const bool tile_on = u < ntiles;
-    const int t0 = ta + u * tt;
-    const int t = t0 + (r >> p.log2_g);
-    const bool rv = tile_on && t < tile_end(u);
-    const int pos = rv ? base + t : -1;
-    const int nb = tile_on ? tile_blocks(u) : 0;
-    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tS = tmem + 256 * u + lane_off;
-    const uint32_t tO = tS + 128;
+    __syncthreads();
+    allow_dependent_launch();
+    return;
+  }
+  // ------------------------------------------------ softmax: warps 4 u .. 4 u + 3 run tile u
+  set_max_regs<true, C::SOFT_REGS>();
+  const int u = warp >> 2;
+  const int r = 32 * (warp & 3) + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const uint32_t tS = tmem + 256 * u + lane_off;
+  const uint32_t tO = tS + 128;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(FULL_MASK, tc_wait(bar, parity));
+  };
+  // What changes from block to block and item to item, in one register (x[] below takes 128, and
+  // a spilled register makes every arrival wait for local memory: 282 -> 370 us): [2:0] the
+  // item's number, [4:3] the block's place in its group of scales, [6:5] the group's number,
+  // parities of [7] the tile's blocks, [8] its items, [9] its Q.
+  uint32_t st = 0;
+  // bfloat16: Q of the tile's next item as float16, each row scaled by a power of two whose
+  // inverse is returned
+  auto convert_q = [&](const PrefillItem& i) -> float {
+    if (u >= i.tiles(tt)) return 1.f;
+    wait(&qbar[u], (st >> 9) & 1);
+    st ^= 1u << 9;
+    float f = 1.f, back = 1.f;
+    if (ok) {
+      uint4* row = reinterpret_cast<uint4*>(sm + u * C::QBYTES + r * 128);
+      constexpr int AT = C::QATOM / 16;
+      float amax = 0.f;
+#pragma unroll 4
+      for (int x = 0; x < HEAD_DIM / 8; ++x) {
+        const uint4 v = row[(x >> 3) * AT + ((x + lane) & 7)];  // lanes start at different units: no bank conflict
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 z = unpack_bf162(w[y]);
+          amax = fmaxf(amax, fmaxf(fabsf(z.x), fabsf(z.y)));
+        }
+      }
+      const int e = min(14 - ((__float_as_int(amax) >> 23) - 127), 126);
+      f = pow2f(e);
+      back = pow2f(-e);
+#pragma unroll 4
+      for (int x = 0; x < HEAD_DIM / 8; ++x) {
+        uint4* at = row + (x >> 3) * AT + ((x + lane) & 7);
+        const uint4 v = *at;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 z = unpack_bf162(w[y]);
+          o[y] = pack_half2(z.x * f, z.y * f);
+        }
+        *at = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&qready[u]);
+    return back;
+  };
+  // A negative `scale` turns the order of the scores around: the largest product is then
+  // the smallest score times the (negative) factor.
+  const bool neg = p.scale_log2 < 0.f;
+  const float hidden = neg ? INFINITY : -INFINITY;
+  auto next_group = [&]() {  // the warp has read its group of scales
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&scfree[(st >> 5) & 1]);
+    st = (st & ~(15u << 3)) | ((st + (1u << 5)) & (3u << 5));
+  };
+  float qinv = 1.f;  // bfloat16: undoes the row's scaling
+  if constexpr (BF16) qinv = convert_q(it);
+#pragma unroll 1
+  for (;;) {
+    int left, seen;  // the tile's blocks to come; the keys of the block that all its rows see, minus one
+    {
+      const PrefillItem i = item(st & 7);
+      left = i.tile_blocks(u, tt);
+      seen = i.base + i.ta + u * tt;
+    }
     float m_used = -INFINITY, l = 0.f;  // log2 units, the value scale's exponent included
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(FULL_MASK, tc_wait(bar, parity));
-    };
-    float qinv = 1.f;  // bfloat16: undoes the row's scaling
-    if constexpr (BF16) {
-      if (nblk > 0) {
-        wait(qbar, 0);
-        if (ok && tile_on) {
-          uint4* row = reinterpret_cast<uint4*>(sm + u * C::QBYTES + r * 128);
-          constexpr int AT = C::QATOM / 16;
-          float amax = 0.f;
-#pragma unroll
-          for (int i = 0; i < HEAD_DIM / 8; ++i) {
-            const uint4 v = row[(i >> 3) * AT + ((i + lane) & 7)];  // lanes start at different units: no bank conflict
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = unpack_bf162(w[k]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          const int e = min(14 - ((__float_as_int(amax) >> 23) - 127), 126);
-          const float f = pow2f(e);
-          qinv = pow2f(-e);
-#pragma unroll
-          for (int i = 0; i < HEAD_DIM / 8; ++i) {
-            uint4* at = row + (i >> 3) * AT + ((i + lane) & 7);
-            const uint4 v = *at;
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 x2 = unpack_bf162(w[k]);
-              o[k] = pack_half2(x2.x * f, x2.y * f);
-            }
-            *at = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(qready);
-      }
-    }
-    // A negative `scale` turns the order of the scores around: the largest product is then
-    // the smallest score times the (negative) factor.
-    const bool neg = p.scale_log2 < 0.f;
-    const float hidden = neg ? INFINITY : -INFINITY;
     uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
-    for (int j = 0; j < nb; ++j) {
-      wait(&sfull[u], j & 1);
+#pragma unroll 1
+    for (; left > 0; --left, seen -= TC_KEYS) {
+      if ((st & (3u << 3)) == 0) wait(&scfull[(st >> 5) & 1], (st >> 6) & 1);
+      wait(&sfull[u], (st >> 7) & 1);
       tc_fence_after_sync();
 #pragma unroll
       for (int c = 0; c < TC_KEYS / 16; ++c) tmem_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
       tmem_wait_ld();
-      const int k0 = j * TC_KEYS;
-      if (k0 + TC_KEYS - 1 > base + t0) {  // a key here may lie past some row of the tile
+      if (seen < TC_KEYS - 1) {  // a key here may lie past some row of the tile
+        const int own = seen + (r >> p.log2_g);  // (rows past the item's end are not written)
+        const int all = seen + ((r & ~31) >> p.log2_g);
 #pragma unroll
-        for (int c = 0; c < TC_KEYS; ++c)
-          if (k0 + c > pos) x[c] = __float_as_uint(hidden);
+        for (int c = 0; c < TC_KEYS; c += 16) {
+          if (c + 15 <= all) continue;  // the whole warp sees the chunk
+#pragma unroll
+          for (int i = c; i < c + 16; ++i)
+            if (i > own) x[i] = __float_as_uint(hidden);
+        }
       }
       // the row's maximum: per chunk of raw scores (the factor is the same), then one fma each
-      const float4* sc = scales + (j % VS) * C::CHUNKS;
+      const float4* sc = scales + ((st >> 3) & 7u) * C::CHUNKS;
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C::CHUNKS; ++c) {
@@ -566,19 +866,20 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       const float m_new = fmaxf(m_used, mx);
       // The exponent's offset moves at the first block and when the row maximum has grown
       // by more than 2^8; O and l then scale by f.
-      const bool need = j > 0 && m_new > m_used + TC_RESCALE_LOG2;
+      const bool none = m_used == -INFINITY;  // nothing in O yet
+      const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
       const float f = need ? ex2(m_used - m_new) : 1.f;
-      if (j == 0 || need) m_used = m_new;
+      if (none || need) m_used = m_new;
       const float bias = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
       if (__any_sync(FULL_MASK, need)) {
 #pragma unroll 1
-        for (int c = 0; c < DO; c += 16) {
-          uint32_t o16[16];
-          tmem_ld16(tO + c, o16);
+        for (int c = 0; c < DO; c += 8) {  // (eight at a time: the scores hold 128 registers)
+          uint32_t o8[8];
+          tmem_ld8(tO + c, o8);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(__uint_as_float(o16[i]) * f);
-          tmem_st16(tO + c, o16);
+          for (int i = 0; i < 8; ++i) o8[i] = __float_as_uint(__uint_as_float(o8[i]) * f);
+          tmem_st8(tO + c, o8);
         }
       }
       l *= f;
@@ -608,68 +909,104 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         tc_fence_before_sync();
         mbar_arrive(&pfull[2 * u + h]);
       }
+      st ^= 1u << 7;
+      if ((st & (3u << 3)) == (3u << 3) || left == 1) {
+        next_group();
+      } else {
+        st += 1u << 3;
+      }
+    }
+    const PrefillItem i = item(st & 7);  // (read again: held over the loop it would cost registers there)
+    const volatile int* flags = infos + (st % C::ITEMS) * 8 + 6;
+    // groups of scales that only the other tile needs
+    for (int b = (i.tile_blocks(u, tt) + C::GROUP - 1) / C::GROUP * C::GROUP; b < i.blocks(tt); b += C::GROUP) {
+      wait(&scfull[(st >> 5) & 1], (st >> 6) & 1);
+      next_group();
+    }
+    st = (st & ~7u) | ((st + 1) & 7u);
+    float qinv_next = 1.f;
+    if constexpr (BF16) {  // before the outputs: the next item's first MMAs wait for nothing else
+      if (has_item(st & 7)) qinv_next = convert_q(item(st & 7));
     }
     // ------------------------------------------------ O / l
-    if (nb > 0) wait(&pvdone[u], 0);
-    const bool have = ok && nb > 0;
-    if (!ok) flags[1] = 1;
-    __syncthreads();  // the other warps' flags are visible past this point
-    tc_fence_after_sync();
-    // O / l through the tile's Q rows in shared memory (its MMAs are over): a thread holds one
-    // row, and rows of different tokens are far apart in `out`, so writing them from here
-    // would touch 32 lines per store.  A warp turns its own 32 rows (6300 -> 1900 cycles per CTA).
-    const float inv = (!have || ctx_bad || flags[0] || flags[1]) ? NAN : 1.f / l;
-    if (nb > 0) {
-      uint8_t* qrow = sm + u * C::QBYTES + r * 128;
+    if (u < i.tiles(tt)) {
+      wait(&pvdone[u], (st >> 8) & 1);
+      st ^= 1u << 8;
+      tc_fence_after_sync();
+      const float inv = !ok || flags[0] ? NAN : 1.f / l;
+      const bool nans = flags[1];
+      const int t0 = i.ta + u * tt;
+      const int t_end = i.tile_end(u, tt);
+      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
+      // exchange their units, so that a store writes 64 bytes of each of eight rows, not 16 of 32
+      // (which took 6300 cycles per item; through shared memory, which the next item's Q needs, 1900).
+      int row = r;
+      use_here(row);  // (what follows from it is not worth registers in the blocks' loop)
 #pragma unroll 1
-      for (int h = 0; h < DO / 64; ++h) {  // one 64-dim atom at a time
+      for (int h = 0; h < DO / 64; ++h) {  // 64 dims at a time
         uint32_t o[64];
-        if (have) {
+        if (ok) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld16(tO + 64 * h + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
           tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) o[c] = 0u;
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t w4[4];
+        for (int c = 0; c < 32; ++c)
+          o[c] = pack2<T>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+        const int pos = t0 + (row >> p.log2_g) < t_end ? i.base + t0 + (row >> p.log2_g) : -1;
+        if (nans) {  // rare: look for the NaN values that the row sees among the item's last blocks
+          uint32_t mask[2] = {0u, 0u};
+#pragma unroll 1
+          for (int key = (i.base + i.ta + 1) / TC_KEYS * TC_KEYS; key <= pos; ++key) {
+            const int phys = __ldg(p.block_tables + static_cast<size_t>(i.s) * p.max_blocks_per_seq + (key >> p.log2_b));
+            if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;  // NaN all over already
+            const uint8_t* at = p.v_cache + ((((static_cast<size_t>(phys) << p.log2_b) + (key & ((1 << p.log2_b) - 1))) *
+                                              p.num_kv_heads + i.kvh) * HEAD_DIM + 64 * h);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w4[i] = have ? pack2<T>(__uint_as_float(o[8 * c + 2 * i]) * inv, __uint_as_float(o[8 * c + 2 * i + 1]) * inv)
-                         : pack2<T>(NAN, NAN);
-          *reinterpret_cast<uint4*>(qrow + h * C::QATOM + ((c ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            for (int c = 0; c < 4; ++c) {
+              const uint4 v = ldg128(at + 16 * c);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t m = nan_codes(w[y]);
+                mask[c >> 1] |= (((m >> 7) & 1u) | ((m >> 14) & 2u) | ((m >> 21) & 4u) | ((m >> 28) & 8u)) << (16 * (c & 1) + 4 * y);
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t m = mask[c >> 4] >> (2 * (c & 15));
+            o[c] |= (m & 1u ? 0x7fffu : 0u) | (m & 2u ? 0x7fff0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint4 a[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            a[c] = make_uint4(o[16 * b + 4 * c], o[16 * b + 4 * c + 1], o[16 * b + 4 * c + 2], o[16 * b + 4 * c + 3]);
+          transpose4(a, row);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int rr = (row & ~3) + c;
+            const int tr = t0 + (rr >> p.log2_g);
+            if (tr < t_end)
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
+                                        (static_cast<size_t>(i.q0 + tr) * p.num_heads + i.kvh * G + (rr & (G - 1))) * HEAD_DIM +
+                                        64 * h + 32 * b + 8 * (row & 3)) = a[c];
+          }
         }
       }
-      __syncwarp();
     }
-    if (tile_on) {  // rows in order, DO / 8 lanes of 16 bytes each
-      constexpr int U = DO / 8;
-      constexpr int RPI = 32 / U;
-      const int unit = lane % U;
-      const int rw = 32 * (warp & 3);
-      const int t_end = tile_end(u);
-#pragma unroll 4
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int rr = rw + i * RPI + lane / U;
-        const int tr = t0 + (rr >> p.log2_g);
-        if (tr < t_end) {
-          const uint4 v = nb > 0 ? *reinterpret_cast<const uint4*>(sm + u * C::QBYTES + rr * 128 + (unit >> 3) * C::QATOM +
-                                                                   (((unit & 7) ^ (rr & 7)) << 4))
-                                 : make_uint4(pack2<T>(NAN, NAN), pack2<T>(NAN, NAN), pack2<T>(NAN, NAN), pack2<T>(NAN, NAN));
-          *reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
-                                    (static_cast<size_t>(q0 + tr) * H + kvh * G + (rr & (G - 1))) * HEAD_DIM + unit * 8) = v;
-        }
-      }
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
-    allow_dependent_launch();
-    return;
+    qinv = qinv_next;
+    if (!has_item(st & 7)) break;
   }
-  // the MMA warp meets the softmax warps at their two barriers
   tc_fence_before_sync();
   __syncthreads();
-  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
   allow_dependent_launch();
 }
 

@@ -273,3 +273,48 @@ def test_prefill_rows_behind_the_last_sequence_are_left_alone():
     api.pa_prefill_fp8_block(out, q, kc, vc, ks, vs, bt, cl, qs, 60, b.scale)
     torch.cuda.synchronize()
     assert (out[93:] == 3.0).all() and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prefill_with_more_work_than_the_gpu_holds(dtype):
+    """768 (sequence, KV head, pair of tiles): most CTAs compute several, of all lengths, among them
+    sequences without new tokens and with a context length that cannot be."""
+    g = np.random.default_rng(31)
+    lens = [int(x) for x in g.integers(1, 400, 48)]
+    new = [min(n, int(x)) for n, x in zip(lens, g.integers(0, 256, 48))]
+    new[3], lens[3], new[40], lens[40] = 256, 700, 1, 900
+    b = Batch(lens, 16, 4, 64, 16, dtype, 32, new=new).poison()
+    ref, tol = b.prefill_reference()
+    bad = [i for i in (7, 30) if new[i] > 0]
+    b.lens[torch.tensor(bad)] = 0
+    o = run_prefill(b)
+    r = b.starts.tolist()
+    for i in bad:
+        assert torch.isnan(o[r[i]:r[i + 1]]).all()
+        ref[r[i]:r[i + 1]], o[r[i]:r[i + 1]] = 0, 0
+    assert_close(o, ref, tol)
+    assert torch.equal(run_prefill(b)[:r[7]], o[:r[7]])  # whichever CTA computes a row, its bits are the same
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prefill_nan_values_reach_only_the_rows_that_see_them(dtype, dim):
+    """A NaN code in a new token's value: the token and those behind it get NaN in that channel of
+    that head; the tokens before it, whose weight for it is 0, keep their bits."""
+    b = Batch([300, 131, 70], 8, 2, dim, 16, dtype, 33, new=[190, 131, 3])
+    at = [(0, 109, 0, 5), (0, 131, 1, 40), (0, 298, 0, 63), (1, 0, 1, 0), (1, 127, 0, dim - 1), (1, 128, 0, 17), (2, 68, 1, 33),
+          (0, 20, 0, 9)]
+    want = None
+    for code in (0, 0x7f, 0xff):
+        for s, p, h, c in at:
+            b.vc[int(b.tables[s, p // b.B]), p % b.B, h, c] = code
+        o = run_prefill(b)
+        if want is None:
+            want = o
+            continue
+        exp, r = want.clone(), b.starts.tolist()
+        for s, p, h, c in at:
+            row = max(r[s], r[s + 1] - b.lens_list[s] + p)  # of the token itself (a cached one: every row)
+            exp[row:r[s + 1], 4 * h:4 * h + 4, c] = float("nan")
+        assert torch.isnan(exp).any() and torch.equal(torch.isnan(o), torch.isnan(exp))
+        assert torch.equal(torch.nan_to_num(o), torch.nan_to_num(exp))
