@@ -24,9 +24,9 @@
 //  - 128 scores per softmax thread leave 40 registers for the rest.  The launch's
 //    512 x 128 registers are shared out: 168 a softmax thread, 112 a producer, 64 the
 //    others; nothing spills.
-// Measured (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of 2048 tokens 235 us,
-// 2 of 16384 2973 us (0.78 of the measured peak), 16 x 512 on 16384 cached 1547 us;
-// bf16, 16 chunks of 509 on 1536 cached 206 us.  One CTA per pair, one MMA warp for
+// Measured (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of 2048 tokens 227 us,
+// 2 of 16384 2974 us (0.78 of the measured peak), 16 x 512 on 16384 cached 1546 us;
+// bf16, 16 chunks of 509 on 1536 cached 201 us.  One CTA per pair, one MMA warp for
 // both tiles: 282, 3005, 1584 and 230 us.
 //
 // The mathematics of the scales is that of pa_block_decode.cuh: with v_b the
@@ -841,9 +841,11 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
 #pragma unroll
         for (int c = 0; c < TC_KEYS; c += 16) {
           if (c + 15 <= all) continue;  // the whole warp sees the chunk
+          const int k = own - c;  // visible keys of the chunk, minus one
+          const uint32_t m = k < 0 ? 0u : k > 15 ? ~0u : (2u << k) - 1u;
 #pragma unroll
-          for (int i = c; i < c + 16; ++i)
-            if (i > own) x[i] = __float_as_uint(hidden);
+          for (int i = 0; i < 16; ++i)
+            if (!(m >> i & 1u)) x[c + i] = __float_as_uint(hidden);
         }
       }
       // the row's maximum: per chunk of raw scores (the factor is the same), then one fma each
@@ -935,70 +937,59 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       tc_fence_after_sync();
       const float inv = !ok || flags[0] ? NAN : 1.f / l;
       const bool nans = flags[1];
-      const int t0 = i.ta + u * tt;
-      const int t_end = i.tile_end(u, tt);
       // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
-      // exchange their units, so that a store writes 64 bytes of each of eight rows, not 16 of 32
-      // (which took 6300 cycles per item; through shared memory, which the next item's Q needs, 1900).
+      // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows (a
+      // thread's own 32 bytes a store took 229 us against 227).  The loop is short because its code runs
+      // once per item: unrolled it waited for instructions (235 us).
       int row = r;
       use_here(row);  // (what follows from it is not worth registers in the blocks' loop)
+      const int t0 = i.ta + u * tt;
+      const int t_end = i.tile_end(u, tt);
+      const int t = t0 + (row >> p.log2_g);
+      T* at[4];
+      bool on[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int rr = (row & ~3) + x;
+        on[x] = t0 + (rr >> p.log2_g) < t_end;
+        at[x] = static_cast<T*>(p.out) + (static_cast<size_t>(i.q0 + t0 + (rr >> p.log2_g)) * p.num_heads + i.kvh * G +
+                                          (rr & (G - 1))) * HEAD_DIM + 8 * (row & 3);
+      }
 #pragma unroll 1
-      for (int h = 0; h < DO / 64; ++h) {  // 64 dims at a time
-        uint32_t o[64];
-        if (ok) {
+      for (int c = 0; c < DO; c += 32) {
+        uint32_t o[32];
+        tmem_ld16(tO + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+        tmem_ld16(tO + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+        tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld16(tO + 64 * h + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * c]));
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) o[c] = 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          o[c] = pack2<T>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
-        const int pos = t0 + (row >> p.log2_g) < t_end ? i.base + t0 + (row >> p.log2_g) : -1;
-        if (nans) {  // rare: look for the NaN values that the row sees among the item's last blocks
-          uint32_t mask[2] = {0u, 0u};
+        for (int d = 0; d < 16; ++d)
+          o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
+        if (nans && t < t_end) {  // rare: look for the NaN values that the row sees among the item's last blocks
+          uint32_t mask = 0;
 #pragma unroll 1
-          for (int key = (i.base + i.ta + 1) / TC_KEYS * TC_KEYS; key <= pos; ++key) {
+          for (int key = (i.base + i.ta + 1) / TC_KEYS * TC_KEYS; key <= i.base + t; ++key) {
             const int phys = __ldg(p.block_tables + static_cast<size_t>(i.s) * p.max_blocks_per_seq + (key >> p.log2_b));
             if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_blocks)) continue;  // NaN all over already
-            const uint8_t* at = p.v_cache + ((((static_cast<size_t>(phys) << p.log2_b) + (key & ((1 << p.log2_b) - 1))) *
-                                              p.num_kv_heads + i.kvh) * HEAD_DIM + 64 * h);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint4 v = ldg128(at + 16 * c);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const uint32_t m = nan_codes(w[y]);
-                mask[c >> 1] |= (((m >> 7) & 1u) | ((m >> 14) & 2u) | ((m >> 21) & 4u) | ((m >> 28) & 8u)) << (16 * (c & 1) + 4 * y);
-              }
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                p.v_cache + ((((static_cast<size_t>(phys) << p.log2_b) + (key & ((1 << p.log2_b) - 1))) * p.num_kv_heads +
+                              i.kvh) * HEAD_DIM + c));
+#pragma unroll 1
+            for (int y = 0; y < 8; ++y) {
+              const uint32_t m = nan_codes(__ldg(v + y));
+              mask |= (((m >> 7) & 1u) | ((m >> 14) & 2u) | ((m >> 21) & 4u) | ((m >> 28) & 8u)) << (4 * y);
             }
           }
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint32_t m = mask[c >> 4] >> (2 * (c & 15));
-            o[c] |= (m & 1u ? 0x7fffu : 0u) | (m & 2u ? 0x7fff0000u : 0u);
-          }
+          for (int d = 0; d < 16; ++d)
+            o[d] |= (mask >> (2 * d) & 1u ? 0x7fffu : 0u) | (mask >> (2 * d) & 2u ? 0x7fff0000u : 0u);
         }
+        uint4 unit[4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint4 a[4];
+        for (int x = 0; x < 4; ++x) unit[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        transpose4(unit, row);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            a[c] = make_uint4(o[16 * b + 4 * c], o[16 * b + 4 * c + 1], o[16 * b + 4 * c + 2], o[16 * b + 4 * c + 3]);
-          transpose4(a, row);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int rr = (row & ~3) + c;
-            const int tr = t0 + (rr >> p.log2_g);
-            if (tr < t_end)
-              *reinterpret_cast<uint4*>(static_cast<T*>(p.out) +
-                                        (static_cast<size_t>(i.q0 + tr) * p.num_heads + i.kvh * G + (rr & (G - 1))) * HEAD_DIM +
-                                        64 * h + 32 * b + 8 * (row & 3)) = a[c];
-          }
-        }
+        for (int x = 0; x < 4; ++x)
+          if (on[x]) *reinterpret_cast<uint4*>(at[x] + c) = unit[x];
       }
     }
     qinv = qinv_next;
