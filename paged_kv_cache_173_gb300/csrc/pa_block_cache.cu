@@ -4,7 +4,7 @@
 //
 //  block_write_kernel   block_size / 16 warps per (run of new tokens in a block, KV head, K or V)
 //  key_bounds_kernel    the same per (run of new tokens in a block, KV head)
-//  block_score_kernel   one warp per (64 blocks of a sequence, KV head)
+//  block_score_kernel   one warp per (32 blocks of a sequence, KV head)
 //  select_kernel        one CTA per (sequence, KV head)
 //
 // "PagedAttention: when the KV cache meets OS paging", section 6, stacks
@@ -34,9 +34,9 @@ __device__ __forceinline__ int slot_block(int64_t slot, int num_slots, int log2_
 // A CTA looks at a stretch of tokens for one KV head and hands each run that
 // begins there to a group of block_size / 16 warps; warp g of the group holds
 // the run's tokens 16 g .. 16 g + 15 in registers, so every element is read
-// once, whatever the block size.  (One warp per run that walked its tokens twice
-// took 153 us for the write and 135 us for the bounds of 8 prompts of 2048
-// tokens, 8 KV heads of 128; this split: see the kernels.)
+// once, whatever the block size.  (8 prompts of 2048 tokens, 8 KV heads of 128,
+// blocks of 16, bf16: 19.3 us for the write, 10.0 us for the bounds; one warp per
+// run that walked its tokens twice took 153 and 135 us.)
 constexpr int kRunRows = 16;      // tokens a warp holds
 constexpr int kMaxStretch = 128;  // tokens a CTA looks at, at most
 constexpr int kMaxGroup = 16;     // warps per group at most: 256-token blocks
@@ -165,6 +165,21 @@ struct RowTile {
   }
 };
 
+// Asks L2 for the rows of one head that a CTA's stretch holds, while the runs are found: the
+// slots, the list and the rows are three waits in turn (write of 8 x 2048 tokens 22.7 -> 19.3 us;
+// the bounds, whose keys the write beside them has just brought into L2, lose 0.4 us by it).
+template <int HEAD_DIM>
+__device__ __forceinline__ void prefetch_rows(const uint4* rows, const RunParams& p, int t0, int h) {
+  constexpr int LINES = HEAD_DIM / 64;  // 128-byte lines of a row
+  if (p.stretch < kRunRows) return;
+  for (int i = threadIdx.x; i < p.stretch * LINES; i += blockDim.x) {
+    const int64_t t = t0 + i / LINES;
+    if (t >= p.num_tokens) break;
+    const uint4* at = rows + (t * p.num_kv_heads + h) * (HEAD_DIM / 8) + i % LINES * 8;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+  }
+}
+
 // 256 threads for blocks of up to 128 tokens (8 groups of one warp ... one of 8), 512
 // for 256.  A warp's rows take 32 registers at d = 128, so 64 in all let 32 warps share an SM.
 constexpr int run_min_ctas(int head_dim, int threads) { return (head_dim > 128 ? 512 : 1024) / threads; }
@@ -210,7 +225,9 @@ __device__ __forceinline__ uint2 move_codes8(const uint2& v, float ratio) {
 }
 
 // Grid (stretch, KV head, K or V).  The write is a copy that shrinks: 3 bytes
-// moved per element, so HBM bounds prompts and latency bounds single tokens.
+// moved per element, so HBM bounds prompts (101 MB in 19.3 us: 5.2 TB/s; the rows are
+// held in registers between the maximum and the codes, which leaves 32 warps per SM)
+// and latency bounds single tokens (64 of them 2.8 us).
 template <typename T, int HEAD_DIM, int THREADS>
 __global__ void __launch_bounds__(THREADS, run_min_ctas(HEAD_DIM, THREADS)) block_write_kernel(const __grid_constant__ BlockWriteParams p) {
   using Tile = RowTile<HEAD_DIM>;
@@ -230,9 +247,10 @@ __global__ void __launch_bounds__(THREADS, run_min_ctas(HEAD_DIM, THREADS)) bloc
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int t0 = blockIdx.x * rp.stretch;
+  const uint4* src = is_v ? p.value : p.key;
+  prefetch_rows<HEAD_DIM>(src, rp, t0, h);
   runs.find(rp, t0);
   const int nruns = runs.total();
-  const uint4* src = is_v ? p.value : p.key;
   uint2* cache = is_v ? p.v_cache : p.k_cache;
   float* scales = is_v ? p.v_scales : p.k_scales;
   for (int k0 = 0; k0 < nruns; k0 += groups) {  // the same trips for every warp
@@ -357,7 +375,7 @@ __device__ __forceinline__ uint32_t nan2(uint32_t w, uint32_t with) {
 }
 
 // Grid (stretch, KV head).  Reads 2 bytes per element and writes 2 per channel
-// and block: HBM bounds prompts, latency single tokens.
+// and block: HBM bounds prompts (36 MB in 10.0 us), latency single tokens (64: 2.9 us).
 template <typename T, int HEAD_DIM, int THREADS>
 __global__ void __launch_bounds__(THREADS, run_min_ctas(HEAD_DIM, THREADS)) key_bounds_kernel(const __grid_constant__ KeyBoundsParams p) {
   using Tile = RowTile<HEAD_DIM>;
@@ -718,7 +736,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 // leading bits: counting by leading bits would put most keys in one bucket, and
 // comparing all keys with three trial values per two bits took 16 us.  Ten bits
 // a round: at most four rounds, usually two.
-// Latency bounds it: the scores of 8192 blocks are 32 KB.
+// Latency bounds it (about 7 us a launch): the scores of 8192 blocks are 32 KB.
 constexpr int kSelThreads = 1024;
 constexpr int kSelKeys = 8;  // per thread; rows of more than 8192 blocks are read again in each round
 constexpr int kSelChunk = kSelThreads * kSelKeys;
@@ -786,6 +804,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   };
   const int chunks = (n + kSelChunk - 1) / kSelChunk;
   load(0);
+  // the first chunk's table entries, on their way while the keys are counted (31.2 -> 30.7 and
+  // 38.9 -> 38.0 us for the sparse steps of the two batches above)
+  int ids[kSelKeys];
+#pragma unroll
+  for (int i = 0; i < kSelKeys; ++i) {
+    const int x = threadIdx.x * kSelKeys + i;
+    ids[i] = x < n ? __ldg(bt + x) : 0;
+  }
   uint32_t lo = 0xffffffffu, hi = 0u;
   for (int ch = 0; ch < chunks; ++ch) {
     if (ch > 0) load(ch);
@@ -866,7 +892,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       if (x >= n) break;
       const bool rival = x >= c0 && x < c1;
       const bool same = any && rival && key[i] == lo;
-      if (!rival || (any && key[i] > lo) || (same && eqs < ties)) out[at++] = __ldg(bt + x);
+      if (!rival || (any && key[i] > lo) || (same && eqs < ties)) out[at++] = ch == 0 ? ids[i] : __ldg(bt + x);
       eqs += same;
     }
     done += (total >> 16) + min(total & 0xffff, max(ties - tied, 0));
