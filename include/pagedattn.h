@@ -510,7 +510,9 @@ int pa_decode_splitk_fp8(void* out, const void* q, const void* k_cache, const vo
  *
  * ("PagedAttention: when the KV cache meets OS paging", section 6, puts the
  * compression inside the block; the block is what a scale can follow without
- * knowing the data in advance.)  head_dim is 64, 128 or 256.
+ * knowing the data in advance.)  head_dim is 64, 128 or 256.  Tables, here and
+ * in block-sparse decode, hold at most 2^31 - 1025 tokens
+ * (max_blocks_per_seq * block_size, else PA_ERR_UNSUPPORTED).
  *
  * A block's scales belong to its contents: whoever copies a block (copy-on-
  * write) copies its scale rows too.  pa_copy_blocks moves them when num_kv_heads

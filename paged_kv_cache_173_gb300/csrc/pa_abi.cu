@@ -321,6 +321,13 @@ int check_block_shape(int block_size, int num_blocks, int num_kv_heads, int head
   return PA_OK;
 }
 
+// The kernels round a context up to whole tiles and look some chunks ahead in 32 bits.
+int check_capacity(int max_blocks, int block_size) {
+  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX - 1024)
+    return fail(PA_ERR_UNSUPPORTED, "a table of %d blocks of %d tokens exceeds 2^31 - 1025 tokens", max_blocks, block_size);
+  return PA_OK;
+}
+
 pa::BlockDecodeArgs block_args(void* out, const void* q, const void* k_cache, const void* v_cache,
                                const float* k_scales, const float* v_scales, const int32_t* tables, int max_blocks,
                                const int32_t* lens, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
@@ -357,6 +364,8 @@ int block_decode_impl(void* out, const void* q, const void* k_cache, const void*
                       int max_num_partitions, void* workspace, size_t workspace_bytes, void* stream) {
   int st = check_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
                         num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  st = check_capacity(max_blocks_per_seq, block_size);
   if (st != PA_OK) return st;
   if (splitk) {
     st = check_splitk(max_blocks_per_seq, block_size, partition_size, max_num_partitions, workspace,
@@ -662,6 +671,8 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const vo
                          none && num_seqs > 0 ? 0 : num_seqs, num_rows, max_query_len, num_heads, num_kv_heads,
                          head_dim, block_size, num_blocks, scale, dtype);
   if (st != PA_OK) return st;
+  st = check_capacity(max_blocks_per_seq, block_size);
+  if (st != PA_OK) return st;
   if (num_seqs == 0 || max_query_len == 0 || num_rows == 0) return ok();
   st = check_side(k_scales, v_scales, "k_scales and v_scales");
   if (st != PA_OK) return st;
@@ -704,6 +715,8 @@ int pa_select_blocks(int32_t* sel_tables, int32_t* sel_lens, const void* q, cons
   int st = check_decode(q, q, key_bounds, key_bounds, block_tables, max_blocks_per_seq, context_lens, num_seqs,
                         num_heads, num_kv_heads, head_dim, block_size, num_blocks, 1.f, dtype);
   if (st != PA_OK) return st;
+  st = check_capacity(max_blocks_per_seq, block_size);
+  if (st != PA_OK) return st;
   if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
   if (num_first < 0 || num_last < 1)
     return fail(PA_ERR_INVALID_ARG, "num_first (%d) must be >= 0 and num_last (%d) >= 1", num_first, num_last);
@@ -737,6 +750,8 @@ int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* 
     return fail(PA_ERR_UNSUPPORTED, "kv_dtype %d must equal dtype %d or be PA_FP8_E4M3", kv_dtype, dtype);
   int st = check_decode(out, q, k_cache, v_cache, sel_tables, max_selected, sel_lens, num_seqs, num_heads,
                         num_kv_heads, head_dim, block_size, num_blocks, scale, dtype);
+  if (st != PA_OK) return st;
+  st = check_capacity(max_selected, block_size);
   if (st != PA_OK) return st;
   if (num_seqs == 0) return ok();
   const bool fp8 = kv_dtype == PA_FP8_E4M3;

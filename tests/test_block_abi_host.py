@@ -234,3 +234,17 @@ def test_the_short_way_declines_what_it_does_not_know(L):
         fast.bind(1, 2)
     with pytest.raises(ValueError):
         fast.bind(*[0] * 7)
+
+
+def test_tables_leave_room_for_rounding_up(L):
+    """A capacity within 1024 tokens of 2^31 is refused: contexts are rounded up in 32 bits."""
+    M = (2 ** 31 - 1) // 16
+    most = (2 ** 31 - 1 - 1024) // 16
+    ws = 2 * 2 * (M + 3) * 4
+    for name, d, key in (("pa_decode_fp8_block", dict(DECODE, stream=None), "M"), ("pa_prefill_fp8_block", PREFILL, "M"),
+                         ("pa_select_blocks", dict(SELECT, wsb=ws), "M"), ("pa_decode_sparse", SPARSE, "K")):
+        for m in (M, most + 1):
+            assert call(L, name, d, **{key: m}) == UNSUPPORTED and "2^31 - 1025" in _lib.last_error()
+        assert call(L, name, d, S=0, **{key: most}) == OK
+    split = dict(DECODE, ps=512, P=M // 32 + 1, ws=A, wsb=2 ** 62, stream=None)
+    assert call(L, "pa_decode_splitk_fp8_block", split, M=M) == UNSUPPORTED

@@ -305,3 +305,63 @@ def test_short_way_takes_good_calls_and_no_others():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert answer(2, kc.view(torch.float8_e4m3fn)) is True
+
+
+class Prompts:
+    """A prefill with more pairs of tiles than the GPU has SMs."""
+
+    def __init__(self, seed, dtype=torch.float16, new=200, scale=None):
+        g = np.random.default_rng(seed)
+        lens = [int(x) for x in g.integers(new, 2 * new, 12)]
+        self.b = Batch(lens, 16, 4, 64, 16, dtype, seed, new=[int(x) for x in g.integers(1, new + 1, 12)])
+        if scale is not None:
+            self.b.scale = scale
+        self.args = self.b.dev("q", "kc", "vc", "ks", "vs", "tables", "lens", "starts")
+        self.out = torch.full_like(self.args[0], float("nan"))
+
+    def run(self, stream=None):
+        api.pa_prefill_fp8_block(self.out, *self.args, max(self.b.new), self.b.scale, stream=stream)
+
+    def check(self):
+        torch.cuda.synchronize()
+        self.b.q = self.args[0].cpu()
+        assert_close(self.out, *self.b.prefill_reference())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_prefill_captured_and_replayed_with_new_queries(dtype):
+    p = Prompts(21, dtype)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p.run()
+        p.run()
+    for seed in (5, 6):
+        p.args[0].copy_(torch.randn(p.args[0].shape, generator=torch.Generator().manual_seed(seed)).to(dtype))
+        p.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        p.check()
+
+
+def test_prefills_and_steps_at_once_on_three_streams():
+    a, b, c = Prompts(22), Prompts(23, torch.bfloat16), Step(batch(24))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(8):
+        for x, s in zip((a, b, c), streams):
+            x.run(s)
+    for x in (a, b, c):
+        x.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_negative_softmax_scale(dtype):
+    p = Prompts(25, dtype, new=100, scale=-0.125)
+    p.run()
+    p.check()
+    b = batch(26, dtype)
+    b.scale = -0.125
+    s = Step(b)
+    s.run()
+    s.check()
