@@ -21,9 +21,8 @@
 //    five blocks of keys when each pair had its own CTA.  A CTA goes on to the next
 //    pair that has not started, and its producers, Q loads and first MMAs overlap
 //    the outputs of the last pair.
-//  - 128 scores per softmax thread leave 40 registers for the rest.  The launch's
-//    512 x 128 registers are shared out: 168 a softmax thread, 112 a producer, 64 the
-//    others; nothing spills.
+//  - 128 scores per softmax thread leave few registers for the rest.  The launch's
+//    512 x 128 registers are shared out by role, so that nothing is spilled in a loop.
 // Measured (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of 2048 tokens 227 us,
 // 2 of 16384 2974 us (0.78 of the measured peak), 16 x 512 on 16384 cached 1546 us;
 // bf16, 16 chunks of 509 on 1536 cached 201 us.  One CTA per pair, one MMA warp for
@@ -71,7 +70,10 @@ struct BlockPrefillParams {
   int num_blocks;
   int pairs;
   int tile_tokens;
-  int by_length;  // grid order: 1: (KV head, sequence, pair), 0: (pair, KV head, sequence)
+  // grid order: (KV head, sequence, pair) or, longest_first = 0, (pair, KV head, sequence).  Ragged
+  // kernels: one dimension, KV head and place in the list of all sequences' pairs, longest first.
+  int longest_first;
+  int num_seqs;
   float scale_log2;
 };
 
@@ -88,7 +90,10 @@ struct BpCfg {
   static constexpr int MMA_WARP = PROD_WARP + PROD_WARPS;
   static constexpr int ITEM_WARP = MMA_WARP + TC_TILES;
   static constexpr int THREADS = SOFT + PROD + 128;
-  static constexpr int SOFT_REGS = 168, PROD_REGS = 112, MMA_REGS = 64;
+  // (d = 64 holds half the codes per producer; with the split of d = 128 it takes 189 us, not 185)
+  static constexpr int SOFT_REGS = HEAD_DIM == 64 ? 168 : 160;
+  static constexpr int PROD_REGS = HEAD_DIM == 64 ? 112 : 120;
+  static constexpr int MMA_REGS = HEAD_DIM == 64 ? 64 : 72;
   // what the warpgroups hold is what the block was launched with
   static_assert(SOFT * SOFT_REGS + PROD * PROD_REGS + 128 * MMA_REGS <= THREADS * 128, "registers");
   static constexpr int DBOX = HEAD_DIM / BOX_DIMS;
@@ -253,11 +258,57 @@ struct PrefillItem {
   __device__ __forceinline__ int blocks(int tt) const { return (kend(tt) + TC_KEYS - 1) / TC_KEYS; }
 };
 
-// The item of a grid index: 0 nothing to do, 1 work, -1 a context length that cannot be.
+// The pairs of query tiles of sequence i (0 past the last).
+__device__ __forceinline__ int pairs_of(const BlockPrefillParams& p, int i) {
+  if (i >= p.num_seqs) return 0;
+  const int n = __ldg(p.query_start_loc + i + 1) - __ldg(p.query_start_loc + i);
+  return n <= 0 ? 0 : min(((n - 1) >> (8 - p.log2_g)) + 1, p.pairs);
+}
+
+// Place `at` of the list of all sequences' pairs, the pairs of highest number first and those of
+// one number in the sequences' order: (pair, sequence), or false past the last.  The whole warp
+// searches; C(x), the pairs numbered above x, is the sum over the sequences of max(0, pairs - 1 - x).
+__device__ __forceinline__ bool ragged_item(const BlockPrefillParams& p, int at, int& pair, int& s) {
+  const int lane = threadIdx.x & 31;
+  auto above = [&](int x) {
+    int n = 0;
+    for (int i = lane; i < p.num_seqs; i += 32) n += max(0, pairs_of(p, i) - 1 - x);
+    return __reduce_add_sync(FULL_MASK, n);
+  };
+  if (at >= above(-1)) return false;
+  int lo = 0, hi = p.pairs - 1;  // the least x with C(x) <= at
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) <= at) hi = mid;
+    else lo = mid + 1;
+  }
+  int rank = at - above(lo);
+  for (int i = 0; i < p.num_seqs; i += 32) {
+    const unsigned has = __ballot_sync(FULL_MASK, pairs_of(p, i + lane) > lo);
+    const int n = __popc(has);
+    if (rank < n) {
+      pair = lo;
+      s = i + static_cast<int>(__fns(has, 0, rank + 1));
+      return true;
+    }
+    rank -= n;
+  }
+  return false;
+}
+
+// The item of a grid index, by whole warps: 0 nothing to do, 1 work, -1 a context length that cannot be.
+template <bool IS_RAGGED>
 __device__ __forceinline__ int find_item(const BlockPrefillParams& p, uint3 id, PrefillItem& it) {
-  const int pair = p.pairs - 1 - static_cast<int>(p.by_length ? id.z : id.x);  // the longest pairs start first
-  it.kvh = p.by_length ? id.x : id.y;
-  it.s = p.by_length ? id.y : id.z;
+  int pair;
+  if constexpr (IS_RAGGED) {
+    it.kvh = id.x % p.num_kv_heads;
+    if (!ragged_item(p, id.x / p.num_kv_heads, pair, it.s)) return 0;
+  } else {
+    const bool lf = p.longest_first;
+    pair = p.pairs - 1 - static_cast<int>(lf ? id.z : id.x);  // the longest pairs start first
+    it.kvh = lf ? id.x : id.y;
+    it.s = lf ? id.y : id.z;
+  }
   it.q0 = __ldg(p.query_start_loc + it.s);
   it.qlen = __ldg(p.query_start_loc + it.s + 1) - it.q0;
   const int ctx = __ldg(p.context_lens + it.s);
@@ -315,7 +366,7 @@ __device__ __forceinline__ void set_max_regs() {
   }
 }
 
-template <typename T, int HEAD_DIM>
+template <typename T, int HEAD_DIM, bool IS_RAGGED>
 __global__ void __launch_bounds__(BpCfg<HEAD_DIM>::THREADS, 1)
 block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   using C = BpCfg<HEAD_DIM>;
@@ -357,7 +408,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   grid_dependency_wait();  // the cache write before this launch has finished
 
   PrefillItem it;
-  const int found = find_item(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it);
+  const int found = find_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it);
   if (found <= 0) {
     if (found < 0) write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
     allow_dependent_launch();
@@ -697,7 +748,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
             fence_proxy_async_smem();
             ask_for_cta(sm + C::RESP_OFF, cbar);
           }
-          const int f = find_item(p, id, i);
+          const int f = find_item<IS_RAGGED>(p, id, i);
           if (f < 0) write_nan_rows<T, HEAD_DIM>(p, i, lane, 32);
           if (f > 0) return true;
         }
@@ -739,7 +790,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       }
       if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
         uint3 id;
-        if (cta_given(sm + C::RESP_OFF, id) && find_item(p, id, it) != 0) write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
+        if (cta_given(sm + C::RESP_OFF, id) && find_item<IS_RAGGED>(p, id, it) != 0)
+          write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
       }
       it.s = -1;
       if (lane == 0) publish(it, published);
@@ -1005,10 +1057,7 @@ template <typename T, int HEAD_DIM>
 cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t stream) {
   using C = BpCfg<HEAD_DIM>;
   const PrefillArgs& a = b.a;
-  auto kern = block_prefill_tc_kernel<T, HEAD_DIM>;
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = ensure_smem(kern, C::SMEM_BYTES, smem_set);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
   BlockPrefillParams p;
   const int group = a.num_heads / a.num_kv_heads;
   e = make_q_map<T>(&p.tmap_q, a.q, HEAD_DIM, a.num_heads, group, a.num_rows);
@@ -1039,8 +1088,24 @@ cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t strea
   // 3098 us).  Where most of the context is cached the pairs are nearly equal, and pairs of one
   // head that run together share its K and V in L2 (16 x 512 on 16384: 1574 us against 1673).
   const int64_t cap = static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
-  p.by_length = cap <= 8 * static_cast<int64_t>(a.max_query_len) && p.pairs <= 65535;
-  cfg.gridDim = p.by_length ? dim3(a.num_kv_heads, a.num_seqs, p.pairs) : dim3(p.pairs, a.num_kv_heads, a.num_seqs);
+  // A grid over (sequence, pair) is mostly empty where one sequence brings many new tokens and the
+  // others few, and an empty CTA takes a quarter of a microsecond of an SM.  The list of all pairs
+  // is searched instead (a prompt of 8192 beside 255 sequences of 1 new token on 1000: 1057 -> 668
+  // us; one of 2048 beside 63 of 1 on 2000: 167 -> 136 us), where the grid would be more than twice
+  // its length: below that the search costs more (64 sequences of 1 to 4096 new tokens: 2330 us by
+  // the grid, 2526 us by the list).
+  const int64_t listed = a.num_rows / (2 * p.tile_tokens) + static_cast<int64_t>(a.num_seqs);
+  const int64_t boxed = static_cast<int64_t>(p.pairs) * a.num_seqs;
+  p.num_seqs = a.num_seqs;
+  const bool ragged = boxed > 2 * listed && a.num_seqs <= 1024 && listed * a.num_kv_heads <= INT32_MAX;
+  p.longest_first = cap <= 8 * static_cast<int64_t>(a.max_query_len) && p.pairs <= 65535;
+  if (ragged) {
+    cfg.gridDim = dim3(static_cast<unsigned>(listed * a.num_kv_heads));
+  } else if (p.longest_first) {
+    cfg.gridDim = dim3(a.num_kv_heads, a.num_seqs, p.pairs);
+  } else {
+    cfg.gridDim = dim3(p.pairs, a.num_kv_heads, a.num_seqs);
+  }
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
@@ -1049,6 +1114,10 @@ cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  static std::atomic<uint64_t> smem_set[2];
+  auto kern = ragged ? block_prefill_tc_kernel<T, HEAD_DIM, true> : block_prefill_tc_kernel<T, HEAD_DIM, false>;
+  e = ensure_smem(kern, C::SMEM_BYTES, smem_set[ragged]);
+  if (e != cudaSuccess) return e;
   e = cudaLaunchKernelEx(&cfg, kern, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

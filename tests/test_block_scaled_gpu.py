@@ -318,3 +318,30 @@ def test_prefill_nan_values_reach_only_the_rows_that_see_them(dtype, dim):
             exp[row:r[s + 1], 4 * h:4 * h + 4, c] = float("nan")
         assert torch.isnan(exp).any() and torch.equal(torch.isnan(o), torch.isnan(exp))
         assert torch.equal(torch.nan_to_num(o), torch.nan_to_num(exp))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prefill_of_prompts_beside_single_tokens(dtype, dim):
+    """Batches whose sequences bring very different numbers of new tokens: prompts, chunks, single
+    tokens, none, and a context length that cannot be."""
+    new = [1] * 70
+    new[0], new[5], new[33], new[40], new[41], new[64], new[69] = 0, 600, 65, 0, 64, 130, 129
+    lens = [n + 37 * (i % 9) for i, n in enumerate(new)]
+    b = Batch([max(n, 1) for n in lens], 4, 1, dim, 16, dtype, 34, new=new).poison()
+    ref, tol = b.prefill_reference()
+    b.lens[64], b.lens[2] = 129, -1
+    o = run_prefill(b)
+    r = b.starts.tolist()
+    for i in (2, 64):
+        assert torch.isnan(o[r[i]:r[i + 1]]).all()
+        ref[r[i]:r[i + 1]], o[r[i]:r[i + 1]] = 0, 0
+    assert_close(o, ref, tol)
+
+
+def test_prefill_of_single_tokens_in_a_large_batch():
+    """1030 sequences, one of them a prompt: more than the list of pairs is searched for."""
+    new = [1] * 1030
+    new[500] = 300
+    b = Batch([max(n, 1 + i % 40) for i, n in enumerate(new)], 4, 4, 64, 16, torch.float16, 35, new=new)
+    assert_close(run_prefill(b), *b.prefill_reference())
