@@ -776,7 +776,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           float a = sk * p.scale_log2;
           a = fabsf(a) >= 7.52316384526264e-37f ? a : copysignf(7.52316384526264e-37f, p.scale_log2);
           const float lv = __log2f(fmaxf(sv, 5.421010862427522e-20f));  // at least 2^-64
-          const float4 v = make_float4(a, lv, ex2(-lv), 0.f);
+          // (ex2 has no subnormal results)
+          const float4 v = make_float4(a, lv, lv <= 126.f ? ex2(-lv) : __frcp_rn(sv), 0.f);
           ok = g < 2 || wait(&scfree[g & 1], ((g >> 1) - 1) & 1);
           if (!ok) break;
           scales[(g & 1) * 32 + lane] = v;

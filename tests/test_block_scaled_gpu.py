@@ -345,3 +345,20 @@ def test_prefill_of_single_tokens_in_a_large_batch():
     new[500] = 300
     b = Batch([max(n, 1 + i % 40) for i, n in enumerate(new)], 4, 4, 64, 16, torch.float16, 35, new=new)
     assert_close(run_prefill(b), *b.prefill_reference())
+
+
+@pytest.mark.parametrize("exponent", [127, 126, -64])
+def test_value_scales_at_both_ends_of_their_range(exponent):
+    """Value scales of 2^127 (whose inverse is subnormal) down to 2^-64, codes small enough for the output type."""
+    b = Batch([150, 33, 1], 8, 2, 128, 16, torch.bfloat16, 36, new=[40, 33, 1])
+    g = torch.Generator().manual_seed(37)
+    b.vc = (torch.randint(0, 0x31, b.vc.shape, generator=g) | (torch.randint(0, 2, b.vc.shape, generator=g) << 7)).to(torch.uint8)
+    b.vs = torch.full_like(b.vs, 2.0 ** exponent)  # at most 0.5 * 2^exponent
+    assert_close(run_prefill(b), *b.prefill_reference())
+    q, kc, vc, ks, vs, bt, cl = b.dev("q", "kc", "vc", "ks", "vs", "tables", "lens")
+    b.q = b.q[(b.starts[1:] - 1).long()]
+    q = b.q.cuda()
+    out = torch.empty_like(q)
+    api.pa_decode_fp8_block(out, q, kc, vc, ks, vs, bt, cl, b.scale)
+    torch.cuda.synchronize()
+    assert_close(out, *b.reference())
