@@ -254,3 +254,28 @@ def test_generation_prompt_then_sparse_steps(dtype):
         api.pa_decode_fp8_block(out, b.q.cuda(), kc, vc, ks, vs, gt, b.lens.cuda(), b.scale)
         ref, tol = b.reference()
         assert_close(out, ref, tol)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("keep,first,last", [(130, 1, 2), (9000, 0, 1), (8192, 4000, 4192), (3, 1, 1)])
+def test_selection_in_rows_of_many_blocks(keep, first, last, ties):
+    """Rows of up to 20000 blocks, more than a CTA holds at once, on both sides of that number; with
+    ties, a handful of different blocks, so that equal scores reach over all of it."""
+    S, Hk, H, d, B, M = 4, 2, 6, 64, 16, 20000
+    g = torch.Generator().manual_seed(41)
+    N = 5 if ties else 30000
+    codes = torch.randint(-127, 128, (N, Hk, 2, d), generator=g, dtype=torch.int32)
+    codes = torch.stack([codes.amin(2), codes.amax(2)], 2).to(torch.int8)
+    exps = torch.randint(-9, 3, (N, Hk), generator=g, dtype=torch.int32)
+    tables = torch.randint(0, N, (S, M), generator=g, dtype=torch.int32)
+    lens = torch.tensor([8192 * B, 8193 * B - 3, M * B - 5, 16384 * B + 1], dtype=torch.int32)
+    q = torch.randn((S, H, d), generator=g).to(torch.float16)
+    want = bo.select(to_np(q), codes.numpy(), exps.numpy(), tables.numpy(), lens.numpy(), B, keep, first, last)
+    st = torch.full((S, Hk, keep), 77, dtype=torch.int32, device="cuda")
+    sl = torch.full((S, Hk), 77, dtype=torch.int32, device="cuda")
+    ws = api.alloc_select_workspace(S, Hk, M, "cuda")
+    ws.fill_(float("nan"))
+    api.pa_select_blocks(st, sl, q.cuda(), codes.cuda(), exps.cuda(), tables.cuda(), lens.cuda(), B, first, last, ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(sl.cpu().numpy(), want[1])
+    assert np.array_equal(st.cpu().numpy(), want[0])
