@@ -1091,7 +1091,7 @@ cudaError_t launch_block_prefill_t(const BlockPrefillArgs& b, cudaStream_t strea
   p.tile_tokens = TC_ROWS / group;
   const int tiles = (a.max_query_len + p.tile_tokens - 1) / p.tile_tokens;
   p.pairs = (tiles + TC_TILES - 1) / TC_TILES;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = a.scale * 1.4426950408889634f + 0.f;  // a scale of -0 becomes +0: the sign decides what masks a score
   p.least_factor = copysignf(kLeastFactor, p.scale_log2);
   if (p.pairs == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};

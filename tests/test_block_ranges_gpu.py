@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_cases import Batch, assert_close
-from test_block_scaled_gpu import run_prefill
+from test_block_scaled_gpu import run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 DTYPES = [torch.float16, torch.bfloat16]
@@ -59,3 +59,15 @@ def test_prefill_bfloat16_queries_of_any_size(size, dim):
     for scale in (usual / size, usual * min(1.0, 1.0 / size)):  # scores of the usual size, or near 0 for small queries
         b.scale = float(np.float32(scale))
         assert_close(run_prefill(b), *b.prefill_reference())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.125, -1e-45])
+def test_softmax_scales_of_either_sign(scale, dtype):
+    b = Batch([300, 131, 20], 8, 2, 64, 16, dtype, 43, new=[140, 131, 20])
+    b.scale = scale
+    assert_close(run_prefill(b), *b.prefill_reference())
+    b.q = b.q[(b.starts[1:] - 1).long()]
+    ref, tol = b.reference()
+    assert_close(run_decode(b), ref, tol)
+    assert_close(run_decode(b, 64), ref, tol)
