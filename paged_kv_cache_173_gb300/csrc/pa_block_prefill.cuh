@@ -506,13 +506,11 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       const unsigned head = it.kvh * HEAD_DIM + c * 16;
       // lane i: the physical block of row group i % 16 (8 rows lie in one pool block)
       auto fetch = [&](int j) { return __ldg(bt + (min(j * TC_KEYS + (lane & 15) * 8, kend - 1) >> p.log2_b)); };
-      auto flag = [&](int f) { *const_cast<volatile int*>(infos + (k % C::ITEMS) * 8 + f) = 1; };
-      // the ids in hand, checked: never read outside the pool; the tiles' outputs become NaN
+      // the ids in hand, checked: never read outside the pool (the warp of the scales, which meets
+      // every id, makes NaN of the item's outputs)
       auto checked = [&](int id) {
         use_here(id);
-        const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-        if (!in) flag(6);
-        return in ? id : 0;
+        return static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks) ? id : 0;
       };
       auto load = [&](uint4 (&d)[HALVES], const uint8_t* pool, int phys, int key) {
         // (slots fit 31 bits)
@@ -569,7 +567,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
               }
             }
           }
-          if (any) flag(7);
+          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * 8 + 7) = 1;
         }
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
@@ -775,7 +773,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           const size_t at = static_cast<size_t>(in ? phys : 0) * p.num_kv_heads + it.kvh;
           const float sk = __ldg(p.k_scales + at);
           const float sv = __ldg(p.v_scales + at);
-          if (!(sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax))
+          // (the item is published, which clears this flag: the first one before the set-up barrier)
+          if (!(in && sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax))
             *const_cast<volatile int*>(infos + (n % C::ITEMS) * 8 + 6) = 1;
           // (a factor of 0 would turn a masked score (-inf) into NaN; bfloat16: see `factor`)
           float a = sk * p.scale_log2;

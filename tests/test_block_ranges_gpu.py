@@ -71,3 +71,24 @@ def test_softmax_scales_of_either_sign(scale, dtype):
     ref, tol = b.reference()
     assert_close(run_decode(b), ref, tol)
     assert_close(run_decode(b, 64), ref, tol)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prefill_ids_outside_the_pool_in_the_first_blocks(dtype, dim):
+    """The first table entries of sequences of several blocks of keys name no block: NaN in every
+    call and every row that reads them, and the other rows keep their bits."""
+    b = Batch([700, 400, 300, 513, 40], 8, 2, dim, 16, dtype, 44, new=[300, 400, 3, 200, 40])
+    want = run_prefill(b)
+    assert torch.isfinite(want).all()
+    r = b.starts.tolist()
+    b.tables[0, 0], b.tables[1, 0], b.tables[3, 5] = b.N, -1, 2 ** 31 - 1
+    b.tables[4, 0] = -(2 ** 31)
+    for _ in range(40):
+        o = run_prefill(b)
+        for s in range(5):
+            rows = o[r[s]:r[s + 1]]
+            assert torch.equal(rows, want[r[s]:r[s + 1]]) if s == 2 else torch.isnan(rows[-1]).all()
+            if s != 2:  # the rows whose causal range holds the entry
+                sees = max(0, (80 if s == 3 else 0) - (b.lens_list[s] - b.new[s]))
+                assert torch.isnan(rows[sees:]).all()
