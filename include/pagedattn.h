@@ -569,13 +569,14 @@ int pa_reshape_and_cache_fp8_block(const void* key, const void* value, void* k_c
  *
  *   q, out   [num_seqs][num_heads][head_dim] of dtype, PA_FP16 or PA_BF16
  *
- * The scales may be any finite numbers >= 0 (a v scale below 2^-64 reads as
- * 2^-64, so a v scale of 0 stands for values below 2.5e-17).  The codes are
- * widened exactly to fp16; bf16 queries are brought into fp16's range by a
- * power of two per row, undone in float32.  Scores, softmax and accumulation
- * are float32; the attention weights enter the P.V product as fp16.  The value
- * scale moves into the exponent of the weight, so blocks of very different
- * scales meet without loss.
+ * The scales may be any finite numbers >= 0.  The codes are widened exactly to
+ * fp16; bf16 queries are brought into fp16's range by a power of two per row,
+ * undone in float32.  Scores, softmax and accumulation are float32; the attention
+ * weights enter the P.V product as fp16, the largest one near 2^15: a weight above
+ * 2^-29 of the largest has 11 bits, a smaller one is off by 2^-40 of the largest at
+ * most, whatever the scales are.  Each block's products are multiplied by its value
+ * scale in float32, and the weights are summed unrounded.  (Value scales below 2^-87
+ * lose bits, those below 2^-110 read as 0.)
  *
  * Other arguments, supported shapes and device-value outcomes as pa_decode; in
  * addition a negative, infinite or NaN scale of a block in the context, or a

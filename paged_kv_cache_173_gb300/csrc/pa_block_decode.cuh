@@ -18,19 +18,25 @@
 //
 // The mathematics of the scales.  Block b of a sequence holds the keys
 // ks_b * code and the values v_b * code.  With s_i the base-2 score of token i
-// (scale * log2(e) * ks_b * q . code_i),
+// (scale * log2(e) * ks_b * q . code_i) and p_i = 2^(s_i - m), m a running maximum,
 //
-//   out = sum_i 2^s_i v_b code_i / sum_i 2^s_i
-//       = sum_i w_i code_i / sum_i w_i / v_b,   w_i = 2^(s_i + log2 v_b - M),
+//   out = sum_b v_b (sum_{i in b} p_i code_i) / sum_i p_i.
 //
-// with M the running maximum of s_i + log2 v_b.  So the value scale moves into
-// the exponent of the one exponential that each score needs anyway: the weights
-// that meet the codes lie in [0, 1] whatever the scales are, the accumulators
-// change scale only when M moves, and the sum takes one multiply per chunk.
-// Nothing is lost when a block of large values stands next to one of tiny
-// values: the dominant products set M.  The rounding of log2 v_b (below 2^-17)
-// is the same in w_i above and below the line, so it weighs a block by 1 + 2^-17
-// at most.
+// The weights of a 16-token chunk, which has one value scale, meet its codes in
+// MMAs of their own, and the products join the accumulators by a float32
+// multiply-add with v_b: what one block's scale is says nothing about the weights
+// of another, and the denominator is the sum of the weights.  (With v_b in the
+// weight's exponent, 2^(s_i + log2 v_b - M), the MMAs accumulate on, but a block of
+// large values that a sequence hardly attends to pushes the weights of all others
+// towards float16's end: 131072 keys behind one by 12 nats whose block's scale is
+// 2^8 times theirs came out 4% short.)
+//
+// A weight is float16: m lies 15 below the largest score, so the largest weight is
+// 2^15, and every weight above 2^-29 of it has 11 bits, a smaller one is off by
+// 2^-40 of it at most.  The sum adds the weights unrounded, in float32.  The
+// accumulators carry v_b 2^-39 and a merge the sums times 2^-39 (the weights' 2^15
+// and room for 2^24 tokens of the largest scale); value scales from 2^-87 on keep
+// all bits.
 //
 // Queries enter the MMAs as float16 beside the widened codes (exact in
 // float16).  A bfloat16 query row is first scaled by the power of two that
@@ -46,7 +52,9 @@ namespace pa {
 
 namespace {
 
-constexpr float kMinValueScale = 5.421010862427522e-20f;  // 2^-64: smaller value scales read as this
+constexpr float kTopWeight = 15.f;                         // log2 of the largest weight: float16 ends at 2^16
+constexpr float kValueUnit = 1.8189894035458565e-12f;      // 2^-39: the accumulators' unit
+constexpr float kValueUnitInv = 549755813888.f;            // 2^39
 
 struct BlockDecodeParams {
   CUtensorMap tmap_k;  // as DecodeParams: [N*B rows][Hk][d], 16-row boxes
@@ -108,25 +116,23 @@ __device__ __forceinline__ void load_q_frags_scaled(uint32_t (&qf)[HEAD_DIM / 16
   }
 }
 
-// The scale of one chunk's keys, and of its values v as log2 v and 1 / v.
+// The scales of one chunk's keys and values, the latter in the accumulators' unit.
 struct ChunkScale {
   float ks;
-  float lv;
-  float vinv;
+  float vs;
   bool bad;  // a scale that is negative, infinite or NaN
 
   __device__ __forceinline__ void set(float k, float v) {
     bad = !(k >= 0.f && k <= kFloatMax && v >= 0.f && v <= kFloatMax);
     ks = k;
-    v = fmaxf(v, kMinValueScale);
-    lv = __log2f(v);
-    vinv = __frcp_rn(v);
+    vs = v * kValueUnit;
   }
 };
 
 // softmax_step (pa_decode.cuh) with a scale per chunk: sl[nt][j] is the
-// base-2 factor of query nt * 8 + 2c + j without the key scale.  P^T enters
-// as float16(w); the running sum adds w / v unrounded.
+// base-2 factor of query nt * 8 + 2c + j without the key scale.  acc.m lies
+// kTopWeight below the largest score.  P^T enters as float16; the running sum
+// adds the weights unrounded.
 template <int HEAD_DIM, int NT, int NSUB>
 __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, const float (&sacc)[NSUB][NT][4],
                                                     const int (&valid)[NSUB], const float (&sl)[NT][2],
@@ -142,10 +148,10 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
       const bool v0 = g < valid[sb];
       const bool v1 = g + 8 < valid[sb];
       const float f0 = sl[nt][0] * cs[sb].ks, f1 = sl[nt][1] * cs[sb].ks;
-      x[sb][0] = v0 ? fmaf(sacc[sb][nt][0], f0, cs[sb].lv) : -INFINITY;
-      x[sb][1] = v0 ? fmaf(sacc[sb][nt][1], f1, cs[sb].lv) : -INFINITY;
-      x[sb][2] = v1 ? fmaf(sacc[sb][nt][2], f0, cs[sb].lv) : -INFINITY;
-      x[sb][3] = v1 ? fmaf(sacc[sb][nt][3], f1, cs[sb].lv) : -INFINITY;
+      x[sb][0] = v0 ? sacc[sb][nt][0] * f0 : -INFINITY;
+      x[sb][1] = v0 ? sacc[sb][nt][1] * f1 : -INFINITY;
+      x[sb][2] = v1 ? sacc[sb][nt][2] * f0 : -INFINITY;
+      x[sb][3] = v1 ? sacc[sb][nt][3] * f1 : -INFINITY;
     }
     float mx0 = fmaxf(x[0][0], x[0][2]);
     float mx1 = fmaxf(x[0][1], x[0][3]);
@@ -159,8 +165,8 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
       mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, off));
     }
-    const float mn0 = fmaxf(acc.m[nt][0], mx0);
-    const float mn1 = fmaxf(acc.m[nt][1], mx1);
+    const float mn0 = fmaxf(acc.m[nt][0], mx0 - kTopWeight);
+    const float mn1 = fmaxf(acc.m[nt][1], mx1 - kTopWeight);
     const float cr0 = ex2(acc.m[nt][0] - mn0);
     const float cr1 = ex2(acc.m[nt][1] - mn1);
     const bool grew = __any_sync(FULL_MASK, (mn0 != acc.m[nt][0]) | (mn1 != acc.m[nt][1]));
@@ -171,8 +177,8 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
     for (int sb = 0; sb < NSUB; ++sb) {
       const float p0 = ex2(x[sb][0] - mn0), p1 = ex2(x[sb][1] - mn1);  // token g
       const float p2 = ex2(x[sb][2] - mn0), p3 = ex2(x[sb][3] - mn1);  // token g + 8
-      sum0 = fmaf(p0 + p2, cs[sb].vinv, sum0);
-      sum1 = fmaf(p1 + p3, cs[sb].vinv, sum1);
+      sum0 += p0 + p2;
+      sum1 += p1 + p3;
       pb[sb][nt][0] = movmatrix_trans(pack_half2(p0, p1));  // P^T tokens 0-7 as the B fragment
       pb[sb][nt][1] = movmatrix_trans(pack_half2(p2, p3));  // P^T tokens 8-15
     }
@@ -185,6 +191,42 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
         acc.o[dm][nt][1] *= cr1;
         acc.o[dm][nt][2] *= cr0;
         acc.o[dm][nt][3] *= cr1;
+      }
+    }
+  }
+}
+
+// O^T += vs * V^T P^T over one chunk's codes: pv_e4m3 (pa_decode.cuh) with the
+// chunk's products apart from the accumulators until they are scaled: NT * d / 4
+// multiply-adds a lane and chunk (64 sequences of 128 to 2048 tokens 29.4 -> 29.7
+// us, 32 of 8192 82.5 -> 84.0 us, split-K of 32 K to 131 K and the sparse steps the
+// same, one of 485 tokens 4.95 -> 4.90 us).
+template <int HEAD_DIM, int NT, int ROW_BYTES, bool MASK>
+__device__ __forceinline__ void pv_e4m3_scaled(WarpAcc<HEAD_DIM, NT>& acc, const uint32_t (&pb)[NT][2], uint32_t vaddr,
+                                               uint32_t tok, uint32_t uo, uint32_t mlo, uint32_t mhi, float vs) {
+  constexpr int UNITS = ROW_BYTES / 16;
+  constexpr int BOXB = CHUNK * ROW_BYTES;
+#pragma unroll
+  for (int u = 0; u < HEAD_DIM / 16; u += 2) {
+    uint32_t r[4];  // tokens 0-7 / 8-15 of unit u, then of unit u + 1
+    ldsm_x4_trans(r, vaddr + (u / UNITS) * BOXB + swizzled<ROW_BYTES>(tok, (u % UNITS) + uo));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[4];  // (tok 2c, 2c+1) at dim 2g, at dim 2g+1; then tokens 2c+8, 2c+9
+      e4m3x4_to_half2x2(__byte_perm(r[2 * h], 0u, 0x3120), a[0], a[1]);
+      e4m3x4_to_half2x2(__byte_perm(r[2 * h + 1], 0u, 0x3120), a[2], a[3]);
+      if constexpr (MASK) {
+        a[0] &= mlo;
+        a[1] &= mlo;
+        a[2] &= mhi;
+        a[3] &= mhi;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16_16816(t, a, pb[nt][0], pb[nt][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc.o[u + h][nt][i] = fmaf(t[i], vs, acc.o[u + h][nt][i]);
       }
     }
   }
@@ -210,12 +252,13 @@ __device__ __forceinline__ void attend_scaled(WarpAcc<HEAD_DIM, NT>& acc, const 
   v_masks(valid_last, lane, mlo, mhi);
 #pragma unroll
   for (int sb = 0; sb < NSUB - 1; ++sb)
-    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[sb], kb + sb * chunk_bytes + half_bytes, tok, uo, mlo, mhi);
+    pv_e4m3_scaled<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[sb], kb + sb * chunk_bytes + half_bytes, tok, uo, mlo, mhi,
+                                                   cs[sb].vs);
   const uint32_t vb = kb + (NSUB - 1) * chunk_bytes + half_bytes;
   if (valid_last == CHUNK) {
-    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi);
+    pv_e4m3_scaled<HEAD_DIM, NT, ROW_BYTES, false>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi, cs[NSUB - 1].vs);
   } else {  // the last chunk of the sequence
-    pv_e4m3<HEAD_DIM, NT, ROW_BYTES, true>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi);
+    pv_e4m3_scaled<HEAD_DIM, NT, ROW_BYTES, true>(acc, pb[NSUB - 1], vb, tok, uo, mlo, mhi, cs[NSUB - 1].vs);
   }
 }
 
@@ -528,14 +571,15 @@ __global__ void __launch_bounds__(BlockShape<HEAD_DIM, NT, kElemBytes<KV>, KIND,
     }
     // no positive sum: a cluster CTA without chunks (weight 0), or NaN scores
     const bool none = !(L > 0.f) && !empty;
-    const float r = any_bad || none ? NAN : (empty ? 0.f : O / L);
+    const float r = any_bad || none ? NAN : (empty ? 0.f : FP8 ? O / L * kValueUnitInv : O / L);
+    const float Lm = FP8 ? L * kValueUnit : L;  // a merge adds r times this: at most 1 in 2^24 tokens
     const size_t qrow = static_cast<size_t>(s) * H + kvh * G + head;
     if (CLUSTER) {
       float* cta = reinterpret_cast<float*>(ring + Cfg::CTA_OFFSET);
       cta[head * HEAD_DIM + d] = r;
       if (d == 0) {
         cta[GMAX * HEAD_DIM + head] = any_bad || none ? 0.f : M;
-        cta[GMAX * HEAD_DIM + GMAX + head] = any_bad || none ? 1.f : L;
+        cta[GMAX * HEAD_DIM + GMAX + head] = any_bad || none ? 1.f : Lm;
       }
     } else if (single) {
       static_cast<T*>(p.out)[qrow * HEAD_DIM + d] = to_elem<T>(r);
@@ -544,7 +588,7 @@ __global__ void __launch_bounds__(BlockShape<HEAD_DIM, NT, kElemBytes<KV>, KIND,
       p.ws_o[row * HEAD_DIM + d] = r;
       if (d == 0) {
         p.ws_m[row] = any_bad || none ? 0.f : M;
-        p.ws_l[row] = any_bad || none ? 1.f : L;
+        p.ws_l[row] = any_bad || none ? 1.f : Lm;
       }
     }
   }

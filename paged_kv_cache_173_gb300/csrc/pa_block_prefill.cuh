@@ -28,8 +28,7 @@
 // bf16, 16 chunks of 509 on 1536 cached 201 us.  One CTA per pair, one MMA warp for
 // both tiles: 282, 3005, 1584 and 230 us.
 //
-// The mathematics of the scales is that of pa_block_decode.cuh: with v_b the
-// value scale of the block of key i,
+// The mathematics of the scales: with v_b the value scale of the block of key i,
 //   w_i = 2^(s_i + log2 v_b - M),   out = sum w_i code_i / sum w_i / v_b,
 // one fused multiply-add per score (key scale and log2 v_b of its 16-key chunk),
 // one multiply per chunk for the sum.  A value scale below 2^-64 reads as 2^-64.

@@ -1,5 +1,5 @@
 """GPU parity of the block-scaled attention at the ends of its ranges: queries, keys and scales of
-zero and of any size."""
+zero and of any size, value scales that differ within a context, one key far ahead of many."""
 from __future__ import annotations
 
 import numpy as np
@@ -7,6 +7,8 @@ import pytest
 import torch
 
 from block_cases import Batch, assert_close
+from block_ranges import Ranges, mixed_scales, one_ahead
+from paged_kv_cache_173_gb300 import api
 from test_block_scaled_gpu import run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +94,43 @@ def test_prefill_ids_outside_the_pool_in_the_first_blocks(dtype, dim):
             if s != 2:  # the rows whose causal range holds the entry
                 sees = max(0, (80 if s == 3 else 0) - (b.lens_list[s] - b.new[s]))
                 assert torch.isnan(rows[sees:]).all()
+
+
+# ------------------------------------------------------------------ weights far below the largest
+AHEAD = [  # keys, nats that one is ahead of the others, the largest element of its value, its place
+    (131072, 12.1, 448.0, 0), (65536, 10.7, 1792.0, 40000), (16384, 10.7, 1792.0, 5), (16384, 10.1, 3584.0, 16383),
+    (4096, 9.0, 60000.0, 2048),
+]
+
+
+def run_sparse(b):
+    """The decode of every sequence over tables per KV head that name all of its blocks."""
+    q, kc, vc, ks, vs, bt, cl = b.dev("q", "kc", "vc", "ks", "vs", "tables", "lens")
+    out = torch.full_like(q, float("nan"))
+    api.pa_decode_sparse(out, q, kc, vc, bt[:, None].expand(-1, b.Hk, -1).contiguous(),
+                         cl[:, None].expand(-1, b.Hk).contiguous(), b.scale, ks, vs)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_decodes(b):
+    ref, tol = b.reference()
+    for got in (run_decode(b), run_decode(b, 64 if b.M <= 1024 else 512), run_decode(b, 4096), run_sparse(b)):
+        assert_close(got, ref, tol)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,gap,outlier,at", AHEAD)
+def test_decode_of_one_key_ahead_of_many(n, gap, outlier, at, dtype):
+    check_decodes(one_ahead(n, gap, outlier, at, dtype))
+
+
+@pytest.mark.parametrize("heads,dim", [(16, 64), (16, 128), (4, 128), (4, 256)])
+def test_decode_of_one_key_ahead_of_many_in_every_shape(heads, dim):
+    check_decodes(one_ahead(16384, 10.7, 1792.0, 9000, torch.bfloat16, heads=heads, dim=dim))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["two", "all"])
+def test_decode_of_blocks_of_very_different_value_scales(kind, dim):
+    check_decodes(mixed_scales(kind, dim))
