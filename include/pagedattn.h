@@ -609,6 +609,13 @@ int pa_decode_splitk_fp8_block(void* out, const void* q, const void* k_cache, co
  * scale gives NaN in the rows that an id outside the pool in its place would.
  * A NaN code gives NaN only in the rows whose causal range holds its token (a
  * key's in all of the row, a value's in its channel).
+ *
+ * The weights enter the P.V product as fp16.  With 2^r the power of two of the
+ * largest v scale among the first 128 keys of (sequence, KV head) (2^-8 where their
+ * values are all zero), a weight is off by 2^-32 of the largest at most where the v
+ * scales lie between 2^(r-12) and 2^(r+10), and by twice that for each power of two
+ * beyond.  A v scale below 2^-64, or below 2^(r-76), reads as that; one of 2^(r+47) or
+ * more gives NaN as a negative one does.
  */
 int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scales, const float* v_scales, const int32_t* block_tables,

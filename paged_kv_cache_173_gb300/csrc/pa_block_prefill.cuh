@@ -28,10 +28,27 @@
 // bf16, 16 chunks of 509 on 1536 cached 201 us.  One CTA per pair, one MMA warp for
 // both tiles: 282, 3005, 1584 and 230 us.
 //
-// The mathematics of the scales: with v_b the value scale of the block of key i,
-//   w_i = 2^(s_i + log2 v_b - M),   out = sum w_i code_i / sum w_i / v_b,
-// one fused multiply-add per score (key scale and log2 v_b of its 16-key chunk),
-// one multiply per chunk for the sum.  A value scale below 2^-64 reads as 2^-64.
+// The mathematics of the scales.  The value scale of a block b is split,
+// v_b = 2^(ref + 3) 2^kappa_b 2^r_b, with 2^ref the power of two of the largest scale
+// among the item's first 128 keys.  2^kappa_b, -15 <= kappa_b <= 7, multiplies the
+// widened codes: exact, and below 2^16.  What is left, 0 <= r_b < 1 for scales of 2^-12
+// to 2^10 times 2^ref (0 for powers of two) and the rest beyond, moves into the exponent of
+// the weight of key i:
+//   w_i = 2^(s_i + r_b - M),   out = 2^(ref + 3) sum w_i 2^kappa_b code_i / sum w_i 2^-r_b,
+// one fused multiply-add per score (key scale and r_b of its 16-key chunk), one
+// multiply per chunk for the sum.  So over 22 powers of two a block's scale says
+// nothing about the float16 weights of the others.  (With all of v_b in the exponent
+// 16384 keys behind one by 10 nats whose block's scale is 2^11 times theirs came out 40%
+// short.)  The largest weight is 2^7 to 2^15: the running maximum M moves when it has
+// grown by 2^8, and stays 7 below; a weight is off by 2^-32 of the largest at most.
+// r_b is held to -64 and more, and above 36 makes NaN of the item: within a spread of
+// 2^100 neither a weight that counts in the sum nor the sum leaves float32.  So a value
+// scale below 2^-76 times 2^ref reads as that, one of 2^47 times 2^ref is refused, and
+// one below 2^-64 reads as 2^-64.
+// (The multiplications, and the scales that the producers load for them, take 1 to 2.6%
+// of the launch.  ref from the largest scale of all of the item's blocks, looked up
+// by the warp of the scales one item ahead, took 3 to 5%: the next item is
+// known too late for it.)
 //
 // bfloat16 queries: the softmax thread of a row scales it in shared memory by
 // the power of two that brings its largest element to [2^14, 2^15) and writes
@@ -115,7 +132,8 @@ struct BpCfg {
   static_assert(GROUP * CHUNKS == 32, "one chunk per lane");
   static constexpr int INFO_OFF = SC_OFF + 2 * GROUP * CHUNKS * 16;
   static constexpr int ITEMS = 4;  // ring of published work items
-  static constexpr int RESP_OFF = INFO_OFF + ITEMS * 32;
+  static constexpr int INFO = 12;  // words of an item
+  static constexpr int RESP_OFF = INFO_OFF + ITEMS * INFO * 4;
   static constexpr int BAR_OFF = RESP_OFF + 16;
   static constexpr int DONE = VSTAGES;  // ring of completed steps
   static_assert(KSTAGES <= VSTAGES, "a step's commit is waited for before its place is used again");
@@ -140,6 +158,29 @@ __device__ __forceinline__ void use_here(float& x) { asm volatile("" : "+f"(x));
 // 2^-100: the least size of the factor that a raw score (below 2^33) is multiplied by; it makes 0 of
 // every score.
 constexpr float kLeastFactor = 7.888609052210118e-31f;
+
+constexpr float kMidWeight = 7.f;  // log2 of the largest weight when the running maximum has just moved
+constexpr int kLeastRest = -64;    // of a value scale's powers of two
+constexpr int kMostRest = 36;
+
+// The bits of a value scale for a maximum; what is no scale does not count.
+__device__ __forceinline__ int scale_bits(float v) { return v <= kFloatMax ? __float_as_int(v) : 0; }
+// The exponent of a value scale: that of 2^-64 for smaller ones (and negative ones, which make NaN elsewhere).
+__device__ __forceinline__ int value_exp(float v) { return (max(__float_as_int(v), (127 - 64) << 23) >> 23) - 127; }
+// ref by the largest bits over the first 128 keys; of values around 1 where those are all zero.
+__device__ __forceinline__ int ref_exp(int bits) {
+  const int e = value_exp(__int_as_float(bits));
+  return e > -64 ? e : -8;
+}
+// The power of two of a value scale that multiplies the codes: 448 * 2^7 < 65504, and
+// 2^-9 * 2^-15 is float16's smallest step.
+__device__ __forceinline__ int kappa(int e, int ref) { return min(max(e - ref - 3, -15), 7); }
+
+// Two float16 times two.
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // 16 codes widened to float16: two 16-byte units.
 __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
@@ -382,7 +423,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float4* scales = reinterpret_cast<float4*>(sm + C::SC_OFF);
-  // [ITEMS][8]: the item (s: -1 past the last), [6] a bad block or scale was met, [7] a masked row may meet a NaN value
+  // [ITEMS][INFO]: the item (s: -1 past the last), [6] a bad block or scale was met, [7] a masked row may meet a NaN
+  // value, [8] ref
   int* infos = reinterpret_cast<int*>(sm + C::INFO_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
   // Phases count over all items of the CTA.
@@ -424,13 +466,13 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       tma_load_3d(sm + u * C::QBYTES + db * C::QATOM, &p.tmap_q, db * BOX_DIMS, i.kvh * G, i.q0 + i.ta + u * tt, &qbar[u]);
   };
   auto publish = [&](const PrefillItem& i, int k) {  // one thread
-    int* f = infos + (k % C::ITEMS) * 8;
+    int* f = infos + (k % C::ITEMS) * C::INFO;
     f[0] = i.s, f[1] = i.kvh, f[2] = i.ta, f[3] = i.q0, f[4] = i.qlen, f[5] = i.base, f[6] = 0, f[7] = 0;
     mbar_arrive(&ifull[k % C::ITEMS]);
   };
   // Item k of the CTA, published.
   auto item = [&](int k) -> PrefillItem {
-    const volatile int* f = infos + (k % C::ITEMS) * 8;
+    const volatile int* f = infos + (k % C::ITEMS) * C::INFO;
     PrefillItem i;
     i.s = f[0], i.kvh = f[1], i.ta = f[2], i.q0 = f[3], i.qlen = f[4], i.base = f[5];
     return i;
@@ -438,7 +480,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   // Waits for it; false past the last (or when the MMA warp gave up).
   auto has_item = [&](int k) -> bool {
     return __all_sync(FULL_MASK, tc_wait(&ifull[k % C::ITEMS], (k / C::ITEMS) & 1)) &&
-           *const_cast<const volatile int*>(infos + (k % C::ITEMS) * 8) >= 0;
+           *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO) >= 0;
   };
   auto read_item = [&](int k, PrefillItem& i) -> bool {
     if (!has_item(k)) return false;
@@ -483,12 +525,17 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
     const int bmask = (1 << p.log2_b) - 1;
     auto rg = [&](int i) { return pw + C::PROD_WARPS * i; };
     uint4 kd[NG][HALVES], vd[NG][HALVES];
-    auto store = [&](const uint4 (&d)[HALVES], uint8_t* stage, int r) {
+    // (scaled: times `by`, two float16)
+    auto store = [&](const uint4 (&d)[HALVES], uint8_t* stage, int r, bool scaled, uint32_t by) {
       uint8_t* drow = stage + r * 128;
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
         uint4 a, b;
         widen16(d[h], a, b);
+        if (scaled) {
+          a = make_uint4(mul_half2(a.x, by), mul_half2(a.y, by), mul_half2(a.z, by), mul_half2(a.w, by));
+          b = make_uint4(mul_half2(b.x, by), mul_half2(b.y, by), mul_half2(b.z, by), mul_half2(b.w, by));
+        }
         // unit u of row r sits at u ^ (r % 8): the eight lanes of two rows write eight different units
         *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c) ^ (r & 7)) << 4)) = a;
         *reinterpret_cast<uint4*>(drow + h * C::KATOM + (((2 * c + 1) ^ (r & 7)) << 4)) = b;
@@ -520,6 +567,10 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       };
       int ids = checked(fetch(0));
       int next = fetch(min(1, nblk - 1));
+      // the value scale of row group lane % 16, as long ahead of its use as the codes
+      auto scale_of = [&]() { return __ldg(p.v_scales + static_cast<size_t>(ids) * p.num_kv_heads + it.kvh); };
+      float vs = scale_of();
+      int ref = 0;
       auto phys = [&](int g) { return __shfl_sync(FULL_MASK, ids, g & 15); };
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
@@ -538,13 +589,18 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           go = false;
           break;
         }
+        // (waited for where the ids are: behind the loads below it would wait for those, too)
+        use_here(vs);
+        if (j == 0) ref = ref_exp(__reduce_max_sync(FULL_MASK, scale_bits(vs)));
+        const int kap = kappa(value_exp(vs), ref);
         ids = checked(next);
         next = fetch(min(j + 2, nblk - 1));  // a whole block before their use
+        vs = scale_of();
         uint8_t* kdst = sm + C::K_OFF + kslot * C::KBYTES;
         uint8_t* vdst = sm + C::V_OFF + vslot * C::KBYTES;
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          store(kd[i], kdst, rg(i) * 8 + r8);
+          store(kd[i], kdst, rg(i) * 8 + r8, false, 0u);
           if (j + 1 < nblk) load(kd[i], p.k_cache, phys(rg(i)), (j + 1) * TC_KEYS + rg(i) * 8 + r8);
         }
         fence_proxy_async_smem();  // the widened rows become visible to the tensor core
@@ -566,11 +622,12 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
               }
             }
           }
-          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * 8 + 7) = 1;
+          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 7) = 1;
         }
+        const uint32_t two = (kap > -15 ? (kap + 15) << 10 : 1 << 9) * 0x10001u;  // 2^kappa twice, as float16
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          store(vd[i], vdst, rg(i) * 8 + r8);
+          store(vd[i], vdst, rg(i) * 8 + r8, true, __shfl_sync(FULL_MASK, two, rg(i) & 15));
           if (j + 1 < nblk) load(vd[i], p.v_cache, phys(rg(i)), (j + 1) * TC_KEYS + rg(i) * 8 + r8);
         }
         fence_proxy_async_smem();
@@ -764,6 +821,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         const int32_t* bt = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
         const int nblk = it.blocks(tt);
         const int kend = it.kend(tt);
+        int ref = 0;
 #pragma unroll 1
         for (int b = 0; b < nblk; b += C::GROUP, ++g) {
           // (chunks past the item's last key repeat the last one: their keys are masked)
@@ -772,15 +830,21 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
           const size_t at = static_cast<size_t>(in ? phys : 0) * p.num_kv_heads + it.kvh;
           const float sk = __ldg(p.k_scales + at);
           const float sv = __ldg(p.v_scales + at);
+          if (b == 0) {  // as the producers have it
+            ref = ref_exp(__reduce_max_sync(FULL_MASK, lane < C::CHUNKS ? scale_bits(sv) : 0));
+            if (lane == 0) *const_cast<volatile int*>(infos + (n % C::ITEMS) * C::INFO + 8) = ref;
+          }
+          // what 2^kappa leaves of the value scale: 2^rest times a mantissa
+          const int e = value_exp(sv);
+          const int rest = max(e - ref - 3 - kappa(e, ref), kLeastRest);
+          const float mant = sv >= 5.421010862427522e-20f ? __int_as_float((__float_as_int(sv) & 0x7fffff) | 0x3f800000) : 1.f;
           // (the item is published, which clears this flag: the first one before the set-up barrier)
-          if (!(in && sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax))
-            *const_cast<volatile int*>(infos + (n % C::ITEMS) * 8 + 6) = 1;
+          if (!(in && sk >= 0.f && sk <= kFloatMax && sv >= 0.f && sv <= kFloatMax && rest <= kMostRest))
+            *const_cast<volatile int*>(infos + (n % C::ITEMS) * C::INFO + 6) = 1;
           // (a factor of 0 would turn a masked score (-inf) into NaN; bfloat16: see `factor`)
           float a = sk * p.scale_log2;
           if constexpr (!BF16) a = fabsf(a) >= kLeastFactor ? a : p.least_factor;
-          const float lv = __log2f(fmaxf(sv, 5.421010862427522e-20f));  // at least 2^-64
-          // (ex2 has no subnormal results)
-          const float4 v = make_float4(a, lv, lv <= 126.f ? ex2(-lv) : __frcp_rn(sv), 0.f);
+          const float4 v = make_float4(a, rest + (mant == 1.f ? 0.f : __log2f(mant)), pow2f(-rest) * __frcp_rn(mant), 0.f);
           ok = g < 2 || wait(&scfree[g & 1], ((g >> 1) - 1) & 1);
           if (!ok) break;
           scales[(g & 1) * 32 + lane] = v;
@@ -886,7 +950,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       left = i.tile_blocks(u, tt);
       seen = i.base + i.ta + u * tt;
     }
-    float m_used = -INFINITY, l = 0.f;  // log2 units, the value scale's exponent included
+    float m_used = -INFINITY, l = 0.f;  // log2 units, the rest of the value scale's exponent included
     uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
 #pragma unroll 1
     for (; left > 0; --left, seen -= TC_KEYS) {
@@ -933,7 +997,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
       const float f = need ? ex2(m_used - m_new) : 1.f;
       if (none || need) m_used = m_new;
-      const float bias = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
+      const float bias = m_used == -INFINITY ? 0.f : kMidWeight - m_used;  // a row that has seen no key yet
       if (__any_sync(FULL_MASK, need)) {
 #pragma unroll 1
         for (int c = 0; c < DO; c += 8) {  // (eight at a time: the scores hold 128 registers)
@@ -947,7 +1011,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       }
       l *= f;
       // the weights, half of the keys at a time: P in the half's first 32 columns; l takes each
-      // chunk's sum divided by its value scale
+      // chunk's sum divided by the rest of its value scale
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -980,7 +1044,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       }
     }
     const PrefillItem i = item(st & 7);  // (read again: held over the loop it would cost registers there)
-    const volatile int* flags = infos + (st % C::ITEMS) * 8 + 6;
+    const volatile int* flags = infos + (st % C::ITEMS) * C::INFO + 6;
     // groups of scales that only the other tile needs
     for (int b = (i.tile_blocks(u, tt) + C::GROUP - 1) / C::GROUP * C::GROUP; b < i.blocks(tt); b += C::GROUP) {
       wait(&scfull[(st >> 5) & 1], (st >> 6) & 1);
@@ -996,7 +1060,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
       wait(&pvdone[u], (st >> 8) & 1);
       st ^= 1u << 8;
       tc_fence_after_sync();
-      const float inv = !ok || flags[0] ? NAN : 1.f / l;
+      const float inv = !ok || flags[0] ? NAN : 8.f / l * pow2f(flags[2]);
       const bool nans = flags[1];
       // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
       // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows (a

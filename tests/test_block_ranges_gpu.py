@@ -134,3 +134,58 @@ def test_decode_of_one_key_ahead_of_many_in_every_shape(heads, dim):
 @pytest.mark.parametrize("kind", ["two", "all"])
 def test_decode_of_blocks_of_very_different_value_scales(kind, dim):
     check_decodes(mixed_scales(kind, dim))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,gap,outlier,at", AHEAD)
+def test_prefill_of_one_key_ahead_of_many(n, gap, outlier, at, dtype):
+    b = one_ahead(n, gap, outlier, at, dtype, new=[9]).prefill()
+    assert_close(run_prefill(b), *b.prefill_reference())
+
+
+@pytest.mark.parametrize("heads,dim", [(16, 64), (16, 128), (1, 128)])
+def test_prefill_of_one_key_ahead_of_many_in_every_shape(heads, dim):
+    b = one_ahead(16384, 10.7, 1792.0, 9000, torch.bfloat16, heads=heads, dim=dim, new=[150 // heads + 2]).prefill()
+    assert_close(run_prefill(b), *b.prefill_reference())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kind", ["two", "wide"])
+def test_prefill_of_blocks_of_very_different_value_scales(kind, dim):
+    b = mixed_scales(kind, dim, new=[130, 40, 20]).prefill()
+    assert_close(run_prefill(b), *b.prefill_reference())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_of_value_scales_far_above_the_first_ones(dim):
+    """2^46 times the largest of the first 128 keys is taken, 2^47 gives NaN to the rows that read it; values
+    of zero in the first 128 keys stand for scales around 2^-8."""
+    b = Ranges([600, 400, 300], 4, 2, dim, 16, torch.bfloat16, 55, new=[40, 30, 20]).prefill()
+    for s in range(3):
+        b.vs[b.tables[s, : -(-b.lens_list[s] // 16)].long()] = 2.0 ** -9
+        b.vs[b.tables[s, 12].long(), 1] = 2.0 ** 37
+    b.vs[b.tables[1, :8].long()] = 2.0 ** -64
+    b.vs[b.tables[1, 12].long(), 1] = 2.0 ** 38
+    b.vc[b.tables[1, :8].long()] = 0
+    ref = b.prefill_reference()
+    assert_close(run_prefill(b), *ref)
+    b.vs[b.tables[0, 12].long(), 1] = 2.0 ** 38
+    b.vs[b.tables[1, 12].long(), 1] = 2.0 ** 39
+    got = run_prefill(b)
+    assert torch.isnan(got[:70, 2:]).all()
+    assert_close(got[:70, :2], ref[0][:70, :2], ref[1][:70, :2])
+    assert_close(got[70:], ref[0][70:], ref[1][70:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prefill_of_many_pairs_with_value_scales_of_their_own(dtype):
+    """More (sequence, KV head, pair of tiles) than the GPU has SMs, each sequence and head with values
+    of a size of its own: a CTA takes several, whose largest scales differ."""
+    g = np.random.default_rng(53)
+    lens = [int(x) for x in g.integers(100, 2600, 24)]
+    new = [min(n, int(x)) for n, x in zip(lens, g.integers(1, 24, 24))]
+    b = Ranges(lens, 32, 16, 64, 16, dtype, 54, new=new).prefill()
+    for s, n in enumerate(lens):
+        size = torch.exp2(torch.randint(-9, 4 if dtype == torch.float16 else 40, (1, 16), generator=torch.Generator().manual_seed(s)).float())
+        b.vs[b.tables[s, :-(-n // 16)].long()] *= size
+    assert_close(run_prefill(b), *b.prefill_reference())
