@@ -7,6 +7,8 @@ missing, every entry point raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -62,7 +64,7 @@ SIGNATURES = {
     "pa_last_error": (ctypes.c_char_p, []),
 }
 
-# The entry points that _fast.so (csrc/py_fast.cpp) calls, in the order its bind() takes.
+# The entry points that the binding's C++ half (csrc/py_fast.cpp) calls, in the order its bind() takes.
 FAST_ENTRIES = ("pa_reshape_and_cache_fp8_block", "pa_update_key_bounds", "pa_decode_fp8_block",
                 "pa_decode_splitk_fp8_block", "pa_prefill_fp8_block", "pa_select_blocks", "pa_decode_sparse")
 
@@ -102,11 +104,15 @@ def fast():
         L = lib()
         with _lock:
             if _fast is None:
+                from .build import fast_path
+                path = fast_path()
                 try:
-                    from . import _fast as m
+                    loader = importlib.machinery.ExtensionFileLoader(__package__ + "._fast", path)
+                    m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+                    loader.exec_module(m)
                 except ImportError as e:
-                    raise RuntimeError("the binding's C++ half (_fast.so) is missing or does not load: build it first "
-                                       "(python -m paged_kv_cache_173_gb300.build)") from e
+                    raise RuntimeError(f"the binding's C++ half for this torch and Python ({path}) is missing or does not "
+                                       "load: build it first (python -m paged_kv_cache_173_gb300.build)") from e
                 m.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in FAST_ENTRIES])
                 _fast = m
     return _fast

@@ -1,5 +1,5 @@
 """Build ``libpagedattn.so`` in-tree with nvcc for GB300 (sm_103a), and
-``_fast.so``, the C++ half of the Python binding, with the host compiler.
+``_fast.<torch and Python>.so``, the C++ half of the Python binding, with the host compiler.
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel, then linked into
 one shared library with the CUDA runtime linked statically, so the library
@@ -21,7 +21,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
-FAST = os.path.join(PKG, "_fast.so")
 FAST_SRC = os.path.join(CSRC, "py_fast.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -55,16 +54,27 @@ def _compile(src: str, ptxas_verbose: bool) -> str:
     return obj
 
 
+def fast_path() -> str:
+    """Where the binding's C++ half for the running torch and Python lies.  It is compiled against
+    their headers and reads their objects, so each pair of them has a file of its own."""
+    import sysconfig
+
+    import torch
+    abi = int(torch.compiled_with_cxx11_abi())
+    return os.path.join(PKG, f"_fast.torch-{torch.__version__}.cxx11abi-{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_fast(force: bool = False) -> str:
     """The binding's C++ half (torch's headers, no CUDA): a CPython extension in the package."""
     deps = [FAST_SRC, os.path.join(INCLUDE, "pagedattn.h")]
-    if not force and os.path.exists(FAST) and all(os.path.getmtime(p) <= os.path.getmtime(FAST) for p in deps):
-        return FAST
+    out = fast_path()
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
-    tmp = FAST + f".tmp{os.getpid()}"
+    tmp = out + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"),
@@ -74,8 +84,8 @@ def build_fast(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on py_fast.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, FAST)
-    return FAST
+    os.replace(tmp, out)
+    return out
 
 
 def build_library(force: bool = False, ptxas_verbose: bool = False) -> str:
