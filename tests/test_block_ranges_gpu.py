@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from block_cases import Batch, assert_close
+from oracle import block_oracle as bo
 from block_ranges import Ranges, mixed_scales, one_ahead
 from paged_kv_cache_173_gb300 import api
 from test_block_scaled_gpu import run_decode, run_prefill
@@ -189,3 +190,18 @@ def test_prefill_of_many_pairs_with_value_scales_of_their_own(dtype):
         size = torch.exp2(torch.randint(-9, 4 if dtype == torch.float16 else 40, (1, 16), generator=torch.Generator().manual_seed(s)).float())
         b.vs[b.tables[s, :-(-n // 16)].long()] *= size
     assert_close(run_prefill(b), *b.prefill_reference())
+
+
+# ------------------------------------------------------------------ bounds of the largest keys
+@pytest.mark.parametrize("dtype,top,exponent", [(torch.float16, 65504.0, 10), (torch.bfloat16, 3.3895313892515355e38, 122)])
+def test_bounds_of_the_largest_keys(dtype, top, exponent):
+    """A block whose bounds hold the largest elements of the type, then smaller ones."""
+    codes, exps = np.zeros((2, 1, 2, 64), np.int8), np.full((2, 1), -100, np.int32)
+    dev = torch.from_numpy(codes).cuda(), torch.from_numpy(exps).cuda()
+    for slots, size in (([16, 17], 1.0), ([18], 2.0 ** -8), ([19, 20, 21], 2.0 ** -3)):
+        key = (torch.linspace(-1.0, 1.0, 64).repeat(len(slots), 1, 1) * size * top).to(dtype)
+        codes, exps = bo.bounds(key.double().numpy(), codes, exps, np.array(slots), 16)
+        api.pa_update_key_bounds(key.cuda(), *dev, torch.tensor(slots).cuda(), 16)
+        torch.cuda.synchronize()
+        assert exps[1, 0] == exponent
+        assert np.array_equal(dev[0].cpu().numpy(), codes) and np.array_equal(dev[1].cpu().numpy(), exps)
