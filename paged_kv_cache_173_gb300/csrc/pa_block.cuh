@@ -40,6 +40,10 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= kFloatMax ? a : 0.f;
 }
 
+// Two to four units in the last place of x above it: a maximum that has room for the roundings of
+// what is taken off it before it is the largest weight's exponent, which float16 bounds.
+__device__ __forceinline__ float rounded_up(float x) { return fmaf(fabsf(x), 2.384185791015625e-7f, x); }
+
 }  // namespace
 
 }  // namespace pa

@@ -165,8 +165,8 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
       mx0 = fmaxf(mx0, __shfl_xor_sync(FULL_MASK, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, off));
     }
-    const float mn0 = fmaxf(acc.m[nt][0], mx0 - kTopWeight);
-    const float mn1 = fmaxf(acc.m[nt][1], mx1 - kTopWeight);
+    const float mn0 = fmaxf(acc.m[nt][0], rounded_up(mx0) - kTopWeight);
+    const float mn1 = fmaxf(acc.m[nt][1], rounded_up(mx1) - kTopWeight);
     const float cr0 = ex2(acc.m[nt][0] - mn0);
     const float cr1 = ex2(acc.m[nt][1] - mn1);
     const bool grew = __any_sync(FULL_MASK, (mn0 != acc.m[nt][0]) | (mn1 != acc.m[nt][1]));

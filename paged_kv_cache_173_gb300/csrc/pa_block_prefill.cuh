@@ -990,7 +990,7 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
         }
         mx = fmaxf(mx, fmaf(e, factor(sc[c].x), sc[c].y));
       }
-      const float m_new = fmaxf(m_used, mx);
+      const float m_new = fmaxf(m_used, rounded_up(mx));  // (a row that sees no key here keeps its own: the other is NaN)
       // The exponent's offset moves at the first block and when the row maximum has grown
       // by more than 2^8; O and l then scale by f.
       const bool none = m_used == -INFINITY;  // nothing in O yet

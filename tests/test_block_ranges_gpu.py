@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_cases import Batch, assert_close
+from block_cases import HALF_STEP, Batch, assert_close
 from oracle import block_oracle as bo
 from block_ranges import Ranges, mixed_scales, one_ahead
 from paged_kv_cache_173_gb300 import api
@@ -190,6 +190,36 @@ def test_prefill_of_many_pairs_with_value_scales_of_their_own(dtype):
         size = torch.exp2(torch.randint(-9, 4 if dtype == torch.float16 else 40, (1, 16), generator=torch.Generator().manual_seed(s)).float())
         b.vs[b.tables[s, :-(-n // 16)].long()] *= size
     assert_close(run_prefill(b), *b.prefill_reference())
+
+
+# ------------------------------------------------------------------ scores of any size
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 23, 2.0 ** 24, 1.3 * 2.0 ** 24, 2.0 ** 25, 1.6 * 2.0 ** 25])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_whose_rounding_is_large(size, sign, dtype):
+    """The best keys score +-`size` (in units of log 2), all others `size` or half of it less: the output is
+    the mean of the best keys' values, whatever a score's last place is worth."""
+    b = Ranges([300, 200], 4, 2, 64, 16, dtype, 56, new=[40, 130])
+    best = [[3, 200, 255], [0, 1, 66]]
+    b.keys16 = torch.zeros_like(b.keys16).float()
+    b.keys16[..., 1] = 224.0 if sign > 0 else 448.0
+    for s in range(2):
+        for p in best[s]:
+            b.keys16[int(b.tables[s, p // 16]), p % 16, :, 1] = 448.0 if sign > 0 else 224.0
+    b.recode()
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 1] = sign
+    b.scale = size / (448.0 if sign > 0 else 224.0) / 1.4426950408889634
+    want, tol = np.zeros((2, 4, 64)), np.zeros((2, 4, 64))
+    for s in range(2):
+        for h in range(4):
+            rows = bo.rows(b.vc.numpy(), b.vs.numpy(), b.tables[s].numpy(), b.lens_list[s], h // 2)[best[s]]
+            want[s, h] = rows.mean(0)
+            tol[s, h] = 2.0 ** -11 * np.abs(rows).mean(0) + HALF_STEP[dtype] * np.abs(want[s, h]) + 2.0 ** -20 * np.abs(rows).max()
+    assert_close(run_prefill(b)[[39, 169]], want, tol)
+    b.q = b.q[:2]
+    for got in (run_decode(b), run_decode(b, 64)):
+        assert_close(got, want, tol)
 
 
 # ------------------------------------------------------------------ bounds of the largest keys
