@@ -10,11 +10,11 @@
 //                        not fill the GPU.
 //
 // HBM bounds it: 2 d bytes per token and KV head.  64 sequences of 128 to 2048
-// tokens, 32/8 heads of 128: 146 MB in 29.3 us (5.0 TB/s; the start, and the tail of
+// tokens, 32/8 heads of 128: 146 MB in 29.7 us (4.9 TB/s; the start, and the tail of
 // the longest sequences, are most of the rest); 32 of 8192, 64/8 heads: 538 MB in
-// 83 us (6.5 TB/s).  With a table per head the 128-byte rows of a block lie 1 KB
-// apart and their neighbours are not wanted: 101 MB in about 24 us.  One sequence
-// of 485 tokens: 4.9 us, latency.
+// 84 us (6.4 TB/s).  With a table per head the 128-byte rows of a block lie 1 KB
+// apart and their neighbours are not wanted: 101 MB in about 24 us, by 256 CTAs on
+// 304 places.  One sequence of 485 tokens: 4.7 us, latency.  (Graph replays.)
 //
 // The mathematics of the scales.  Block b of a sequence holds the keys
 // ks_b * code and the values v_b * code.  With s_i the base-2 score of token i
@@ -198,9 +198,10 @@ __device__ __forceinline__ void softmax_step_scaled(WarpAcc<HEAD_DIM, NT>& acc, 
 
 // O^T += vs * V^T P^T over one chunk's codes: pv_e4m3 (pa_decode.cuh) with the
 // chunk's products apart from the accumulators until they are scaled: NT * d / 4
-// multiply-adds a lane and chunk (64 sequences of 128 to 2048 tokens 29.4 -> 29.7
-// us, 32 of 8192 82.5 -> 84.0 us, split-K of 32 K to 131 K and the sparse steps the
-// same, one of 485 tokens 4.95 -> 4.90 us).
+// multiply-adds a lane and chunk (with all of the scale in the exponent 64 sequences
+// of 128 to 2048 tokens took 29.4 us, now 29.7; 32 of 8192 82.5 and 84.0 us; d = 256, 32
+// of 128 to 4096, 36.7 and 38.0 us; split-K of 32 K to 131 K, the sparse steps and one of
+// 485 tokens as long as now).
 template <int HEAD_DIM, int NT, int ROW_BYTES, bool MASK>
 __device__ __forceinline__ void pv_e4m3_scaled(WarpAcc<HEAD_DIM, NT>& acc, const uint32_t (&pb)[NT][2], uint32_t vaddr,
                                                uint32_t tok, uint32_t uo, uint32_t mlo, uint32_t mhi, float vs) {
@@ -266,6 +267,7 @@ __device__ __forceinline__ void attend_scaled(WarpAcc<HEAD_DIM, NT>& acc, const 
 // per SM that the registers are bounded for (0: unbounded).  Measured on one GPU
 // through graph replays, E4M3 pools, beside the shapes of the pool-scaled decode
 // (DecodeShape: 4 warps x 2 stages x 2 chunks up to d = 128):
+// (The figures compare shapes of one kernel, before the products were scaled apart.)
 //  - single launch, d = 128, groups up to 8: 8 x 2 x 1.  A CTA that walks a long
 //    sequence alone is paced by its warps' chains, and eight of them halve its
 //    share of each (64 sequences of 128 to 2048 tokens, 32/8 heads: 31.2 -> 29.3
@@ -276,7 +278,7 @@ __device__ __forceinline__ void attend_scaled(WarpAcc<HEAD_DIM, NT>& acc, const 
 //  - split-K, whose CTAs cover a partition: many small CTAs overlap their
 //    beginnings and ends.  d = 128: 2 x 2 x 2, six per SM (32 K to 131 K tokens, 512
 //    per partition: 139.8 -> 129.4 us); groups of 16: 2 x 2 x 1 (227 -> 175 us);
-//    d = 256: 2 x 2 x 1 (82.5 -> 80.0 us).
+//    d = 256: 2 x 2 x 1 (82.5 -> 80.0 us), five per SM now (6: 84.6 us, 5: 82.8 us).
 template <int HEAD_DIM, int NT, int ELEM, int KIND, bool PER_HEAD>
 struct BlockShape {
   using Base = DecodeShape<HEAD_DIM, ELEM, KIND>;
@@ -286,7 +288,7 @@ struct BlockShape {
   static constexpr int WARPS = WIDE ? 8 : SMALL ? 2 : Base::WARPS;
   static constexpr int STAGES = WIDE || SMALL ? 2 : Base::STAGES;
   static constexpr int CPS = FP8 && (HEAD_DIM == 64 || (HEAD_DIM == 128 && !WIDE && (!SMALL || NT == 1))) ? 2 : 1;
-  static constexpr int MIN_CTAS = WIDE ? 2 : SMALL ? (NT == 1 ? 6 : 5) : 0;
+  static constexpr int MIN_CTAS = WIDE ? 2 : SMALL ? (NT == 1 && HEAD_DIM < 256 ? 6 : 5) : 0;
 };
 // Tokens of table capacity per CTA of a cluster, at least (a context of 485: 6.0 us
 // with 512, 4.9 us with 128).
