@@ -627,8 +627,8 @@ int pa_prefill_fp8_block(void* out, const void* q, const void* k_cache, const vo
 /*
  * Block-sparse decode.  Of a long context, each new token attends to a bounded
  * number of blocks per KV head: the first ones, the last ones and those whose
- * keys can score highest.  What can score highest is read from bounds of each
- * block's keys, kept in 8 bits beside the pool (of any element type):
+ * keys score highest by an estimate, which is made from bounds of each block's
+ * keys, kept in 8 bits beside the pool (of any element type):
  *
  *   key_bounds  [num_blocks][num_kv_heads][2][head_dim] int8: per channel c the
  *               codes lo_c, hi_c in [-127, 127]
@@ -672,8 +672,10 @@ size_t pa_select_workspace_bytes(int num_seqs, int num_kv_heads, int max_blocks_
 /*
  * pa_select_blocks -- choose the blocks that each (sequence, KV head) reads.
  *
- * The score of block b of sequence s for KV head h, a bound of the largest
- * score that one of its keys can reach:
+ * The score of block b of sequence s for KV head h, an estimate of the largest
+ * score that one of its keys can reach (the largest one that the bounds leave room
+ * for, for the query rounded to whole numbers; where a key was infinite or NaN the
+ * bounds leave out what it can reach):
  *
  *   qi_c  = rint(q_c / 2^f), f the smallest number >= -100 with max|q| <= 255 * 2^f
  *           over the finite elements of the query head's row (an infinite

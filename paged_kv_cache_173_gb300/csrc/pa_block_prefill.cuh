@@ -23,10 +23,11 @@
 //    the outputs of the last pair.
 //  - 128 scores per softmax thread leave few registers for the rest.  The launch's
 //    512 x 128 registers are shared out by role, so that nothing is spilled in a loop.
-// Measured (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of 2048 tokens 227 us,
-// 2 of 16384 2974 us (0.78 of the measured peak), 16 x 512 on 16384 cached 1546 us;
-// bf16, 16 chunks of 509 on 1536 cached 201 us.  One CTA per pair, one MMA warp for
-// both tiles: 282, 3005, 1584 and 230 us.
+// Measured through graph replays (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of
+// 2048 tokens 231 us, 2 of 16384 2998 us (0.77 of the measured peak), 16 x 512 on 16384
+// cached 1551 us; bf16, 16 chunks of 509 on 1536 cached 205 us.  Before the codes were
+// multiplied by a part of the value scale: 226, 2955, 1535 and 203 us; with that, one CTA per
+// pair and one MMA warp for both tiles: 282, 3005, 1584 and 230 us.
 //
 // The mathematics of the scales.  The value scale of a block b is split,
 // v_b = 2^(ref + 3) 2^kappa_b 2^r_b, with 2^ref the power of two of the largest scale
@@ -107,7 +108,7 @@ struct BpCfg {
   static constexpr int MMA_WARP = PROD_WARP + PROD_WARPS;
   static constexpr int ITEM_WARP = MMA_WARP + TC_TILES;
   static constexpr int THREADS = SOFT + PROD + 128;
-  // (d = 64 holds half the codes per producer; with the split of d = 128 it takes 189 us, not 185)
+  // (d = 64 holds half the codes per producer; with the split of d = 128 it took 189 us, not 185)
   static constexpr int SOFT_REGS = HEAD_DIM == 64 ? 168 : 160;
   static constexpr int PROD_REGS = HEAD_DIM == 64 ? 112 : 120;
   static constexpr int MMA_REGS = HEAD_DIM == 64 ? 64 : 72;
@@ -428,8 +429,8 @@ block_prefill_tc_kernel(const __grid_constant__ BlockPrefillParams p) {
   int* infos = reinterpret_cast<int*>(sm + C::INFO_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
   // Phases count over all items of the CTA.
-  uint64_t* kfull = bars;                  // [KS] K of a block is widened (96 arrivals)
-  uint64_t* vfull = kfull + KS;            // [VS] V of a block is widened (96 arrivals)
+  uint64_t* kfull = bars;                  // [KS] K of a block is widened (128 arrivals)
+  uint64_t* vfull = kfull + KS;            // [VS] V of a block is widened (128 arrivals)
   // step n: P V of block n - 1, then Q K^T of block n.  One commit per step and tile frees K of
   // block n and V of block n - 1.
   uint64_t* done = vfull + VS;             // [DONE] both tiles' MMAs of a step have completed
