@@ -29,7 +29,7 @@
 // weight's exponent, 2^(s_i + log2 v_b - M), the MMAs accumulate on, but a block of
 // large values that a sequence hardly attends to pushes the weights of all others
 // towards float16's end: 131072 keys behind one by 12 nats whose block's scale is
-// 2^8 times theirs came out 4% short.)
+// 2^8 times theirs came out 5% short.)
 //
 // A weight is float16: m lies 15 below the largest score, so the largest weight is
 // 2^15, and every weight above 2^-29 of it has 11 bits, a smaller one is off by

@@ -26,8 +26,8 @@
 // Measured through graph replays (fp16, 32/8 heads of 128, blocks of 16): 8 prompts of
 // 2048 tokens 231 us, 2 of 16384 2998 us (0.77 of the measured peak), 16 x 512 on 16384
 // cached 1551 us; bf16, 16 chunks of 509 on 1536 cached 205 us.  Before the codes were
-// multiplied by a part of the value scale: 226, 2955, 1535 and 203 us; with that, one CTA per
-// pair and one MMA warp for both tiles: 282, 3005, 1584 and 230 us.
+// multiplied by a part of the value scale: 226, 2955, 1535 and 203 us; and before that, with
+// one CTA per pair and one MMA warp for both tiles: 282, 3005, 1584 and 230 us.
 //
 // The mathematics of the scales.  The value scale of a block b is split,
 // v_b = 2^(ref + 3) 2^kappa_b 2^r_b, with 2^ref the power of two of the largest scale
