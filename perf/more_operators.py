@@ -433,11 +433,12 @@ def _extend(st):
     last_at = (had - 1).clamp(min=0).long()
     last = tables[row, last_at].long()
     copy = (new > 0) & (lens % block != 0) & (counts[last.clamp(min=0)] > 1)
-    need = torch.where(new > 0, want - had + copy.to(torch.int32), torch.zeros_like(new)).long()
+    fits = lens + new <= width * block
+    need = torch.where((new > 0) & fits, want - had + copy.to(torch.int32), torch.zeros_like(new)).long()
     upto = torch.cumsum(need, 0)
     free = counts == 0
     total = free.sum()
-    ok = (lens + new <= width * block) & ((need == 0) | (upto <= total))
+    ok = fits & ((need == 0) | (upto <= total))
     need = torch.where(ok, need, torch.zeros_like(need))
     copy &= ok
     # the free blocks in order, and each sequence's among them
