@@ -736,6 +736,183 @@ int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* 
                      int dtype, int kv_dtype, void* stream);
 
 /*
+ * pa_prefill_packed -- attention over whole prompts whose keys and values are the new
+ * tokens' own rows, packed one prompt behind the other; on request each token's key
+ * and value rows go into the pools in the same launch.
+ *
+ * A prompt that is not cached yet needs nothing from the pools: this is pa_prefill for
+ * context_lens[s] = qlen with the cache write of pa_reshape_and_cache in it (as
+ * pa_append_and_decode holds the write of a decode step), and without its way through
+ * the block table ("in-depth reading", section 5.1, item 5; "vAttention", paged against
+ * contiguous prefill).  Sequence s owns the rows [query_start_loc[s],
+ * query_start_loc[s + 1]); for each of its rows t and query heads h
+ *
+ *   out[t][h][:] = sum_{u <= t} softmax_u(scale * q[t][h] . key[u][h / G]) value[u][h / G],
+ *
+ * u over the sequence's own rows.
+ *
+ *   q                 rows of q_stride elements, a token's heads [num_heads][head_dim]
+ *                     first in each; key, value likewise with k_stride, v_stride and
+ *                     num_kv_heads.  So all three may be parts of one projection's
+ *                     rows.  Strides are multiples of 8 elements.
+ *   out               [num_rows][num_heads][head_dim] of dtype, contiguous
+ *   query_start_loc   [num_seqs + 1] int32, non-decreasing, starting at 0.  Rows
+ *                     behind the last sequence are left as they were, in out and pools.
+ *   max_query_len     >= every prompt's length (sizes the grid; rows past it are neither
+ *                     computed nor written into the pools)
+ *   k_cache, v_cache,
+ *   slot_mapping      all NULL: no write.  Otherwise as pa_reshape_and_cache, one slot per
+ *                     row, pools of dtype and of any block size; the written rows are
+ *                     bit-exact copies
+ *   head_dim          64 or 128; num_heads / num_kv_heads <= 16, any whole number
+ *
+ * Scores, softmax and accumulation are float32.  The weights enter P.V rounded to the
+ * values' type (fp16: 11 bits, the largest weight near 2^15; bf16: 8 bits), each off by
+ * half a step of its own, and are summed unrounded.
+ *
+ * Device-value outcomes: rows of a sequence that ends before it starts are left as they
+ * were; a start or end outside [0, num_rows] counts as the nearest of the two.  What is not
+ * finite in a row of q, key or value reaches only the rows that see it: in a value it
+ * makes its channel not finite (NaN, or the infinity itself).  Nothing is read or written
+ * out of bounds.
+ */
+int pa_prefill_packed(void* out, const void* q, int64_t q_stride, const void* key, int64_t k_stride,
+                      const void* value, int64_t v_stride, void* k_cache, void* v_cache,
+                      const int64_t* slot_mapping, const int32_t* query_start_loc, int num_seqs,
+                      int num_rows, int max_query_len, int num_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, float scale, int dtype, void* stream);
+
+/*
+ * The sequences' blocks on the device.  Which sequence holds which blocks, kept where the
+ * kernels read it, so that a step (and a captured graph of steps) can grow, fork, cut and
+ * free sequences without the host:
+ *
+ *   block_tables  [num_seqs][max_blocks_per_seq] int32, as everywhere
+ *   context_lens  [num_seqs] int32; 0: the row is unused
+ *   ref_counts    [num_blocks] int32, 16-byte aligned: how many table rows hold the block.
+ *                 A block whose count is 0 is free.  A program keeps a block for itself
+ *                 (a cached prefix) by adding to its count.
+ *
+ * ("Unveiling the NVIDIA driver stack: GPU page tables and vLLM PagedAttention", section
+ * 4, and "in-depth reading", section 2.4: blocks are handed out on demand, shared with a
+ * reference count and copied on write.)  Counts and tables that agree stay in agreement;
+ * the results do not depend on the order in which threads run.  Tables hold at most
+ * 2^31 - 1025 tokens.  Calls that change the same tables or counts are ordered by the
+ * caller (one stream).  An id outside [0, num_blocks) in a table is passed over, and a
+ * sequence whose length is negative or past its table's capacity is left alone.
+ */
+
+/*
+ * pa_sequence_workspace_bytes -- size of the workspace of pa_extend_sequences and
+ * pa_compact_blocks: an int32 per block (rounded up to 4) and 16 more.  Returns 0 for
+ * non-positive arguments.
+ */
+size_t pa_sequence_workspace_bytes(int num_blocks);
+
+/*
+ * pa_extend_sequences -- room for new tokens: sequence s grows by
+ * n = query_start_loc[s + 1] - query_start_loc[s] >= 0 tokens.
+ *
+ * Sequences that bring tokens take, in their order, the lowest free blocks:
+ *
+ *   ceil((len + n) / B) - ceil(len / B)  new ones behind their last, and before these
+ *   one in the place of a last block that is partly filled and has a count above 1: the
+ *   sequence leaves the shared block (its count falls by 1) and the pair (old, new) is
+ *   asked for in block_copies.  (Where all holders of a block leave it in one call,
+ *   it is free afterwards.)
+ *
+ * Then context_lens[s] += n, and the tokens' slots are written.  Blocks that the call
+ * itself frees are not handed out by it, so that their contents are there for the copies.
+ *
+ *   query_start_loc  [num_seqs + 1] int32, as for pa_prefill
+ *   slot_mapping     [num_tokens] int64, written: slot of each new token; -1 for tokens of
+ *                    sequences that were refused and from query_start_loc[num_seqs] on
+ *   block_copies     [num_seqs][2] int64, written: (source, destination) of the block to
+ *                    copy, or (-1, -1); as pa_copy_blocks and pa_copy_layer_blocks take it.
+ *                    Copy before the new tokens are written.
+ *   left             [2] int32, written: the free blocks that were not handed out, and the
+ *                    number of sequences that were refused
+ *   workspace        device buffer of workspace_bytes >= pa_sequence_workspace_bytes(
+ *                    num_blocks), 16-byte aligned; scratch, contents on entry ignored
+ *
+ * Refused, and left as they were, are: the first sequence whose blocks are not there and
+ * every later one that needs a block; a sequence that would outgrow its table; one whose
+ * partly filled last block lies outside the pool; one whose range of tokens is reversed or
+ * leaves [0, num_tokens].
+ */
+int pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                        int32_t* ref_counts, const int32_t* query_start_loc, int64_t* slot_mapping,
+                        int64_t* block_copies, int32_t* left, int num_seqs, int num_tokens,
+                        int num_blocks, int block_size, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * pa_truncate_sequences -- cut sequences to a length; 0 frees them.
+ *
+ * Where 0 <= new_lens[s] < context_lens[s], the table entries from ceil(new_lens[s] / B) on
+ * become -1, their blocks' counts fall by 1 each, and context_lens[s] = new_lens[s].  Other
+ * sequences stay as they are.
+ *
+ *   new_lens  [num_seqs] int32
+ */
+int pa_truncate_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                          int32_t* ref_counts, const int32_t* new_lens, int num_seqs, int num_blocks,
+                          int block_size, void* stream);
+
+/*
+ * pa_fork_sequences -- sequence s becomes a copy of sequence fork_from[s] and shares its
+ * blocks: it takes over the length and the table entries, and their counts grow by 1.
+ *
+ *   fork_from  [num_seqs] int32; negative: no fork
+ *
+ * Left alone is a sequence that is not empty (context_lens[s] != 0), and one whose source
+ * lies outside the batch or is itself named to be forked onto (fork_from >= 0).
+ */
+int pa_fork_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
+                      int32_t* ref_counts, const int32_t* fork_from, int num_seqs, int num_blocks,
+                      int block_size, void* stream);
+
+/*
+ * pa_compact_blocks -- plan the moves that bring the used blocks to the front of the pool,
+ * at most max_moves of them, and write the tables and counts as they are afterwards.
+ *
+ * Move i takes the i-th used block from the top (count != 0) to the i-th free block from the
+ * bottom, as long as that lies below it.  After all such moves the used blocks are the
+ * first ones and the rest of the pool is free.
+ *
+ *   moves       [max_moves][2] int64, written: (source, destination), then (-1, -1); as
+ *               pa_copy_layer_blocks takes it.  Copy before the sources' blocks are handed
+ *               out again.
+ *   num_moves   [1] int32, written
+ *   tables_out  [num_seqs][max_blocks_per_seq] int32 and
+ *   counts_out  [num_blocks] int32 (16-byte aligned), written: what block_tables and
+ *               ref_counts are after the moves.  Each may be the input itself, otherwise they do
+ *               not overlap it.  Entries past a context are copied as they are.
+ *   workspace   as pa_extend_sequences
+ */
+int pa_compact_blocks(int64_t* moves, int max_moves, int32_t* num_moves, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* context_lens, const int32_t* ref_counts,
+                      int32_t* tables_out, int32_t* counts_out, int num_seqs, int num_blocks,
+                      int block_size, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_copy_layer_blocks -- pa_copy_blocks for the pools of all layers in one launch: keys,
+ * values, or whatever else is kept per block (scales, bounds).
+ *
+ * For every pool l < num_pools and every pair i < num_pairs:
+ *   pool l's block block_mapping[2i + 1] = its block block_mapping[2i], a bit-exact copy.
+ *
+ *   pools        pool l starts at pools + l * pool_stride bytes and holds num_blocks blocks
+ *                of block_bytes each; pool_stride >= num_blocks * block_bytes
+ *   block_bytes  a multiple of 4, as the pools' addresses are (16 and more is faster)
+ *
+ * Pairs as pa_copy_blocks: one with an id outside [0, num_blocks), or with equal ids, is
+ * skipped; destinations are distinct and none is the source of another pair.
+ */
+int pa_copy_layer_blocks(void* pools, int64_t pool_stride, int num_pools, int64_t block_bytes,
+                         const int64_t* block_mapping, int num_pairs, int num_blocks, void* stream);
+
+/*
  * pa_selftest_wait -- checks, on the device, the bounded wait that every
  * pipeline of this library uses on its mbarriers (TMA copies landing, MMAs
  * completing, softmax threads handing over P): a wait that runs past its

@@ -27,6 +27,7 @@ PA_FP8_E4M3 = 2
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_int64
 _SZ = ctypes.c_size_t
 SIGNATURES = {
     "pa_reshape_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
@@ -59,6 +60,13 @@ SIGNATURES = {
     "pa_select_workspace_bytes": (_SZ, [_I, _I, _I]),
     "pa_select_blocks": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _SZ, _P]),
     "pa_decode_sparse": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
+    "pa_prefill_packed": (_I, [_P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "pa_sequence_workspace_bytes": (_SZ, [_I]),
+    "pa_extend_sequences": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P]),
+    "pa_truncate_sequences": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "pa_fork_sequences": (_I, [_P, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "pa_compact_blocks": (_I, [_P, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _SZ, _P]),
+    "pa_copy_layer_blocks": (_I, [_P, _L, _I, _L, _P, _I, _I, _P]),
     "pa_selftest_wait": (_I, [_P, ctypes.c_uint, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_last_error": (ctypes.c_char_p, []),

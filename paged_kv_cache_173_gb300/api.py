@@ -602,6 +602,161 @@ def pa_decode_sparse(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, 
           _ptr(sel_lens, "sel_lens", torch.int32, i), S, H, Hk, d, B, N, float(scale), code, kv))
 
 
+# ---------------------------------------------------------------------------
+# Whole prompts in packed rows, and the sequences' blocks on the device.
+# ---------------------------------------------------------------------------
+def _ptr_rows(t: torch.Tensor, name: str, dtype: torch.dtype, index: int):
+    """Pointer and row stride (elements) of a [rows, heads, d] tensor whose rows are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    rows, heads, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of one token of {name} must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else heads * d
+
+
+def pa_prefill_packed(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                      query_start_loc: torch.Tensor, max_query_len: int, scale: float,
+                      k_cache: Optional[torch.Tensor] = None, v_cache: Optional[torch.Tensor] = None,
+                      slot_mapping: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Causal attention over whole prompts: q [rows, H, d], key and value [rows, Hk, d] (rows
+    of any stride: parts of one projection's output will do), sequence s owning the rows
+    query_start_loc[s] .. query_start_loc[s+1].  With k_cache, v_cache [N, B, Hk, d] and
+    slot_mapping [rows] (int64) the key and value rows go into the pools as well."""
+    i = _cuda_index(q)
+    R, H, d = q.shape
+    Hk = key.shape[1] if key.dim() == 3 else 0
+    if out.shape != q.shape or key.shape != (R, Hk, d) or value.shape != key.shape:
+        raise ValueError("q/out must be [rows, H, d] and key/value [rows, Hk, d]")
+    if query_start_loc.dim() != 1 or query_start_loc.shape[0] < 1:
+        raise ValueError("query_start_loc must be [S + 1]")
+    S = query_start_loc.shape[0] - 1
+    dt = q.dtype
+    code = _dtype_code(q)
+    N = B = 0
+    pools = (None, None, None)
+    if k_cache is not None or v_cache is not None or slot_mapping is not None:
+        if k_cache is None or v_cache is None or slot_mapping is None:
+            raise ValueError("k_cache, v_cache and slot_mapping are given together or not at all")
+        if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, d) or v_cache.shape != k_cache.shape:
+            raise ValueError(f"k_cache and v_cache must be [N, B, Hk, d] with Hk = {Hk}, d = {d}")
+        if slot_mapping.shape != (R,):
+            raise ValueError("slot_mapping must be [rows]")
+        N, B = k_cache.shape[:2]
+        pools = (_ptr(k_cache, "k_cache", dt, i), _ptr(v_cache, "v_cache", dt, i),
+                 _ptr(slot_mapping, "slot_mapping", torch.int64, i))
+    _run(_lib.lib().pa_prefill_packed, "pa_prefill_packed", i, stream,
+         (_ptr(out, "out", dt, i), *_ptr_rows(q, "q", dt, i), *_ptr_rows(key, "key", dt, i),
+          *_ptr_rows(value, "value", dt, i), *pools, _ptr(query_start_loc, "query_start_loc", torch.int32, i), S, R,
+          int(max_query_len), H, Hk, d, B, N, float(scale), code))
+
+
+def pa_sequence_workspace_bytes(num_blocks: int) -> int:
+    return int(_lib.lib().pa_sequence_workspace_bytes(num_blocks))
+
+
+def alloc_sequence_workspace(num_blocks: int, device) -> torch.Tensor:
+    """An int32 device buffer of the size pa_sequence_workspace_bytes states."""
+    return torch.empty(max(1, pa_sequence_workspace_bytes(num_blocks) // 4), dtype=torch.int32, device=device)
+
+
+def _sequence_args(block_tables, context_lens, ref_counts):
+    """Device index, S, M, N and the pointers of the sequences' tables, lengths and counts."""
+    i = _cuda_index(block_tables)
+    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],):
+        raise ValueError("block_tables must be [S, M] and context_lens [S]")
+    if ref_counts.dim() != 1:
+        raise ValueError("ref_counts must be [N]")
+    S, M = block_tables.shape
+    return i, S, M, ref_counts.shape[0], (_ptr(block_tables, "block_tables", torch.int32, i), M,
+                                          _ptr(context_lens, "context_lens", torch.int32, i),
+                                          _ptr(ref_counts, "ref_counts", torch.int32, i))
+
+
+def pa_extend_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_counts: torch.Tensor,
+                        query_start_loc: torch.Tensor, slot_mapping: torch.Tensor, block_copies: torch.Tensor,
+                        left: torch.Tensor, block_size: int, workspace: torch.Tensor,
+                        stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Make room for query_start_loc[s+1] - query_start_loc[s] new tokens of each sequence: free
+    blocks (ref_counts [N] == 0) go into block_tables [S, M] and context_lens [S] grows.  Writes
+    the tokens' slots (slot_mapping, int64), the copies that shared last blocks need
+    (block_copies [S, 2], int64) and left [2] (free blocks, refused sequences)."""
+    i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
+    if query_start_loc.shape != (S + 1,):
+        raise ValueError("query_start_loc must be [S + 1]")
+    if slot_mapping.dim() != 1 or block_copies.shape != (S, 2) or left.shape != (2,):
+        raise ValueError("slot_mapping must be [tokens], block_copies [S, 2] and left [2]")
+    _run(_lib.lib().pa_extend_sequences, "pa_extend_sequences", i, stream,
+         head + (_ptr(query_start_loc, "query_start_loc", torch.int32, i),
+                 _ptr(slot_mapping, "slot_mapping", torch.int64, i), _ptr(block_copies, "block_copies", torch.int64, i),
+                 _ptr(left, "left", torch.int32, i), S, slot_mapping.shape[0], N, int(block_size),
+                 _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()))
+
+
+def pa_truncate_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_counts: torch.Tensor,
+                          new_lens: torch.Tensor, block_size: int,
+                          stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Cut each sequence with 0 <= new_lens[s] < context_lens[s] to new_lens[s] tokens (0: free it)
+    and give its blocks back."""
+    i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
+    if new_lens.shape != (S,):
+        raise ValueError("new_lens must be [S]")
+    _run(_lib.lib().pa_truncate_sequences, "pa_truncate_sequences", i, stream,
+         head + (_ptr(new_lens, "new_lens", torch.int32, i), S, N, int(block_size)))
+
+
+def pa_fork_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_counts: torch.Tensor,
+                      fork_from: torch.Tensor, block_size: int, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Each empty sequence with fork_from[s] >= 0 becomes a copy of that sequence and shares its blocks."""
+    i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
+    if fork_from.shape != (S,):
+        raise ValueError("fork_from must be [S]")
+    _run(_lib.lib().pa_fork_sequences, "pa_fork_sequences", i, stream,
+         head + (_ptr(fork_from, "fork_from", torch.int32, i), S, N, int(block_size)))
+
+
+def pa_compact_blocks(moves: torch.Tensor, num_moves: torch.Tensor, block_tables: torch.Tensor,
+                      context_lens: torch.Tensor, ref_counts: torch.Tensor, tables_out: torch.Tensor,
+                      counts_out: torch.Tensor, block_size: int, workspace: torch.Tensor,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Plan at most len(moves) moves of the highest used blocks to the lowest free ones: moves
+    [max, 2] (int64), num_moves [1] (int32), and the tables and counts after them (tables_out,
+    counts_out: the inputs themselves, or others).  Follow with pa_copy_layer_blocks."""
+    i, S, M, N, (tables, _, lens, counts) = _sequence_args(block_tables, context_lens, ref_counts)
+    if moves.dim() != 2 or moves.shape[1] != 2 or num_moves.shape != (1,):
+        raise ValueError("moves must be [max_moves, 2] and num_moves [1]")
+    if tables_out.shape != block_tables.shape or counts_out.shape != ref_counts.shape:
+        raise ValueError("tables_out must be [S, M] and counts_out [N]")
+    _run(_lib.lib().pa_compact_blocks, "pa_compact_blocks", i, stream,
+         (_ptr(moves, "moves", torch.int64, i), moves.shape[0], _ptr(num_moves, "num_moves", torch.int32, i), tables, M,
+          lens, counts, _ptr(tables_out, "tables_out", torch.int32, i), _ptr(counts_out, "counts_out", torch.int32, i), S,
+          N, int(block_size), _ptr(workspace, "workspace", workspace.dtype, i),
+          workspace.numel() * workspace.element_size()))
+
+
+def pa_copy_layer_blocks(pools: torch.Tensor, block_mapping: torch.Tensor,
+                         stream: Optional[torch.cuda.Stream] = None) -> None:
+    """For each row (src, dst) of block_mapping [n, 2] (int64) and each layer l of pools [L, N, ...]
+    (any type; a layer's blocks contiguous): pools[l, dst] = pools[l, src]."""
+    i = _cuda_index(pools)
+    if pools.dim() < 3:
+        raise ValueError("pools must be [L, N, ...]: the pools of L layers")
+    if block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
+        raise ValueError("block_mapping must be [n, 2]")
+    L, N = pools.shape[:2]
+    if L == 0 or pools.numel() == 0:
+        return
+    if not pools[0].is_contiguous():
+        raise ValueError("the blocks of one layer must be contiguous")
+    width = pools.element_size()
+    _run(_lib.lib().pa_copy_layer_blocks, "pa_copy_layer_blocks", i, stream,
+         (pools.data_ptr(), pools.stride(0) * width, L, pools.numel() // (L * N) * width,
+          _ptr(block_mapping, "block_mapping", torch.int64, i), block_mapping.shape[0], N))
+
+
 def pa_selftest_wait(device=None, limit_us: int = 20000,
                      stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Run the library's bounded-wait self-test on `device` (default: the current CUDA

@@ -281,6 +281,44 @@ int check_reshape(const void* key, const void* value, const void* k_cache, const
   return PA_OK;
 }
 
+// The kernels round a context up to whole tiles and look some chunks ahead in 32 bits.
+int check_capacity(int max_blocks, int block_size) {
+  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX - 1024)
+    return fail(PA_ERR_UNSUPPORTED, "a table of %d blocks of %d tokens exceeds 2^31 - 1025 tokens", max_blocks, block_size);
+  return PA_OK;
+}
+
+// The checks shared by the calls on the sequences' blocks.
+int check_sequences(const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                    const int32_t* ref_counts, int num_seqs, int num_blocks, int block_size) {
+  if (!block_size_supported(block_size))
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d is not supported (16, 32, 64, 128 or 256)", block_size);
+  if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs %d is negative", num_seqs);
+  if (num_seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "num_seqs %d exceeds 65535", num_seqs);
+  if (max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq %d must be positive", max_blocks_per_seq);
+  if (num_blocks <= 0) return fail(PA_ERR_INVALID_ARG, "num_blocks %d must be positive", num_blocks);
+  const int st = check_capacity(max_blocks_per_seq, block_size);
+  if (st != PA_OK) return st;
+  if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size exceeds 2^31 - 1 token slots");
+  if (!ref_counts || (num_seqs > 0 && (!block_tables || !context_lens)))
+    return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(ref_counts, 16)) return fail(PA_ERR_INVALID_ARG, "ref_counts must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return fail(PA_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
+  return PA_OK;
+}
+
+int check_sequence_workspace(const void* workspace, size_t workspace_bytes, int num_blocks) {
+  if (!workspace) return fail(PA_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned(workspace, 16)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const size_t need = pa_sequence_workspace_bytes(num_blocks);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID_ARG, "workspace_bytes %zu < %zu required", workspace_bytes, need);
+  return PA_OK;
+}
+
 // The checks shared by both prefills.
 int check_prefill(const void* out, const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
@@ -318,13 +356,6 @@ int check_block_shape(int block_size, int num_blocks, int num_kv_heads, int head
   if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
   if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
     return fail(PA_ERR_UNSUPPORTED, "num_blocks * block_size exceeds 2^31 - 1 token slots");
-  return PA_OK;
-}
-
-// The kernels round a context up to whole tiles and look some chunks ahead in 32 bits.
-int check_capacity(int max_blocks, int block_size) {
-  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX - 1024)
-    return fail(PA_ERR_UNSUPPORTED, "a table of %d blocks of %d tokens exceeds 2^31 - 1025 tokens", max_blocks, block_size);
   return PA_OK;
 }
 
@@ -795,6 +826,143 @@ int pa_splitk_reduce(void* out, const void* workspace, size_t workspace_bytes,
                    block_size, num_seqs, num_heads, head_dim, partition_size, max_num_partitions};
   return cuda_status(pa::launch_splitk_reduce(a, static_cast<cudaStream_t>(stream)),
                      "split-K reduce launch");
+}
+
+int pa_prefill_packed(void* out, const void* q, int64_t q_stride, const void* key, int64_t k_stride, const void* value,
+                      int64_t v_stride, void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                      const int32_t* query_start_loc, int num_seqs, int num_rows, int max_query_len, int num_heads,
+                      int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale, int dtype,
+                      void* stream) {
+  if (dtype != PA_FP16 && dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "dtype %d is not supported (PA_FP16 or PA_BF16)", dtype);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(PA_ERR_UNSUPPORTED, "packed prefill supports head_dim 64 or 128 (got %d)", head_dim);
+  if (num_heads <= 0 || num_kv_heads <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_heads (%d) and num_kv_heads (%d) must be positive", num_heads, num_kv_heads);
+  if (num_heads % num_kv_heads != 0)
+    return fail(PA_ERR_UNSUPPORTED, "num_heads %d is not a multiple of num_kv_heads %d", num_heads, num_kv_heads);
+  if (num_heads / num_kv_heads > 16)
+    return fail(PA_ERR_UNSUPPORTED, "query group size %d exceeds 16", num_heads / num_kv_heads);
+  if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
+  if (num_seqs < 0 || num_rows < 0 || max_query_len < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_seqs (%d), num_rows (%d) and max_query_len (%d) must be >= 0", num_seqs, num_rows,
+                max_query_len);
+  if (num_seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "num_seqs %d exceeds 65535", num_seqs);
+  if (num_rows > INT32_MAX - 1024) return fail(PA_ERR_UNSUPPORTED, "num_rows %d exceeds 2^31 - 1025", num_rows);
+  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+  const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  const int64_t most = int64_t{1} << 38;  // a tensor map's strides end at 2^40 bytes
+  if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+    return fail(PA_ERR_INVALID_ARG, "q_stride, k_stride and v_stride must hold a token's heads");
+  if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || q_stride > most || k_stride > most || v_stride > most)
+    return fail(PA_ERR_UNSUPPORTED, "q_stride, k_stride and v_stride must be multiples of 8 elements, at most 2^38");
+  if (num_seqs == 0 || num_rows == 0 || max_query_len == 0) return ok();
+  const bool cache = k_cache || v_cache || slot_mapping;
+  if (cache) {
+    if (!k_cache || !v_cache || !slot_mapping)
+      return fail(PA_ERR_INVALID_ARG, "k_cache, v_cache and slot_mapping are given together or not at all");
+    if (block_size <= 0 || num_blocks <= 0)
+      return fail(PA_ERR_INVALID_ARG, "block_size (%d) and num_blocks (%d) must be positive", block_size, num_blocks);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8))
+      return fail(PA_ERR_INVALID_ARG, "the caches must be 16-byte aligned, slot_mapping 8-byte aligned");
+  }
+  if (!out || !q || !key || !value || !query_start_loc) return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16))
+    return fail(PA_ERR_INVALID_ARG, "out, q, key and value must be 16-byte aligned");
+  if (!aligned(query_start_loc, 4)) return fail(PA_ERR_INVALID_ARG, "query_start_loc must be 4-byte aligned");
+  pa::PackedPrefillArgs a{dtype, out, q, key, value, q_stride, k_stride, v_stride, k_cache, v_cache, slot_mapping,
+                          query_start_loc, num_seqs, num_rows, max_query_len < num_rows ? max_query_len : num_rows,
+                          num_heads, num_kv_heads, head_dim,
+                          cache ? static_cast<int64_t>(num_blocks) * block_size : 0, scale};
+  return cuda_status(pa::launch_packed_prefill(a, static_cast<cudaStream_t>(stream)), "packed prefill launch");
+}
+
+size_t pa_sequence_workspace_bytes(int num_blocks) {
+  if (num_blocks <= 0) return 0;
+  return ((static_cast<size_t>(num_blocks) + 3) / 4 * 4 + 16) * sizeof(int32_t);
+}
+
+int pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens, int32_t* ref_counts,
+                        const int32_t* query_start_loc, int64_t* slot_mapping, int64_t* block_copies, int32_t* left,
+                        int num_seqs, int num_tokens, int num_blocks, int block_size, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  int st = check_sequences(block_tables, max_blocks_per_seq, context_lens, ref_counts, num_seqs, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d is negative", num_tokens);
+  if (num_tokens > INT32_MAX - 65536) return fail(PA_ERR_UNSUPPORTED, "num_tokens %d is too large", num_tokens);
+  if (!query_start_loc || !left || (num_tokens > 0 && !slot_mapping) || (num_seqs > 0 && !block_copies))
+    return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(query_start_loc, 4) || !aligned(left, 4) || !aligned(slot_mapping, 8) || !aligned(block_copies, 8))
+    return fail(PA_ERR_INVALID_ARG, "query_start_loc and left must be 4-byte aligned, slot_mapping and block_copies "
+                "8-byte aligned");
+  st = check_sequence_workspace(workspace, workspace_bytes, num_blocks);
+  if (st != PA_OK) return st;
+  pa::ExtendArgs a{{block_tables, context_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size},
+                   query_start_loc, slot_mapping, block_copies, left, num_tokens, workspace};
+  return cuda_status(pa::launch_extend(a, static_cast<cudaStream_t>(stream)), "extend launch");
+}
+
+int pa_truncate_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens, int32_t* ref_counts,
+                          const int32_t* new_lens, int num_seqs, int num_blocks, int block_size, void* stream) {
+  const int st = check_sequences(block_tables, max_blocks_per_seq, context_lens, ref_counts, num_seqs, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0) return ok();
+  if (!new_lens || !aligned(new_lens, 4)) return fail(PA_ERR_INVALID_ARG, "new_lens must be a 4-byte aligned pointer");
+  const pa::SequenceArgs a{block_tables, context_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size};
+  return cuda_status(pa::launch_truncate(a, new_lens, static_cast<cudaStream_t>(stream)), "truncate launch");
+}
+
+int pa_fork_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens, int32_t* ref_counts,
+                      const int32_t* fork_from, int num_seqs, int num_blocks, int block_size, void* stream) {
+  const int st = check_sequences(block_tables, max_blocks_per_seq, context_lens, ref_counts, num_seqs, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0) return ok();
+  if (!fork_from || !aligned(fork_from, 4)) return fail(PA_ERR_INVALID_ARG, "fork_from must be a 4-byte aligned pointer");
+  const pa::SequenceArgs a{block_tables, context_lens, ref_counts, num_seqs, max_blocks_per_seq, num_blocks, block_size};
+  return cuda_status(pa::launch_fork(a, fork_from, static_cast<cudaStream_t>(stream)), "fork launch");
+}
+
+int pa_compact_blocks(int64_t* moves, int max_moves, int32_t* num_moves, const int32_t* block_tables,
+                      int max_blocks_per_seq, const int32_t* context_lens, const int32_t* ref_counts,
+                      int32_t* tables_out, int32_t* counts_out, int num_seqs, int num_blocks, int block_size,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_sequences(block_tables, max_blocks_per_seq, context_lens, ref_counts, num_seqs, num_blocks, block_size);
+  if (st != PA_OK) return st;
+  if (max_moves < 0) return fail(PA_ERR_INVALID_ARG, "max_moves %d is negative", max_moves);
+  if (max_moves > INT32_MAX / 2) return fail(PA_ERR_UNSUPPORTED, "max_moves %d is too large", max_moves);
+  if ((max_moves > 0 && !moves) || !num_moves || !counts_out || (num_seqs > 0 && !tables_out))
+    return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(moves, 8) || !aligned(num_moves, 4) || !aligned(tables_out, 4) || !aligned(counts_out, 16))
+    return fail(PA_ERR_INVALID_ARG, "moves must be 8-byte, counts_out 16-byte, num_moves and tables_out 4-byte aligned");
+  st = check_sequence_workspace(workspace, workspace_bytes, num_blocks);
+  if (st != PA_OK) return st;
+  const pa::CompactArgs a{moves, num_moves, block_tables, context_lens, ref_counts, tables_out, counts_out, num_seqs,
+                          max_blocks_per_seq, num_blocks, block_size, max_moves, workspace};
+  return cuda_status(pa::launch_compact(a, static_cast<cudaStream_t>(stream)), "compact launch");
+}
+
+int pa_copy_layer_blocks(void* pools, int64_t pool_stride, int num_pools, int64_t block_bytes,
+                         const int64_t* block_mapping, int num_pairs, int num_blocks, void* stream) {
+  if (num_pools < 0 || num_pairs < 0)
+    return fail(PA_ERR_INVALID_ARG, "num_pools (%d) and num_pairs (%d) must be >= 0", num_pools, num_pairs);
+  if (num_pairs > INT32_MAX / 2) return fail(PA_ERR_UNSUPPORTED, "num_pairs %d is too large", num_pairs);
+  if (num_pools > 65535) return fail(PA_ERR_UNSUPPORTED, "num_pools %d exceeds 65535", num_pools);
+  if (num_blocks <= 0 || block_bytes <= 0)
+    return fail(PA_ERR_INVALID_ARG, "num_blocks (%d) and block_bytes (%lld) must be positive", num_blocks,
+                (long long)block_bytes);
+  if (block_bytes % 4 != 0 || block_bytes > (int64_t{1} << 30))
+    return fail(PA_ERR_UNSUPPORTED, "block_bytes %lld must be a multiple of 4, at most 2^30", (long long)block_bytes);
+  if (num_pools > 1) {
+    if (pool_stride % 4 != 0) return fail(PA_ERR_UNSUPPORTED, "pool_stride %lld is not a multiple of 4", (long long)pool_stride);
+    if (pool_stride < static_cast<int64_t>(num_blocks) * block_bytes)
+      return fail(PA_ERR_INVALID_ARG, "pool_stride %lld does not hold num_blocks * block_bytes", (long long)pool_stride);
+  }
+  if (num_pools == 0 || num_pairs == 0) return ok();
+  if (!pools || !block_mapping) return fail(PA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(pools, 4) || !aligned(block_mapping, 8))
+    return fail(PA_ERR_INVALID_ARG, "pools must be 4-byte aligned, block_mapping 8-byte aligned");
+  const pa::CopyLayerArgs a{pools, pool_stride, num_pools, block_bytes, block_mapping, num_pairs, num_blocks};
+  return cuda_status(pa::launch_copy_layers(a, static_cast<cudaStream_t>(stream)), "copy_layer_blocks launch");
 }
 
 }  // extern "C"

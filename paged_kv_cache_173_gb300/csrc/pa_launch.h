@@ -189,6 +189,77 @@ struct BlockPrefillArgs {
   const float* v_scales;
 };
 
+// Whole prompts in packed rows; the pools (null: none) take the new tokens' rows.
+struct PackedPrefillArgs {
+  int dtype;
+  void* out;
+  const void* q;
+  const void* key;
+  const void* value;
+  int64_t q_stride;  // elements from one token's row to the next
+  int64_t k_stride;
+  int64_t v_stride;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slot_mapping;
+  const int32_t* query_start_loc;
+  int num_seqs;
+  int num_rows;
+  int max_query_len;
+  int num_heads;
+  int num_kv_heads;
+  int head_dim;
+  int64_t num_slots;  // num_blocks * block_size
+  float scale;
+};
+
+// The sequences' tables, lengths and the blocks' counts of holders.
+struct SequenceArgs {
+  int32_t* block_tables;
+  int32_t* context_lens;
+  int32_t* ref_counts;
+  int num_seqs;
+  int max_blocks_per_seq;
+  int num_blocks;
+  int block_size;
+};
+
+struct ExtendArgs {
+  SequenceArgs a;
+  const int32_t* query_start_loc;
+  int64_t* slot_mapping;
+  int64_t* block_copies;
+  int32_t* left;
+  int num_tokens;
+  void* workspace;
+};
+
+struct CompactArgs {
+  int64_t* moves;
+  int32_t* num_moves;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* ref_counts;
+  int32_t* tables_out;
+  int32_t* counts_out;
+  int num_seqs;
+  int max_blocks_per_seq;
+  int num_blocks;
+  int block_size;
+  int max_moves;
+  void* workspace;
+};
+
+struct CopyLayerArgs {
+  void* pools;
+  int64_t pool_stride;  // bytes
+  int num_pools;
+  int64_t block_bytes;
+  const int64_t* block_mapping;
+  int num_pairs;
+  int num_blocks;
+};
+
 // Record a formatted message as the calling thread's last error; returns status.
 int set_last_error(int status, const char* fmt, ...);
 
@@ -231,6 +302,15 @@ cudaError_t launch_sparse_decode_f16(const BlockDecodeArgs& a, cudaStream_t stre
 cudaError_t launch_sparse_decode_bf16(const BlockDecodeArgs& a, cudaStream_t stream);
 // prefill over block-scaled pools (pa_block_prefill.cu)
 cudaError_t launch_block_prefill(const BlockPrefillArgs& a, cudaStream_t stream);
+
+// prefill of packed prompts (pa_packed_prefill.cu)
+cudaError_t launch_packed_prefill(const PackedPrefillArgs& a, cudaStream_t stream);
+// the sequences' blocks (pa_sequences.cu)
+cudaError_t launch_truncate(const SequenceArgs& a, const int32_t* new_lens, cudaStream_t stream);
+cudaError_t launch_fork(const SequenceArgs& a, const int32_t* fork_from, cudaStream_t stream);
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_copy_layers(const CopyLayerArgs& a, cudaStream_t stream);
 
 // Workspace geometry shared by the partition kernel and the reduce kernel:
 // o [S][H][P][d], then m [S][H][P], then l [S][H][P], float32.

@@ -1,0 +1,472 @@
+"""Packed prefill against float64, and the whole run of a request: room for a prompt, its
+attention with the cache write, samples forked off it, decode steps, compaction.
+
+Tolerance of an output, from the arithmetic.  With w_i the exact weights (sum 1), A =
+sum w_i |v_i| and S the largest sum |q_c k_c| * scale:
+  - the weights enter P.V in the values' type: half a step of each, 2^-11 A (fp16) or
+    2^-8 A (bf16); they are summed unrounded.  fp16: the largest weight is 2^7 or more, a
+    weight below 2^-14 is off by 2^-25: 2^-32 of the largest for each of n, times max |v|;
+  - scores, the exponential and the float32 sums as for the block operators:
+    2 (d + 4) 2^-24 S A + 2 (2^-22 + (n / 8 + 16) 2^-24) A;
+  - the output is rounded once: half a step, and half of fp16's smallest step, 2^-25.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from block_cases import HALF_STEP, to_np
+from oracle import sequence_oracle as so
+from paged_kv_cache_173_gb300 import api
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+class Prompts:
+    """Prompts in packed rows, drawn on the CPU from a seed, with pools and slots."""
+
+    def __init__(self, lens, H, Hk, d, dtype, seed, fused=False, pad=0, block=16, cache=True):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.H, self.Hk, self.d, self.dtype, self.B = list(lens), H, Hk, d, dtype, block
+        self.rows = sum(lens) + pad
+        self.starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+        self.q = (torch.randn((self.rows, H, d), generator=g) * 0.8).to(dtype)
+        self.k = (torch.randn((self.rows, Hk, d), generator=g) * torch.exp(0.5 * torch.randn((Hk, d), generator=g))).to(dtype)
+        self.v = (torch.randn((self.rows, Hk, d), generator=g) * torch.exp(0.7 * torch.randn((self.rows, Hk, 1), generator=g))).to(dtype)
+        self.scale = float(np.float32(d ** -0.5))
+        self.max_len = max(lens) if len(lens) else 0
+        self.fused, self.cache = fused, cache
+        self.N = self.rows // block + 3
+        self.slots = torch.randperm(self.N * block, generator=g)[:self.rows]
+
+    def start(self):
+        if self.fused:  # parts of the rows of one projection
+            qkv = torch.cat([self.q, self.k, self.v], 1).cuda()
+            self.dq, self.dk, self.dv = qkv[:, :self.H], qkv[:, self.H:self.H + self.Hk], qkv[:, self.H + self.Hk:]
+        else:
+            self.dq, self.dk, self.dv = self.q.cuda(), self.k.cuda(), self.v.cuda()
+        self.out = torch.full((self.rows, self.H, self.d), 7.0, dtype=self.dtype, device="cuda")
+        self.dst = torch.from_numpy(self.starts).cuda()
+        self.dsl = self.slots.cuda()
+        self.kc, self.vc = (torch.full((self.N, self.B, self.Hk, self.d), x, dtype=self.dtype, device="cuda") for x in (3.0, 5.0))
+        return self
+
+    def run(self, stream=None):
+        extra = (self.kc, self.vc, self.dsl) if self.cache else ()
+        api.pa_prefill_packed(self.out, self.dq, self.dk, self.dv, self.dst, self.max_len, self.scale, *extra, stream=stream)
+        return self
+
+    def reference(self):
+        """(out, tolerance) of every row, NaN where none is computed."""
+        q, k, v = to_np(self.q), to_np(self.k), to_np(self.v)
+        with np.errstate(all="ignore"):
+            out, A, S = so.attention(q, k, v, self.starts, self.scale, self.max_len)
+            n, top = max(self.lens, default=1), np.abs(np.where(np.isfinite(v), v, 0)).max(initial=0)
+            sums = 2.0 ** -22 + (n / 8 + 16) * 2.0 ** -24
+            tiny = n * 2.0 ** -32 * top + 2.0 ** -25 if self.dtype == F16 else 2.0 ** -100
+            tol = (HALF_STEP[self.dtype] * (A + np.abs(out)) + A * (2 * (self.d + 4) * 2.0 ** -24 * S[..., None] + 2 * sums) + tiny)
+        return out, tol
+
+    def check(self):
+        torch.cuda.synchronize()
+        got = to_np(self.out)
+        want, tol = self.reference()
+        done = np.zeros(self.rows, bool)
+        for a, n in zip(self.starts, self.lens):
+            done[a:a + min(n, self.max_len)] = True
+        assert (got[~done] == 7.0).all()
+        err = np.abs(got[done] - want[done])
+        assert np.isfinite(got[done]).all() and (err <= tol[done]).all(), \
+            (np.argwhere(~(err <= tol[done]))[:4].tolist(), float(np.nanmax(err / tol[done])))
+        self.check_pools(done)
+
+    def check_pools(self, done):
+        if not self.cache:
+            return
+        for pool, new, empty in ((self.kc, self.k, 3.0), (self.vc, self.v, 5.0)):
+            want = torch.full_like(pool, empty).cpu().flatten(0, 1)
+            ok = torch.from_numpy(done) & (self.slots >= 0) & (self.slots < self.N * self.B)
+            want[self.slots[ok]] = new[ok]
+            assert torch.equal(pool.cpu().flatten(0, 1).view(torch.int16), want.view(torch.int16))
+
+
+HEADS = [(1, 1), (4, 4), (8, 2), (6, 2), (7, 1), (10, 2), (16, 1), (12, 1), (22, 2), (13, 1), (32, 8)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", HEADS)
+def test_groups(H, Hk, d, dtype):
+    Prompts([37, 1, 130, 2, 300], H, Hk, d, dtype, H + d, fused=H % 2 == 0, pad=3).start().run().check()
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [31], [32], [33], [63, 64, 65], [127, 128, 129], [255, 256, 257], [511, 1, 513],
+                                  [1] * 50, [16] * 40, [0, 5, 0, 0, 9, 0], [700, 3, 3, 650]])
+@pytest.mark.parametrize("H,Hk,d,dtype", [(4, 1, 128, F16), (8, 8, 128, BF16), (5, 1, 64, F16), (2, 2, 64, BF16)])
+def test_lengths(lens, H, Hk, d, dtype):
+    Prompts(lens, H, Hk, d, dtype, sum(lens), fused=True, pad=1).start().run().check()
+
+
+@pytest.mark.parametrize("H,Hk,d,dtype,n", [(2, 1, 128, F16, 2500), (1, 1, 64, BF16, 2100), (3, 1, 128, BF16, 1900)])
+def test_long_prompts(H, Hk, d, dtype, n):
+    Prompts([n, 300], H, Hk, d, dtype, n).start().run().check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_more_items_than_the_gpu_has_processors(dtype):
+    rng = np.random.default_rng(1)
+    Prompts([int(x) for x in rng.integers(1, 200, 60)], 16, 8, 64, dtype, 2).start().run().check()
+
+
+@pytest.mark.parametrize("lens", [[900] + [1] * 80, [1] * 300 + [600], [257] * 3 + [2] * 70])
+def test_one_long_prompt_among_short_ones(lens):
+    Prompts(lens, 8, 2, 128, F16, len(lens)).start().run().check()
+
+
+@pytest.mark.parametrize("block", [1, 5, 16, 48, 256])
+def test_pools_of_any_block_size(block):
+    Prompts([40, 200], 4, 2, 64, BF16, block, block=block).start().run().check()
+
+
+def test_slots_that_write_nothing():
+    p = Prompts([90, 30], 4, 2, 128, F16, 3)
+    p.slots[::7] = -1
+    p.slots[3::11] = p.N * p.B + torch.arange(len(p.slots[3::11])) * 2 ** 33
+    p.slots[5] = -2 ** 60
+    p.start().run().check()
+    p = Prompts([90, 30], 4, 2, 128, F16, 3, cache=False).start().run()
+    p.check()
+    assert bool((p.kc == 3.0).all())
+
+
+def test_rows_past_the_largest_length_are_left():
+    p = Prompts([90, 30, 200], 4, 2, 64, F16, 4)
+    p.max_len = 77
+    p.start().run().check()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.11, 3.0, 1e-30, -1e-30])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scales(scale, dtype):
+    p = Prompts([150, 20], 8, 2, 64, dtype, 5)
+    p.scale = float(np.float32(scale))
+    p.start().run().check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_peaked_and_flat_weights(dtype):
+    p = Prompts([400], 4, 1, 128, dtype, 6)
+    p.q *= 8  # scores of some hundred
+    p.start().run().check()
+    p = Prompts([400], 4, 1, 128, dtype, 7)
+    p.q.zero_()
+    p.start().run().check()
+    p = Prompts([300], 2, 1, 64, dtype, 8)  # the maximum grows from key to key
+    p.k[:] = (torch.arange(300)[:, None, None] * 0.2).to(dtype)
+    p.q.fill_(1.0)
+    p.start().run().check()
+
+
+def test_large_and_tiny_values():
+    p = Prompts([200], 2, 1, 64, BF16, 9)
+    p.v = (p.v.float() * 1e30).to(BF16)
+    p.start().run().check()
+    p.v = (p.v.float() * 1e-50).to(BF16)
+    p.start().run().check()
+    p = Prompts([200], 2, 1, 64, F16, 10)
+    p.v.fill_(65504.0)
+    p.start().run().check()
+
+
+def finite_elsewhere(p, changed):
+    """Run p with and without what `changed` does to its inputs: rows that do not see it are the same bits.
+    Returns both outputs."""
+    p.start().run()
+    clean = p.out.clone()
+    changed(p)
+    p.start().run()
+    torch.cuda.synchronize()
+    return clean.float().cpu(), p.out.float().cpu()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 1, 63, 64, 100, 127, 128, 200, 259])
+@pytest.mark.parametrize("G", [1, 4, 7])
+def test_what_is_not_finite_reaches_the_rows_that_see_it(dtype, bad, at, G):
+    lens = [260, 150]
+
+    def value(p):
+        p.v[at, 0, 5] = bad
+
+    clean, got = finite_elsewhere(Prompts(lens, 2 * G, 2, 64, dtype, at, pad=2), value)
+    assert torch.equal(got[:at], clean[:at]) and torch.equal(got[260:], clean[260:])
+    seen = got[at:260, :G]
+    assert not torch.isfinite(seen[..., 5]).any()
+    others = [c for c in range(64) if c != 5]
+    assert torch.equal(seen[..., others], clean[at:260, :G][..., others])
+    assert torch.equal(got[at:260, G:], clean[at:260, G:])
+
+    def key(p):
+        p.k[at, 0, 5] = bad
+
+    clean, got = finite_elsewhere(Prompts(lens, 2 * G, 2, 64, dtype, at, pad=2), key)
+    assert torch.equal(got[:at], clean[:at]) and torch.equal(got[260:], clean[260:])
+    if bad != bad:
+        assert got[at:260, :G].isnan().all()
+
+    def query(p):
+        p.q[at, 1] = bad
+
+    clean, got = finite_elsewhere(Prompts(lens, 2 * G, 2, 64, dtype, at, pad=2), query)
+    assert got[at, 1].isnan().all()
+    mask = torch.ones(got.shape[:2], dtype=torch.bool)
+    mask[at, 1] = False
+    assert torch.equal(got[mask], clean[mask])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_behind_the_last_sequence_do_not_matter(dtype):
+    def spoil(p):
+        for t in (p.q, p.k, p.v):
+            t[-40:] = float("nan")
+
+    p = Prompts([100, 30], 4, 2, 128, dtype, 11, pad=40)
+    clean, got = finite_elsewhere(p, spoil)
+    assert torch.equal(clean, got) and bool((got[-40:] == 7.0).all())
+
+
+def test_many_infinities_in_every_channel():
+    def value(p):
+        p.v[70:90, 0] = float("inf")
+        p.v[80:100, 0, ::2] = -float("inf")
+
+    clean, got = finite_elsewhere(Prompts([220], 4, 1, 128, F16, 12), value)
+    assert torch.equal(got[:70], clean[:70]) and not torch.isfinite(got[70:]).any()
+    assert (got[75] == float("inf")).all() and got[99, :, ::2].isnan().all()
+
+
+@pytest.mark.parametrize("starts", [[0, 60, 40, 100], [0, 50, 120, 100], [0, 0, 0, 100], [0, 100, 100, 100]])
+def test_starts_that_cannot_be_read_nothing_outside(starts):
+    p = Prompts([30, 30, 40], 4, 2, 64, F16, 13).start()
+    p.dst = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    p.max_len = 120
+    p.run()
+    torch.cuda.synchronize()
+    if starts[1] == 0 or starts[1] == 100:
+        p.starts, p.lens = np.array([0, 100]), [100]
+        p.check()
+
+
+def test_a_single_row_of_any_stride():
+    for n, H, Hk in ((1, 4, 2), (1, 1, 1), (3, 1, 1)):
+        p = Prompts([n], H, Hk, 64, F16, n).start()
+        wide = torch.randn((n, 8 * 64), device="cuda").half()
+        wide[:, :H * 64] = p.dq.flatten(1)
+        p.dq = wide[:, :H * 64].unflatten(1, (H, 64))
+        p.run().check()
+
+
+def test_rows_further_apart_than_32_bits():
+    n, wide = 1100, 1 << 21  # 4.6 GB of rows, elements past 2^31
+    p = Prompts([n], 4, 2, 64, BF16, 14).start()
+    big = torch.zeros((n, wide), dtype=BF16, device="cuda")
+    parts = []
+    for x, at in ((p.dq, 0), (p.dk, 1 << 20), (p.dv, (1 << 21) - 128)):
+        m = x.shape[1] * 64
+        big[:, at:at + m] = x.flatten(1)
+        parts.append(big[:, at:at + m].unflatten(1, (x.shape[1], 64)))
+    p.dq, p.dk, p.dv = parts
+    p.run().check()
+
+
+def test_pools_past_four_gigabytes():
+    N, B, Hk, d = 150000, 16, 8, 128
+    p = Prompts([50], 8, Hk, d, F16, 15).start()
+    p.kc, p.vc = (torch.zeros((N, B, Hk, d), dtype=F16, device="cuda") for _ in range(2))
+    slots = torch.arange(50) + N * B - 50
+    p.dsl = slots.cuda()
+    p.run()
+    torch.cuda.synchronize()
+    assert torch.equal(p.kc.flatten(0, 1)[slots.cuda()].cpu(), p.k) and torch.equal(p.vc.flatten(0, 1)[slots.cuda()].cpu(), p.v)
+    assert not p.kc[0].any()
+    p.cache = False
+    p.check()
+
+
+def test_captured_and_replayed_with_new_contents_and_lengths():
+    p = Prompts([150, 70, 90], 8, 2, 128, BF16, 16, pad=10).start()
+    p.max_len = 200
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        p.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p.run()
+    for seed, lens in ((17, [10, 200, 100]), (18, [200, 0, 1]), (19, [107, 107, 106])):
+        n = Prompts(lens, 8, 2, 128, BF16, seed, pad=320 - sum(lens))
+        for a, b in ((p.dq, n.q), (p.dk, n.k), (p.dv, n.v), (p.dsl, n.slots), (p.dst, torch.from_numpy(n.starts))):
+            a.copy_(b)
+        p.out.fill_(7.0)
+        p.kc.fill_(3.0), p.vc.fill_(5.0)
+        graph.replay()
+        n.out, n.kc, n.vc, n.N = p.out, p.kc, p.vc, p.N
+        n.max_len = 200
+        n.check()
+
+
+def test_two_calls_at_once_on_two_streams_and_repeatably():
+    a = Prompts([300, 200, 5], 16, 4, 128, F16, 20).start()
+    b = Prompts([33] * 30, 12, 4, 64, BF16, 21, fused=True).start()
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    first = None
+    for _ in range(4):
+        a.run(sa), b.run(sb)
+        torch.cuda.synchronize()
+        if first is not None:
+            assert torch.equal(first[0], a.out) and torch.equal(first[1], b.out)
+        first = a.out.clone(), b.out.clone()
+    a.check(), b.check()
+
+
+def test_empty_calls_do_nothing():
+    p = Prompts([10], 4, 2, 64, F16, 22).start()
+    before = p.out.clone(), p.kc.clone()
+    p.max_len = 0
+    p.run()
+    api.pa_prefill_packed(p.out[:0], p.dq[:0], p.dk[:0], p.dv[:0], p.dst, 5, 0.1, p.kc, p.vc, p.dsl[:0])
+    api.pa_prefill_packed(p.out, p.dq, p.dk, p.dv, p.dst[:1], 5, 0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(before[0], p.out) and torch.equal(before[1], p.kc)
+
+
+def test_binding_refuses_what_it_cannot_take():
+    p = Prompts([10, 20], 4, 2, 64, F16, 23).start()
+    good = dict(out=p.out, q=p.dq, key=p.dk, value=p.dv, query_start_loc=p.dst, max_query_len=20, scale=0.1, k_cache=p.kc,
+                v_cache=p.vc, slot_mapping=p.dsl)
+    for error, kw in [(TypeError, dict(q=p.dq.float())), (TypeError, dict(key=p.dk.bfloat16())), (ValueError, dict(key=p.dk[:9])),
+                      (ValueError, dict(value=p.dv[:, :1])), (ValueError, dict(out=p.out[:3])), (ValueError, dict(value=p.dv.cpu())),
+                      (ValueError, dict(k_cache=None)), (ValueError, dict(slot_mapping=None)), (ValueError, dict(slot_mapping=p.dsl[:4])),
+                      (TypeError, dict(slot_mapping=p.dsl.int())), (TypeError, dict(query_start_loc=p.dst.long())),
+                      (ValueError, dict(query_start_loc=p.dst[:0])), (ValueError, dict(v_cache=p.vc[:, :, :1])),
+                      (TypeError, dict(k_cache=p.kc.bfloat16(), v_cache=p.vc.bfloat16())),
+                      (ValueError, dict(q=p.dq.transpose(0, 1).contiguous().transpose(0, 1))),
+                      (ValueError, dict(out=torch.zeros((30, 8, 64), dtype=F16, device="cuda")[:, ::2]))]:
+        with pytest.raises(error):
+            api.pa_prefill_packed(**{**good, **kw})
+    odd = torch.zeros((30, 4 * 64 + 4), dtype=F16, device="cuda")[:, :256].unflatten(1, (4, 64))
+    with pytest.raises(api.PagedAttnError):  # rows that do not start on 16 bytes
+        api.pa_prefill_packed(**{**good, "q": odd})
+    with pytest.raises(api.PagedAttnError):  # every row the same
+        api.pa_prefill_packed(**{**good, "key": p.dk[:1].expand(30, 2, 64)})
+    with pytest.raises(api.PagedAttnError):
+        api.pa_prefill_packed(**{**good, "scale": float("nan")})
+    torch.cuda.synchronize()
+    assert bool((p.out == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,H,Hk,d,B", [(F16, 8, 2, 128, 16), (BF16, 6, 2, 64, 32)])
+def test_requests_from_prompt_to_compaction(dtype, H, Hk, d, B):
+    """Two layers: prompts come in, attend and are written; samples fork off them and grow by a token
+    of their own each; decode attends; some leave, the pool is made dense, decode attends again."""
+    layers, S, M, N = 2, 8, 12, 60
+    rng, g = np.random.default_rng(0), torch.Generator().manual_seed(0)
+    scale = float(np.float32(d ** -0.5))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    tables, lens = torch.full((S, M), -1, dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    counts = torch.zeros(N, dtype=torch.int32, device="cuda")
+    counts[torch.from_numpy(rng.permutation(N)[:9]).cuda()] = 1  # blocks that somebody else holds
+    pools = torch.full((layers, 2, N, B, Hk, d), float("nan"), dtype=dtype, device="cuda")
+    flat = pools.view(layers * 2, N, B, Hk, d)
+    space = api.alloc_sequence_workspace(N, "cuda")
+    copies, left = torch.empty((S, 2), dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    hist = [[[np.zeros((0, Hk, d))] * 2 for _ in range(layers)] for _ in range(S)]  # every sequence's keys and values
+
+    def new_rows(n):
+        return [(torch.randn((n, Hk, d), generator=g).to(dtype), torch.randn((n, Hk, d), generator=g).to(dtype)) for _ in range(layers)]
+
+    def grow(new):
+        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        slots = torch.empty(int(starts[-1]), dtype=torch.int64, device="cuda")
+        api.pa_extend_sequences(tables, lens, counts, torch.from_numpy(starts).cuda(), slots, copies, left, B, space)
+        api.pa_copy_layer_blocks(flat, copies)
+        rows = new_rows(int(starts[-1]))
+        for s in range(S):
+            for x in range(layers):
+                hist[s][x] = [np.concatenate([h, to_np(r[starts[s]:starts[s + 1]])]) for h, r in zip(hist[s][x], rows[x])]
+        return starts, slots, rows
+
+    def close(got, q, s, x, upto):
+        k, v = (h[:upto] for h in hist[s][x])
+        for h in range(H):
+            sc = k[:, h // (H // Hk)] @ to_np(q)[h] * scale
+            w = np.exp(sc - sc.max())
+            w /= w.sum()
+            want, A = w @ v[:, h // (H // Hk)], w @ np.abs(v[:, h // (H // Hk)])
+            tol = HALF_STEP[dtype] * (A + np.abs(want)) + 1e-4 * A + 2.0 ** -20
+            assert (np.abs(to_np(got)[h] - want) <= tol).all()
+
+    # prompts
+    new = [50, 33, 0, 0, 0, 0, 0, 0]
+    starts, slots, rows = grow(new)
+    assert left.tolist()[1] == 0
+    for x in range(layers):
+        q = torch.randn((sum(new), H, d), generator=g).to(dtype)
+        out = torch.empty((sum(new), H, d), dtype=dtype, device="cuda")
+        api.pa_prefill_packed(out, q.cuda(), rows[x][0].cuda(), rows[x][1].cuda(), torch.from_numpy(starts).cuda(), 50, scale,
+                              pools[x, 0], pools[x, 1], slots)
+        for t in (0, 17, 49, 50, 82):
+            s = 0 if t < 50 else 1
+            close(out[t], q[t], s, x, t - int(starts[s]) + 1)
+
+    def decode_all():
+        torch.cuda.synchronize()
+        now = lens.tolist()
+        assert now == [len(hist[s][0][0]) for s in range(S)]
+        want = so.holders(tables.cpu().numpy(), lens.cpu().numpy(), N, B)
+        assert (counts.cpu().numpy() - want).sum() == 9
+        for x in range(layers):
+            q = torch.randn((S, H, d), generator=g).to(dtype)
+            out = torch.empty((S, H, d), dtype=dtype, device="cuda")
+            api.pa_decode(out, q.cuda(), pools[x, 0], pools[x, 1], tables, lens, scale)
+            for s in range(S):
+                if now[s]:
+                    close(out[s], q[s], s, x, now[s])
+
+    decode_all()
+    # samples, each with tokens of its own
+    source = [-1, -1, 0, 0, 1, 1, 1, -1]
+    api.pa_fork_sequences(tables, lens, counts, i32(*source), B)
+    for s, f in enumerate(source):
+        if f >= 0:
+            hist[s] = [list(h) for h in hist[f]]
+    for step in ([1, 0, 1, 1, 1, 1, 0, 0], [2, 1, 1, 0, 3, 20, 1, 0], [1, 1, 1, 1, 1, 1, 1, 1]):
+        starts, slots, rows = grow(step)
+        for x in range(layers):
+            api.pa_reshape_and_cache(rows[x][0].cuda(), rows[x][1].cuda(), pools[x, 0], pools[x, 1], slots)
+        decode_all()
+    # some leave, one takes tokens back; the rest moves together
+    to = [0, -1, 40, -1, -1, 0, -1, -1]
+    api.pa_truncate_sequences(tables, lens, counts, i32(*to), B)
+    for s, n in enumerate(to):
+        if n >= 0:
+            hist[s] = [[h[:n] for h in layer] for layer in hist[s]]
+    moves, num = torch.empty((N, 2), dtype=torch.int64, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    api.pa_compact_blocks(moves, num, tables, lens, counts, tables, counts, B, space)
+    api.pa_copy_layer_blocks(flat, moves)
+    flat[:, int((counts != 0).sum()):] = float("nan")  # what was given back
+    assert int(num) > 0
+    decode_all()

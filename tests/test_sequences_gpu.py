@@ -1,0 +1,371 @@
+"""The calls on the sequences' blocks against the oracle: every result is a whole number, so all
+of them are equal to it, in any state: full pools, refused sequences, shared blocks, bad values."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import sequence_oracle as so
+from paged_kv_cache_173_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+class Server:
+    """Tables, lengths and counts on the device beside the oracle's; every call is made of both and compared."""
+
+    def __init__(self, S, M, N, B, seed=0):
+        self.S, self.M, self.N, self.B = S, M, N, B
+        self.rng = np.random.default_rng(seed)
+        self.set(np.full((S, M), -1, np.int32), np.zeros(S, np.int32), np.zeros(N, np.int32))
+        self.ws = torch.full((api.pa_sequence_workspace_bytes(N) // 4,), 0x7F7F7F7F, dtype=torch.int32, device="cuda")
+
+    def set(self, tables, lens, counts):
+        self.host = (tables, lens, counts)
+        self.tables, self.lens, self.counts = (dev(x) for x in self.host)
+
+    def same(self):
+        torch.cuda.synchronize()
+        for name, got, want in zip(("tables", "lens", "counts"), (self.tables, self.lens, self.counts), self.host):
+            got = got.cpu().numpy()
+            assert np.array_equal(got, want), (name, np.argwhere(got != want)[:5].tolist())
+
+    def extend(self, new, spare=3, starts=None, stream=None):
+        if starts is None:
+            starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        T = max(0, int(starts[-1]) + spare)
+        slots = torch.full((T,), 77, dtype=torch.int64, device="cuda")
+        copies = torch.full((self.S, 2), 77, dtype=torch.int64, device="cuda")
+        left = torch.full((2,), 77, dtype=torch.int32, device="cuda")
+        self.ws.fill_(0x7F7F7F7F)
+        api.pa_extend_sequences(self.tables, self.lens, self.counts, dev(starts.astype(np.int32)), slots, copies, left, self.B, self.ws)
+        *self.host, want_slots, want_copies, want_left = so.extend(*self.host, starts, T, self.B)
+        self.same()
+        assert np.array_equal(slots.cpu().numpy(), want_slots)
+        assert np.array_equal(copies.cpu().numpy(), want_copies)
+        assert np.array_equal(left.cpu().numpy(), want_left), (left, want_left)
+        return want_slots, want_copies, want_left
+
+    def truncate(self, to):
+        api.pa_truncate_sequences(self.tables, self.lens, self.counts, dev(np.asarray(to, np.int32)), self.B)
+        self.host = so.truncate(*self.host, np.asarray(to), self.B)
+        self.same()
+
+    def fork(self, source):
+        api.pa_fork_sequences(self.tables, self.lens, self.counts, dev(np.asarray(source, np.int32)), self.B)
+        self.host = so.fork(*self.host, np.asarray(source), self.B)
+        self.same()
+
+    def compact(self, limit, in_place=True):
+        moves = torch.full((limit, 2), 77, dtype=torch.int64, device="cuda")
+        num = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+        to, co = (self.tables, self.counts) if in_place else (torch.full_like(self.tables, 77), torch.full_like(self.counts, 77))
+        before = self.host
+        api.pa_compact_blocks(moves, num, self.tables, self.lens, self.counts, to, co, self.B, self.ws)
+        want_moves, want_num, tables, counts = so.compact(*self.host, limit, self.B)
+        if not in_place:
+            self.same()
+            self.tables, self.counts = to, co
+        self.host = (tables, before[1], counts)
+        self.same()
+        assert int(num) == want_num and np.array_equal(moves.cpu().numpy(), want_moves)
+        return want_moves[:want_num]
+
+    def any_call(self, most):
+        rng, S = self.rng, self.S
+        op = rng.integers(0, 6)
+        if op <= 1:
+            return self.extend(rng.integers(0, most, S) * (rng.random(S) < 0.5))
+        if op == 2:
+            return self.truncate(np.where(rng.random(S) < 0.4, rng.integers(-1, self.M * self.B, S), -1))
+        if op == 3:
+            self.truncate(np.where(rng.random(S) < 0.2, 0, -1))
+            return self.fork(np.where(rng.random(S) < 0.5, rng.integers(-1, S + 1, S), -1))
+        return self.compact(int(rng.integers(0, self.N + 2)), bool(op == 4))
+
+
+@pytest.mark.parametrize("S,M,N,B,most", [
+    (1, 1, 1, 16, 3), (1, 40, 33, 16, 90), (5, 7, 30, 16, 40), (17, 9, 100, 32, 100), (64, 33, 700, 16, 200),
+    (300, 5, 1000, 64, 100), (9, 12, 70, 256, 900), (1100, 4, 3000, 16, 20), (40, 130, 4099, 16, 700), (3, 50, 127, 128, 2000)])
+def test_random_walks(S, M, N, B, most):
+    s = Server(S, M, N, B, seed=S + N)
+    for _ in range(25):
+        s.any_call(most)
+    assert np.array_equal(s.host[2], so.holders(s.host[0], s.host[1], N, B))
+
+
+def test_many_sequences_and_a_large_pool():
+    s = Server(20000, 3, 150001, 16, seed=3)
+    for _ in range(2):
+        s.extend(s.rng.integers(0, 20, s.S))
+        s.truncate(np.where(s.rng.random(s.S) < 0.5, s.rng.integers(0, 12, s.S), -1))
+        s.fork(np.where(s.rng.random(s.S) < 0.5, s.rng.integers(0, s.S, s.S), -1))
+        s.extend(s.rng.integers(0, 3, s.S))
+        s.compact(1000)
+        s.compact(150001, False)
+
+
+def test_a_pool_of_four_million_blocks():
+    N = 4 * 1024 * 1024 + 5
+    s = Server(2, 2000, N, 16, seed=4)
+    counts = (s.rng.random(N) < 0.999).astype(np.int32)
+    counts[-3:] = 0
+    s.set(s.host[0], s.host[1], counts)
+    s.extend(np.array([2000 * 16, 1500 * 16]))
+    s.extend(np.array([0, 400 * 16]))
+    s.compact(3000)
+
+
+def test_all_sequences_of_the_largest_batch():
+    S = 65535
+    s = Server(S, 1, S - 7, 16, seed=5)
+    slots, _, left = s.extend(np.full(S, 2))
+    assert left.tolist() == [0, 7] and (slots[-14 - 3:] == -1).all()
+    s.truncate(np.where(np.arange(S) % 2 == 0, 0, -1))
+    s.extend(np.where(np.arange(S) % 2 == 0, 16, 0))
+
+
+def test_a_full_pool_refuses_in_order():
+    s = Server(4, 4, 6, 16)
+    _, _, left = s.extend(np.array([40, 33, 1, 0]))  # 3 + 3 blocks, then nothing is left
+    assert left.tolist() == [0, 1] and s.host[1].tolist() == [40, 33, 0, 0]
+    _, _, left = s.extend(np.array([8, 16, 0, 1]))   # room in the last block; one more block; none
+    assert left.tolist() == [0, 2] and s.host[1].tolist() == [48, 33, 0, 0]
+    _, _, left = s.extend(np.array([17, 15, 1, 1]))  # the table ends; fits; nothing left
+    assert left.tolist() == [0, 3] and s.host[1].tolist() == [48, 48, 0, 0]
+    s.truncate([16, 0, -1, 5])
+    _, _, left = s.extend(np.array([0, 64, 20, 1]))  # 4 of 5 blocks, then 2 of 1: the next is refused too
+    assert left.tolist() == [1, 2]
+
+
+def test_a_shared_last_block_is_copied_once_for_each_that_grows():
+    s = Server(5, 3, 20, 16)
+    s.extend(np.array([20, 0, 0, 0, 0]))
+    s.fork([-1, 0, 0, 0, -1])
+    s.fork([-1, -1, -1, -1, 1])
+    assert s.host[2][:2].tolist() == [5, 5]
+    _, copies, _ = s.extend(np.array([0, 1, 15, 0, 0]))
+    assert copies.tolist() == [[-1, -1], [1, 2], [1, 3], [-1, -1], [-1, -1]]
+    _, copies, _ = s.extend(np.array([1, 1, 1, 1, 1]))  # all that are left leave it: it is free afterwards
+    assert copies[:, 0].tolist() == [1, -1, -1, 1, 1] and s.host[2][1] == 0
+    s.truncate([16, -1, -1, -1, -1])
+    _, copies, _ = s.extend(np.array([3, 0, 0, 0, 0]))  # a whole shared block needs no copy
+    assert copies[0].tolist() == [-1, -1]
+
+
+def test_forks_that_are_left_alone():
+    s = Server(6, 3, 20, 16)
+    s.extend(np.array([20, 0, 30, 0, 0, 0]))
+    # onto a live one, from an empty one, from oneself, from outside, from one that is forked onto
+    s.fork([2, 3, -1, 3, 6, 3])
+    assert s.host[1].tolist() == [20, 0, 30, 0, 0, 0]
+    s.fork([-1, 0, -1, 1, -7, 2])
+    assert s.host[1].tolist() == [20, 20, 30, 0, 0, 30]
+
+
+def test_bad_values_are_passed_over():
+    s = Server(6, 3, 20, 16)
+    s.extend(np.array([20, 20, 20, 20, 20, 0]))
+    tables, lens, counts = (x.copy() for x in s.host)
+    tables[0, 1], tables[1, 0], tables[2, 1] = 20, -5, 2 ** 31 - 1  # ids outside the pool
+    lens[3], lens[4] = 49, -3  # a length past the table, a negative one
+    s.set(tables, lens, counts)
+    s.extend(np.array([1, 1, 1, 1, 1, 1]))
+    s.fork([-1, -1, -1, -1, -1, 1])
+    s.truncate([0, 0, 5, 0, 0, 3])
+    s.compact(20)
+    s.set(tables, lens, counts)
+    s.compact(20, False)
+
+
+@pytest.mark.parametrize("starts", [[0, 5, 3, 9], [0, 5, 100, 8], [-4, 2, 3, 5], [0, 0, 0, 0], [2, 4, 6, 8]])
+def test_starts_that_cannot_be_refuse_their_sequences_only(starts):
+    s = Server(3, 3, 20, 16)
+    starts = np.array(starts, np.int32)
+    slots = torch.full((12,), 77, dtype=torch.int64, device="cuda")
+    copies, left = torch.empty((3, 2), dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    api.pa_extend_sequences(s.tables, s.lens, s.counts, dev(starts), slots, copies, left, 16, s.ws)
+    *s.host, want_slots, want_copies, want_left = so.extend(*s.host, starts, 12, 16)
+    s.same()
+    assert np.array_equal(copies.cpu().numpy(), want_copies) and np.array_equal(left.cpu().numpy(), want_left)
+    if (np.diff(starts) >= 0).all():
+        got = slots.cpu().numpy()
+        assert np.array_equal(got[max(0, starts[0]):], want_slots[max(0, starts[0]):])
+
+
+def test_no_sequences_and_no_tokens():
+    s = Server(2, 3, 20, 16)
+    empty, none = s.tables[:0], s.lens[:0]
+    slots, left = torch.full((4,), 5, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    api.pa_extend_sequences(empty, none, s.counts, torch.zeros(1, dtype=torch.int32, device="cuda"), slots,
+                            torch.zeros((0, 2), dtype=torch.int64, device="cuda"), left, 16, s.ws)
+    assert slots.tolist() == [-1] * 4 and left.tolist() == [20, 0]
+    api.pa_truncate_sequences(empty, none, s.counts, none, 16)
+    api.pa_fork_sequences(empty, none, s.counts, none, 16)
+    num = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    api.pa_compact_blocks(torch.empty((0, 2), dtype=torch.int64, device="cuda"), num, empty, none, s.counts, empty, s.counts, 16, s.ws)
+    assert int(num) == 0
+    s.extend(np.array([0, 0]), spare=0)
+
+
+@pytest.mark.parametrize("L,N,inner,dtype,pad", [
+    (1, 5, (16, 2, 64), torch.float16, 0), (3, 40, (16, 8, 128), torch.bfloat16, 0), (7, 33, (2,), torch.float32, 0),
+    (2, 30, (3, 5), torch.float32, 1), (4, 9, (2, 2, 128), torch.int8, 0), (2, 6, (256, 8, 128), torch.float16, 8),
+    (32, 700, (1,), torch.float32, 0), (64, 300, (16, 1, 64), torch.float16, 0)])
+def test_copy_of_layers(L, N, inner, dtype, pad):
+    g = torch.Generator().manual_seed(L * N)
+    size = int(np.prod(inner))
+    flat = torch.randint(-100, 100, (L, N * size + pad), generator=g).to(dtype).cuda()
+    pools = flat[:, :N * size].view(L, N, *inner) if pad == 0 else flat.as_strided(
+        (L, N) + inner, (N * size + pad, size) + tuple(int(np.prod(inner[i + 1:])) for i in range(len(inner))))
+    perm = torch.randperm(N, generator=g)
+    n = N // 2
+    pairs = torch.stack([perm[:n], perm[n:2 * n]], 1)
+    bad = torch.tensor([[-1, 0], [0, -1], [N, 1], [1, N], [2, 2], [-1, -1], [2 ** 40, 0], [0, 2 ** 40]])
+    both = torch.cat([pairs, bad])[torch.randperm(n + len(bad), generator=g)]
+    want = flat.clone()
+    view = want.as_strided(pools.shape, pools.stride())
+    view[:, pairs[:, 1]] = pools[:, pairs[:, 0]]
+    api.pa_copy_layer_blocks(pools, both.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(flat, want)
+
+
+def test_copy_of_more_pairs_than_one_round_holds():
+    pools = torch.arange(2 * 9000 * 4, dtype=torch.int32, device="cuda").view(2, 9000, 4)
+    pairs = torch.stack([torch.arange(4500), torch.arange(4500) + 4500], 1)
+    want = pools.clone()
+    want[:, 4500:] = want[:, :4500]
+    api.pa_copy_layer_blocks(pools, pairs.cuda())
+    assert torch.equal(pools, want)
+
+
+def test_copy_past_four_gigabytes():
+    N, size = 70000, 16 * 8 * 128  # 2.3 GB a pool
+    pools = torch.zeros((3, N, size), dtype=torch.float16, device="cuda")
+    pools[:, 7] = torch.arange(3, device="cuda").half()[:, None] + 1
+    api.pa_copy_layer_blocks(pools, torch.tensor([[7, N - 1]]).cuda())
+    assert pools[:, N - 1].float().mean(1).tolist() == [1, 2, 3] and not pools[:, N - 2].any()
+
+
+def test_captured_steps_replay_with_new_contents():
+    B, S, N = 16, 40, 400
+    s = Server(S, 20, N, B, seed=6)
+    s.extend(s.rng.integers(1, 60, S))
+    to, source, starts = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (S, S, S + 1))
+    slots, copies = torch.zeros(300, dtype=torch.int64, device="cuda"), torch.zeros((S, 2), dtype=torch.int64, device="cuda")
+    left, num = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    moves = torch.zeros((50, 2), dtype=torch.int64, device="cuda")
+    pools = torch.randn((3, N, 8), device="cuda")
+
+    def step():
+        api.pa_truncate_sequences(s.tables, s.lens, s.counts, to, B)
+        api.pa_fork_sequences(s.tables, s.lens, s.counts, source, B)
+        api.pa_extend_sequences(s.tables, s.lens, s.counts, starts, slots, copies, left, B, s.ws)
+        api.pa_copy_layer_blocks(pools, copies)
+        api.pa_compact_blocks(moves, num, s.tables, s.lens, s.counts, s.tables, s.counts, B, s.ws)
+        api.pa_copy_layer_blocks(pools, moves)
+
+    keep = [x.clone() for x in (s.tables, s.lens, s.counts, pools)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    for x, y in zip((s.tables, s.lens, s.counts, pools), keep):
+        x.copy_(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    want = pools.cpu().numpy()
+    for _ in range(6):
+        cut = np.where(s.rng.random(S) < 0.4, s.rng.integers(0, 60, S) * (s.rng.random(S) < 0.5), -1)
+        src = np.where(s.rng.random(S) < 0.5, s.rng.integers(0, S, S), -1)
+        begin = np.concatenate([[0], np.cumsum(s.rng.integers(0, 7, S))]).astype(np.int32)
+        for x, y in ((to, cut), (source, src), (starts, begin)):
+            x.copy_(torch.from_numpy(y.astype(np.int32)))
+        graph.replay()
+        s.host = so.fork(*so.truncate(*s.host, cut, B), src, B)
+        *s.host, want_slots, want_copies, want_left = so.extend(*s.host, begin, 300, B)
+        want_moves, n, tables, counts = so.compact(*s.host, 50, B)
+        s.host = (tables, s.host[1], counts)
+        s.same()
+        assert np.array_equal(slots.cpu().numpy(), want_slots) and np.array_equal(left.cpu().numpy(), want_left)
+        assert np.array_equal(copies.cpu().numpy(), want_copies) and np.array_equal(moves.cpu().numpy(), want_moves)
+        for pairs in (want_copies, want_moves):
+            old = want.copy()
+            for a, b in pairs.tolist():
+                if a >= 0:
+                    want[:, b] = old[:, a]
+        assert np.array_equal(pools.cpu().numpy(), want)
+
+
+def test_two_servers_on_two_streams():
+    servers = [Server(50, 12, 300, 16, seed=x) for x in (7, 8)]
+    news = [s.rng.integers(0, 30, (8, 50)) for s in servers]
+    streams = [torch.cuda.Stream() for _ in servers]
+    bufs = [[(dev(np.concatenate([[0], np.cumsum(n)]).astype(np.int32)), torch.empty(int(n.sum()), dtype=torch.int64, device="cuda"),
+              torch.empty((50, 2), dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda"))
+             for n in new] for new in news]
+    half = torch.full((50,), 20, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(8):
+        for s, st, b in zip(servers, streams, bufs):
+            api.pa_extend_sequences(s.tables, s.lens, s.counts, *b[i], s.B, s.ws, stream=st)
+            api.pa_truncate_sequences(s.tables, s.lens, s.counts, half, s.B, stream=st)
+    for s, new, b in zip(servers, news, bufs):
+        for i in range(8):
+            starts = b[i][0].cpu().numpy()
+            *s.host, slots, _, left = so.extend(*s.host, starts, int(starts[-1]), s.B)
+            assert np.array_equal(b[i][1].cpu().numpy(), slots) and np.array_equal(b[i][3].cpu().numpy(), left)
+            s.host = so.truncate(*s.host, half.cpu().numpy(), s.B)
+        s.same()
+
+
+def test_binding_refuses_what_it_cannot_take():
+    s = Server(4, 3, 20, 16)
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = lambda *n: torch.zeros(n, dtype=torch.int64, device="cuda")  # noqa: E731
+    good = dict(block_tables=s.tables, context_lens=s.lens, ref_counts=s.counts, query_start_loc=i32(5), slot_mapping=i64(3),
+                block_copies=i64(4, 2), left=i32(2), block_size=16, workspace=s.ws)
+    for error, kw in [(TypeError, dict(ref_counts=s.counts.long())), (ValueError, dict(ref_counts=s.counts.view(4, 5))),
+                      (ValueError, dict(context_lens=s.lens[:3])), (ValueError, dict(block_tables=s.tables.t())),
+                      (ValueError, dict(query_start_loc=i32(4))), (TypeError, dict(query_start_loc=i64(5))),
+                      (TypeError, dict(slot_mapping=i32(3))), (ValueError, dict(block_copies=i64(3, 2))),
+                      (ValueError, dict(left=i32(1))), (ValueError, dict(workspace=s.ws.cpu())),
+                      (api.PagedAttnError, dict(workspace=s.ws[:10])), (api.PagedAttnError, dict(block_size=20)),
+                      (ValueError, dict(slot_mapping=i64(6)[::2]))]:
+        with pytest.raises(error):
+            api.pa_extend_sequences(**{**good, **kw})
+    with pytest.raises(ValueError):
+        api.pa_truncate_sequences(s.tables, s.lens, s.counts, i32(3), 16)
+    with pytest.raises(TypeError):
+        api.pa_fork_sequences(s.tables, s.lens, s.counts, i64(4), 16)
+    with pytest.raises(ValueError):
+        api.pa_compact_blocks(i64(4, 3), i32(1), s.tables, s.lens, s.counts, s.tables, s.counts, 16, s.ws)
+    with pytest.raises(ValueError):
+        api.pa_compact_blocks(i64(4, 2), i32(1), s.tables, s.lens, s.counts, s.tables[:, :2], s.counts, 16, s.ws)
+    with pytest.raises(ValueError):
+        api.pa_copy_layer_blocks(torch.zeros((2, 4, 8), device="cuda").transpose(1, 2), i64(1, 2))
+    with pytest.raises(TypeError):
+        api.pa_copy_layer_blocks(torch.zeros((2, 4, 8), device="cuda"), i32(1, 2))
+    with pytest.raises(ValueError):
+        api.pa_copy_layer_blocks(torch.zeros((2, 4), device="cuda"), i64(1, 2))
+    with pytest.raises(api.PagedAttnError):  # blocks of 3 bytes
+        api.pa_copy_layer_blocks(torch.zeros((2, 4, 3), dtype=torch.uint8, device="cuda"), i64(1, 2))
+    with pytest.raises(api.PagedAttnError):  # layers that overlap
+        api.pa_copy_layer_blocks(torch.zeros(100, device="cuda").as_strided((2, 4, 8), (16, 8, 1)), i64(1, 2))
+    s.same()
