@@ -75,6 +75,8 @@ SIGNATURES = {
 # The entry points that the binding's C++ half (csrc/py_fast.cpp) calls, in the order its bind() takes.
 FAST_ENTRIES = ("pa_reshape_and_cache_fp8_block", "pa_update_key_bounds", "pa_decode_fp8_block",
                 "pa_decode_splitk_fp8_block", "pa_prefill_fp8_block", "pa_select_blocks", "pa_decode_sparse")
+FAST_SEQUENCE_ENTRIES = ("pa_prefill_packed", "pa_extend_sequences", "pa_truncate_sequences", "pa_fork_sequences",
+                         "pa_compact_blocks", "pa_copy_layer_blocks")  # those of its bind_sequences()
 
 _lib: Optional[ctypes.CDLL] = None
 _fast = None
@@ -121,7 +123,9 @@ def fast():
                 except ImportError as e:
                     raise RuntimeError(f"the binding's C++ half for this torch and Python ({path}) is missing or does not "
                                        "load: build it first (python -m paged_kv_cache_173_gb300.build)") from e
-                m.bind(*[ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in FAST_ENTRIES])
+                address = lambda n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value  # noqa: E731
+                m.bind(*map(address, FAST_ENTRIES))
+                m.bind_sequences(*map(address, FAST_SEQUENCE_ENTRIES))
                 _fast = m
     return _fast
 

@@ -626,6 +626,11 @@ def pa_prefill_packed(out: torch.Tensor, q: torch.Tensor, key: torch.Tensor, val
     of any stride: parts of one projection's output will do), sequence s owning the rows
     query_start_loc[s] .. query_start_loc[s+1].  With k_cache, v_cache [N, B, Hk, d] and
     slot_mapping [rows] (int64) the key and value rows go into the pools as well."""
+    if q.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().packed(out, q, key, value, query_start_loc, max_query_len, scale, k_cache, v_cache, slot_mapping, dev, sp):
+            return
     i = _cuda_index(q)
     R, H, d = q.shape
     Hk = key.shape[1] if key.dim() == 3 else 0
@@ -684,6 +689,12 @@ def pa_extend_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor, 
     blocks (ref_counts [N] == 0) go into block_tables [S, M] and context_lens [S] grows.  Writes
     the tokens' slots (slot_mapping, int64), the copies that shared last blocks need
     (block_copies [S, 2], int64) and left [2] (free blocks, refused sequences)."""
+    if block_tables.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().extend(block_tables, context_lens, ref_counts, query_start_loc, slot_mapping, block_copies, left,
+                              block_size, workspace, dev, sp):
+            return
     i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
     if query_start_loc.shape != (S + 1,):
         raise ValueError("query_start_loc must be [S + 1]")
@@ -701,6 +712,11 @@ def pa_truncate_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor
                           stream: Optional[torch.cuda.Stream] = None) -> None:
     """Cut each sequence with 0 <= new_lens[s] < context_lens[s] to new_lens[s] tokens (0: free it)
     and give its blocks back."""
+    if block_tables.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().truncate(block_tables, context_lens, ref_counts, new_lens, block_size, dev, sp):
+            return
     i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
     if new_lens.shape != (S,):
         raise ValueError("new_lens must be [S]")
@@ -711,6 +727,11 @@ def pa_truncate_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor
 def pa_fork_sequences(block_tables: torch.Tensor, context_lens: torch.Tensor, ref_counts: torch.Tensor,
                       fork_from: torch.Tensor, block_size: int, stream: Optional[torch.cuda.Stream] = None) -> None:
     """Each empty sequence with fork_from[s] >= 0 becomes a copy of that sequence and shares its blocks."""
+    if block_tables.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().fork(block_tables, context_lens, ref_counts, fork_from, block_size, dev, sp):
+            return
     i, S, M, N, head = _sequence_args(block_tables, context_lens, ref_counts)
     if fork_from.shape != (S,):
         raise ValueError("fork_from must be [S]")
@@ -725,6 +746,12 @@ def pa_compact_blocks(moves: torch.Tensor, num_moves: torch.Tensor, block_tables
     """Plan at most len(moves) moves of the highest used blocks to the lowest free ones: moves
     [max, 2] (int64), num_moves [1] (int32), and the tables and counts after them (tables_out,
     counts_out: the inputs themselves, or others).  Follow with pa_copy_layer_blocks."""
+    if block_tables.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().compact(moves, num_moves, block_tables, context_lens, ref_counts, tables_out, counts_out,
+                               block_size, workspace, dev, sp):
+            return
     i, S, M, N, (tables, _, lens, counts) = _sequence_args(block_tables, context_lens, ref_counts)
     if moves.dim() != 2 or moves.shape[1] != 2 or num_moves.shape != (1,):
         raise ValueError("moves must be [max_moves, 2] and num_moves [1]")
@@ -741,6 +768,11 @@ def pa_copy_layer_blocks(pools: torch.Tensor, block_mapping: torch.Tensor,
                          stream: Optional[torch.cuda.Stream] = None) -> None:
     """For each row (src, dst) of block_mapping [n, 2] (int64) and each layer l of pools [L, N, ...]
     (any type; a layer's blocks contiguous): pools[l, dst] = pools[l, src]."""
+    if pools.is_cuda:
+        dev = _get_device()
+        sp = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _lib.fast().copy_layers(pools, block_mapping, dev, sp):
+            return
     i = _cuda_index(pools)
     if pools.dim() < 3:
         raise ValueError("pools must be [L, N, ...]: the pools of L layers")

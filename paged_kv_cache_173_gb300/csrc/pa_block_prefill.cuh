@@ -63,6 +63,7 @@
 
 #include "pa_block.cuh"
 #include "pa_prefill.cuh"
+#include "pa_tc.cuh"
 
 namespace pa {
 
@@ -150,12 +151,6 @@ struct BpCfg {
 
 __device__ __forceinline__ uint4 ldg128(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-// What is computed from x is computed after this point.  A value loaded an
-// iteration ahead would otherwise be turned into an address right behind its
-// load, and the warp would wait there.
-__device__ __forceinline__ void use_here(int& x) { asm volatile("" : "+r"(x)); }
-__device__ __forceinline__ void use_here(float& x) { asm volatile("" : "+f"(x)); }
-
 // 2^-100: the least size of the factor that a raw score (below 2^33) is multiplied by; it makes 0 of
 // every score.
 constexpr float kLeastFactor = 7.888609052210118e-31f;
@@ -191,101 +186,10 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
   e4m3x4_to_half2x2(c.w, b.z, b.w);
 }
 
-// Pairs of float32 in one 64-bit register pair: one instruction for both.
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack_f32x2(float x) { return pack_f32x2(__float_as_uint(x), __float_as_uint(x)); }
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// The MMAs and the commit of pa_ptx.cuh issued by one elected lane of a warp that
-// runs them together.
-__device__ __forceinline__ void umma_f16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
-}
-__device__ __forceinline__ void umma_f16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                  bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u));
-}
-__device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // ---------------------------------------------------------------- work items
 // An item is a pair of query tiles of one (sequence, KV head).  A CTA starts with
 // the item of its own grid index and then takes over CTAs that have not started
 // yet, one at a time: cancelling one hands over its index.
-
-// Ask for a CTA of this grid that has not started; the answer lands in `resp`.
-__device__ __forceinline__ void ask_for_cta(void* resp, uint64_t* bar) {
-  mbar_arrive_expect_tx(bar, 16);
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-          smem_addr(resp)),
-      "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Whether the answer names a CTA, and its grid index.
-__device__ __forceinline__ bool cta_given(const void* resp, uint3& id) {
-  uint32_t got;
-  asm volatile(
-      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%4];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
-      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
-      : "=&r"(got), "=&r"(id.x), "=&r"(id.y), "=&r"(id.z)
-      : "r"(smem_addr(resp))
-      : "memory");
-  return got != 0;
-}
 
 struct PrefillItem {
   int s, kvh;
@@ -381,36 +285,6 @@ __device__ __forceinline__ void write_nan_rows(const BlockPrefillParams& p, cons
 
 // The bytes of a word of codes that are NaN, as 0x80 each.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-// The four lanes 4 i .. 4 i + 3 exchange: lane q's unit a[c] goes to a[q] of lane c.
-__device__ __forceinline__ void transpose4(uint4 (&a)[4], int lane) {
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = o == 1 ? 2 * i : i;
-      const uint4 x = up ? a[c] : a[c + o];
-      uint4 y;
-      y.x = __shfl_xor_sync(FULL_MASK, x.x, o);
-      y.y = __shfl_xor_sync(FULL_MASK, x.y, o);
-      y.z = __shfl_xor_sync(FULL_MASK, x.z, o);
-      y.w = __shfl_xor_sync(FULL_MASK, x.w, o);
-      if (up) a[c] = y;
-      else a[c + o] = y;
-    }
-  }
-}
-
-// The registers of each thread of the calling warpgroup from here on.
-template <bool UP, int N>
-__device__ __forceinline__ void set_max_regs() {
-  if constexpr (UP) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-  }
-}
 
 template <typename T, int HEAD_DIM, bool IS_RAGGED>
 __global__ void __launch_bounds__(BpCfg<HEAD_DIM>::THREADS, 1)

@@ -1,0 +1,913 @@
+// pa_packed_prefill.cuh -- causal attention over whole prompts in packed rows, on the
+// tcgen05 tensor cores, with the cache write of the prompts' keys and values.
+//
+//  packed_prefill_tc_kernel  one CTA per SM; an item of work is a pair of query tiles of
+//                            a (KV head, sequence), a tile up to 128 rows (128 / G tokens
+//                            x G heads, G any group up to 16).  Q K^T and P V in tensor
+//                            memory (S 128 and O 128 columns per tile, P over S), one
+//                            softmax thread per row with the block's 128 scores in
+//                            registers.
+//
+// Warps: two warpgroups of softmax (a tile each), one that writes the item's own keys and
+// values into the pools and makes masked values safe, and one with an MMA warp per tile, a
+// warp for the work items and one for the loads of K and V (TMA, 128 keys at a time).
+//
+// The method: causal multi-query attention ("in-depth reading", section 5.1, item 5;
+// "vAttention", contiguous prefill), online softmax of "vLLM PagedAttention source
+// walk-through", section 3.4.
+#pragma once
+
+#include "pa_block.cuh"
+#include "pa_prefill.cuh"
+#include "pa_tc.cuh"
+
+namespace pa {
+
+namespace {
+
+struct PackedParams {
+  CUtensorMap tmap_q;  // q as rows x heads x dims: box of 64 dims x G heads x 128 / G rows, 128-byte swizzle
+  CUtensorMap tmap_k;  // key likewise: 64 dims x 1 head x 128 rows
+  CUtensorMap tmap_v;
+  void* out;
+  const void* key;
+  const void* value;
+  int64_t k_stride;  // elements
+  int64_t v_stride;
+  void* k_cache;  // null: no cache write
+  void* v_cache;
+  const int64_t* slot_mapping;
+  int64_t num_slots;
+  const int32_t* query_start_loc;
+  uint64_t pair_magic;  // ceil(2^64 / tokens of a pair): the high half of a product with it divides
+  int num_seqs;
+  int num_rows;
+  int max_query_len;
+  int num_heads;
+  int num_kv_heads;
+  int group;
+  int inv_g;  // 65536 / group + 1: r / group = r * inv_g >> 16 for the rows r < 128 of a tile
+  int tile_tokens;
+  int pairs;
+  // grid order: (KV head, sequence, pair) or, longest_first = 0, (pair, KV head, sequence).  Ragged
+  // kernels: one dimension, KV head and place in the list of all sequences' pairs, longest first.
+  int longest_first;
+  float scale_log2;
+};
+
+template <typename T, int HEAD_DIM>
+struct PpCfg {
+  static constexpr bool BF16 = !std::is_same<T, __half>::value;
+  static constexpr int SOFT = TC_TILES * TC_ROWS;  // softmax threads
+  static constexpr int SIDE_WARP = SOFT / 32;      // cache write, masked values
+  static constexpr int SIDE = 128;
+  static constexpr int MMA_WARP = SIDE_WARP + SIDE / 32;
+  static constexpr int ITEM_WARP = MMA_WARP + TC_TILES;
+  static constexpr int LOAD_WARP = ITEM_WARP + 1;
+  static constexpr int THREADS = SOFT + SIDE + 128;
+  static constexpr int SOFT_REGS = 184;
+  static constexpr int SIDE_REGS = 64;
+  static constexpr int MMA_REGS = 80;
+  // what the warpgroups hold is what the block was launched with
+  static_assert(SOFT * SOFT_REGS + SIDE * SIDE_REGS + 128 * MMA_REGS <= THREADS * 128, "registers");
+  static constexpr int DBOX = HEAD_DIM / BOX_DIMS;
+  static constexpr int QATOM = TC_ROWS * 128;
+  static constexpr int QBYTES = DBOX * QATOM;
+  static constexpr int KATOM = TC_KEYS * 128;
+  static constexpr int KBYTES = DBOX * KATOM;
+  static constexpr int SMEM_MAX = 227 * 1024;
+  static constexpr int RESERVE = 1024 + 1024;  // base alignment slack, items, barriers
+  static constexpr int STAGES_FIT = (SMEM_MAX - RESERVE - TC_TILES * QBYTES) / KBYTES;
+  static constexpr int KSTAGES = STAGES_FIT / 2 < 4 ? STAGES_FIT / 2 : 4;
+  static constexpr int VSTAGES = STAGES_FIT - KSTAGES < 4 ? STAGES_FIT - KSTAGES : 4;
+  static_assert(KSTAGES >= 2 && VSTAGES >= 2 && KSTAGES <= VSTAGES, "the rings");
+  static constexpr int K_OFF = TC_TILES * QBYTES;
+  static constexpr int V_OFF = K_OFF + KSTAGES * KBYTES;
+  static constexpr int INFO_OFF = V_OFF + VSTAGES * KBYTES;
+  // Published items.  The loads run at most VSTAGES blocks, so as many items, ahead of the outputs that
+  // are still being written, and the next one is published when they begin one.
+  static constexpr int ITEMS = 8;
+  static_assert(VSTAGES + 3 <= ITEMS, "the ring of items");
+  static constexpr int INFO = 8;  // words of an item
+  static constexpr int RESP_OFF = INFO_OFF + ITEMS * INFO * 4;
+  static constexpr int BAR_OFF = RESP_OFF + 16;
+  static constexpr int DONE = VSTAGES;  // ring of completed steps
+  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 7 * TC_TILES + ITEMS + 2;
+  static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
+  static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
+  static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
+  static_assert(SMEM_BYTES <= SMEM_MAX, "shared memory");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t ID_S = umma_idesc_f16(TC_ROWS, TC_KEYS, BF16, false);
+  static constexpr uint32_t ID_PV = umma_idesc_f16(TC_ROWS, HEAD_DIM, BF16, true);
+  // log2 of the largest weight when the running maximum has just moved; it may grow by 2^8 from there.
+  // float16: up to 2^15, so that small weights keep their bits.  bfloat16 has float32's range, and weights
+  // of 2^-8 at most keep a sum of 2^8 of its largest values within it.
+  static constexpr float MID = BF16 ? -16.f : 7.f;
+};
+
+// ---------------------------------------------------------------- work items
+struct PackedItem {
+  int s, kvh;
+  int ta;    // first token of tile 0
+  int q0;    // row of the sequence's first token
+  int qlen;  // its tokens
+
+  __device__ __forceinline__ int tiles(int tt) const { return ta + tt < qlen ? 2 : 1; }
+  // one past tile u's last token, which is as many keys as its last row sees, and the key blocks that it meets
+  __device__ __forceinline__ int tile_end(int u, int tt) const { return min(qlen, ta + (u + 1) * tt); }
+  __device__ __forceinline__ int tile_blocks(int u, int tt) const {
+    return u < tiles(tt) ? (tile_end(u, tt) + TC_KEYS - 1) / TC_KEYS : 0;
+  }
+  __device__ __forceinline__ int kend(int tt) const { return tile_end(1, tt); }
+  __device__ __forceinline__ int blocks(int tt) const { return (kend(tt) + TC_KEYS - 1) / TC_KEYS; }
+  // The first block with a key that some row of the item does not see.  The item's last block is always one:
+  // ta is even, so ta + 1 tokens fill no block.
+  __device__ __forceinline__ int first_masked() const { return ta / TC_KEYS; }
+};
+
+// The rows of sequence i: the first one, and how many are computed (at most 0: none).
+__device__ __forceinline__ int rows_of(const PackedParams& p, int i, int& q0) {
+  q0 = min(max(__ldg(p.query_start_loc + i), 0), p.num_rows);
+  return min(min(max(__ldg(p.query_start_loc + i + 1), 0), p.num_rows) - q0, p.max_query_len);
+}
+
+// The pairs of query tiles of sequence i (0 past the last).
+__device__ __forceinline__ int pairs_of(const PackedParams& p, int i) {
+  if (i >= p.num_seqs) return 0;
+  int q0;
+  const int n = rows_of(p, i, q0);
+  return n <= 0 ? 0 : static_cast<int>(__umul64hi(static_cast<uint64_t>(n - 1), p.pair_magic)) + 1;
+}
+
+// Place `at` of the list of all sequences' pairs, the pairs of highest number first and those of
+// one number in the sequences' order: (pair, sequence), or false past the last.  The whole warp
+// searches; C(x), the pairs numbered above x, is the sum over the sequences of max(0, pairs - 1 - x).
+__device__ __forceinline__ bool listed_pair(const PackedParams& p, int at, int& pair, int& s) {
+  const int lane = threadIdx.x & 31;
+  auto above = [&](int x) {
+    int n = 0;
+    for (int i = lane; i < p.num_seqs; i += 32) n += max(0, pairs_of(p, i) - 1 - x);
+    return __reduce_add_sync(kFullMask, n);
+  };
+  if (at >= above(-1)) return false;
+  int lo = 0, hi = p.pairs - 1;  // the least x with C(x) <= at
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) <= at) hi = mid;
+    else lo = mid + 1;
+  }
+  int rank = at - above(lo);
+  for (int i = 0; i < p.num_seqs; i += 32) {
+    const unsigned has = __ballot_sync(kFullMask, pairs_of(p, i + lane) > lo);
+    const int n = __popc(has);
+    if (rank < n) {
+      pair = lo;
+      s = i + static_cast<int>(__fns(has, 0, rank + 1));
+      return true;
+    }
+    rank -= n;
+  }
+  return false;
+}
+
+// The item of a grid index, by whole warps; false: nothing to do.
+template <bool IS_RAGGED>
+__device__ __forceinline__ bool find_packed_item(const PackedParams& p, uint3 id, PackedItem& it) {
+  int pair;
+  if constexpr (IS_RAGGED) {
+    it.kvh = id.x % p.num_kv_heads;
+    if (!listed_pair(p, id.x / p.num_kv_heads, pair, it.s)) return false;
+  } else {
+    const bool lf = p.longest_first;
+    pair = p.pairs - 1 - static_cast<int>(lf ? id.z : id.x);  // the longest pairs start first
+    it.kvh = lf ? id.x : id.y;
+    it.s = lf ? id.y : id.z;
+  }
+  it.qlen = rows_of(p, it.s, it.q0);
+  it.ta = 2 * pair * p.tile_tokens;
+  return it.ta < it.qlen;
+}
+
+// NaN in the rows of an item, by `n` threads.
+template <typename T, int HEAD_DIM>
+__device__ __forceinline__ void write_nan_rows(const PackedParams& p, const PackedItem& it, int i, int n) {
+  constexpr int U = HEAD_DIM / 8;
+  const uint32_t v = pack2<T>(NAN, NAN);
+  const int rows = (it.kend(p.tile_tokens) - it.ta) * p.group;
+#pragma unroll 1
+  for (; i < rows * U; i += n) {
+    const int r = i / U;
+    const int t = r / p.group;
+    T* row = static_cast<T*>(p.out) + (static_cast<size_t>(it.q0 + it.ta + t) * p.num_heads + it.kvh * p.group + r -
+                                       t * p.group) * HEAD_DIM;
+    reinterpret_cast<uint4*>(row)[i % U] = make_uint4(v, v, v, v);
+  }
+}
+
+// The halves of a pair of elements that are infinite or NaN, as ones in all of their bits: an exponent of
+// all ones carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t EXP = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t ONE = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+  return ((((w & EXP) + ONE) & 0x80008000u) >> 15) * 0xffffu;
+}
+
+// An output element `o` that also takes a value `v` that is not finite (16-bit patterns): v, or NaN where o is
+// not finite and another.
+template <typename T>
+__device__ __forceinline__ uint32_t join_not_finite(uint32_t o, uint32_t v) {
+  return not_finite<T>(o) && o != v ? 0x7fffu : v;
+}
+
+// Whether `ok` holds in all THREADS threads that meet at named barrier 1.
+template <int THREADS>
+__device__ __forceinline__ bool all_meet(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "n"(THREADS)
+      : "memory");
+  return all != 0;
+}
+
+template <typename T, int HEAD_DIM, bool IS_RAGGED>
+__global__ void __launch_bounds__(PpCfg<T, HEAD_DIM>::THREADS, 1)
+packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
+  using C = PpCfg<T, HEAD_DIM>;
+  constexpr int KS = C::KSTAGES;
+  constexpr int VS = C::VSTAGES;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  // [ITEMS][INFO]: the item (s: -1 past the last), [5] a masked row may meet a value that is not finite
+  int* infos = reinterpret_cast<int*>(sm + C::INFO_OFF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+  // Phases count over all items of the CTA.
+  uint64_t* kfull = bars;                  // [KS] K of a block landed
+  uint64_t* vfull = kfull + KS;            // [VS] V of a block may be multiplied
+  uint64_t* vraw = vfull + VS;             // [VS] V of a block that some row does not see all of has landed
+  // step n: P V of block n - 1, then Q K^T of block n.  One commit per step and tile frees K of
+  // block n and V of block n - 1.
+  uint64_t* done = vraw + VS;              // [DONE] both tiles' MMAs of a step have completed
+  uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
+  uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
+  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the last P V of the tile's item has completed
+  uint64_t* qbar = pvdone + TC_TILES;      // [tile] Q of the tile's next item landed
+  uint64_t* drain = qbar + TC_TILES;       // [tile] every MMA issued has completed
+  uint64_t* turn = drain + TC_TILES;       // [tile] its MMA warp may issue the next step
+  uint64_t* ifull = turn + TC_TILES;       // [ITEMS] an item is published
+  uint64_t* begun = ifull + C::ITEMS;      // the loads of the next item begin
+  uint64_t* cbar = begun + 1;              // the answer about another CTA landed
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::SLOT_OFF);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = p.group;
+  const int tt = p.tile_tokens;
+
+  grid_dependency_wait();
+
+  PackedItem it;
+  if (!find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it)) {
+    allow_dependent_launch();
+    return;
+  }
+  auto load_q = [&](const PackedItem& i, int u) {  // one thread
+    mbar_arrive_expect_tx(&qbar[u], C::DBOX * tt * G * 128);
+    for (int db = 0; db < C::DBOX; ++db)
+      tma_load_3d(sm + u * C::QBYTES + db * C::QATOM, &p.tmap_q, db * BOX_DIMS, i.kvh * G, i.q0 + i.ta + u * tt, &qbar[u]);
+  };
+  auto publish = [&](const PackedItem& i, int k) {  // one thread
+    int* f = infos + (k % C::ITEMS) * C::INFO;
+    f[0] = i.s, f[1] = i.kvh, f[2] = i.ta, f[3] = i.q0, f[4] = i.qlen, f[5] = 0;
+    mbar_arrive(&ifull[k % C::ITEMS]);
+  };
+  // Item k of the CTA, published.
+  auto item = [&](int k) -> PackedItem {
+    const volatile int* f = infos + (k % C::ITEMS) * C::INFO;
+    PackedItem i;
+    i.s = f[0], i.kvh = f[1], i.ta = f[2], i.q0 = f[3], i.qlen = f[4];
+    return i;
+  };
+  // Waits for it; false past the last (or when the warp of the items gave up).
+  auto has_item = [&](int k) -> bool {
+    return __all_sync(kFullMask, tc_wait(&ifull[k % C::ITEMS], (k / C::ITEMS) & 1)) &&
+           *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO) >= 0;
+  };
+  auto read_item = [&](int k, PackedItem& i) -> bool {
+    if (!has_item(k)) return false;
+    i = item(k);
+    return true;
+  };
+
+  if (warp == C::MMA_WARP && lane == 0) {
+    for (int i = 0; i < KS; ++i) mbar_init(&kfull[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&vfull[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&vraw[i], 1);
+    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], TC_TILES);
+    for (int i = 0; i < TC_TILES; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[2 * i], TC_ROWS);
+      mbar_init(&pfull[2 * i + 1], TC_ROWS);
+      mbar_init(&pvdone[i], 2);
+      mbar_init(&qbar[i], 1);
+      mbar_init(&drain[i], 1);
+      mbar_init(&turn[i], 1);
+    }
+    for (int i = 0; i < C::ITEMS; ++i) mbar_init(&ifull[i], 1);
+    mbar_init(begun, 1);
+    mbar_init(cbar, 1);
+    fence_mbar_init();
+    for (int u = 0; u < it.tiles(tt); ++u) load_q(it, u);
+    publish(it, 0);
+    ask_for_cta(sm + C::RESP_OFF, cbar);
+  }
+  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tslot;
+
+  if (warp >= C::SIDE_WARP && warp < C::MMA_WARP) {
+    // ------------------------------------------------ the cache write, and values that rows must not meet
+    set_max_regs<false, C::SIDE_REGS>();
+    const int tid = threadIdx.x - C::SIDE_WARP * 32;
+    constexpr int U = HEAD_DIM / 8;  // 16-byte units of a row
+    // the item's own tokens' rows into the pools
+    auto write_cache = [&](const PackedItem& i) {
+      const int n = (i.kend(tt) - i.ta) * 2 * U;
+      const int64_t row0 = i.q0 + i.ta;
+      constexpr int AT_ONCE = 2;
+#pragma unroll 1
+      for (int x0 = tid; x0 < n; x0 += AT_ONCE * C::SIDE) {
+        uint4 v[AT_ONCE];
+        int64_t slot[AT_ONCE];
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+          const int x = x0 + a * C::SIDE;
+          slot[a] = -1;
+          if (x >= n) continue;
+          const int64_t row = row0 + x / (2 * U);
+          slot[a] = __ldg(p.slot_mapping + row);
+          const T* src = (x / U & 1 ? static_cast<const T*>(p.value) + row * p.v_stride
+                                    : static_cast<const T*>(p.key) + row * p.k_stride) + i.kvh * HEAD_DIM;
+          v[a] = __ldg(reinterpret_cast<const uint4*>(src) + x % U);
+        }
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+          const int x = x0 + a * C::SIDE;
+          if (slot[a] < 0 || slot[a] >= p.num_slots) continue;
+          uint4* dst = static_cast<uint4*>(x / U & 1 ? p.v_cache : p.k_cache) + (slot[a] * p.num_kv_heads + i.kvh) * U;
+          dst[x % U] = v[a];
+        }
+      }
+    };
+    bool go = true;
+    int n0 = 0;         // blocks of the items before
+    uint32_t used = 0;  // parities of vraw
+#pragma unroll 1
+    for (int k = 0; go; ++k) {
+      const int nblk = it.blocks(tt);
+      const int kend = it.kend(tt);
+      const int jm = it.first_masked();
+      // (a short prompt's first block is waited for: its rows are written behind it)
+      if (p.slot_mapping && jm > 0) write_cache(it);
+#pragma unroll 1
+      for (int j = jm; j < nblk; ++j) {
+        const int slot = (n0 + j) % VS;
+        const bool landed = __all_sync(kFullMask, tc_wait(&vraw[slot], (used >> slot) & 1));
+        used ^= 1u << slot;
+        // A weight of 0 times a value that is not finite must not occur: rows past the item's last key become
+        // zeros; what is not finite in rows that some tokens see and others do not enters as 0, and the rows
+        // that see it take it at the end.  A row per thread.
+        const int key = j * TC_KEYS + tid;
+        uint8_t* row = sm + C::V_OFF + slot * C::KBYTES + tid * 128;
+        if (!landed) {
+        } else if (key >= kend) {
+#pragma unroll
+          for (int x = 0; x < U; ++x)
+            *reinterpret_cast<uint4*>(row + (x >> 3) * C::KATOM + ((x + tid) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        } else if (key > it.ta) {
+          uint32_t any = 0;
+#pragma unroll 4
+          for (int x = 0; x < U; ++x) {  // (threads start at different units: no bank conflict)
+            uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * C::KATOM + ((x + tid) & 7) * 16);
+            uint4 w = *at;
+            const uint4 m = make_uint4(not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w));
+            const uint32_t bad = m.x | m.y | m.z | m.w;
+            if (bad) *at = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
+            any |= bad;
+          }
+          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5) = 1;
+        }
+        fence_proxy_async_smem();
+        go = all_meet<C::SIDE>(landed);  // (the warps go on or give up together)
+        if (!go) break;
+        if (tid == 0) mbar_arrive(&vfull[slot]);
+      }
+      if (go && p.slot_mapping && jm == 0) write_cache(it);
+      n0 += nblk;
+      go = go && all_meet<C::SIDE>(read_item(k + 1, it));
+    }
+    __syncthreads();
+    allow_dependent_launch();
+    return;
+  }
+
+  if (warp >= C::MMA_WARP) {
+    set_max_regs<false, C::MMA_REGS>();
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFullMask, tc_wait(bar, parity)) != 0; };
+    if (warp < C::ITEM_WARP) {
+      // ---------------------------------------------- MMA issue: warp u, tile u
+      // The whole warp runs the loop and one elected lane issues: every value stays uniform, so descriptors
+      // sit in uniform registers.
+      const int u = __shfl_sync(kFullMask, warp - C::MMA_WARP, 0);
+      const uint64_t dq = umma_desc_sw128(smem_addr(sm + u * C::QBYTES), 16, 1024);    // Q, K-major
+      const uint64_t dk = umma_desc_sw128(smem_addr(sm + C::K_OFF), 16, 1024);         // K, K-major
+      const uint64_t dv = umma_desc_sw128(smem_addr(sm + C::V_OFF), C::KATOM, 1024);   // V, MN-major
+      const uint32_t tP = tmem + 256 * u;
+      const uint32_t tO = tP + 128;
+      // stages of the next block's K and of the current one's V, parities of the phases
+      int kslot = 0, vslot = 0, dslot = 0;
+      uint32_t kpar = 0, vpar = 0, spar = 0, ppar = 0, qpar = 0, tpar = u ^ 1;
+      bool q_open = it.tiles(tt) > u;  // Q was asked for and not waited for
+      // Three barriers at once, a lane each: the waits cost a hundred cycles together, not each.
+      // (A test, not a wait that suspends: that one sleeps past the completion of one lane's
+      // barrier while another lane's is open.)  The limit is some seconds.
+      auto wait3 = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2) -> bool {
+        uint64_t* b = lane == 0 ? b0 : lane == 1 ? b1 : b2;
+        const uint32_t par = lane == 0 ? p0 : lane == 1 ? p1 : p2;
+#pragma unroll 1
+        for (int i = 0; i < 1 << 26; ++i)
+          if (__all_sync(kFullMask, mbar_test(b, par))) return true;
+        return false;
+      };
+      auto qk = [&]() {
+        const uint64_t kj = umma_desc_add(dk, kslot * C::KBYTES);
+#pragma unroll
+        for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * C::QATOM + ((ks & 3) << 5);
+          const uint32_t koff = (ks >> 2) * C::KATOM + ((ks & 3) << 5);
+          umma_f16_elect(tP, umma_desc_add(dq, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
+        }
+      };
+      auto first_qk = [&]() -> bool {  // of an item
+        if (!wait3(&qbar[u], qpar, &qbar[u], qpar, &kfull[kslot], kpar)) return false;
+        tc_fence_after_sync();
+        qpar ^= 1;
+        q_open = false;
+        qk();
+        umma_commit_elect(&sfull[u]);
+        return true;
+      };
+      auto end_step = [&]() {
+        umma_commit_elect(&done[dslot]);
+        dslot = dslot + 1 == C::DONE ? 0 : dslot + 1;
+        kpar ^= kslot + 1 == KS;
+        kslot = kslot + 1 == KS ? 0 : kslot + 1;
+      };
+      // The tiles' MMAs take turns, so that one tile's run under the other's softmax.
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(&turn[u ^ 1]);
+        __syncwarp();
+      };
+      // P V of the current block in the tile's turn, and Q K^T of the next one; first: the item's
+      // first block, last: the tile's last one
+      auto step = [&](bool first, bool last) -> bool {
+        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &pfull[2 * u], ppar)) return false;
+        tpar ^= 1;
+        tc_fence_after_sync();
+        const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
+        // the first 64 keys while the softmax writes the weights of the others
+#pragma unroll
+        for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
+          umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, !first || kk > 0);
+        uint64_t* p1 = &pfull[2 * u + 1];
+        if (!wait3(p1, ppar, p1, ppar, last ? p1 : &kfull[kslot], last ? ppar : kpar)) return false;
+        ppar ^= 1;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
+          umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
+        if (!last) qk();
+        pass_turn();
+        if (last) {
+          if (lane == 0) mbar_arrive(&pvdone[u]);
+          umma_commit_elect(&pvdone[u]);
+        } else {
+          umma_commit_elect(&sfull[u]);
+          spar ^= 1;
+        }
+        return true;
+      };
+      // a step of the item in which the tile has no block: at the pace of the other tile
+      auto no_step = [&]() -> bool {
+        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &vfull[vslot], vpar)) return false;
+        tpar ^= 1;
+        pass_turn();
+        return true;
+      };
+      auto next_v = [&]() {
+        vpar ^= vslot + 1 == VS;
+        vslot = vslot + 1 == VS ? 0 : vslot + 1;
+      };
+      int nb, nblk;  // blocks of the tile and of the item
+      auto lengths = [&](const PackedItem& i) {
+        nb = __shfl_sync(kFullMask, i.tile_blocks(u, tt), 0);
+        nblk = __shfl_sync(kFullMask, i.blocks(tt), 0);
+      };
+      lengths(it);
+      bool ok = nb == 0 || first_qk();
+      if (ok) end_step();
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        // all blocks but the item's last
+#pragma unroll 1
+        for (int j = 0; j + 1 < nblk; ++j) {
+          ok = j < nb ? step(j == 0, j + 1 == nb) : no_step();
+          if (!ok) break;
+          end_step();
+          next_v();
+        }
+        if (!ok) break;
+        // the last one, and Q K^T of the next item's first
+        const bool more = has_item(k + 1);
+        const int last_nb = nb, last = nblk - 1;
+        if (more) lengths(item(k + 1));
+        if (more && nb > 0) {
+          if (last_nb > 0) ok = wait(&sfull[u], spar);  // the tile's last S is there: its Q has been read
+          if (!ok) break;
+          if (lane == 0) load_q(item(k + 1), u);
+          q_open = true;
+          __syncwarp();
+        }
+        ok = last < last_nb ? step(last == 0, true) : no_step();
+        if (!ok) break;
+        if (last_nb > 0) spar ^= 1;
+        if (!more) break;
+        if (nb > 0) {
+          ok = first_qk();
+          if (!ok) break;
+        }
+        end_step();
+        next_v();
+      }
+      umma_commit_elect(&drain[u]);  // every MMA finishes before the TMEM is released
+      wait(&drain[u], 0);
+      if (q_open) wait(&qbar[u], qpar);  // (after a wait ran out)
+      tc_fence_before_sync();
+    } else if (warp == C::ITEM_WARP) {
+      // ---------------------------------------------- items: one ahead of the loads
+      int asked = 0;
+      bool open = true;  // an answer is on its way
+      bool ok = true;
+      auto next_item = [&](PackedItem& i) -> bool {
+        while (open) {
+          if (!wait(cbar, asked & 1)) {
+            open = ok = false;
+            break;
+          }
+          ++asked;
+          uint3 id;
+          open = cta_given(sm + C::RESP_OFF, id);
+          __syncwarp();  // every lane has read the answer
+          if (!open) break;
+          if (lane == 0) {
+            fence_proxy_async_smem();
+            ask_for_cta(sm + C::RESP_OFF, cbar);
+          }
+          if (find_packed_item<IS_RAGGED>(p, id, i)) return true;
+        }
+        return false;
+      };
+      int k = 1;
+#pragma unroll 1
+      for (;; ++k) {
+        ok = wait(begun, (k - 1) & 1);
+        if (!ok || !next_item(it)) break;
+        if (lane == 0) publish(it, k);
+        __syncwarp();
+      }
+      if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
+        uint3 id;
+        if (cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it))
+          write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
+      }
+      it.s = -1;
+      if (lane == 0) publish(it, k);
+    } else {
+      // ---------------------------------------------- loads of K and V
+      bool go = true;
+      int n = 0;  // blocks asked for, over all items
+      uint32_t raw = 0, rawpar = 0;  // per stage of V: its last copy reports to vraw; the parity of the next that does
+#pragma unroll 1
+      for (int k = 0; go; ++k) {
+        if (lane == 0) mbar_arrive(begun);
+        const int nblk = it.blocks(tt);
+        const int jm = it.first_masked();
+#pragma unroll 1
+        for (int j = 0; j < nblk; ++j, ++n) {
+          const int kslot = n % KS;
+          const int vslot = n % VS;
+          // K's stage is free after step n - KS, V's after step n - VS + 1
+          const int step = max(n - KS, n - VS + 1);
+          if (step >= 0 && !wait(&done[step % C::DONE], (step / C::DONE) & 1)) {
+            go = false;
+            break;
+          }
+          raw &= ~(1u << vslot);
+          if (j >= jm) raw |= 1u << vslot, rawpar ^= 1u << vslot;
+          if (lane == 0) {
+            uint64_t* vb = j < jm ? &vfull[vslot] : &vraw[vslot];
+            mbar_arrive_expect_tx(&kfull[kslot], C::KBYTES);
+            for (int db = 0; db < C::DBOX; ++db)
+              tma_load_3d(sm + C::K_OFF + kslot * C::KBYTES + db * C::KATOM, &p.tmap_k, db * BOX_DIMS, it.kvh,
+                          it.q0 + j * TC_KEYS, &kfull[kslot]);
+            mbar_arrive_expect_tx(vb, C::KBYTES);
+            for (int db = 0; db < C::DBOX; ++db)
+              tma_load_3d(sm + C::V_OFF + vslot * C::KBYTES + db * C::KATOM, &p.tmap_v, db * BOX_DIMS, it.kvh,
+                          it.q0 + j * TC_KEYS, vb);
+          }
+          __syncwarp();
+        }
+        go = go && read_item(k + 1, it);
+      }
+      // the copies in flight land before the shared memory is released
+      for (int x = max(0, n - KS); x < n; ++x) wait(&kfull[x % KS], (x / KS) & 1);
+      for (int x = max(0, n - VS); x < n; ++x) {
+        const int vslot = x % VS;
+        if (raw >> vslot & 1) wait(&vraw[vslot], (rawpar >> vslot & 1) ^ 1);
+        else wait(&vfull[vslot], (x / VS) & 1);
+      }
+    }
+    __syncthreads();
+    allow_dependent_launch();
+    return;
+  }
+  // ------------------------------------------------ softmax: warps 4 u .. 4 u + 3 run tile u
+  set_max_regs<true, C::SOFT_REGS>();
+  const int u = warp >> 2;
+  const int r = 32 * (warp & 3) + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const uint32_t tS = tmem + 256 * u + lane_off;
+  const uint32_t tO = tS + 128;
+  auto token_of = [&](int row) { return row * p.inv_g >> 16; };  // of the tile
+  const int own_t = token_of(r);
+  const int least_t = token_of(r & ~31);
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = __all_sync(kFullMask, tc_wait(bar, parity));
+  };
+  // A negative `scale` turns the order of the scores around: the largest product is then
+  // the smallest score times the (negative) factor.
+  const float a = p.scale_log2;
+  const bool neg = a < 0.f;
+  const float hidden = neg ? INFINITY : -INFINITY;
+  const uint64_t a2 = pack_f32x2(a);
+  uint32_t spar = 0, vpar = 0;  // of the tile's blocks, of its items
+#pragma unroll 1
+  for (int k = 0;; ++k) {
+    int left, seen;  // the tile's blocks to come; the keys of the block that all its rows see, minus one
+    {
+      const PackedItem i = item(k);
+      left = i.tile_blocks(u, tt);
+      seen = i.ta + u * tt;
+    }
+    float m_used = -INFINITY, l = 0.f;  // log2 units
+    uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
+#pragma unroll 1
+    for (; left > 0; --left, seen -= TC_KEYS) {
+      wait(&sfull[u], spar);
+      spar ^= 1;
+      tc_fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < TC_KEYS / 16; ++c) tmem_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
+      tmem_wait_ld();
+      if (seen < TC_KEYS - 1) {  // a key here may lie past some row of the tile
+        const int own = seen + own_t;  // (rows past the item's end are not written)
+        const int all = seen + least_t;
+#pragma unroll
+        for (int c = 0; c < TC_KEYS; c += 16) {
+          if (c + 15 <= all) continue;  // the whole warp sees the chunk
+          const int kv = own - c;  // visible keys of the chunk, minus one
+          const uint32_t m = kv < 0 ? 0u : kv > 15 ? ~0u : (2u << kv) - 1u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!(m >> i & 1u)) x[c + i] = __float_as_uint(hidden);
+        }
+      }
+      // the row's maximum
+      float e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(x[c]);
+      if (!neg) {
+#pragma unroll
+        for (int i = 4; i < TC_KEYS; i += 8)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            e[c] = i + 4 + c < TC_KEYS ? fmaxf(fmaxf(e[c], __uint_as_float(x[i + c])), __uint_as_float(x[i + 4 + c]))
+                                       : fmaxf(e[c], __uint_as_float(x[i + c]));
+        e[0] = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+      } else {
+#pragma unroll
+        for (int i = 4; i < TC_KEYS; i += 4)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = fminf(e[c], __uint_as_float(x[i + c]));
+        e[0] = fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
+      }
+      const float m_new = fmaxf(m_used, rounded_up(e[0] * a));  // (a row that sees no key here keeps its own: the other is NaN)
+      // The exponent's offset moves at the first block and when the row maximum has grown
+      // by more than 2^8; O and l then scale by f.
+      const bool none = m_used == -INFINITY;  // nothing in O yet
+      const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
+      const float f = need ? ex2(m_used - m_new) : 1.f;
+      if (none || need) m_used = m_new;
+      const float bias = m_used == -INFINITY ? 0.f : C::MID - m_used;  // a row that has seen no key yet
+      if (__any_sync(kFullMask, need)) {
+#pragma unroll 1
+        for (int c = 0; c < HEAD_DIM; c += 16) {
+          uint32_t o16[16];
+          tmem_ld16(tO + c, o16);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(__uint_as_float(o16[i]) * f);
+          tmem_st16(tO + c, o16);
+        }
+      }
+      const uint64_t b2 = pack_f32x2(bias);
+      // the weights, half of the keys at a time: P in the half's 32 columns
+      uint64_t sum2[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 32 * h; i < 32 * h + 32; ++i) {
+          const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(x[2 * i], x[2 * i + 1]), a2, b2));
+          const float p0 = ex2(t.x), p1 = ex2(t.y);
+          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+          x[i] = pack2<T>(p0, p1);
+        }
+        tmem_st16(tS + 32 * h, &x[32 * h]);
+        tmem_st16(tS + 32 * h + 16, &x[32 * h + 16]);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(&pfull[2 * u + h]);
+      }
+      const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+      l = fmaf(l, f, s2.x + s2.y);
+    }
+    // ------------------------------------------------ O / l
+    const PackedItem i = item(k);  // (read again: held over the loop it would cost registers there)
+    if (u < i.tiles(tt)) {
+      wait(&pvdone[u], vpar);
+      vpar ^= 1;
+      tc_fence_after_sync();
+      const float inv = ok ? 1.f / l : NAN;
+      const bool fix = *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5);
+      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
+      // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows.  The loop
+      // is short because its code runs once per item.
+      int row = r;
+      use_here(row);  // (what follows from it is not worth registers in the blocks' loop)
+      const int t0 = i.ta + u * tt;
+      const int t_end = i.tile_end(u, tt);
+      const int t = t0 + token_of(row);
+      T* at[4];
+      bool on[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int rr = (row & ~3) + y;
+        const int q = token_of(rr);
+        on[y] = t0 + q < t_end;  // (rows past the tile's last token count as the next one's)
+        at[y] = static_cast<T*>(p.out) + (static_cast<size_t>(i.q0 + t0 + q) * p.num_heads + i.kvh * G + rr - q * G) * HEAD_DIM +
+                8 * (row & 3);
+      }
+#pragma unroll 1
+      for (int c = 0; c < HEAD_DIM; c += 32) {
+        uint32_t o[32];
+        tmem_ld16(tO + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+        tmem_ld16(tO + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+          o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
+        if (fix && t < t_end) {  // rare: take the values that are not finite among the keys that entered as 0
+#pragma unroll 1
+          for (int key = i.ta + 1; key <= t; ++key) {
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
+                                                                  i.kvh * HEAD_DIM + c);
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              const uint32_t w = __ldg(v + d);
+              const uint32_t m = not_finite<T>(w);
+              if (m & 0xffffu) o[d] = (o[d] & 0xffff0000u) | join_not_finite<T>(o[d] & 0xffffu, w & 0xffffu);
+              if (m >> 16) o[d] = (o[d] & 0xffffu) | join_not_finite<T>(o[d] >> 16, w >> 16) << 16;
+            }
+          }
+        }
+        uint4 unit[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) unit[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        transpose4(unit, row);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (on[y]) *reinterpret_cast<uint4*>(at[y] + c) = unit[y];
+      }
+    }
+    if (!has_item(k + 1)) break;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
+  allow_dependent_launch();
+}
+
+// x as [rows][heads][HEAD_DIM] with rows of `stride` elements: boxes of 64 dims x `box_heads` x `box_rows`, 128-byte
+// swizzled.
+template <typename T>
+cudaError_t make_rows_map(CUtensorMap* map, const void* x, int head_dim, int heads, int64_t rows, int64_t stride, int box_heads,
+                          int box_rows) {
+  EncodeTiledFn enc = nullptr;
+  const cudaError_t e = encode_fn(&enc);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {BOX_DIMS, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = enc(map, tma_dtype<T>(), 3, const_cast<void*>(x), dims, strides, box, estride,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int HEAD_DIM>
+cudaError_t launch_packed_prefill_t(const PackedPrefillArgs& a, cudaStream_t stream) {
+  using C = PpCfg<T, HEAD_DIM>;
+  PackedParams p;
+  const int group = a.num_heads / a.num_kv_heads;
+  p.tile_tokens = TC_ROWS / group;
+  cudaError_t e = make_rows_map<T>(&p.tmap_q, a.q, HEAD_DIM, a.num_heads, a.num_rows, a.q_stride, group, p.tile_tokens);
+  if (e == cudaSuccess)
+    e = make_rows_map<T>(&p.tmap_k, a.key, HEAD_DIM, a.num_kv_heads, a.num_rows, a.k_stride, 1, TC_KEYS);
+  if (e == cudaSuccess)
+    e = make_rows_map<T>(&p.tmap_v, a.value, HEAD_DIM, a.num_kv_heads, a.num_rows, a.v_stride, 1, TC_KEYS);
+  if (e != cudaSuccess) return e;
+  p.out = a.out;
+  p.key = a.key;
+  p.value = a.value;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.k_cache = a.k_cache;
+  p.v_cache = a.v_cache;
+  p.slot_mapping = a.slot_mapping;
+  p.num_slots = a.num_slots;
+  p.query_start_loc = a.query_start_loc;
+  p.num_seqs = a.num_seqs;
+  p.num_rows = a.num_rows;
+  p.max_query_len = a.max_query_len;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = group;
+  p.inv_g = 65536 / group + 1;
+  const int pair_tokens = TC_TILES * p.tile_tokens;
+  p.pair_magic = ~uint64_t{0} / pair_tokens + 1;  // (2^64 is no multiple of it or ends in zeros: either way rounded up)
+  p.pairs = (a.max_query_len + pair_tokens - 1) / pair_tokens;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  // a factor of 0 would turn a masked score (an infinity) into NaN; 2^-149 makes 0 of every score
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1.401298464324817e-45f;
+  // A grid over (sequence, pair) is mostly empty where one sequence is long and the others are short, and an
+  // empty CTA takes a quarter of a microsecond of an SM: the list of all pairs is searched instead where
+  // the grid would be more than twice its length (see pa_block_prefill.cuh, which measured both).
+  const int64_t listed = a.num_rows / pair_tokens + static_cast<int64_t>(a.num_seqs);
+  const int64_t boxed = static_cast<int64_t>(p.pairs) * a.num_seqs;
+  const bool ragged = boxed > 2 * listed && a.num_seqs <= 1024 && listed * a.num_kv_heads <= INT32_MAX;
+  p.longest_first = p.pairs <= 65535;
+  cudaLaunchConfig_t cfg = {};
+  if (ragged) {
+    cfg.gridDim = dim3(static_cast<unsigned>(listed * a.num_kv_heads));
+  } else if (p.longest_first) {
+    cfg.gridDim = dim3(a.num_kv_heads, a.num_seqs, p.pairs);
+  } else {
+    cfg.gridDim = dim3(p.pairs, a.num_kv_heads, a.num_seqs);
+  }
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static std::atomic<uint64_t> smem_set[2];
+  auto kern = ragged ? packed_prefill_tc_kernel<T, HEAD_DIM, true> : packed_prefill_tc_kernel<T, HEAD_DIM, false>;
+  e = ensure_smem(kern, C::SMEM_BYTES, smem_set[ragged]);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace pa

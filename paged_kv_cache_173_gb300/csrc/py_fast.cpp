@@ -1,4 +1,5 @@
-// py_fast.cpp -- the short way from Python into the per-block entry points.
+// py_fast.cpp -- the short way from Python into the per-block entry points, packed
+// prefill and the calls on the sequences' blocks.
 //
 // A small decode step is paced by the host: checking eight tensors from Python
 // and calling through ctypes takes 7 to 10 us, the kernels 3 to 5.  Each function
@@ -27,6 +28,12 @@ decltype(&pa_decode_splitk_fp8_block) g_splitk;
 decltype(&pa_prefill_fp8_block) g_prefill;
 decltype(&pa_select_blocks) g_select;
 decltype(&pa_decode_sparse) g_sparse;
+decltype(&pa_prefill_packed) g_packed;
+decltype(&pa_extend_sequences) g_extend;
+decltype(&pa_truncate_sequences) g_truncate;
+decltype(&pa_fork_sequences) g_fork;
+decltype(&pa_compact_blocks) g_compact;
+decltype(&pa_copy_layer_blocks) g_copy_layers;
 
 constexpr int64_t kIntMax = 0x7fffffff;
 
@@ -77,6 +84,20 @@ struct Args {
     const at::Tensor* t = tensor(i);
     ok = ok && t->scalar_type() == type && t->sizes() == c10::IntArrayRef(shape);
     return ok ? t->data_ptr() : nullptr;
+  }
+  // A CUDA tensor of the call's device, [rows, heads, d], each row contiguous; `stride` gets the rows' distance.
+  void* rows(int i, at::ScalarType type, std::initializer_list<int64_t> shape, int64_t& stride) {
+    if (!ok || !THPVariable_Check(a[i])) {
+      ok = false;
+      return nullptr;
+    }
+    const at::Tensor& t = THPVariable_Unpack(a[i]);
+    ok = t.is_cuda() && t.get_device() == device && t.scalar_type() == type && t.sizes() == c10::IntArrayRef(shape);
+    if (!ok) return nullptr;
+    const int64_t h = t.size(1), d = t.size(2);
+    ok = (d == 1 || t.stride(2) == 1) && (h == 1 || t.stride(1) == d);
+    stride = t.size(0) > 1 ? t.stride(0) : h * d;
+    return t.data_ptr();
   }
   void* codes(int i, c10::IntArrayRef shape) {
     const at::Tensor* t = tensor(i);
@@ -237,6 +258,136 @@ PA_FAST(sparse) {
                          static_cast<int32_t*>(len), S, H, Hk, d, B, N, scale, code, kv, st);
 } PA_GUARD
 
+// out, q, key, value, query_start_loc, max_query_len, scale, k_cache or None, v_cache or None, slot_mapping or None
+PA_FAST(packed) {
+  Args x(args, n, 12);
+  const at::Tensor* out = x.tensor(0); const at::Tensor* qsl = x.tensor(4);
+  if (!x.ok || out->dim() != 3 || qsl->dim() != 1 || qsl->size(0) < 1 || !THPVariable_Check(args[2])) return answer(false);
+  const at::Tensor& key = THPVariable_Unpack(args[2]);
+  if (key.dim() != 3) return answer(false);
+  const int64_t R = out->size(0), H = out->size(1), d = out->size(2), Hk = key.size(1), S = qsl->size(0) - 1;
+  const at::ScalarType dt = out->scalar_type(); const int code = dtype_code(dt);
+  int64_t qs = 0, ks = 0, vs = 0, N = 0, B = 0;
+  void* o = x.typed(0, dt, {R, H, d}); void* q = x.rows(1, dt, {R, H, d}, qs);
+  void* k = x.rows(2, dt, {R, Hk, d}, ks); void* v = x.rows(3, dt, {R, Hk, d}, vs);
+  void* st = x.typed(4, at::kInt, {S + 1}); const long maxq = x.integer(5); const float scale = x.real(6);
+  void* kc = nullptr; void* vc = nullptr; void* sm = nullptr; void* stream = x.stream(11);
+  if (args[7] != Py_None || args[8] != Py_None || args[9] != Py_None) {
+    const at::Tensor* pool = x.tensor(7);
+    if (!x.ok || pool->dim() != 4) return answer(false);
+    N = pool->size(0), B = pool->size(1);
+    kc = x.typed(7, dt, {N, B, Hk, d}); vc = x.typed(8, dt, {N, B, Hk, d}); sm = x.typed(9, at::kLong, {R});
+  }
+  if (!x.ok || code < 0 || !fits({R, H, d, Hk, S, N, B, maxq})) return answer(false);
+  return launch(g_packed, o, q, qs, k, ks, v, vs, kc, vc, static_cast<int64_t*>(sm), static_cast<int32_t*>(st), S, R, maxq,
+                H, Hk, d, B, N, scale, code, stream);
+} PA_GUARD
+
+// The tables, lengths and counts that begin a call on the sequences' blocks.
+struct Sequences {
+  int64_t S = 0, M = 0, N = 0;
+  int32_t* tables = nullptr;
+  int32_t* lens = nullptr;
+  int32_t* counts = nullptr;
+
+  Sequences(Args& x, int i) {
+    const at::Tensor* bt = x.tensor(i); const at::Tensor* rc = x.tensor(i + 2);
+    if (!x.ok || bt->dim() != 2 || rc->dim() != 1) {
+      x.ok = false;
+      return;
+    }
+    S = bt->size(0), M = bt->size(1), N = rc->size(0);
+    tables = static_cast<int32_t*>(x.typed(i, at::kInt, {S, M}));
+    lens = static_cast<int32_t*>(x.typed(i + 1, at::kInt, {S}));
+    counts = static_cast<int32_t*>(x.typed(i + 2, at::kInt, {N}));
+    x.ok = x.ok && fits({S, M, N});
+  }
+};
+
+// block_tables, context_lens, ref_counts, query_start_loc, slot_mapping, block_copies, left, block_size, workspace
+PA_FAST(extend) {
+  Args x(args, n, 11);
+  const Sequences q(x, 0); const at::Tensor* slots = x.tensor(4); const at::Tensor* ws = x.tensor(8);
+  if (!x.ok || slots->dim() != 1) return answer(false);
+  const int64_t T = slots->size(0);
+  void* st = x.typed(3, at::kInt, {q.S + 1}); void* sm = x.typed(4, at::kLong, {T});
+  void* bc = x.typed(5, at::kLong, {q.S, 2}); void* left = x.typed(6, at::kInt, {2});
+  const long B = x.integer(7); void* stream = x.stream(10);
+  if (!x.ok || !fits({T, B})) return answer(false);
+  return launch(g_extend, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(st), static_cast<int64_t*>(sm),
+                static_cast<int64_t*>(bc), static_cast<int32_t*>(left), q.S, T, q.N, B, ws->data_ptr(), ws->nbytes(), stream);
+} PA_GUARD
+
+// block_tables, context_lens, ref_counts, new_lens (fork: fork_from), block_size
+template <class F>
+PyObject* per_sequence(F f, PyObject* const* args, Py_ssize_t n) {
+  Args x(args, n, 7);
+  const Sequences q(x, 0);
+  void* what = x.ok ? x.typed(3, at::kInt, {q.S}) : nullptr;
+  const long B = x.integer(4); void* stream = x.stream(6);
+  if (!x.ok || !fits({B})) return answer(false);
+  return launch(f, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(what), q.S, q.N, B, stream);
+}
+PA_FAST(truncate) { return per_sequence(g_truncate, args, n); } PA_GUARD
+PA_FAST(fork) { return per_sequence(g_fork, args, n); } PA_GUARD
+
+// moves, num_moves, block_tables, context_lens, ref_counts, tables_out, counts_out, block_size, workspace
+PA_FAST(compact) {
+  Args x(args, n, 11);
+  const at::Tensor* moves = x.tensor(0); const Sequences q(x, 2); const at::Tensor* ws = x.tensor(8);
+  if (!x.ok || moves->dim() != 2) return answer(false);
+  const int64_t K = moves->size(0);
+  void* m = x.typed(0, at::kLong, {K, 2}); void* num = x.typed(1, at::kInt, {1});
+  void* to = x.typed(5, at::kInt, {q.S, q.M}); void* co = x.typed(6, at::kInt, {q.N});
+  const long B = x.integer(7); void* stream = x.stream(10);
+  if (!x.ok || !fits({K, B})) return answer(false);
+  return launch(g_compact, static_cast<int64_t*>(m), K, static_cast<int32_t*>(num), q.tables, q.M, q.lens, q.counts,
+                static_cast<int32_t*>(to), static_cast<int32_t*>(co), q.S, q.N, B, ws->data_ptr(), ws->nbytes(), stream);
+} PA_GUARD
+
+// pools [L, N, ...], block_mapping
+PA_FAST(copy_layers) {
+  Args x(args, n, 4);
+  const at::Tensor* bm = x.tensor(1);
+  if (!x.ok || bm->dim() != 2 || !THPVariable_Check(args[0])) return answer(false);
+  const at::Tensor& pools = THPVariable_Unpack(args[0]);
+  const int64_t pairs = bm->size(0);
+  void* m = x.typed(1, at::kLong, {pairs, 2}); void* stream = x.stream(3);
+  if (!x.ok || !pools.is_cuda() || pools.get_device() != x.device || pools.dim() < 3 || pools.numel() == 0) return answer(false);
+  int64_t inner = 1;  // elements of a layer, if they are contiguous
+  for (int64_t i = pools.dim() - 1; i > 0; --i) {
+    if (pools.size(i) != 1 && pools.stride(i) != inner) return answer(false);
+    inner *= pools.size(i);
+  }
+  const int64_t L = pools.size(0), N = pools.size(1), width = pools.element_size();
+  if (!fits({L, N, pairs})) return answer(false);
+  return launch(g_copy_layers, pools.data_ptr(), pools.stride(0) * width, L, inner / N * width, static_cast<int64_t*>(m),
+                pairs, N, stream);
+} PA_GUARD
+
+// bind_sequences(packed, extend, truncate, fork, compact, copy_layers): the entry points' addresses
+PyObject* bind_sequences_(PyObject*, PyObject* const* args, Py_ssize_t n) noexcept {
+  void* p[6];
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind_sequences takes six addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 6; ++i) {
+    p[i] = PyLong_AsVoidPtr(args[i]);
+    if (p[i] == nullptr) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_sequences: a null address");
+      return nullptr;
+    }
+  }
+  g_packed = reinterpret_cast<decltype(g_packed)>(p[0]);
+  g_extend = reinterpret_cast<decltype(g_extend)>(p[1]);
+  g_truncate = reinterpret_cast<decltype(g_truncate)>(p[2]);
+  g_fork = reinterpret_cast<decltype(g_fork)>(p[3]);
+  g_compact = reinterpret_cast<decltype(g_compact)>(p[4]);
+  g_copy_layers = reinterpret_cast<decltype(g_copy_layers)>(p[5]);
+  Py_RETURN_NONE;
+}
+
 // bind(write, bounds, decode, splitk, prefill, select, sparse): the entry points' addresses
 PyObject* bind_(PyObject*, PyObject* const* args, Py_ssize_t n) noexcept {
   void* p[7];
@@ -264,7 +415,9 @@ PyObject* bind_(PyObject*, PyObject* const* args, Py_ssize_t n) noexcept {
 #define PA_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name##_)), METH_FASTCALL, nullptr }
 PyMethodDef g_methods[] = {PA_METHOD(bind),    PA_METHOD(write),  PA_METHOD(bounds), PA_METHOD(decode), PA_METHOD(splitk),
-                           PA_METHOD(prefill), PA_METHOD(select), PA_METHOD(sparse), {nullptr, nullptr, 0, nullptr}};
+                           PA_METHOD(prefill), PA_METHOD(select), PA_METHOD(sparse), PA_METHOD(bind_sequences),
+                           PA_METHOD(packed),  PA_METHOD(extend), PA_METHOD(truncate), PA_METHOD(fork), PA_METHOD(compact),
+                           PA_METHOD(copy_layers), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

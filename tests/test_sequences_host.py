@@ -170,3 +170,18 @@ def test_oracle_attention_matches_torch():
         assert np.allclose(out[a:b], want.numpy(), atol=1e-12)
     assert (np.abs(out) <= A_ + 1e-12).all()
     assert np.isnan(so.attention(q.numpy(), k.numpy(), v.numpy(), [0, 5, 5, 12], 0.3, 3)[0][3]).all()
+
+
+def test_the_short_way_declines_what_it_does_not_know(L):
+    fast = _lib.fast()
+    x = torch.zeros(2, 3, 4, dtype=torch.float16)
+    for name, n in dict(packed=12, extend=11, truncate=7, fork=7, compact=11, copy_layers=4).items():
+        f = getattr(fast, name)
+        assert f() is False and f(*[None] * n) is False and f(*[x] * n) is False
+        assert f(*[x] * (n - 2), 0, 0) is False                 # host tensors
+        assert f(*[x] * (n - 2), -1, 0) is False and f(*[x] * (n - 2), 0, 1 << 70) is False
+        assert f(*[object()] * (n - 2), 1 << 70, 0) is False    # numbers past 64 bits
+    with pytest.raises(TypeError):
+        fast.bind_sequences(1, 2)
+    with pytest.raises(ValueError):
+        fast.bind_sequences(*[0] * 6)
