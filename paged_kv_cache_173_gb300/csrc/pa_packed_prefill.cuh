@@ -65,8 +65,8 @@ struct PpCfg {
   static constexpr int ITEM_WARP = MMA_WARP + TC_TILES;
   static constexpr int LOAD_WARP = ITEM_WARP + 1;
   static constexpr int THREADS = SOFT + SIDE + 128;
-  static constexpr int SOFT_REGS = 184;
-  static constexpr int SIDE_REGS = 64;
+  static constexpr int SOFT_REGS = 168;
+  static constexpr int SIDE_REGS = 96;
   static constexpr int MMA_REGS = 80;
   // what the warpgroups hold is what the block was launched with
   static_assert(SOFT * SOFT_REGS + SIDE * SIDE_REGS + 128 * MMA_REGS <= THREADS * 128, "registers");
@@ -76,7 +76,7 @@ struct PpCfg {
   static constexpr int KATOM = TC_KEYS * 128;
   static constexpr int KBYTES = DBOX * KATOM;
   static constexpr int SMEM_MAX = 227 * 1024;
-  static constexpr int RESERVE = 1024 + 1024;  // base alignment slack, items, barriers
+  static constexpr int RESERVE = 1024 + 2048;  // base alignment slack, items, barriers
   static constexpr int STAGES_FIT = (SMEM_MAX - RESERVE - TC_TILES * QBYTES) / KBYTES;
   static constexpr int KSTAGES = STAGES_FIT / 2 < 4 ? STAGES_FIT / 2 : 4;
   static constexpr int VSTAGES = STAGES_FIT - KSTAGES < 4 ? STAGES_FIT - KSTAGES : 4;
@@ -89,10 +89,11 @@ struct PpCfg {
   static constexpr int ITEMS = 8;
   static_assert(VSTAGES + 3 <= ITEMS, "the ring of items");
   static constexpr int INFO = 8;  // words of an item
-  static constexpr int RESP_OFF = INFO_OFF + ITEMS * INFO * 4;
+  static constexpr int SUM_OFF = INFO_OFF + ITEMS * INFO * 4;  // [tile][row] sum of the weights
+  static constexpr int RESP_OFF = SUM_OFF + TC_TILES * TC_ROWS * 4;
   static constexpr int BAR_OFF = RESP_OFF + 16;
   static constexpr int DONE = VSTAGES;  // ring of completed steps
-  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 7 * TC_TILES + ITEMS + 2;
+  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 10 * TC_TILES + ITEMS + 2;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
   static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
@@ -104,6 +105,8 @@ struct PpCfg {
   // float16: up to 2^15, so that small weights keep their bits.  bfloat16 has float32's range, and weights
   // of 2^-8 at most keep a sum of 2^8 of its largest values within it.
   static constexpr float MID = BF16 ? -16.f : 7.f;
+  // The largest sum of 64 weights that leaves the maximum where it is (64 equal ones at the maximum: 2^(MID + 6)).
+  static constexpr float LIMIT = BF16 ? 0.25f : 32768.f;
 };
 
 // ---------------------------------------------------------------- work items
@@ -254,13 +257,17 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   uint64_t* done = vraw + VS;              // [DONE] both tiles' MMAs of a step have completed
   uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
-  uint64_t* pvdone = pfull + 2 * TC_TILES; // [tile] the last P V of the tile's item has completed
-  uint64_t* qbar = pvdone + TC_TILES;      // [tile] Q of the tile's next item landed
+  uint64_t* pvhalf = pfull + 2 * TC_TILES; // [tile] P V of the first 64 keys of that block has completed
+  uint64_t* pvdone = pvhalf + TC_TILES;    // [tile] the last P V of the tile's item has completed
+  uint64_t* lready = pvdone + TC_TILES;    // [tile] the sums of the item's weights are stored (128 arrivals)
+  uint64_t* ofree = lready + TC_TILES;     // [tile] the sums and O of the item are read (128 arrivals)
+  uint64_t* qbar = ofree + TC_TILES;       // [tile] Q of the tile's next item landed
   uint64_t* drain = qbar + TC_TILES;       // [tile] every MMA issued has completed
   uint64_t* turn = drain + TC_TILES;       // [tile] its MMA warp may issue the next step
   uint64_t* ifull = turn + TC_TILES;       // [ITEMS] an item is published
   uint64_t* begun = ifull + C::ITEMS;      // the loads of the next item begin
   uint64_t* cbar = begun + 1;              // the answer about another CTA landed
+  float* sums = reinterpret_cast<float*>(sm + C::SUM_OFF);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::SLOT_OFF);
 
   const int warp = threadIdx.x >> 5;
@@ -312,7 +319,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[2 * i], TC_ROWS);
       mbar_init(&pfull[2 * i + 1], TC_ROWS);
+      mbar_init(&pvhalf[i], 1);
       mbar_init(&pvdone[i], 2);
+      mbar_init(&lready[i], TC_ROWS);
+      mbar_init(&ofree[i], C::SIDE);
       mbar_init(&qbar[i], 1);
       mbar_init(&drain[i], 1);
       mbar_init(&turn[i], 1);
@@ -336,33 +346,95 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     set_max_regs<false, C::SIDE_REGS>();
     const int tid = threadIdx.x - C::SIDE_WARP * 32;
     constexpr int U = HEAD_DIM / 8;  // 16-byte units of a row
-    // the item's own tokens' rows into the pools
+    // The item's own tokens' rows into the pools: 2 U lanes take the key's and the value's units of a token, four
+    // tokens of theirs on the way at a time.
     auto write_cache = [&](const PackedItem& i) {
-      const int n = (i.kend(tt) - i.ta) * 2 * U;
-      const int64_t row0 = i.q0 + i.ta;
-      constexpr int AT_ONCE = 2;
+      constexpr int AT_ONCE = 4;
+      constexpr int STEP = C::SIDE / (2 * U);  // tokens apart
+      const int end = i.kend(tt) - i.ta;
+      int me = tid;
+      use_here(me);  // (what follows from it is not worth registers elsewhere)
+      const int unit = me % U;
+      const bool is_v = me / U & 1;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const T* src = (is_v ? static_cast<const T*>(p.value) : static_cast<const T*>(p.key)) + (i.q0 + i.ta) * stride +
+                     i.kvh * HEAD_DIM + unit * 8;
+      uint4* dst = static_cast<uint4*>(is_v ? p.v_cache : p.k_cache) + i.kvh * U + unit;
+      const int64_t* slots = p.slot_mapping + i.q0 + i.ta;
 #pragma unroll 1
-      for (int x0 = tid; x0 < n; x0 += AT_ONCE * C::SIDE) {
+      for (int t0 = me / (2 * U); t0 < end; t0 += AT_ONCE * STEP) {
         uint4 v[AT_ONCE];
         int64_t slot[AT_ONCE];
 #pragma unroll
         for (int a = 0; a < AT_ONCE; ++a) {
-          const int x = x0 + a * C::SIDE;
-          slot[a] = -1;
-          if (x >= n) continue;
-          const int64_t row = row0 + x / (2 * U);
-          slot[a] = __ldg(p.slot_mapping + row);
-          const T* src = (x / U & 1 ? static_cast<const T*>(p.value) + row * p.v_stride
-                                    : static_cast<const T*>(p.key) + row * p.k_stride) + i.kvh * HEAD_DIM;
-          v[a] = __ldg(reinterpret_cast<const uint4*>(src) + x % U);
+          const int t = t0 + a * STEP;
+          slot[a] = t < end ? __ldg(slots + t) : -1;
+          if (t < end) v[a] = __ldg(reinterpret_cast<const uint4*>(src + t * stride));
         }
 #pragma unroll
-        for (int a = 0; a < AT_ONCE; ++a) {
-          const int x = x0 + a * C::SIDE;
-          if (slot[a] < 0 || slot[a] >= p.num_slots) continue;
-          uint4* dst = static_cast<uint4*>(x / U & 1 ? p.v_cache : p.k_cache) + (slot[a] * p.num_kv_heads + i.kvh) * U;
-          dst[x % U] = v[a];
+        for (int a = 0; a < AT_ONCE; ++a)
+          if (slot[a] >= 0 && slot[a] < p.num_slots) dst[slot[a] * p.num_kv_heads * U] = v[a];
+      }
+    };
+    // O / l of tile u of item k: a row per thread
+    const uint32_t tO = tmem + 128 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    uint32_t opar = 0;  // parities of lready and pvdone, a bit per tile
+    auto outputs = [&](const PackedItem& i, int k, int u) {
+      const bool done_ok = __all_sync(kFullMask, tc_wait(&lready[u], opar >> u & 1)) &&
+                           __all_sync(kFullMask, tc_wait(&pvdone[u], opar >> u & 1));
+      opar ^= 1u << u;
+      tc_fence_after_sync();
+      const float inv = done_ok ? 1.f / sums[u * TC_ROWS + tid] : NAN;
+      const bool fix = *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5);
+      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
+      // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows.
+      int row = tid;
+      use_here(row);
+      const int t0 = i.ta + u * tt;
+      const int t_end = i.tile_end(u, tt);
+      const int t = t0 + (row * p.inv_g >> 16);
+      uint4* base = static_cast<uint4*>(p.out) + (static_cast<size_t>(i.q0 + t0) * p.num_heads + i.kvh * G) * U + (row & 3);
+      uint32_t at[4];  // 16-byte units from there (below 128 tokens x 2^20 heads x 16); ~0: past the tile's last token
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int rr = (row & ~3) + y;
+        const int q = rr * p.inv_g >> 16;
+        at[y] = t0 + q < t_end ? static_cast<uint32_t>(q * p.num_heads + rr - q * G) * U : ~0u;
+      }
+#pragma unroll 1
+      for (int c = 0; c < HEAD_DIM; c += 32) {
+        uint32_t o[32];
+        tmem_ld16(tO + 256 * u + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+        tmem_ld16(tO + 256 * u + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+        tmem_wait_ld();
+        if (c + 32 == HEAD_DIM) {  // all of O is in registers
+          tc_fence_before_sync();
+          mbar_arrive(&ofree[u]);
         }
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+          o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
+        if (fix && t < t_end) {  // rare: take the values that are not finite among the keys that entered as 0
+#pragma unroll 1
+          for (int key = i.ta + 1; key <= t; ++key) {
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
+                                                                  i.kvh * HEAD_DIM + c);
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+              const uint32_t w = __ldg(v + d);
+              const uint32_t m = not_finite<T>(w);
+              if (m & 0xffffu) o[d] = (o[d] & 0xffff0000u) | join_not_finite<T>(o[d] & 0xffffu, w & 0xffffu);
+              if (m >> 16) o[d] = (o[d] & 0xffffu) | join_not_finite<T>(o[d] >> 16, w >> 16) << 16;
+            }
+          }
+        }
+        uint4 unit[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) unit[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        transpose4(unit, row);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (at[y] != ~0u) base[at[y] + c / 8] = unit[y];
       }
     };
     bool go = true;
@@ -373,19 +445,21 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       const int nblk = it.blocks(tt);
       const int kend = it.kend(tt);
       const int jm = it.first_masked();
-      // (a short prompt's first block is waited for: its rows are written behind it)
-      if (p.slot_mapping && jm > 0) write_cache(it);
 #pragma unroll 1
-      for (int j = jm; j < nblk; ++j) {
+      for (int j = jm - 1; go && j < nblk; ++j) {
+        if (j < jm) {  // before the masked blocks, unless the first of them is the item's first: that is waited for
+          if (jm > 0 && p.slot_mapping) write_cache(it);
+          continue;
+        }
         const int slot = (n0 + j) % VS;
-        const bool landed = __all_sync(kFullMask, tc_wait(&vraw[slot], (used >> slot) & 1));
+        const bool here = __all_sync(kFullMask, tc_wait(&vraw[slot], (used >> slot) & 1));
         used ^= 1u << slot;
         // A weight of 0 times a value that is not finite must not occur: rows past the item's last key become
         // zeros; what is not finite in rows that some tokens see and others do not enters as 0, and the rows
         // that see it take it at the end.  A row per thread.
         const int key = j * TC_KEYS + tid;
         uint8_t* row = sm + C::V_OFF + slot * C::KBYTES + tid * 128;
-        if (!landed) {
+        if (!here) {
         } else if (key >= kend) {
 #pragma unroll
           for (int x = 0; x < U; ++x)
@@ -404,14 +478,17 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
           if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5) = 1;
         }
         fence_proxy_async_smem();
-        go = all_meet<C::SIDE>(landed);  // (the warps go on or give up together)
+        go = all_meet<C::SIDE>(here);  // (the warps go on or give up together)
         if (!go) break;
         if (tid == 0) mbar_arrive(&vfull[slot]);
       }
       if (go && p.slot_mapping && jm == 0) write_cache(it);
+#pragma unroll 1
+      for (int u = 0; go && u < it.tiles(tt); ++u) outputs(it, k, u);
       n0 += nblk;
       go = go && all_meet<C::SIDE>(read_item(k + 1, it));
     }
+    tc_fence_before_sync();
     __syncthreads();
     allow_dependent_launch();
     return;
@@ -433,6 +510,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       // stages of the next block's K and of the current one's V, parities of the phases
       int kslot = 0, vslot = 0, dslot = 0;
       uint32_t kpar = 0, vpar = 0, spar = 0, ppar = 0, qpar = 0, tpar = u ^ 1;
+      uint32_t opar = 0;
+      bool was = false;                // the tile had an item before
       bool q_open = it.tiles(tt) > u;  // Q was asked for and not waited for
       // Three barriers at once, a lane each: the waits cost a hundred cycles together, not each.
       // (A test, not a wait that suspends: that one sleeps past the completion of one lane's
@@ -479,12 +558,18 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       auto step = [&](bool first, bool last) -> bool {
         if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &pfull[2 * u], ppar)) return false;
         tpar ^= 1;
+        if (first) {  // O of the tile's item before is read
+          if (was && !wait3(&ofree[u], opar, &ofree[u], opar, &ofree[u], opar)) return false;
+          opar ^= was;
+          was = true;
+        }
         tc_fence_after_sync();
         const uint64_t vj = umma_desc_add(dv, vslot * C::KBYTES);
         // the first 64 keys while the softmax writes the weights of the others
 #pragma unroll
         for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
           umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, !first || kk > 0);
+        umma_commit_elect(&pvhalf[u]);
         uint64_t* p1 = &pfull[2 * u + 1];
         if (!wait3(p1, ppar, p1, ppar, last ? p1 : &kfull[kslot], last ? ppar : kpar)) return false;
         ppar ^= 1;
@@ -588,7 +673,12 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       for (;; ++k) {
         ok = wait(begun, (k - 1) & 1);
         if (!ok || !next_item(it)) break;
-        if (lane == 0) publish(it, k);
+        if (lane == 0) {
+          publish(it, k);
+          for (int u = 0; u < it.tiles(tt); ++u)  // Q is loaded late, when its place is free: from L2 then
+            for (int db = 0; db < C::DBOX; ++db)
+              tma_prefetch_3d(&p.tmap_q, db * BOX_DIMS, it.kvh * G, it.q0 + it.ta + u * tt);
+        }
         __syncwarp();
       }
       if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
@@ -667,154 +757,146 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   const bool neg = a < 0.f;
   const float hidden = neg ? INFINITY : -INFINITY;
   const uint64_t a2 = pack_f32x2(a);
-  uint32_t spar = 0, vpar = 0;  // of the tile's blocks, of its items
+  uint32_t spar = 0, opar = 0;  // parities of the tile's blocks, of its items' outputs
+  bool stored = false;
 #pragma unroll 1
   for (int k = 0;; ++k) {
     int left, seen;  // the tile's blocks to come; the keys of the block that all its rows see, minus one
+    int tiles;
     {
       const PackedItem i = item(k);
+      tiles = i.tiles(tt);
       left = i.tile_blocks(u, tt);
       seen = i.ta + u * tt;
     }
     float m_used = -INFINITY, l = 0.f;  // log2 units
     uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
+    auto load_half = [&](int h) {
+#pragma unroll
+      for (int c = TC_HALF * h; c < TC_HALF * (h + 1); c += 16) tmem_ld16(tS + c, *reinterpret_cast<uint32_t(*)[16]>(&x[c]));
+      tmem_wait_ld();  // (at once: a register that a load still fills must not meet a branch)
+    };
+    // Hides the scores v of 16 keys, of which the first kv + 1 are visible.
+    auto hide = [&](uint32_t* v, int kv) {
+      const uint32_t m = kv < 0 ? 0u : kv > 15 ? ~0u : (2u << kv) - 1u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!(m >> i & 1u)) v[i] = __float_as_uint(hidden);
+    };
+    // The weights of a half once more, with the offsets of the rows with `low` at the maximum of their scores, and O
+    // and l after them; returns the row's sum.  Rare: a row's sum came out above the limit.
+    auto again = [&](int h, int low, int seen) -> float {
+      if (h == 1) {  // the first half's P V adds to O at this time
+        wait(&pvhalf[u], spar ^ 1);
+        tc_fence_after_sync();
+      }
+      uint32_t v[16];
+      const int own = seen + own_t - TC_HALF * h;
+      float top = neg ? INFINITY : -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < TC_HALF; c += 16) {
+        tmem_ld16(tS + TC_HALF * h + c, v);
+        tmem_wait_ld();
+        hide(v, own - c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = neg ? fminf(top, __uint_as_float(v[i])) : fmaxf(top, __uint_as_float(v[i]));
+      }
+      const float m_new = low ? fmaxf(m_used, rounded_up(top * a)) : m_used;
+      const float f = low ? ex2(m_used - m_new) : 1.f;
+      m_used = m_new;
+      l *= f;
+#pragma unroll 1
+      for (int c = 0; c < HEAD_DIM; c += 16) {
+        tmem_ld16(tO + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+        tmem_st16(tO + c, v);
+      }
+      const float bias = m_used == -INFINITY ? 0.f : C::MID - m_used;
+      float sum = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < TC_HALF; c += 16) {  // (P goes over scores that were read)
+        tmem_ld16(tS + TC_HALF * h + c, v);
+        tmem_wait_ld();
+        hide(v, own - c);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), a, bias)), p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), a, bias));
+          sum += p0 + p1;
+          w[i] = pack2<T>(p0, p1);
+        }
+        tmem_st8(tS + 32 * h + c / 2, w);
+      }
+      return sum;
+    };
 #pragma unroll 1
     for (; left > 0; --left, seen -= TC_KEYS) {
       wait(&sfull[u], spar);
       spar ^= 1;
       tc_fence_after_sync();
-#pragma unroll
-      for (int c = 0; c < TC_KEYS / 16; ++c) tmem_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
-      tmem_wait_ld();
-      if (seen < TC_KEYS - 1) {  // a key here may lie past some row of the tile
-        const int own = seen + own_t;  // (rows past the item's end are not written)
-        const int all = seen + least_t;
-#pragma unroll
-        for (int c = 0; c < TC_KEYS; c += 16) {
-          if (c + 15 <= all) continue;  // the whole warp sees the chunk
-          const int kv = own - c;  // visible keys of the chunk, minus one
-          const uint32_t m = kv < 0 ? 0u : kv > 15 ? ~0u : (2u << kv) - 1u;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!(m >> i & 1u)) x[c + i] = __float_as_uint(hidden);
-        }
-      }
-      // the row's maximum
-      float e[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(x[c]);
-      if (!neg) {
-#pragma unroll
-        for (int i = 4; i < TC_KEYS; i += 8)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            e[c] = i + 4 + c < TC_KEYS ? fmaxf(fmaxf(e[c], __uint_as_float(x[i + c])), __uint_as_float(x[i + 4 + c]))
-                                       : fmaxf(e[c], __uint_as_float(x[i + c]));
-        e[0] = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
-      } else {
-#pragma unroll
-        for (int i = 4; i < TC_KEYS; i += 4)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = fminf(e[c], __uint_as_float(x[i + c]));
-        e[0] = fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
-      }
-      const float m_new = fmaxf(m_used, rounded_up(e[0] * a));  // (a row that sees no key here keeps its own: the other is NaN)
-      // The exponent's offset moves at the first block and when the row maximum has grown
-      // by more than 2^8; O and l then scale by f.
-      const bool none = m_used == -INFINITY;  // nothing in O yet
-      const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
-      const float f = need ? ex2(m_used - m_new) : 1.f;
-      if (none || need) m_used = m_new;
-      const float bias = m_used == -INFINITY ? 0.f : C::MID - m_used;  // a row that has seen no key yet
-      if (__any_sync(kFullMask, need)) {
-#pragma unroll 1
-        for (int c = 0; c < HEAD_DIM; c += 16) {
-          uint32_t o16[16];
-          tmem_ld16(tO + c, o16);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(__uint_as_float(o16[i]) * f);
-          tmem_st16(tO + c, o16);
-        }
-      }
-      const uint64_t b2 = pack_f32x2(bias);
-      // the weights, half of the keys at a time: P in the half's 32 columns
-      uint64_t sum2[2] = {0, 0};
+      // Half of the keys at a time, so that the first weights are on their way to the MMA while the second half is
+      // at work.  The exponent's offset stays where it is as long as the weights' own sum says that they fit:
+      // the maximum of a half is looked for at the first scores, and where its weights came out too large.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        uint32_t* y = x + TC_HALF * h;
+        load_half(h);
+        if (seen + least_t < TC_HALF * (h + 1) - 1) {  // a key here may lie past some row of the warp
 #pragma unroll
-        for (int i = 32 * h; i < 32 * h + 32; ++i) {
-          const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(x[2 * i], x[2 * i + 1]), a2, b2));
+          for (int c = 0; c < TC_HALF; c += 16)
+            if (seen + least_t < TC_HALF * h + c + 15) hide(y + c, seen + own_t - TC_HALF * h - c);
+        }
+        // (an opaque truth value: folded into the selection below, `m_used == -inf ? max(m_used, x) : m_used` has
+        // come out as max(m_used, x))
+        int none = m_used == -INFINITY;
+        use_here(none);
+        if (__any_sync(kFullMask, none)) {  // a row's first scores
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(y[c]);
+#pragma unroll
+          for (int i = 4; i < TC_HALF; i += 4)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              e[c] = neg ? fminf(e[c], __uint_as_float(y[i + c])) : fmaxf(e[c], __uint_as_float(y[i + c]));
+          const float top = neg ? fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+          // (a row that sees no key here stays without: its maximum is NaN)
+          if (none) m_used = fmaxf(m_used, rounded_up(top * a));
+        }
+        const uint64_t b2 = pack_f32x2(m_used == -INFINITY ? 0.f : C::MID - m_used);  // (0: a row that has seen no key yet)
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < TC_HALF / 2; ++i) {
+          const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(y[2 * i], y[2 * i + 1]), a2, b2));
           const float p0 = ex2(t.x), p1 = ex2(t.y);
           sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
-          x[i] = pack2<T>(p0, p1);
+          y[i] = pack2<T>(p0, p1);  // (its place was consumed)
         }
-        tmem_st16(tS + 32 * h, &x[32 * h]);
-        tmem_st16(tS + 32 * h + 16, &x[32 * h + 16]);
+        const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+        float sum = s2.x + s2.y;
+        if (__any_sync(kFullMask, sum > C::LIMIT)) {
+          sum = again(h, sum > C::LIMIT, seen);
+        } else {  // P in the half's 32 columns, over scores that are in registers
+          tmem_st16(tS + 32 * h, &y[0]);
+          tmem_st16(tS + 32 * h + 16, &y[16]);
+        }
+        l += sum;
         tmem_wait_st();
         tc_fence_before_sync();
         mbar_arrive(&pfull[2 * u + h]);
       }
-      const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
-      l = fmaf(l, f, s2.x + s2.y);
     }
-    // ------------------------------------------------ O / l
-    const PackedItem i = item(k);  // (read again: held over the loop it would cost registers there)
-    if (u < i.tiles(tt)) {
-      wait(&pvdone[u], vpar);
-      vpar ^= 1;
-      tc_fence_after_sync();
-      const float inv = ok ? 1.f / l : NAN;
-      const bool fix = *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5);
-      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
-      // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows.  The loop
-      // is short because its code runs once per item.
-      int row = r;
-      use_here(row);  // (what follows from it is not worth registers in the blocks' loop)
-      const int t0 = i.ta + u * tt;
-      const int t_end = i.tile_end(u, tt);
-      const int t = t0 + token_of(row);
-      T* at[4];
-      bool on[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int rr = (row & ~3) + y;
-        const int q = token_of(rr);
-        on[y] = t0 + q < t_end;  // (rows past the tile's last token count as the next one's)
-        at[y] = static_cast<T*>(p.out) + (static_cast<size_t>(i.q0 + t0 + q) * p.num_heads + i.kvh * G + rr - q * G) * HEAD_DIM +
-                8 * (row & 3);
+    // the sums for the warps of the outputs, which have read the last item's
+    if (u < tiles) {
+      if (stored) {
+        wait(&ofree[u], opar);
+        opar ^= 1;
       }
-#pragma unroll 1
-      for (int c = 0; c < HEAD_DIM; c += 32) {
-        uint32_t o[32];
-        tmem_ld16(tO + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-        tmem_ld16(tO + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int d = 0; d < 16; ++d)
-          o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
-        if (fix && t < t_end) {  // rare: take the values that are not finite among the keys that entered as 0
-#pragma unroll 1
-          for (int key = i.ta + 1; key <= t; ++key) {
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
-                                                                  i.kvh * HEAD_DIM + c);
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-              const uint32_t w = __ldg(v + d);
-              const uint32_t m = not_finite<T>(w);
-              if (m & 0xffffu) o[d] = (o[d] & 0xffff0000u) | join_not_finite<T>(o[d] & 0xffffu, w & 0xffffu);
-              if (m >> 16) o[d] = (o[d] & 0xffffu) | join_not_finite<T>(o[d] >> 16, w >> 16) << 16;
-            }
-          }
-        }
-        uint4 unit[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) unit[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-        transpose4(unit, row);
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (on[y]) *reinterpret_cast<uint4*>(at[y] + c) = unit[y];
-      }
+      stored = true;
+      sums[u * TC_ROWS + r] = ok ? l : NAN;
+      mbar_arrive(&lready[u]);
     }
     if (!has_item(k + 1)) break;
   }
