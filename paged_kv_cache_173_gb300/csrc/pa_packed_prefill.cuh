@@ -76,7 +76,7 @@ struct PpCfg {
   static constexpr int KATOM = TC_KEYS * 128;
   static constexpr int KBYTES = DBOX * KATOM;
   static constexpr int SMEM_MAX = 227 * 1024;
-  static constexpr int RESERVE = 1024 + 2048;  // base alignment slack, items, barriers
+  static constexpr int RESERVE = 3072;  // items, sums, barriers
   static constexpr int STAGES_FIT = (SMEM_MAX - RESERVE - TC_TILES * QBYTES) / KBYTES;
   static constexpr int KSTAGES = STAGES_FIT / 2 < 4 ? STAGES_FIT / 2 : 4;
   static constexpr int VSTAGES = STAGES_FIT - KSTAGES < 4 ? STAGES_FIT - KSTAGES : 4;
@@ -93,12 +93,17 @@ struct PpCfg {
   static constexpr int RESP_OFF = SUM_OFF + TC_TILES * TC_ROWS * 4;
   static constexpr int BAR_OFF = RESP_OFF + 16;
   static constexpr int DONE = VSTAGES;  // ring of completed steps
-  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 10 * TC_TILES + ITEMS + 2;
+  static constexpr int NBARS = KSTAGES + 2 * VSTAGES + DONE + 11 * TC_TILES + ITEMS + 2;
   static constexpr int SLOT_OFF = BAR_OFF + 8 * NBARS;
   static constexpr int LAYOUT_BYTES = SLOT_OFF + 16;
-  static constexpr int SMEM_BYTES = LAYOUT_BYTES + 1024;
+  static constexpr int SMEM_BYTES = LAYOUT_BYTES;
   static_assert(SMEM_BYTES <= SMEM_MAX, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
+  // A tile's 256 columns: S 128, then O.  With 64 channels there is room for P beside S, and Q K^T of a block runs as
+  // soon as the softmax has read the scores of the one before (EARLY); else P goes over S, and it runs behind P V.
+  static constexpr bool EARLY = HEAD_DIM == 64;
+  static constexpr int P_COL = EARLY ? 128 : 0;
+  static constexpr int O_COL = EARLY ? 192 : 128;
   static constexpr uint32_t ID_S = umma_idesc_f16(TC_ROWS, TC_KEYS, BF16, false);
   static constexpr uint32_t ID_PV = umma_idesc_f16(TC_ROWS, HEAD_DIM, BF16, true);
   // log2 of the largest weight when the running maximum has just moved; it may grow by 2^8 from there.
@@ -244,7 +249,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   constexpr int VS = C::VSTAGES;
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sm = smem_raw;  // (a constant address: rounded up here, it and what follows from it cost registers in every role)
   // [ITEMS][INFO]: the item (s: -1 past the last), [5] a masked row may meet a value that is not finite
   int* infos = reinterpret_cast<int*>(sm + C::INFO_OFF);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
@@ -258,7 +263,9 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   uint64_t* sfull = done + C::DONE;        // [tile] S of the tile's next block is in TMEM
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
   uint64_t* pvhalf = pfull + 2 * TC_TILES; // [tile] P V of the first 64 keys of that block has completed
-  uint64_t* pvdone = pvhalf + TC_TILES;    // [tile] the last P V of the tile's item has completed
+                                           // (EARLY: of the block)
+  uint64_t* sfree = pvhalf + TC_TILES;     // [tile] EARLY: S of the block is read (128 arrivals)
+  uint64_t* pvdone = sfree + TC_TILES;     // [tile] the last P V of the tile's item has completed
   uint64_t* lready = pvdone + TC_TILES;    // [tile] the sums of the item's weights are stored (128 arrivals)
   uint64_t* ofree = lready + TC_TILES;     // [tile] the sums and O of the item are read (128 arrivals)
   uint64_t* qbar = ofree + TC_TILES;       // [tile] Q of the tile's next item landed
@@ -280,6 +287,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   PackedItem it;
   if (!find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it)) {
     allow_dependent_launch();
+    return;
+  }
+  if (smem_addr(smem_raw) & 1023u) {  // not as declared
+    write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
     return;
   }
   auto load_q = [&](const PackedItem& i, int u) {  // one thread
@@ -320,6 +331,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       mbar_init(&pfull[2 * i], TC_ROWS);
       mbar_init(&pfull[2 * i + 1], TC_ROWS);
       mbar_init(&pvhalf[i], 1);
+      mbar_init(&sfree[i], TC_ROWS);
       mbar_init(&pvdone[i], 2);
       mbar_init(&lready[i], TC_ROWS);
       mbar_init(&ofree[i], C::SIDE);
@@ -342,11 +354,11 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   const uint32_t tmem = *tslot;
 
   if (warp >= C::SIDE_WARP && warp < C::MMA_WARP) {
-    // ------------------------------------------------ the cache write, and values that rows must not meet
+    // ------------------------------------------------ the cache write and the outputs
     set_max_regs<false, C::SIDE_REGS>();
     const int tid = threadIdx.x - C::SIDE_WARP * 32;
     constexpr int U = HEAD_DIM / 8;  // 16-byte units of a row
-    // The item's own tokens' rows into the pools: 2 U lanes take the key's and the value's units of a token, four
+    // The item's own tokens' rows into the pools: 2 U lanes take the key's and the value's units of a token, eight
     // tokens of theirs on the way at a time.
     auto write_cache = [&](const PackedItem& i) {
       constexpr int AT_ONCE = 4;
@@ -377,7 +389,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       }
     };
     // O / l of tile u of item k: a row per thread
-    const uint32_t tO = tmem + 128 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t tO = tmem + C::O_COL + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     uint32_t opar = 0;  // parities of lready and pvdone, a bit per tile
     auto outputs = [&](const PackedItem& i, int k, int u) {
       const bool done_ok = __all_sync(kFullMask, tc_wait(&lready[u], opar >> u & 1)) &&
@@ -386,41 +398,31 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       tc_fence_after_sync();
       const float inv = done_ok ? 1.f / sums[u * TC_ROWS + tid] : NAN;
       const bool fix = *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5);
-      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes
-      // exchange their 16-byte units, so that a store writes 64 bytes of each of eight rows.
       int row = tid;
       use_here(row);
-      const int t0 = i.ta + u * tt;
-      const int t_end = i.tile_end(u, tt);
-      const int t = t0 + (row * p.inv_g >> 16);
-      uint4* base = static_cast<uint4*>(p.out) + (static_cast<size_t>(i.q0 + t0) * p.num_heads + i.kvh * G) * U + (row & 3);
-      uint32_t at[4];  // 16-byte units from there (below 128 tokens x 2^20 heads x 16); ~0: past the tile's last token
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int rr = (row & ~3) + y;
-        const int q = rr * p.inv_g >> 16;
-        at[y] = t0 + q < t_end ? static_cast<uint32_t>(q * p.num_heads + rr - q * G) * U : ~0u;
-      }
+      const int q = row * p.inv_g >> 16;
+      const int t = i.ta + u * tt + q;
+      const bool on = t < i.tile_end(u, tt);  // (rows past the tile's last token count as the next one's)
+      uint4* dst = static_cast<uint4*>(p.out) + (static_cast<size_t>(i.q0 + t) * p.num_heads + i.kvh * G + row - q * G) * U;
 #pragma unroll 1
-      for (int c = 0; c < HEAD_DIM; c += 32) {
-        uint32_t o[32];
-        tmem_ld16(tO + 256 * u + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-        tmem_ld16(tO + 256 * u + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+      for (int c = 0; c < HEAD_DIM; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tO + 256 * u + c, o);
         tmem_wait_ld();
-        if (c + 32 == HEAD_DIM) {  // all of O is in registers
+        if (c + 16 == HEAD_DIM) {  // all of O is read
           tc_fence_before_sync();
           mbar_arrive(&ofree[u]);
         }
 #pragma unroll
-        for (int d = 0; d < 16; ++d)
+        for (int d = 0; d < 8; ++d)
           o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
-        if (fix && t < t_end) {  // rare: take the values that are not finite among the keys that entered as 0
+        if (fix && on) {  // rare: take the values that are not finite among the keys that entered as 0
 #pragma unroll 1
           for (int key = i.ta + 1; key <= t; ++key) {
             const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
                                                                   i.kvh * HEAD_DIM + c);
 #pragma unroll
-            for (int d = 0; d < 16; ++d) {
+            for (int d = 0; d < 8; ++d) {
               const uint32_t w = __ldg(v + d);
               const uint32_t m = not_finite<T>(w);
               if (m & 0xffffu) o[d] = (o[d] & 0xffff0000u) | join_not_finite<T>(o[d] & 0xffffu, w & 0xffffu);
@@ -428,65 +430,19 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
             }
           }
         }
-        uint4 unit[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) unit[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-        transpose4(unit, row);
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (at[y] != ~0u) base[at[y] + c / 8] = unit[y];
+        if (on) {
+          dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[c / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
       }
     };
     bool go = true;
-    int n0 = 0;         // blocks of the items before
-    uint32_t used = 0;  // parities of vraw
 #pragma unroll 1
     for (int k = 0; go; ++k) {
-      const int nblk = it.blocks(tt);
-      const int kend = it.kend(tt);
-      const int jm = it.first_masked();
+      if (p.slot_mapping) write_cache(it);
 #pragma unroll 1
-      for (int j = jm - 1; go && j < nblk; ++j) {
-        if (j < jm) {  // before the masked blocks, unless the first of them is the item's first: that is waited for
-          if (jm > 0 && p.slot_mapping) write_cache(it);
-          continue;
-        }
-        const int slot = (n0 + j) % VS;
-        const bool here = __all_sync(kFullMask, tc_wait(&vraw[slot], (used >> slot) & 1));
-        used ^= 1u << slot;
-        // A weight of 0 times a value that is not finite must not occur: rows past the item's last key become
-        // zeros; what is not finite in rows that some tokens see and others do not enters as 0, and the rows
-        // that see it take it at the end.  A row per thread.
-        const int key = j * TC_KEYS + tid;
-        uint8_t* row = sm + C::V_OFF + slot * C::KBYTES + tid * 128;
-        if (!here) {
-        } else if (key >= kend) {
-#pragma unroll
-          for (int x = 0; x < U; ++x)
-            *reinterpret_cast<uint4*>(row + (x >> 3) * C::KATOM + ((x + tid) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        } else if (key > it.ta) {
-          uint32_t any = 0;
-#pragma unroll 4
-          for (int x = 0; x < U; ++x) {  // (threads start at different units: no bank conflict)
-            uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * C::KATOM + ((x + tid) & 7) * 16);
-            uint4 w = *at;
-            const uint4 m = make_uint4(not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w));
-            const uint32_t bad = m.x | m.y | m.z | m.w;
-            if (bad) *at = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
-            any |= bad;
-          }
-          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5) = 1;
-        }
-        fence_proxy_async_smem();
-        go = all_meet<C::SIDE>(here);  // (the warps go on or give up together)
-        if (!go) break;
-        if (tid == 0) mbar_arrive(&vfull[slot]);
-      }
-      if (go && p.slot_mapping && jm == 0) write_cache(it);
-#pragma unroll 1
-      for (int u = 0; go && u < it.tiles(tt); ++u) outputs(it, k, u);
-      n0 += nblk;
-      go = go && all_meet<C::SIDE>(read_item(k + 1, it));
+      for (int u = 0; u < it.tiles(tt); ++u) outputs(it, k, u);
+      go = all_meet<C::SIDE>(read_item(k + 1, it));  // (the warps go on or give up together)
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -505,8 +461,9 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       const uint64_t dq = umma_desc_sw128(smem_addr(sm + u * C::QBYTES), 16, 1024);    // Q, K-major
       const uint64_t dk = umma_desc_sw128(smem_addr(sm + C::K_OFF), 16, 1024);         // K, K-major
       const uint64_t dv = umma_desc_sw128(smem_addr(sm + C::V_OFF), C::KATOM, 1024);   // V, MN-major
-      const uint32_t tP = tmem + 256 * u;
-      const uint32_t tO = tP + 128;
+      const uint32_t tS = tmem + 256 * u;
+      const uint32_t tP = tS + C::P_COL;
+      const uint32_t tO = tS + C::O_COL;
       // stages of the next block's K and of the current one's V, parities of the phases
       int kslot = 0, vslot = 0, dslot = 0;
       uint32_t kpar = 0, vpar = 0, spar = 0, ppar = 0, qpar = 0, tpar = u ^ 1;
@@ -530,11 +487,14 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
         for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
           const uint32_t off = (ks >> 2) * C::QATOM + ((ks & 3) << 5);
           const uint32_t koff = (ks >> 2) * C::KATOM + ((ks & 3) << 5);
-          umma_f16_elect(tP, umma_desc_add(dq, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
+          umma_f16_elect(tS, umma_desc_add(dq, off), umma_desc_add(kj, koff), C::ID_S, ks > 0);
         }
       };
+      uint32_t fpar = 0;  // EARLY: of sfree
       auto first_qk = [&]() -> bool {  // of an item
-        if (!wait3(&qbar[u], qpar, &qbar[u], qpar, &kfull[kslot], kpar)) return false;
+        const bool busy = C::EARLY && was;  // (S of the tile's item before)
+        if (!wait3(&qbar[u], qpar, busy ? &sfree[u] : &qbar[u], busy ? fpar : qpar, &kfull[kslot], kpar)) return false;
+        fpar ^= busy;
         tc_fence_after_sync();
         qpar ^= 1;
         q_open = false;
@@ -548,7 +508,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
         kpar ^= kslot + 1 == KS;
         kslot = kslot + 1 == KS ? 0 : kslot + 1;
       };
-      // The tiles' MMAs take turns, so that one tile's run under the other's softmax.
+      // The tiles' MMAs take turns, so that one tile's run under the other's softmax.  (Not EARLY: there the softmax
+      // warps of both tiles have work all the time.)
       auto pass_turn = [&]() {
         if (lane == 0) mbar_arrive(&turn[u ^ 1]);
         __syncwarp();
@@ -556,7 +517,18 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       // P V of the current block in the tile's turn, and Q K^T of the next one; first: the item's
       // first block, last: the tile's last one
       auto step = [&](bool first, bool last) -> bool {
-        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &pfull[2 * u], ppar)) return false;
+        if constexpr (C::EARLY) {
+          if (!last) {
+            if (!wait3(&sfree[u], fpar, &sfree[u], fpar, &kfull[kslot], kpar)) return false;
+            fpar ^= 1;
+            tc_fence_after_sync();
+            qk();
+            umma_commit_elect(&sfull[u]);
+            spar ^= 1;
+          }
+        }
+        uint64_t* const go = C::EARLY ? &vfull[vslot] : &turn[u];
+        if (!wait3(go, C::EARLY ? vpar : tpar, &vfull[vslot], vpar, &pfull[2 * u], ppar)) return false;
         tpar ^= 1;
         if (first) {  // O of the tile's item before is read
           if (was && !wait3(&ofree[u], opar, &ofree[u], opar, &ofree[u], opar)) return false;
@@ -569,20 +541,25 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
 #pragma unroll
         for (int kk = 0; kk < TC_KEYS / 32; ++kk)  // 16 keys = 8 columns of P
           umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, !first || kk > 0);
-        umma_commit_elect(&pvhalf[u]);
+        if constexpr (!C::EARLY) umma_commit_elect(&pvhalf[u]);
         uint64_t* p1 = &pfull[2 * u + 1];
-        if (!wait3(p1, ppar, p1, ppar, last ? p1 : &kfull[kslot], last ? ppar : kpar)) return false;
+        const bool k_too = !C::EARLY && !last;
+        if (!wait3(p1, ppar, p1, ppar, k_too ? &kfull[kslot] : p1, k_too ? kpar : ppar)) return false;
         ppar ^= 1;
         tc_fence_after_sync();
 #pragma unroll
         for (int kk = TC_KEYS / 32; kk < TC_KEYS / 16; ++kk)
           umma_f16_ts_elect(tO, tP + 8 * kk, umma_desc_add(vj, kk * 2048), C::ID_PV, true);
-        if (!last) qk();
-        pass_turn();
+        if constexpr (C::EARLY) {
+          umma_commit_elect(&pvhalf[u]);
+        } else {
+          if (!last) qk();
+          pass_turn();
+        }
         if (last) {
           if (lane == 0) mbar_arrive(&pvdone[u]);
           umma_commit_elect(&pvdone[u]);
-        } else {
+        } else if (!C::EARLY) {
           umma_commit_elect(&sfull[u]);
           spar ^= 1;
         }
@@ -590,9 +567,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       };
       // a step of the item in which the tile has no block: at the pace of the other tile
       auto no_step = [&]() -> bool {
-        if (!wait3(&turn[u], tpar, &vfull[vslot], vpar, &vfull[vslot], vpar)) return false;
+        if (!wait3(C::EARLY ? &vfull[vslot] : &turn[u], C::EARLY ? vpar : tpar, &vfull[vslot], vpar, &vfull[vslot], vpar))
+          return false;
         tpar ^= 1;
-        pass_turn();
+        if constexpr (!C::EARLY) pass_turn();
         return true;
       };
       auto next_v = [&]() {
@@ -668,26 +646,73 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
         }
         return false;
       };
+      // A weight of 0 times a value that is not finite must not occur.  In blocks that some rows do not see all of,
+      // keys past the item's last become zeros; what is not finite in keys that some tokens see and others do
+      // not enters as 0, and the rows that see it take it at the end.
+      constexpr int U = HEAD_DIM / 8;  // 16-byte units of a row
+      int n0 = 0;          // blocks of the items before
+      uint32_t seen = 0;   // parities of vraw
+      auto make_safe = [&](const PackedItem& i, int k) -> bool {
+        const int nblk = i.blocks(tt), kend = i.kend(tt), ta = i.ta;
+#pragma unroll 1
+        for (int j = i.first_masked(); j < nblk; ++j) {
+          const int slot = (n0 + j) % VS;
+          if (!wait(&vraw[slot], seen >> slot & 1)) return false;
+          seen ^= 1u << slot;
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int x = max(0, ta + 1 - j * TC_KEYS) & ~31 | lane; x < TC_KEYS; x += 32) {  // a row per lane
+            const int key = j * TC_KEYS + x;
+            if (key <= ta) continue;
+            uint8_t* row = sm + C::V_OFF + slot * C::KBYTES + x * 128;
+            if (key >= kend) {
+#pragma unroll
+              for (int y = 0; y < U; ++y)  // (from different units on: no bank conflict)
+                *reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+#pragma unroll 4
+            for (int y = 0; y < U; ++y) {
+              uint4* at = reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16);
+              const uint4 w = *at;
+              const uint4 m = make_uint4(not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w));
+              const uint32_t bad = m.x | m.y | m.z | m.w;
+              if (bad) *at = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
+              any |= bad;
+            }
+          }
+          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5) = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&vfull[slot]);
+        }
+        n0 += nblk;
+        return true;
+      };
       int k = 1;
 #pragma unroll 1
       for (;; ++k) {
+        const PackedItem now = it;
         ok = wait(begun, (k - 1) & 1);
-        if (!ok || !next_item(it)) break;
-        if (lane == 0) {
+        const bool more = ok && next_item(it);
+        if (more && lane == 0) {
           publish(it, k);
           for (int u = 0; u < it.tiles(tt); ++u)  // Q is loaded late, when its place is free: from L2 then
             for (int db = 0; db < C::DBOX; ++db)
               tma_prefetch_3d(&p.tmap_q, db * BOX_DIMS, it.kvh * G, it.q0 + it.ta + u * tt);
         }
         __syncwarp();
+        if (ok) ok = make_safe(now, k - 1);
+        if (!ok || !more) break;
       }
+      const int last = ok ? k : k + 1;  // (a wait ran out behind an item that is published)
       if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
         uint3 id;
         if (cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it))
           write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
       }
       it.s = -1;
-      if (lane == 0) publish(it, k);
+      if (lane == 0) publish(it, last);
     } else {
       // ---------------------------------------------- loads of K and V
       bool go = true;
@@ -743,7 +768,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   const int r = 32 * (warp & 3) + lane;
   const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
   const uint32_t tS = tmem + 256 * u + lane_off;
-  const uint32_t tO = tS + 128;
+  const uint32_t tP = tS + C::P_COL;
+  const uint32_t tO = tS + C::O_COL;
   auto token_of = [&](int row) { return row * p.inv_g >> 16; };  // of the tile
   const int own_t = token_of(r);
   const int least_t = token_of(r & ~31);
@@ -827,7 +853,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
           sum += p0 + p1;
           w[i] = pack2<T>(p0, p1);
         }
-        tmem_st8(tS + 32 * h + c / 2, w);
+        tmem_st8(tP + 32 * h + c / 2, w);
       }
       return sum;
     };
@@ -836,56 +862,128 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       wait(&sfull[u], spar);
       spar ^= 1;
       tc_fence_after_sync();
-      // Half of the keys at a time, so that the first weights are on their way to the MMA while the second half is
-      // at work.  The exponent's offset stays where it is as long as the weights' own sum says that they fit:
-      // the maximum of a half is looked for at the first scores, and where its weights came out too large.
+      if constexpr (C::EARLY) {
+        // All scores at once, so that their place is free for the next block's.
+        load_half(0);
+        load_half(1);
+        tc_fence_before_sync();
+        mbar_arrive(&sfree[u]);
+        if (seen + least_t < TC_KEYS - 1) {  // a key here may lie past some row of the warp
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t* y = x + TC_HALF * h;
-        load_half(h);
-        if (seen + least_t < TC_HALF * (h + 1) - 1) {  // a key here may lie past some row of the warp
-#pragma unroll
-          for (int c = 0; c < TC_HALF; c += 16)
-            if (seen + least_t < TC_HALF * h + c + 15) hide(y + c, seen + own_t - TC_HALF * h - c);
+          for (int c = 0; c < TC_KEYS; c += 16)
+            if (seen + least_t < c + 15) hide(x + c, seen + own_t - c);
         }
-        // (an opaque truth value: folded into the selection below, `m_used == -inf ? max(m_used, x) : m_used` has
-        // come out as max(m_used, x))
-        int none = m_used == -INFINITY;
-        use_here(none);
-        if (__any_sync(kFullMask, none)) {  // a row's first scores
-          float e[4];
+        float e[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(y[c]);
+        for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(x[c]);
+        if (!neg) {
 #pragma unroll
-          for (int i = 4; i < TC_HALF; i += 4)
+          for (int i = 4; i < TC_KEYS - 4; i += 8)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              e[c] = neg ? fminf(e[c], __uint_as_float(y[i + c])) : fmaxf(e[c], __uint_as_float(y[i + c]));
-          const float top = neg ? fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
-          // (a row that sees no key here stays without: its maximum is NaN)
-          if (none) m_used = fmaxf(m_used, rounded_up(top * a));
+            for (int c = 0; c < 4; ++c) e[c] = fmaxf(fmaxf(e[c], __uint_as_float(x[i + c])), __uint_as_float(x[i + 4 + c]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) e[c] = fmaxf(e[c], __uint_as_float(x[TC_KEYS - 4 + c]));
+          e[0] = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+        } else {
+#pragma unroll
+          for (int i = 4; i < TC_KEYS; i += 4)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) e[c] = fminf(e[c], __uint_as_float(x[i + c]));
+          e[0] = fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
         }
+        // The exponent's offset moves at the first block and when the row maximum has grown by more than 2^8; O and l
+        // then scale by f.  (A row that sees no key here keeps its own: the other is NaN.)
+        const float m_new = fmaxf(m_used, rounded_up(e[0] * a));
+        const bool none = m_used == -INFINITY;  // nothing in O yet
+        const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
+        const float f = need ? ex2(m_used - m_new) : 1.f;
+        if (none || need) m_used = m_new;
         const uint64_t b2 = pack_f32x2(m_used == -INFINITY ? 0.f : C::MID - m_used);  // (0: a row that has seen no key yet)
         uint64_t sum2[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < TC_HALF / 2; ++i) {
-          const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(y[2 * i], y[2 * i + 1]), a2, b2));
-          const float p0 = ex2(t.x), p1 = ex2(t.y);
-          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
-          y[i] = pack2<T>(p0, p1);  // (its place was consumed)
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 32 * h; i < 32 * h + 32; ++i) {
+            const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(x[2 * i], x[2 * i + 1]), a2, b2));
+            const float p0 = ex2(t.x), p1 = ex2(t.y);
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+            x[i] = pack2<T>(p0, p1);  // (its place was consumed)
+          }
+          if (h == 0) {
+            wait(&pvhalf[u], spar);  // P V of the block before: it has read P and O stands
+            tc_fence_after_sync();
+            if (__any_sync(kFullMask, need)) {
+#pragma unroll 1
+              for (int c = 0; c < HEAD_DIM; c += 8) {  // (eight at a time: the scores hold registers)
+                uint32_t o8[8];
+                tmem_ld8(tO + c, o8);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o8[i] = __float_as_uint(__uint_as_float(o8[i]) * f);
+                tmem_st8(tO + c, o8);
+              }
+            }
+          }
+          tmem_st16(tP + 32 * h, &x[32 * h]);
+          tmem_st16(tP + 32 * h + 16, &x[32 * h + 16]);
+          tmem_wait_st();
+          tc_fence_before_sync();
+          mbar_arrive(&pfull[2 * u + h]);
         }
         const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
-        float sum = s2.x + s2.y;
-        if (__any_sync(kFullMask, sum > C::LIMIT)) {
-          sum = again(h, sum > C::LIMIT, seen);
-        } else {  // P in the half's 32 columns, over scores that are in registers
-          tmem_st16(tS + 32 * h, &y[0]);
-          tmem_st16(tS + 32 * h + 16, &y[16]);
+        l = fmaf(l, f, s2.x + s2.y);
+      } else {
+        // Half of the keys at a time, so that the first weights are on their way to the MMA while the second half is
+        // at work.  The exponent's offset stays where it is as long as the weights' own sum says that they fit:
+        // the maximum of a half is looked for at the first scores, and where its weights came out too large.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t* y = x + TC_HALF * h;
+          load_half(h);
+          if (seen + least_t < TC_HALF * (h + 1) - 1) {  // a key here may lie past some row of the warp
+#pragma unroll
+            for (int c = 0; c < TC_HALF; c += 16)
+              if (seen + least_t < TC_HALF * h + c + 15) hide(y + c, seen + own_t - TC_HALF * h - c);
+          }
+          // (an opaque truth value: folded into the selection below, `m_used == -inf ? max(m_used, x) : m_used` has
+          // come out as max(m_used, x))
+          int none = m_used == -INFINITY;
+          use_here(none);
+          if (__any_sync(kFullMask, none)) {  // a row's first scores
+            float e[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(y[c]);
+#pragma unroll
+            for (int i = 4; i < TC_HALF; i += 4)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                e[c] = neg ? fminf(e[c], __uint_as_float(y[i + c])) : fmaxf(e[c], __uint_as_float(y[i + c]));
+            const float top = neg ? fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+            // (a row that sees no key here stays without: its maximum is NaN)
+            if (none) m_used = fmaxf(m_used, rounded_up(top * a));
+          }
+          const uint64_t b2 = pack_f32x2(m_used == -INFINITY ? 0.f : C::MID - m_used);  // (0: a row that has seen no key yet)
+          uint64_t sum2[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < TC_HALF / 2; ++i) {
+            const float2 t = unpack_f32x2(fma_f32x2(pack_f32x2(y[2 * i], y[2 * i + 1]), a2, b2));
+            const float p0 = ex2(t.x), p1 = ex2(t.y);
+            sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+            y[i] = pack2<T>(p0, p1);  // (its place was consumed)
+          }
+          const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+          float sum = s2.x + s2.y;
+          if (__any_sync(kFullMask, sum > C::LIMIT)) {
+            sum = again(h, sum > C::LIMIT, seen);
+          } else {  // P in the half's 32 columns, over scores that are in registers
+            tmem_st16(tP + 32 * h, &y[0]);
+            tmem_st16(tP + 32 * h + 16, &y[16]);
+          }
+          l += sum;
+          tmem_wait_st();
+          tc_fence_before_sync();
+          mbar_arrive(&pfull[2 * u + h]);
         }
-        l += sum;
-        tmem_wait_st();
-        tc_fence_before_sync();
-        mbar_arrive(&pfull[2 * u + h]);
       }
     }
     // the sums for the warps of the outputs, which have read the last item's
