@@ -84,8 +84,8 @@ struct PpCfg {
   static constexpr int K_OFF = TC_TILES * QBYTES;
   static constexpr int V_OFF = K_OFF + KSTAGES * KBYTES;
   static constexpr int INFO_OFF = V_OFF + VSTAGES * KBYTES;
-  // Published items.  The loads run at most VSTAGES blocks, so as many items, ahead of the outputs that
-  // are still being written, and the next one is published when they begin one.
+  // Published items.  The MMAs are at most one item ahead of the outputs that are still being written, the loads
+  // VSTAGES blocks, so as many items, ahead of them, and one more is published.
   static constexpr int ITEMS = 8;
   static_assert(VSTAGES + 3 <= ITEMS, "the ring of items");
   static constexpr int INFO = 8;  // words of an item
@@ -272,7 +272,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   uint64_t* drain = qbar + TC_TILES;       // [tile] every MMA issued has completed
   uint64_t* turn = drain + TC_TILES;       // [tile] its MMA warp may issue the next step
   uint64_t* ifull = turn + TC_TILES;       // [ITEMS] an item is published
-  uint64_t* begun = ifull + C::ITEMS;      // the loads of the next item begin
+  uint64_t* begun = ifull + C::ITEMS;      // the loads of an item come to its last three blocks
   uint64_t* cbar = begun + 1;              // the answer about another CTA landed
   float* sums = reinterpret_cast<float*>(sm + C::SUM_OFF);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::SLOT_OFF);
@@ -361,7 +361,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     // The item's own tokens' rows into the pools: 2 U lanes take the key's and the value's units of a token, eight
     // tokens of theirs on the way at a time.
     auto write_cache = [&](const PackedItem& i) {
-      constexpr int AT_ONCE = 4;
+      constexpr int AT_ONCE = 8;
       constexpr int STEP = C::SIDE / (2 * U);  // tokens apart
       const int end = i.kend(tt) - i.ta;
       int me = tid;
@@ -398,41 +398,62 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       tc_fence_after_sync();
       const float inv = done_ok ? 1.f / sums[u * TC_ROWS + tid] : NAN;
       const bool fix = *const_cast<const volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5);
+      // A thread holds one row, and rows of different tokens are far apart in `out`: four lanes exchange their
+      // 16-byte units, so that a store writes 64 bytes of each of eight rows.
       int row = tid;
       use_here(row);
-      const int q = row * p.inv_g >> 16;
-      const int t = i.ta + u * tt + q;
-      const bool on = t < i.tile_end(u, tt);  // (rows past the tile's last token count as the next one's)
-      uint4* dst = static_cast<uint4*>(p.out) + (static_cast<size_t>(i.q0 + t) * p.num_heads + i.kvh * G + row - q * G) * U;
+      const int t0 = i.ta + u * tt;
+      const int t_end = i.tile_end(u, tt);
+      uint4* base = static_cast<uint4*>(p.out) + (static_cast<size_t>(i.q0 + t0) * p.num_heads + i.kvh * G) * U;
+      uint32_t at[4];  // 16-byte units from there (below 128 tokens x 2^20 heads x 16); ~0: past the tile's last token
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int rr = (row & ~3) + y;
+        const int q = rr * p.inv_g >> 16;  // (rows past the tile's last token count as the next one's)
+        at[y] = t0 + q < t_end ? static_cast<uint32_t>(q * p.num_heads + rr - q * G) * U + (row & 3) : ~0u;
+      }
 #pragma unroll 1
-      for (int c = 0; c < HEAD_DIM; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(tO + 256 * u + c, o);
+      for (int c = 0; c < HEAD_DIM; c += 32) {
+        uint32_t o[32];
+        tmem_ld16(tO + 256 * u + c, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+        tmem_ld16(tO + 256 * u + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
         tmem_wait_ld();
-        if (c + 16 == HEAD_DIM) {  // all of O is read
+        if (c + 32 == HEAD_DIM) {  // all of O is read
           tc_fence_before_sync();
           mbar_arrive(&ofree[u]);
         }
+        uint4 unit[4];
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-          o[d] = pack2<T>(__uint_as_float(o[2 * d]) * inv, __uint_as_float(o[2 * d + 1]) * inv);
-        if (fix && on) {  // rare: take the values that are not finite among the keys that entered as 0
-#pragma unroll 1
-          for (int key = i.ta + 1; key <= t; ++key) {
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
-                                                                  i.kvh * HEAD_DIM + c);
+        for (int y = 0; y < 4; ++y) {
+          uint32_t w[4];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              const uint32_t w = __ldg(v + d);
-              const uint32_t m = not_finite<T>(w);
-              if (m & 0xffffu) o[d] = (o[d] & 0xffff0000u) | join_not_finite<T>(o[d] & 0xffffu, w & 0xffffu);
-              if (m >> 16) o[d] = (o[d] & 0xffffu) | join_not_finite<T>(o[d] >> 16, w >> 16) << 16;
-            }
-          }
+          for (int d = 0; d < 4; ++d)
+            w[d] = pack2<T>(__uint_as_float(o[8 * y + 2 * d]) * inv, __uint_as_float(o[8 * y + 2 * d + 1]) * inv);
+          unit[y] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (on) {
-          dst[c / 8] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[c / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        transpose4(unit, row);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (at[y] != ~0u) base[at[y] + c / 8] = unit[y];
+      }
+      if (fix) {  // rare: the row takes the values that are not finite among the keys that entered as 0
+        __syncwarp();
+        const int q = row * p.inv_g >> 16;
+        uint32_t* o = reinterpret_cast<uint32_t*>(base + (static_cast<size_t>(q) * p.num_heads + row - q * G) * U);
+#pragma unroll 1
+        for (int key = t0 + q < t_end ? i.ta + 1 : INT32_MAX; key <= t0 + q; ++key) {
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.value) + (i.q0 + key) * p.v_stride +
+                                                                i.kvh * HEAD_DIM);
+#pragma unroll 1
+          for (int d = 0; d < HEAD_DIM / 2; ++d) {
+            const uint32_t w = __ldg(v + d);
+            const uint32_t m = not_finite<T>(w);
+            if (m == 0) continue;
+            const uint32_t x = o[d];
+            const uint32_t lo = m & 0xffffu ? join_not_finite<T>(x & 0xffffu, w & 0xffffu) : x & 0xffffu;
+            const uint32_t hi = m >> 16 ? join_not_finite<T>(x >> 16, w >> 16) : x >> 16;
+            o[d] = lo | hi << 16;
+          }
         }
       }
     };
@@ -623,96 +644,130 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       if (q_open) wait(&qbar[u], qpar);  // (after a wait ran out)
       tc_fence_before_sync();
     } else if (warp == C::ITEM_WARP) {
-      // ---------------------------------------------- items: one ahead of the loads
-      int asked = 0;
-      bool open = true;  // an answer is on its way
-      bool ok = true;
-      auto next_item = [&](PackedItem& i) -> bool {
-        while (open) {
-          if (!wait(cbar, asked & 1)) {
-            open = ok = false;
-            break;
-          }
-          ++asked;
-          uint3 id;
-          open = cta_given(sm + C::RESP_OFF, id);
-          __syncwarp();  // every lane has read the answer
-          if (!open) break;
-          if (lane == 0) {
-            fence_proxy_async_smem();
-            ask_for_cta(sm + C::RESP_OFF, cbar);
-          }
-          if (find_packed_item<IS_RAGGED>(p, id, i)) return true;
+      // ---------------------------------------------- items, and values that rows must not meet
+      int asked = 0;     // answers that were taken
+      bool open = true;  // one is on its way
+      auto ask = [&]() {
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          ask_for_cta(sm + C::RESP_OFF, cbar);
         }
-        return false;
+        open = true;
       };
       // A weight of 0 times a value that is not finite must not occur.  In blocks that some rows do not see all of,
       // keys past the item's last become zeros; what is not finite in keys that some tokens see and others do
       // not enters as 0, and the rows that see it take it at the end.
       constexpr int U = HEAD_DIM / 8;  // 16-byte units of a row
-      int n0 = 0;          // blocks of the items before
-      uint32_t seen = 0;   // parities of vraw
-      auto make_safe = [&](const PackedItem& i, int k) -> bool {
-        const int nblk = i.blocks(tt), kend = i.kend(tt), ta = i.ta;
+      auto make_safe = [&](uint8_t* stage, int key0, int ta, int kend) -> bool {  // whether something was not finite
+        uint32_t any = 0;
 #pragma unroll 1
-        for (int j = i.first_masked(); j < nblk; ++j) {
-          const int slot = (n0 + j) % VS;
-          if (!wait(&vraw[slot], seen >> slot & 1)) return false;
-          seen ^= 1u << slot;
-          uint32_t any = 0;
-#pragma unroll 1
-          for (int x = max(0, ta + 1 - j * TC_KEYS) & ~31 | lane; x < TC_KEYS; x += 32) {  // a row per lane
-            const int key = j * TC_KEYS + x;
-            if (key <= ta) continue;
-            uint8_t* row = sm + C::V_OFF + slot * C::KBYTES + x * 128;
-            if (key >= kend) {
+        for (int x = (max(0, ta + 1 - key0) & ~31) | lane; x < TC_KEYS; x += 32) {  // a row per lane
+          const int key = key0 + x;
+          if (key <= ta) continue;
+          uint8_t* row = stage + x * 128;
+          if (key >= kend) {
 #pragma unroll
-              for (int y = 0; y < U; ++y)  // (from different units on: no bank conflict)
-                *reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-#pragma unroll 4
-            for (int y = 0; y < U; ++y) {
-              uint4* at = reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16);
-              const uint4 w = *at;
-              const uint4 m = make_uint4(not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w));
-              const uint32_t bad = m.x | m.y | m.z | m.w;
-              if (bad) *at = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
-              any |= bad;
-            }
+            for (int y = 0; y < U; ++y)  // (from different units on: no bank conflict)
+              *reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            continue;
           }
-          if (any) *const_cast<volatile int*>(infos + (k % C::ITEMS) * C::INFO + 5) = 1;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&vfull[slot]);
+#pragma unroll 4
+          for (int y = 0; y < U; ++y) {
+            uint4* at = reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16);
+            const uint4 w = *at;
+            const uint4 m = make_uint4(not_finite<T>(w.x), not_finite<T>(w.y), not_finite<T>(w.z), not_finite<T>(w.w));
+            const uint32_t bad = m.x | m.y | m.z | m.w;
+            if (bad) *at = make_uint4(w.x & ~m.x, w.y & ~m.y, w.z & ~m.z, w.w & ~m.w);
+            any |= bad;
+          }
         }
-        n0 += nblk;
-        return true;
+        return any != 0;
       };
-      int k = 1;
+      // Whichever comes first: a block of V to look through, or an item to find because the loads come to the end of
+      // the last one.  (Found at once it would be taken from CTAs that are free sooner.)
+      int found = 1, begins = 0;    // items published, starts of loads taken
+      int at = 0, n0 = 0;           // the item whose values are next, and the blocks of those before
+      int j = it.first_masked();    // its next block
+      uint32_t seen = 0;            // parities of vraw
+      bool more = true, ok = true;
+      PackedItem now = it;          // item `at`
+      uint64_t idle = 0;            // since when there is nothing to do
 #pragma unroll 1
-      for (;; ++k) {
-        const PackedItem now = it;
-        ok = wait(begun, (k - 1) & 1);
-        const bool more = ok && next_item(it);
-        if (more && lane == 0) {
-          publish(it, k);
-          for (int u = 0; u < it.tiles(tt); ++u)  // Q is loaded late, when its place is free: from L2 then
-            for (int db = 0; db < C::DBOX; ++db)
-              tma_prefetch_3d(&p.tmap_q, db * BOX_DIMS, it.kvh * G, it.q0 + it.ta + u * tt);
+      while (more || at < found) {
+        bool did = false;
+        if (at < found) {
+          const int slot = (n0 + j) % VS;
+          if (__all_sync(kFullMask, mbar_test(&vraw[slot], seen >> slot & 1))) {
+            seen ^= 1u << slot;
+            if (make_safe(sm + C::V_OFF + slot * C::KBYTES, j * TC_KEYS, now.ta, now.kend(tt)))
+              *const_cast<volatile int*>(infos + (at % C::ITEMS) * C::INFO + 5) = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[slot]);
+            if (++j == now.blocks(tt)) {
+              n0 += j;
+              if (++at < found) {
+                now = item(at);
+                j = now.first_masked();
+              }
+            }
+            did = true;
+          }
         }
-        __syncwarp();
-        if (ok) ok = make_safe(now, k - 1);
-        if (!ok || !more) break;
+        if (more && __all_sync(kFullMask, mbar_test(begun, begins & 1))) {
+          ++begins;
+          did = true;
+          if (!open) ask();
+          for (;;) {
+            if (!wait(cbar, asked & 1)) {
+              ok = false;
+              break;
+            }
+            ++asked;
+            uint3 id;
+            more = cta_given(sm + C::RESP_OFF, id);
+            open = false;
+            __syncwarp();  // every lane has read the answer
+            if (!more) {
+              it.s = -1;
+              break;
+            }
+            const bool has = find_packed_item<IS_RAGGED>(p, id, it);
+            if (!has || it.blocks(tt) <= 4) ask();
+            if (has) break;
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            publish(it, found);
+            if (more)
+              for (int u = 0; u < it.tiles(tt); ++u)  // Q is loaded late, when its place is free: from L2 then
+                for (int db = 0; db < C::DBOX; ++db)
+                  tma_prefetch_3d(&p.tmap_q, db * BOX_DIMS, it.kvh * G, it.q0 + it.ta + u * tt);
+          }
+          __syncwarp();
+          if (more && at == found++) {
+            now = it;
+            j = now.first_masked();
+          }
+        }
+        if (did) {
+          idle = 0;
+        } else if (idle == 0) {
+          idle = global_timer_ns();
+        } else if (__any_sync(kFullMask, global_timer_ns() - idle > WAIT_LIMIT_NS)) {
+          ok = false;
+          break;
+        } else {
+          __nanosleep(32);
+        }
       }
-      const int last = ok ? k : k + 1;  // (a wait ran out behind an item that is published)
-      if (!ok && open && wait(cbar, asked & 1)) {  // a wait ran out: NaN in what was asked for
+      if (!ok) {  // a wait ran out: no more items, and NaN in what was asked for
         uint3 id;
-        if (cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it))
+        if (open && wait(cbar, asked & 1) && cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it))
           write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
+        it.s = -1;
+        if (more && lane == 0) publish(it, found);
       }
-      it.s = -1;
-      if (lane == 0) publish(it, last);
     } else {
       // ---------------------------------------------- loads of K and V
       bool go = true;
@@ -720,7 +775,6 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       uint32_t raw = 0, rawpar = 0;  // per stage of V: its last copy reports to vraw; the parity of the next that does
 #pragma unroll 1
       for (int k = 0; go; ++k) {
-        if (lane == 0) mbar_arrive(begun);
         const int nblk = it.blocks(tt);
         const int jm = it.first_masked();
 #pragma unroll 1
@@ -736,6 +790,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
           raw &= ~(1u << vslot);
           if (j >= jm) raw |= 1u << vslot, rawpar ^= 1u << vslot;
           if (lane == 0) {
+            if (j == max(0, nblk - 3)) mbar_arrive(begun);
             uint64_t* vb = j < jm ? &vfull[vslot] : &vraw[vslot];
             mbar_arrive_expect_tx(&kfull[kslot], C::KBYTES);
             for (int db = 0; db < C::DBOX; ++db)
