@@ -222,6 +222,19 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return ((((w & EXP) + ONE) & 0x80008000u) >> 15) * 0xffffu;
 }
 
+// Pair by pair the larger of a >= 0 and |b|, NaN where one is.
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r =
+        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
 // An output element `o` that also takes a value `v` that is not finite (16-bit patterns): v, or NaN where o is
 // not finite and another.
 template <typename T>
@@ -282,15 +295,44 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   const int G = p.group;
   const int tt = p.tile_tokens;
 
+  // What needs no input is set up while the kernel before this one ends.
+  if (warp == C::MMA_WARP && lane == 0) {
+    for (int i = 0; i < KS; ++i) mbar_init(&kfull[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&vfull[i], 1);
+    for (int i = 0; i < VS; ++i) mbar_init(&vraw[i], 1);
+    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], TC_TILES);
+    for (int i = 0; i < TC_TILES; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[2 * i], TC_ROWS);
+      mbar_init(&pfull[2 * i + 1], TC_ROWS);
+      mbar_init(&pvhalf[i], 1);
+      mbar_init(&sfree[i], TC_ROWS);
+      mbar_init(&pvdone[i], 2);
+      mbar_init(&lready[i], TC_ROWS);
+      mbar_init(&ofree[i], C::SIDE);
+      mbar_init(&qbar[i], 1);
+      mbar_init(&drain[i], 1);
+      mbar_init(&turn[i], 1);
+    }
+    for (int i = 0; i < C::ITEMS; ++i) mbar_init(&ifull[i], 1);
+    mbar_init(begun, 1);
+    mbar_init(cbar, 1);
+    fence_mbar_init();
+    tma_prefetch_map(&p.tmap_q);
+    tma_prefetch_map(&p.tmap_k);
+    tma_prefetch_map(&p.tmap_v);
+  }
+  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
   grid_dependency_wait();
+  allow_dependent_launch();
 
   PackedItem it;
-  if (!find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it)) {
-    allow_dependent_launch();
-    return;
-  }
-  if (smem_addr(smem_raw) & 1023u) {  // not as declared
-    write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
+  const bool found_one = find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it);
+  const bool aligned = (smem_addr(smem_raw) & 1023u) == 0;  // (as declared)
+  if (!found_one || !aligned) {
+    if (found_one) write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
+    __syncwarp();
+    if (warp == 0) tmem_dealloc(*tslot, C::TMEM_COLS);
     return;
   }
   auto load_q = [&](const PackedItem& i, int u) {  // one thread
@@ -322,32 +364,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   };
 
   if (warp == C::MMA_WARP && lane == 0) {
-    for (int i = 0; i < KS; ++i) mbar_init(&kfull[i], 1);
-    for (int i = 0; i < VS; ++i) mbar_init(&vfull[i], 1);
-    for (int i = 0; i < VS; ++i) mbar_init(&vraw[i], 1);
-    for (int i = 0; i < C::DONE; ++i) mbar_init(&done[i], TC_TILES);
-    for (int i = 0; i < TC_TILES; ++i) {
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[2 * i], TC_ROWS);
-      mbar_init(&pfull[2 * i + 1], TC_ROWS);
-      mbar_init(&pvhalf[i], 1);
-      mbar_init(&sfree[i], TC_ROWS);
-      mbar_init(&pvdone[i], 2);
-      mbar_init(&lready[i], TC_ROWS);
-      mbar_init(&ofree[i], C::SIDE);
-      mbar_init(&qbar[i], 1);
-      mbar_init(&drain[i], 1);
-      mbar_init(&turn[i], 1);
-    }
-    for (int i = 0; i < C::ITEMS; ++i) mbar_init(&ifull[i], 1);
-    mbar_init(begun, 1);
-    mbar_init(cbar, 1);
-    fence_mbar_init();
     for (int u = 0; u < it.tiles(tt); ++u) load_q(it, u);
     publish(it, 0);
     ask_for_cta(sm + C::RESP_OFF, cbar);
   }
-  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -467,7 +487,6 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     }
     tc_fence_before_sync();
     __syncthreads();
-    allow_dependent_launch();
     return;
   }
 
@@ -671,7 +690,14 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
               *reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             continue;
           }
-#pragma unroll 4
+          uint32_t top = 0;  // the largest magnitudes of the row's pairs, NaN above all: one instruction a pair
+#pragma unroll
+          for (int y = 0; y < U; ++y) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16);
+            top = max_abs<T>(max_abs<T>(max_abs<T>(max_abs<T>(top, w.x), w.y), w.z), w.w);
+          }
+          if (not_finite<T>(top) == 0) continue;
+#pragma unroll 1
           for (int y = 0; y < U; ++y) {
             uint4* at = reinterpret_cast<uint4*>(row + (y >> 3) * C::KATOM + ((y + x) & 7) * 16);
             const uint4 w = *at;
@@ -814,7 +840,6 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       }
     }
     __syncthreads();
-    allow_dependent_launch();
     return;
   }
   // ------------------------------------------------ softmax: warps 4 u .. 4 u + 3 run tile u
@@ -828,6 +853,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   auto token_of = [&](int row) { return row * p.inv_g >> 16; };  // of the tile
   const int own_t = token_of(r);
   const int least_t = token_of(r & ~31);
+  const int most_t = token_of(r | 31);
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = __all_sync(kFullMask, tc_wait(bar, parity));
@@ -949,7 +975,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
         // The exponent's offset moves at the first block and when the row maximum has grown by more than 2^8; O and l
         // then scale by f.  (A row that sees no key here keeps its own: the other is NaN.)
         const float m_new = fmaxf(m_used, rounded_up(e[0] * a));
-        const bool none = m_used == -INFINITY;  // nothing in O yet
+        int none = m_used == -INFINITY;  // nothing in O yet (opaque as below)
+        use_here(none);
         const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
         const float f = need ? ex2(m_used - m_new) : 1.f;
         if (none || need) m_used = m_new;
@@ -994,6 +1021,16 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t* y = x + TC_HALF * h;
+          if (h == 1 && seen + most_t < TC_HALF) {  // nobody of the warp sees a key of the second half
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = 0u;
+            tmem_st16(tP + 32, &y[0]);
+            tmem_st16(tP + 48, &y[0]);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(&pfull[2 * u + 1]);
+            continue;
+          }
           load_half(h);
           if (seen + least_t < TC_HALF * (h + 1) - 1) {  // a key here may lie past some row of the warp
 #pragma unroll
@@ -1056,7 +1093,6 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, C::TMEM_COLS);
-  allow_dependent_launch();
 }
 
 // x as [rows][heads][HEAD_DIM] with rows of `stride` elements: boxes of 64 dims x `box_heads` x `box_rows`, 128-byte
