@@ -146,29 +146,35 @@ struct Totals {
   int rows[CTAS], free[CTAS];
 };
 
-// A thread looks at 32 counts in a row, the CTA at kSpan at a time: one prefix sum places all of their free blocks.
-constexpr int kSpan = kThreads * 32;
+// A thread looks at up to 32 counts in a row: one prefix sum over the CTA places all of their free blocks.  Where the
+// CTA's part [a, b) is short, each looks at fewer.
+struct Span {
+  int width;  // counts per thread
 
-// Bit i: counts[at + i] is 0 (counts from b on are not).  at is a multiple of 32.
-__device__ __forceinline__ uint32_t free_mask(const int32_t* counts, int at, int b) {
-  uint32_t m = 0;
+  __device__ __forceinline__ Span(int a, int b) : width(min(32, (b - a + 4 * kThreads - 1) / (4 * kThreads) * 4)) {}
+  __device__ __forceinline__ int size() const { return max(4, width) * kThreads; }
+  // the thread's first count of the span that begins at t
+  __device__ __forceinline__ int at(int t) const { return t + width * static_cast<int>(threadIdx.x); }
+  // Bit i: the thread's count i is 0 (counts from b on are not).
+  __device__ __forceinline__ uint32_t free_mask(const int32_t* counts, int t, int b) const {
+    const int first = at(t);
+    b = min(b, first + width);
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    int4 c = make_int4(1, 1, 1, 1);
-    if (at + i + 4 <= b) {
-      c = *reinterpret_cast<const int4*>(counts + at + i);
-    } else {
-      if (at + i < b) c.x = counts[at + i];
-      if (at + i + 1 < b) c.y = counts[at + i + 1];
-      if (at + i + 2 < b) c.z = counts[at + i + 2];
+    for (int i = 0; i < 32; i += 4) {
+      int4 c = make_int4(1, 1, 1, 1);
+      if (first + i + 4 <= b) {
+        c = *reinterpret_cast<const int4*>(counts + first + i);
+      } else {
+        if (first + i < b) c.x = counts[first + i];
+        if (first + i + 1 < b) c.y = counts[first + i + 1];
+        if (first + i + 2 < b) c.z = counts[first + i + 2];
+      }
+      m |= ((c.x == 0) | (c.y == 0) << 1 | (c.z == 0) << 2 | static_cast<uint32_t>(c.w == 0) << 3) << i;
     }
-    m |= ((c.x == 0) | (c.y == 0) << 1 | (c.z == 0) << 2 | static_cast<uint32_t>(c.w == 0) << 3) << i;
+    return m;
   }
-  return m;
-}
-
-// The place of a thread's first count of the span that begins at `at`.
-__device__ __forceinline__ int count_at(int at) { return min(at, INT32_MAX - kSpan) + 32 * static_cast<int>(threadIdx.x); }
+};
 
 // The part of [0, n) that CTA `rank` of `ctas` scans: whole groups of 32.
 __device__ __forceinline__ void part_of(int n, int rank, int ctas, int& a, int& b) {
@@ -204,10 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   // the free blocks of the CTA's part of the pool (read first: these loads wait for nothing)
   int a, b;
   part_of(p.num_blocks, rank, CTAS, a, b);
+  const Span span(a, b);
   uint32_t mask = 0;  // of the last span
   int found = 0;
-  for (int at = a; at < b; at += kSpan) {
-    mask = free_mask(p.ref_counts, count_at(at), b);
+  for (int t = a; t < b; t += span.size()) {
+    mask = span.free_mask(p.ref_counts, t, b);
     found += __popc(mask);
   }
 
@@ -271,15 +278,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
   // the list of those that can be handed out
   const int most = min(all_rows, all_free);
-  if (b - a <= kSpan) {  // (the usual pool: the counts were read once)
+  if (b - a <= span.size()) {  // (the usual pool: the counts were read once)
     for (int k = free_before + free_here; mask != 0 && k < most; ++k, mask &= mask - 1)
-      list[k] = count_at(a) + __ffs(static_cast<int>(mask)) - 1;
+      list[k] = span.at(a) + __ffs(static_cast<int>(mask)) - 1;
   } else {
-    for (int t = a, before_span = free_before; t < b && before_span < most; t += kSpan) {
-      mask = free_mask(p.ref_counts, count_at(t), b);
+    for (int t = a, before_span = free_before; t < b && before_span < most; t += span.size()) {
+      mask = span.free_mask(p.ref_counts, t, b);
       int total;
       int k = before_span + cta_scan(__popc(mask), cap, buf, total);
-      for (; mask != 0 && k < most; ++k, mask &= mask - 1) list[k] = count_at(t) + __ffs(static_cast<int>(mask)) - 1;
+      for (; mask != 0 && k < most; ++k, mask &= mask - 1) list[k] = span.at(t) + __ffs(static_cast<int>(mask)) - 1;
       before_span += total;
     }
   }
@@ -399,10 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
   part_of(p.num_blocks, rank, CTAS, a, b);
   if (tid == 0) high = 0;
   if constexpr (CTAS > 1) cluster.sync();  // every CTA's shared memory is there
+  const Span span(a, b);
   uint32_t mask = 0;  // of the last span
   int found = 0;
-  for (int at = a; at < b; at += kSpan) {
-    mask = free_mask(p.ref_counts, count_at(at), b);
+  for (int t = a; t < b; t += span.size()) {
+    mask = span.free_mask(p.ref_counts, t, b);
     found += __popc(mask);
   }
   int free_total;
@@ -421,12 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
   // of those from the top goes to the i-th of these from the bottom.
   const int used = p.num_blocks - all_free;
   int above = 0;
-  for (int t = a, before_span = free_before; t < b; t += kSpan) {
-    const int at = count_at(t);
-    if (b - a > kSpan) mask = free_mask(p.ref_counts, at, b);
+  for (int t = a, before_span = free_before; t < b; t += span.size()) {
+    const int at = span.at(t);
+    const int end = min(b, at + span.width);
+    if (b - a > span.size()) mask = span.free_mask(p.ref_counts, t, b);
     int total;
     const int k0 = before_span + cta_scan(__popc(mask), cap, buf, total);  // free blocks below the thread's
-    const uint32_t in = b - at >= 32 ? ~0u : b > at ? (1u << (b - at)) - 1u : 0u;
+    const uint32_t in = end - at >= 32 ? ~0u : end > at ? (1u << (end - at)) - 1u : 0u;
     const uint32_t low = used - at >= 32 ? ~0u : used > at ? (1u << (used - at)) - 1u : 0u;  // those below `used`
     int k = k0;
     for (uint32_t m = mask & low; m != 0 && k < p.max_moves; m &= m - 1, ++k)
