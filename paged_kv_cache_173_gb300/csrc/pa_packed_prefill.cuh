@@ -89,6 +89,9 @@ struct PpCfg {
   static constexpr int ITEMS = 8;
   static_assert(VSTAGES + 3 <= ITEMS, "the ring of items");
   static constexpr int INFO = 8;  // words of an item
+  // An item of more blocks asks for its successor near its end: an item that is taken waits for the CTA that took it,
+  // while others are free (one prompt of 2048 tokens, two items a CTA: 43 us asked for at once).
+  static constexpr int ASK_AT_ONCE = 4;
   static constexpr int SUM_OFF = INFO_OFF + ITEMS * INFO * 4;  // [tile][row] sum of the weights
   static constexpr int RESP_OFF = SUM_OFF + TC_TILES * TC_ROWS * 4;
   static constexpr int BAR_OFF = RESP_OFF + 16;
@@ -366,7 +369,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   if (warp == C::MMA_WARP && lane == 0) {
     for (int u = 0; u < it.tiles(tt); ++u) load_q(it, u);
     publish(it, 0);
-    ask_for_cta(sm + C::RESP_OFF, cbar);
+    if (it.blocks(tt) <= C::ASK_AT_ONCE) ask_for_cta(sm + C::RESP_OFF, cbar);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -664,8 +667,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       tc_fence_before_sync();
     } else if (warp == C::ITEM_WARP) {
       // ---------------------------------------------- items, and values that rows must not meet
-      int asked = 0;     // answers that were taken
-      bool open = true;  // one is on its way
+      int asked = 0;                                 // answers that were taken
+      bool open = it.blocks(tt) <= C::ASK_AT_ONCE;  // one is on its way
       auto ask = [&]() {
         if (lane == 0) {
           fence_proxy_async_smem();
@@ -759,7 +762,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
               break;
             }
             const bool has = find_packed_item<IS_RAGGED>(p, id, it);
-            if (!has || it.blocks(tt) <= 4) ask();
+            if (!has || it.blocks(tt) <= C::ASK_AT_ONCE) ask();
             if (has) break;
           }
           if (!ok) break;
