@@ -827,7 +827,8 @@ size_t pa_sequence_workspace_bytes(int num_blocks);
  *
  *   query_start_loc  [num_seqs + 1] int32, as for pa_prefill
  *   slot_mapping     [num_tokens] int64, written: slot of each new token; -1 for tokens of
- *                    sequences that were refused and from query_start_loc[num_seqs] on
+ *                    sequences that were refused and for those before query_start_loc[0]
+ *                    or from query_start_loc[num_seqs] on
  *   block_copies     [num_seqs][2] int64, written: (source, destination) of the block to
  *                    copy, or (-1, -1); as pa_copy_blocks and pa_copy_layer_blocks take it.
  *                    Copy before the new tokens are written.
@@ -835,6 +836,7 @@ size_t pa_sequence_workspace_bytes(int num_blocks);
  *                    number of sequences that were refused
  *   workspace        device buffer of workspace_bytes >= pa_sequence_workspace_bytes(
  *                    num_blocks), 16-byte aligned; scratch, contents on entry ignored
+ *                    (calls that may run at the same time have one each)
  *
  * Refused, and left as they were, are: the first sequence whose blocks are not there and
  * every later one that needs a block; a sequence that would outgrow its table; one whose
@@ -879,7 +881,8 @@ int pa_fork_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* co
  *
  * Move i takes the i-th used block from the top (count != 0) to the i-th free block from the
  * bottom, as long as that lies below it.  After all such moves the used blocks are the
- * first ones and the rest of the pool is free.
+ * first ones and the rest of the pool is free.  A block that a program keeps for itself
+ * moves like the others: moves says where to.
  *
  *   moves       [max_moves][2] int64, written: (source, destination), then (-1, -1); as
  *               pa_copy_layer_blocks takes it.  Copy before the sources' blocks are handed
@@ -888,7 +891,8 @@ int pa_fork_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* co
  *   tables_out  [num_seqs][max_blocks_per_seq] int32 and
  *   counts_out  [num_blocks] int32 (16-byte aligned), written: what block_tables and
  *               ref_counts are after the moves.  Each may be the input itself, otherwise they do
- *               not overlap it.  Entries past a context are copied as they are.
+ *               not overlap it.  Entries past a context are copied as they are; a length past the
+ *               table's capacity counts as all of the table.
  *   workspace   as pa_extend_sequences
  */
 int pa_compact_blocks(int64_t* moves, int max_moves, int32_t* num_moves, const int32_t* block_tables,

@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     p.slot_mapping[t] = slot;
   }
-  const int end = max(0, __ldg(p.query_start_loc + p.num_seqs));
+  const int begin = min(p.num_tokens, __ldg(p.query_start_loc)), end = max(0, __ldg(p.query_start_loc + p.num_seqs));
+  for (int t = rank * kThreads + tid; t < begin; t += CTAS * kThreads) p.slot_mapping[t] = -1;
   for (int t = end + rank * kThreads + tid; t < p.num_tokens; t += CTAS * kThreads) p.slot_mapping[t] = -1;
 }
 
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(256) rewrite_kernel(const __grid_constant__ Re
   const size_t at = static_cast<size_t>(s) * p.max_blocks_per_seq + i;
   int id = p.block_tables[at];
   const int used = __ldg(p.space);
-  if (len > 0 && i < blocks_of(len, p.log2_b) && id >= used && id < p.num_blocks) {
+  if (len > 0 && i <= (len - 1) >> p.log2_b && id >= used && id < p.num_blocks) {
     const int m = __ldg(p.space + 4 + id);
     // (a table that names a block which nobody holds: its place in the workspace is not of this call)
     if (static_cast<unsigned>(m) < static_cast<unsigned>(__ldg(p.space + 1)) && p.moves[2 * static_cast<size_t>(m)] == id)

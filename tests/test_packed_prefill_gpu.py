@@ -67,10 +67,13 @@ class Prompts:
         return self
 
     def reference(self):
-        """(out, tolerance) of every row, NaN where none is computed."""
+        """(out, tolerance) of every row, NaN where none is computed.  Keys of -inf weigh nothing, nor do they count
+        in the scores' sums (their scores are -inf, without an error)."""
         q, k, v = to_np(self.q), to_np(self.k), to_np(self.v)
         with np.errstate(all="ignore"):
             out, A, S = so.attention(q, k, v, self.starts, self.scale, self.max_len)
+            if np.isneginf(k).any():
+                S = so.attention(q, np.where(np.isneginf(k), 0, k), v, self.starts, self.scale, self.max_len)[2]
             n, top = max(self.lens, default=1), np.abs(np.where(np.isfinite(v), v, 0)).max(initial=0)
             sums = 2.0 ** -22 + (n / 8 + 16) * 2.0 ** -24
             tiny = n * 2.0 ** -32 * top + 2.0 ** -25 if self.dtype == F16 else 2.0 ** -100
@@ -175,6 +178,55 @@ def test_peaked_and_flat_weights(dtype):
     p.k[:] = (torch.arange(300)[:, None, None] * 0.2).to(dtype)
     p.q.fill_(1.0)
     p.start().run().check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("step", [0.02, 0.2, 1.0])
+@pytest.mark.parametrize("first", [0, 31, 40, 64, 65, 100, 127, 128, 150, 192, 257])
+def test_a_maximum_that_grows(first, step, d, dtype):
+    """Equal scores up to a key, from there each one larger than the one before; in q's second head falling ones."""
+    p = Prompts([400], 2, 1, d, dtype, first)
+    p.k[:] = ((torch.arange(400) - first).clamp(min=0)[:, None, None] * step).to(dtype)
+    p.q.fill_(1.0)
+    p.q[:, 1] = -1.0
+    p.start().run().check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [0, 5, 63, 64, 100, 127, 128, 200, 256, 383])
+@pytest.mark.parametrize("top", [3.0, 30.0])
+def test_one_large_score(top, at, d, dtype):
+    """One key far above all others: by less and by more than the offset of the block before allows for."""
+    p = Prompts([400], 2, 1, d, dtype, at)
+    p.k *= 0.1
+    p.q.fill_(1.0)
+    p.k[at] = top
+    p.start().run().check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("a,b", [(0, 1), (0, 64), (0, 128), (0, 129), (0, 200), (0, 300), (64, 128), (100, 300), (128, 256), (3, 399)])
+def test_keys_of_minus_infinity(a, b, d, dtype):
+    """Scores of -inf weigh nothing; a row that sees only such keys has no answer."""
+    p = Prompts([400], 2, 1, d, dtype, a + b)
+    p.q = p.q.abs() + 0.01
+    p.k[a:b] = -float("inf")
+    p.start().run()
+    torch.cuda.synchronize()
+    got = to_np(p.out)
+    want, tol = p.reference()
+    empty = np.isnan(want).any(axis=(1, 2))
+    assert empty[:b].all() and not empty[b:].any() if a == 0 else not empty.any()
+    assert np.isnan(got[empty]).all()
+    err = np.abs(got - want)[~empty]
+    assert np.isfinite(got[~empty]).all() and (err <= tol[~empty]).all(), np.argwhere(~(err <= tol[~empty]))[:4].tolist()
+
+
+def test_many_sequences_beside_a_long_one():
+    Prompts([1] * 600 + [1100] + [3] * 600, 4, 2, 64, F16, 30).start().run().check()
 
 
 def test_large_and_tiny_values():

@@ -166,6 +166,105 @@ def test_a_shared_last_block_is_copied_once_for_each_that_grows():
     assert copies[0].tolist() == [-1, -1]
 
 
+@pytest.mark.parametrize("S,N,T", [(1024, 16384, 4096), (1024, 16384, 4097), (1024, 16385, 4096), (1025, 16384, 4096),
+                                   (1, 16384, 4097), (1023, 16383, 4095), (1024, 262144, 4096), (1024, 262145 + 31, 4097)])
+def test_sizes_on_both_sides_of_every_choice(S, N, T):
+    s = Server(S, 300, N, 16, seed=T)
+    new = np.full(S, T // S)
+    new[S // 2] += T - new.sum()
+    s.extend(new, spare=0)
+    s.truncate(np.where(s.rng.random(S) < 0.5, s.rng.integers(0, 3, S), -1))
+    s.fork(np.where(s.rng.random(S) < 0.5, s.rng.integers(0, S, S), -1))
+    counts = s.host[2].copy()
+    counts[s.rng.permutation(N)[:N // 2]] += 1  # blocks that somebody else holds
+    s.set(s.host[0], s.host[1], counts)
+    s.compact(N // 3)
+    s.extend(new, spare=0)
+    s.compact(N + 1, False)
+
+
+def test_compaction_with_one_result_in_place():
+    for tables_in, counts_in in ((True, False), (False, True)):
+        s = Server(6, 5, 40, 16, seed=9)
+        s.extend(np.array([50, 20, 80, 3, 16, 17]))
+        s.truncate([0, -1, 20, -1, 0, -1])
+        moves, num = torch.zeros((9, 2), dtype=torch.int64, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        to = s.tables if tables_in else torch.full_like(s.tables, 77)
+        co = s.counts if counts_in else torch.full_like(s.counts, 77)
+        api.pa_compact_blocks(moves, num, s.tables, s.lens, s.counts, to, co, 16, s.ws)
+        want, n, tables, counts = so.compact(*s.host, 9, 16)
+        s.tables, s.counts, s.host = to, co, (tables, s.host[1], counts)
+        s.same()
+        assert n > 0 and int(num) == n and np.array_equal(moves.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 16, 49, -2 ** 31])
+def test_a_length_past_the_table_in_a_compaction(length):
+    s = Server(2, 3, 20, 16)
+    s.extend(np.array([48, 48]))
+    lens = s.host[1].copy()
+    lens[1] = length
+    counts = s.host[2].copy()
+    counts[:2] = 0
+    s.set(s.host[0], lens, counts)
+    s.compact(20)
+
+
+def test_two_graphs_in_turn_on_one_workspace():
+    B, S, N = 16, 30, 20000
+    servers = [Server(S, 20, N, B, seed=x) for x in (10, 11)]
+    ws = servers[0].ws
+    starts = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    outs, graphs = [], []
+    for s in servers:
+        o = (torch.zeros(200, dtype=torch.int64, device="cuda"), torch.zeros((S, 2), dtype=torch.int64, device="cuda"),
+             torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros((40, 2), dtype=torch.int64, device="cuda"),
+             torch.zeros(1, dtype=torch.int32, device="cuda"))
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            api.pa_compact_blocks(o[3], o[4], s.tables, s.lens, s.counts, s.tables, s.counts, B, ws)
+            api.pa_extend_sequences(s.tables, s.lens, s.counts, starts, *o[:3], B, ws)
+        outs.append(o)
+        graphs.append(graph)
+    for i in range(6):
+        begin = np.concatenate([[0], np.cumsum(servers[0].rng.integers(0, 7, S))]).astype(np.int32)
+        starts.copy_(torch.from_numpy(begin))
+        order = (0, 1) if i % 2 else (1, 0)
+        for x in order:
+            graphs[x].replay()
+        for x in order:
+            s, o = servers[x], outs[x]
+            moves, _, tables, counts = so.compact(*s.host, 40, B)
+            s.host = (tables, s.host[1], counts)
+            *s.host, slots, copies, left = so.extend(*s.host, begin, 200, B)
+            s.same()
+            for got, want in zip(o, (slots, copies, left, moves)):
+                assert np.array_equal(got.cpu().numpy(), want)
+            cut = np.where(s.rng.random(S) < 0.3, 0, -1)
+            s.truncate(cut)
+
+
+def test_the_short_way_takes_the_calls():
+    from paged_kv_cache_173_gb300 import _lib
+    s = Server(4, 3, 20, 16)
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = lambda *n: torch.zeros(n, dtype=torch.int64, device="cuda")  # noqa: E731
+    at = (torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream)
+    fast, state = _lib.fast(), (s.tables, s.lens, s.counts)
+    assert fast.extend(*state, i32(5), i64(3), i64(4, 2), i32(2), 16, s.ws, *at) is True
+    assert fast.truncate(*state, i32(4), 16, *at) is True and fast.fork(*state, i32(4) - 1, 16, *at) is True
+    assert fast.compact(i64(4, 2), i32(1), *state, s.tables, s.counts, 16, s.ws, *at) is True
+    pools = torch.zeros((2, 20, 16, 2, 64), dtype=torch.float16, device="cuda")
+    assert fast.copy_layers(pools, i64(3, 2), *at) is True
+    q, kv = torch.zeros((5, 4, 64), device="cuda").half(), torch.zeros((5, 2, 64), device="cuda").half()
+    starts = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    for cache in ((None, None, None), (pools[0], pools[1], i64(5))):
+        assert fast.packed(torch.empty_like(q), q, kv, kv, starts, 5, 0.1, *cache, *at) is True
+    torch.cuda.synchronize()
+    s.same()
+
+
 def test_forks_that_are_left_alone():
     s = Server(6, 3, 20, 16)
     s.extend(np.array([20, 0, 30, 0, 0, 0]))
@@ -202,8 +301,7 @@ def test_starts_that_cannot_be_refuse_their_sequences_only(starts):
     s.same()
     assert np.array_equal(copies.cpu().numpy(), want_copies) and np.array_equal(left.cpu().numpy(), want_left)
     if (np.diff(starts) >= 0).all():
-        got = slots.cpu().numpy()
-        assert np.array_equal(got[max(0, starts[0]):], want_slots[max(0, starts[0]):])
+        assert np.array_equal(slots.cpu().numpy(), want_slots)
 
 
 def test_no_sequences_and_no_tokens():
