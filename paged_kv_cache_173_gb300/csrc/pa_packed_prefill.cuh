@@ -12,9 +12,9 @@
 // at a time).
 //
 // The bound is the tensor cores: 4 x 128 x 128 x d multiply-adds per pair and 128 keys, 2062
-// cycles at d = 128; at d = 64 the exponentials of the softmax (its 256 x 128 scores alone take
-// 1530 cycles of the four schedulers).  Long prompts take 2700 and 2500 cycles.  What stands
-// against the rest:
+// cycles at d = 128; at d = 64 the softmax, whose 256 x 128 scores take the four schedulers
+// 1530 cycles (1024 of them the exponentials).  Long prompts take 2700 and 2500 cycles.  What
+// stands against the rest:
 //  - A tile's chain (scores, weights, P V, next scores) is longer than its MMAs.  Two tiles
 //    alternate; the weights leave in halves; the offset of the exponent is taken from the block
 //    before, and the weights' own sum says whether it holds, so that no maximum is looked for
