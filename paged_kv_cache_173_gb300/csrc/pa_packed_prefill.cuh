@@ -177,44 +177,93 @@ __device__ __forceinline__ int pairs_of(const PackedParams& p, int i) {
   return n <= 0 ? 0 : static_cast<int>(__umul64hi(static_cast<uint64_t>(n - 1), p.pair_magic)) + 1;
 }
 
+// What a warp's last search of the list found: the pair, C of it, and the length of the list (-1: no search yet).
+struct ListPlace {
+  int pair = 0, c = 0, total = -1;
+};
+
 // Place `at` of the list of all sequences' pairs, the pairs of highest number first and those of
 // one number in the sequences' order: (pair, sequence), or false past the last.  The whole warp
-// searches; C(x), the pairs numbered above x, is the sum over the sequences of max(0, pairs - 1 - x).
-__device__ __forceinline__ bool listed_pair(const PackedParams& p, int at, int& pair, int& s) {
+// searches; C(x), the pairs numbered above x, is the sum over the sequences of max(0, pairs - 1 - x),
+// and the pair the least x with C(x) <= at (-1: past the last).  The place found before narrows the search:
+// among prompts of one pair nothing is left of it.  A pass over the sequences takes four values of x, and a lane
+// has four of the sequences on their way.  (One value and one sequence at a time, from scratch: a prompt of 1024
+// beside 1000 of one token 659 us, now 155; one of 8192 beside 255 of one 238, now 179.)
+__device__ __forceinline__ bool listed_pair(const PackedParams& p, int at, int& pair, int& s, ListPlace& known) {
+  constexpr int X = 4, SEQS = 4;
   const int lane = threadIdx.x & 31;
-  auto above = [&](int x) {
-    int n = 0;
-    for (int i = lane; i < p.num_seqs; i += 32) n += max(0, pairs_of(p, i) - 1 - x);
-    return __reduce_add_sync(kFullMask, n);
-  };
-  if (at >= above(-1)) return false;
-  int lo = 0, hi = p.pairs - 1;  // the least x with C(x) <= at
+  int lo = -1, hi = p.pairs - 1;  // the least x is in [lo, hi]
+  int c_hi = 0;                   // C(hi)
+  if (known.total >= 0) {
+    if (at >= known.total) return false;
+    lo = 0;
+    if (at >= known.c) hi = known.pair, c_hi = known.c;
+    else lo = known.pair + 1;
+  }
+#pragma unroll 1
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (above(mid) <= at) hi = mid;
-    else lo = mid + 1;
-  }
-  int rank = at - above(lo);
-  for (int i = 0; i < p.num_seqs; i += 32) {
-    const unsigned has = __ballot_sync(kFullMask, pairs_of(p, i + lane) > lo);
-    const int n = __popc(has);
-    if (rank < n) {
-      pair = lo;
-      s = i + static_cast<int>(__fns(has, 0, rank + 1));
-      return true;
+    int n[X];
+#pragma unroll
+    for (int k = 0; k < X; ++k) n[k] = 0;
+    const int wide = hi - lo;
+#pragma unroll 1
+    for (int i = lane; i < p.num_seqs; i += 32 * SEQS) {
+      int m[SEQS];
+#pragma unroll
+      for (int y = 0; y < SEQS; ++y) m[y] = pairs_of(p, i + 32 * y) - 1 - lo;
+#pragma unroll
+      for (int k = 0; k < X; ++k)
+#pragma unroll
+        for (int y = 0; y < SEQS; ++y) n[k] += max(0, m[y] - wide * k / X);
     }
-    rank -= n;
+    int from = lo, to = hi;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < X; ++k) {
+      const int x = lo + wide * k / X;
+      const int c = __reduce_add_sync(kFullMask, n[k]);
+      if (k == 0 && lo < 0) known.total = c;
+      if (!found) {
+        if (c <= at) {
+          found = true;
+          to = x;
+          c_hi = c;
+        } else {
+          from = x + 1;
+        }
+      }
+    }
+    lo = from;
+    hi = to;
   }
-  return false;
+  if (hi < 0) return false;
+  known.pair = pair = hi;
+  known.c = c_hi;
+  s = -1;
+  int rank = at - c_hi;
+#pragma unroll 1
+  for (int i = 0; i < p.num_seqs; i += 32 * SEQS) {
+    unsigned has[SEQS];
+#pragma unroll
+    for (int y = 0; y < SEQS; ++y) has[y] = __ballot_sync(kFullMask, pairs_of(p, i + 32 * y + lane) > hi);
+#pragma unroll
+    for (int y = 0; y < SEQS; ++y) {
+      const int n = __popc(has[y]);
+      if (rank >= 0 && rank < n) s = i + 32 * y + static_cast<int>(__fns(has[y], 0, rank + 1));
+      rank -= n;
+    }
+    if (rank < 0) break;
+  }
+  return s >= 0;
 }
 
 // The item of a grid index, by whole warps; false: nothing to do.
 template <bool IS_RAGGED>
-__device__ __forceinline__ bool find_packed_item(const PackedParams& p, uint3 id, PackedItem& it) {
+__device__ __forceinline__ bool find_packed_item(const PackedParams& p, uint3 id, PackedItem& it, ListPlace& known) {
   int pair;
   if constexpr (IS_RAGGED) {
     it.kvh = id.x % p.num_kv_heads;
-    if (!listed_pair(p, id.x / p.num_kv_heads, pair, it.s)) return false;
+    if (!listed_pair(p, id.x / p.num_kv_heads, pair, it.s, known)) return false;
   } else {
     const bool lf = p.longest_first;
     pair = p.pairs - 1 - static_cast<int>(lf ? id.z : id.x);  // the longest pairs start first
@@ -356,7 +405,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   allow_dependent_launch();
 
   PackedItem it;
-  const bool found_one = find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it);
+  ListPlace known;
+  const bool found_one = find_packed_item<IS_RAGGED>(p, make_uint3(blockIdx.x, blockIdx.y, blockIdx.z), it, known);
   const bool aligned = (smem_addr(smem_raw) & 1023u) == 0;  // (as declared)
   if (!found_one || !aligned) {
     if (found_one) write_nan_rows<T, HEAD_DIM>(p, it, threadIdx.x, C::THREADS);
@@ -787,7 +837,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
               it.s = -1;
               break;
             }
-            const bool has = find_packed_item<IS_RAGGED>(p, id, it);
+            const bool has = find_packed_item<IS_RAGGED>(p, id, it, known);
             if (!has || it.blocks(tt) <= C::ASK_AT_ONCE) ask();
             if (has) break;
           }
@@ -818,7 +868,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       }
       if (!ok) {  // a wait ran out: no more items, and NaN in what was asked for
         uint3 id;
-        if (open && wait(cbar, asked & 1) && cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it))
+        if (open && wait(cbar, asked & 1) && cta_given(sm + C::RESP_OFF, id) && find_packed_item<IS_RAGGED>(p, id, it, known))
           write_nan_rows<T, HEAD_DIM>(p, it, lane, 32);
         it.s = -1;
         if (more && lane == 0) publish(it, found);
@@ -1177,12 +1227,15 @@ cudaError_t launch_packed_prefill_t(const PackedPrefillArgs& a, cudaStream_t str
   p.scale_log2 = a.scale * 1.4426950408889634f;
   // a factor of 0 would turn a masked score (an infinity) into NaN; 2^-149 makes 0 of every score
   if (p.scale_log2 == 0.f) p.scale_log2 = 1.401298464324817e-45f;
-  // A grid over (sequence, pair) is mostly empty where one sequence is long and the others are short, and an
-  // empty CTA takes a quarter of a microsecond of an SM: the list of all pairs is searched instead where
-  // the grid would be more than twice its length (see pa_block_prefill.cuh, which measured both).
+  // A grid over (sequence, pair) is mostly empty where one sequence is long and the others are short, and an empty
+  // CTA takes half a microsecond of an SM: the list of all pairs is searched instead where the grid is much longer.
+  // A search takes 2.6 us per 1000 sequences, so the more of them, the longer.  Measured, list against grid, one
+  // prompt beside others: 2048, 63 of one token (ratio 22) 30 against 59 us; 8192, 2000 of 20 (96) 653 against
+  // 3366; 1024, 4000 of one (16; here the grid) 1479 against 1432; 2000, 4000 of 100 (12; the grid) 7400 against 3266.
   const int64_t listed = a.num_rows / pair_tokens + static_cast<int64_t>(a.num_seqs);
   const int64_t boxed = static_cast<int64_t>(p.pairs) * a.num_seqs;
-  const bool ragged = boxed > 2 * listed && a.num_seqs <= 1024 && listed * a.num_kv_heads <= INT32_MAX;
+  const int64_t ratio = a.num_seqs > 256 ? a.num_seqs / 128 : 2;
+  const bool ragged = boxed > ratio * listed && listed * a.num_kv_heads <= INT32_MAX;
   p.longest_first = p.pairs <= 65535;
   cudaLaunchConfig_t cfg = {};
   if (ragged) {

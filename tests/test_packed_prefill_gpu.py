@@ -225,8 +225,23 @@ def test_keys_of_minus_infinity(a, b, d, dtype):
     assert np.isfinite(got[~empty]).all() and (err <= tol[~empty]).all(), np.argwhere(~(err <= tol[~empty]))[:4].tolist()
 
 
-def test_many_sequences_beside_a_long_one():
-    Prompts([1] * 600 + [1100] + [3] * 600, 4, 2, 64, F16, 30).start().run().check()
+@pytest.mark.parametrize("lens", [[1] * 600 + [1100] + [3] * 600, [1] * 3000 + [900], [2] * 1500 + [2600], [40] * 127 + [0] * 130 + [2000],
+                                  [1, 200] * 130 + [3000, 2900], list(range(300)), list(range(300, 0, -1)) + [2000]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_sequences_beside_long_ones(lens, d):
+    Prompts(lens, 4, 2, d, F16, 30).start().run().check()
+
+
+def test_a_list_of_sequences_in_no_order_stays_inside():
+    rng = np.random.default_rng(31)
+    for top in (3000, 100):
+        p = Prompts([3000], 4, 2, 64, BF16, 31).start()
+        p.dst = torch.from_numpy(rng.integers(-100, top + 100, 201).astype(np.int32)).cuda()
+        guard = p.kc.clone()
+        p.dsl.fill_(-1)
+        p.run()
+        torch.cuda.synchronize()
+        assert torch.equal(p.kc, guard)
 
 
 def test_large_and_tiny_values():
