@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   }
 
   // the tokens' slots: in the last block, or in those that were handed out
-  const int t0 = n > 0 ? max(0, starts[0]) : 0;
+  // (starts are held to [0, num_tokens]: one near 2^31 plus a thread's number would be negative)
+  const int t0 = n > 0 ? min(p.num_tokens, max(0, starts[0])) : 0;
   const int t1 = n > 0 ? min(p.num_tokens, starts[n]) : 0;
   for (int t = t0 + tid; t < t1; t += kThreads) {
     int lo = 0, hi = n - 1;
@@ -383,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     p.slot_mapping[t] = slot;
   }
-  const int begin = min(p.num_tokens, __ldg(p.query_start_loc)), end = max(0, __ldg(p.query_start_loc + p.num_seqs));
+  const int begin = min(p.num_tokens, __ldg(p.query_start_loc));
+  const int end = min(p.num_tokens, max(0, __ldg(p.query_start_loc + p.num_seqs)));
   for (int t = rank * kThreads + tid; t < begin; t += CTAS * kThreads) p.slot_mapping[t] = -1;
   for (int t = end + rank * kThreads + tid; t < p.num_tokens; t += CTAS * kThreads) p.slot_mapping[t] = -1;
 }

@@ -467,3 +467,28 @@ def test_binding_refuses_what_it_cannot_take():
     with pytest.raises(api.PagedAttnError):  # layers that overlap
         api.pa_copy_layer_blocks(torch.zeros(100, device="cuda").as_strided((2, 4, 8), (16, 8, 1)), i64(1, 2))
     s.same()
+
+
+TOP = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("S", [4, 20, 1500])  # the last: several CTAs
+@pytest.mark.parametrize("starts", [[TOP] * 5, [TOP - 1023] * 4 + [TOP], [0, 5, TOP - 1, TOP, TOP], [-2 ** 31, TOP - 7, TOP, TOP, TOP],
+                                    [-2 ** 31] * 5, [0, 3, 3, 7, TOP], [TOP, 0, 4, 4, 9]])
+def test_starts_near_the_ends_of_32_bits(starts, S):
+    """Slots are written for the tokens there are, whatever the starts say; the first and the last sequences of
+    the batch (and of every CTA) take the bad ones."""
+    T = 12
+    front = np.asarray(starts, np.int64)
+    starts = np.concatenate([front[:3], np.full(S - 4, front[2]), front[3:]])
+    s = Server(S, 3, 20, 16)
+    room = torch.full((T + 128,), 77, dtype=torch.int64, device="cuda")
+    slots = room[64:64 + T]
+    copies, left = torch.empty((S, 2), dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    api.pa_extend_sequences(s.tables, s.lens, s.counts, dev(starts.astype(np.int32)), slots, copies, left, 16, s.ws)
+    *s.host, want_slots, want_copies, want_left = so.extend(*s.host, starts, T, 16)
+    s.same()
+    assert np.array_equal(copies.cpu().numpy(), want_copies) and left.tolist()[0] == want_left[0]
+    if (np.diff(starts) >= 0).all():
+        assert np.array_equal(slots.cpu().numpy(), want_slots)
+    assert bool((room[:64] == 77).all()) and bool((room[64 + T:] == 77).all())
