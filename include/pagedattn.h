@@ -766,10 +766,10 @@ int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* 
  *                     bit-exact copies
  *   head_dim          64 or 128; num_heads / num_kv_heads <= 16, any whole number
  *
- * Scores, softmax and accumulation are float32.  The weights enter P.V rounded to the
- * values' type, each off by half a step of its own at most, and are summed unrounded:
- * fp16 11 bits (the largest weight is 2^7 to 2^15, so one below 2^-21 of it is off by
- * 2^-32 of it), bf16 8 bits.
+ * Scores, softmax and accumulation are float32, for scores of any size that float32
+ * holds.  The weights enter P.V rounded to the values' type, each off by half a step of
+ * its own at most, and are summed unrounded: fp16 11 bits (the largest weight is 2^7, less
+ * 1% at most, to 2^15, so one below 2^-21 of it is off by 2^-32 of it), bf16 8 bits.
  *
  * Device-value outcomes: rows of a sequence that ends before it starts are left as they
  * were; a start or end outside [0, num_rows] counts as the nearest of the two.  What is not

@@ -129,8 +129,9 @@ struct PpCfg {
   static constexpr int SMEM_BYTES = LAYOUT_BYTES;
   static_assert(SMEM_BYTES <= SMEM_MAX, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
-  // A tile's 256 columns: S 128, then O.  With 64 channels there is room for P beside S, and Q K^T of a block runs as
-  // soon as the softmax has read the scores of the one before (EARLY); else P goes over S, and it runs behind P V.
+  // A tile's 256 columns: S 128, then O.  With 64 channels there is room for P beside S, and Q K^T of a block runs
+  // ahead of P V of the one before, once the softmax is done with the scores of that (EARLY); else P goes over S, and
+  // it runs behind P V.
   static constexpr bool EARLY = HEAD_DIM == 64;
   static constexpr int P_COL = EARLY ? 128 : 0;
   static constexpr int O_COL = EARLY ? 192 : 128;
@@ -142,6 +143,12 @@ struct PpCfg {
   static constexpr float MID = BF16 ? -16.f : 7.f;
   // The largest sum of 64 weights that leaves the maximum where it is (64 equal ones at the maximum: 2^(MID + 6)).
   static constexpr float LIMIT = BF16 ? 0.25f : 32768.f;
+  // A weight's exponent is x a + (MID - m) for the score x, one FMA, with m = rounded_up(t a) of the score t that the
+  // row is measured from: m lies |m| 2^-22 above t a, and MID - m is rounded by 2^-24 of it at most.  While it is
+  // below this bound, that makes the weights smaller by 2^-6 of a power of two; from 2^27 on they would all be 0 in
+  // fp16.  Past the bound t is taken off first, (x - t) a + MID, which holds for scores of any size: a warp with such
+  // a row weighs its scores once more, from tensor memory, at twice the time.
+  static constexpr float WIDE = 65536.f;
 };
 
 // ---------------------------------------------------------------- work items
@@ -356,7 +363,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   uint64_t* pfull = sfull + TC_TILES;      // [tile][half] P of 64 keys of that block is written (128 arrivals)
   uint64_t* pvhalf = pfull + 2 * TC_TILES; // [tile] P V of the first 64 keys of that block has completed
                                            // (EARLY: of the block)
-  uint64_t* sfree = pvhalf + TC_TILES;     // [tile] EARLY: S of the block is read (128 arrivals)
+  uint64_t* sfree = pvhalf + TC_TILES;     // [tile] EARLY: S of the block is done with (128 arrivals)
   uint64_t* pvdone = sfree + TC_TILES;     // [tile] the last P V of the tile's item has completed
   uint64_t* lready = pvdone + TC_TILES;    // [tile] the sums of the item's weights are stored (128 arrivals)
   uint64_t* ofree = lready + TC_TILES;     // [tile] the sums and O of the item are read (128 arrivals)
@@ -448,6 +455,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     publish(it, 0);
     if (it.blocks(tt) <= C::ASK_AT_ONCE) ask_for_cta(sm + C::RESP_OFF, cbar);
   }
+  // Rows of the tiles that a group leaves over are no query's: zeros, whose scores need no care.
+  for (int i = tt * G * 8 + static_cast<int>(threadIdx.x); i < TC_ROWS * 8; i += C::THREADS)
+    for (int b = 0; b < TC_TILES * C::DBOX; ++b) *reinterpret_cast<uint4*>(sm + b * C::QATOM + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  if (tt * G < TC_ROWS) fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -944,6 +955,14 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
   const bool neg = a < 0.f;
   const float hidden = neg ? INFINITY : -INFINITY;
   const uint64_t a2 = pack_f32x2(a);
+  auto further = [&](float x, float y) { return neg ? fminf(x, y) : fmaxf(x, y); };  // (of NaN and y: y)
+  auto is_wide = [&](float bias) { return !(fabsf(bias) <= C::WIDE); };  // (also where t a is infinite or t is `hidden`)
+  // What weights measured from t0 are multiplied by to be measured from t1.
+  auto moved = [&](float t0, float t1) -> float {
+    const float b0 = C::MID - rounded_up(t0 * a), b1 = C::MID - rounded_up(t1 * a);
+    const bool w0 = is_wide(b0), w1 = is_wide(b1);
+    return ex2(w0 ? (w1 ? (t0 - t1) * a : fmaf(t0, a, b1 - C::MID)) : w1 ? fmaf(-t1, a, C::MID - b0) : b1 - b0);
+  };
   uint32_t spar = 0, opar = 0;  // parities of the tile's blocks, of its items' outputs
   bool stored = false;
 #pragma unroll 1
@@ -956,7 +975,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       left = i.tile_blocks(u, tt);
       seen = i.ta + u * tt;
     }
-    float m_used = -INFINITY, l = 0.f;  // log2 units
+    float t_used = hidden, l = 0.f;  // the score that weights are measured from (`hidden`: no score yet), their sum
+    float bias = 0.f;                // EARLY: the exponents' offset (0: no score yet)
     uint32_t x[TC_KEYS];  // the block's raw scores, later its weights
     auto load_half = [&](int h) {
 #pragma unroll
@@ -970,8 +990,40 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       for (int i = 0; i < 16; ++i)
         if (!(m >> i & 1u)) v[i] = __float_as_uint(hidden);
     };
-    // The weights of a half once more, with the offsets of the rows with `low` at the maximum of their scores, and O
-    // and l after them; returns the row's sum.  Rare: a row's sum came out above the limit.
+    // The score to take off first, and the exponent's offset, of a row that is measured from t_used.
+    auto offsets = [&](float& off, float& bias) {
+      const bool none = t_used == hidden;
+      const float b = C::MID - rounded_up(t_used * a);
+      const bool wide = !none && is_wide(b);
+      off = wide ? t_used : 0.f;
+      bias = none ? 0.f : wide ? C::MID : b;
+    };
+    // The weights of a half from its scores in TMEM, measured from t_used, 16 at a time, and their sums as the unrolled
+    // code adds them: rows that need no care get the same bits.  (P goes over scores that were read, or beside them.)
+    auto reweigh = [&](int h, int seen, uint64_t (&sum2)[2]) {
+      uint32_t v[16];
+      const int own = seen + own_t - TC_HALF * h;
+      float off, bias;
+      offsets(off, bias);
+#pragma unroll 1
+      for (int c = 0; c < TC_HALF; c += 16) {
+        tmem_ld16(tS + TC_HALF * h + c, v);
+        tmem_wait_ld();
+        hide(v, own - c);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]) - off, a, bias));
+          const float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]) - off, a, bias));
+          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+          w[i] = pack2<T>(p0, p1);
+        }
+        tmem_st8(tP + 32 * h + c / 2, w);
+      }
+    };
+    // The weights of a half once more, those of the rows with `low` measured from the maximum of their scores, and O
+    // and l after them; returns the row's sum.  Rare: a row's sum came out above the limit, or its scores are wide (then
+    // its sum said nothing).
     auto again = [&](int h, int low, int seen) -> float {
       if (h == 1) {  // the first half's P V adds to O at this time
         wait(&pvhalf[u], spar ^ 1);
@@ -979,44 +1031,33 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       }
       uint32_t v[16];
       const int own = seen + own_t - TC_HALF * h;
-      float top = neg ? INFINITY : -INFINITY;
+      float top = t_used;
 #pragma unroll 1
       for (int c = 0; c < TC_HALF; c += 16) {
         tmem_ld16(tS + TC_HALF * h + c, v);
         tmem_wait_ld();
         hide(v, own - c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = neg ? fminf(top, __uint_as_float(v[i])) : fmaxf(top, __uint_as_float(v[i]));
+        for (int i = 0; i < 16; ++i) top = further(top, __uint_as_float(v[i]));
       }
-      const float m_new = low ? fmaxf(m_used, rounded_up(top * a)) : m_used;
-      const float f = low ? ex2(m_used - m_new) : 1.f;
-      m_used = m_new;
-      l *= f;
+      if (t_used != hidden && is_wide(C::MID - rounded_up(t_used * a))) low = (top - t_used) * a > TC_RESCALE_LOG2;
+      if (__any_sync(kFullMask, low)) {  // (never at an item's first scores, when O is still the last item's)
+        const float f = low ? moved(t_used, top) : 1.f;
+        if (low) t_used = top;
+        l *= f;
 #pragma unroll 1
-      for (int c = 0; c < HEAD_DIM; c += 16) {
-        tmem_ld16(tO + c, v);
-        tmem_wait_ld();
+        for (int c = 0; c < HEAD_DIM; c += 16) {
+          tmem_ld16(tO + c, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-        tmem_st16(tO + c, v);
-      }
-      const float bias = m_used == -INFINITY ? 0.f : C::MID - m_used;
-      float sum = 0.f;
-#pragma unroll 1
-      for (int c = 0; c < TC_HALF; c += 16) {  // (P goes over scores that were read)
-        tmem_ld16(tS + TC_HALF * h + c, v);
-        tmem_wait_ld();
-        hide(v, own - c);
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), a, bias)), p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), a, bias));
-          sum += p0 + p1;
-          w[i] = pack2<T>(p0, p1);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          tmem_st16(tO + c, v);
         }
-        tmem_st8(tP + 32 * h + c / 2, w);
       }
-      return sum;
+      uint64_t sum2[2] = {0, 0};
+      reweigh(h, seen, sum2);
+      const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
+      return s2.x + s2.y;
     };
 #pragma unroll 1
     for (; left > 0; --left, seen -= TC_KEYS) {
@@ -1024,11 +1065,10 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       spar ^= 1;
       tc_fence_after_sync();
       if constexpr (C::EARLY) {
-        // All scores at once, so that their place is free for the next block's.
+        // All scores at once.  Their place is free for the next block's when the first half's weights are done: until then
+        // a warp may have to weigh them once more.  (Given free as they are loaded, 8 x 2048 tokens take 171 us, so 164.)
         load_half(0);
         load_half(1);
-        tc_fence_before_sync();
-        mbar_arrive(&sfree[u]);
         if (seen + least_t < TC_KEYS - 1) {  // a key here may lie past some row of the warp
 #pragma unroll
           for (int c = 0; c < TC_KEYS; c += 16)
@@ -1052,15 +1092,19 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
             for (int c = 0; c < 4; ++c) e[c] = fminf(e[c], __uint_as_float(x[i + c]));
           e[0] = fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
         }
-        // The exponent's offset moves at the first block and when the row maximum has grown by more than 2^8; O and l
-        // then scale by f.  (A row that sees no key here keeps its own: the other is NaN.)
-        const float m_new = fmaxf(m_used, rounded_up(e[0] * a));
-        int none = m_used == -INFINITY;  // nothing in O yet (opaque as below)
+        // Weights are measured from another score at the first block and when the row maximum has grown by more than
+        // 2^8; O and l then scale by f.
+        const float top = e[0];
+        const bool far = (top - t_used) * a > TC_RESCALE_LOG2;  // (a row without a score yet: by an infinity)
+        int none = t_used == hidden;                            // nothing in O yet (opaque as below)
         use_here(none);
-        const bool need = !none && m_new > m_used + TC_RESCALE_LOG2;
-        const float f = need ? ex2(m_used - m_new) : 1.f;
-        if (none || need) m_used = m_new;
-        const uint64_t b2 = pack_f32x2(m_used == -INFINITY ? 0.f : C::MID - m_used);  // (0: a row that has seen no key yet)
+        const bool need = far && !none;
+        const float b_new = C::MID - rounded_up(top * a);
+        float f = need ? ex2(b_new - bias) : 1.f;
+        if (far) bias = b_new;
+        const bool wide = is_wide(bias);
+        const uint64_t b2 = pack_f32x2(bias);
+        bool wide_rows = false;
         uint64_t sum2[2] = {0, 0};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1074,7 +1118,14 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
           if (h == 0) {
             wait(&pvhalf[u], spar);  // P V of the block before: it has read P and O stands
             tc_fence_after_sync();
-            if (__any_sync(kFullMask, need)) {
+            bool scale_o = false;
+            if (__any_sync(kFullMask, need || wide)) {
+              scale_o = __any_sync(kFullMask, need);
+              wide_rows = __any_sync(kFullMask, wide);
+              if (wide_rows && need) f = moved(t_used, top);
+            }
+            if (far) t_used = top;
+            if (scale_o) {
 #pragma unroll 1
               for (int c = 0; c < HEAD_DIM; c += 8) {  // (eight at a time: the scores hold registers)
                 uint32_t o8[8];
@@ -1085,6 +1136,19 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
                 tmem_st8(tO + c, o8);
               }
             }
+            if (wide_rows) {  // rare: the weights of both halves once more
+              sum2[0] = sum2[1] = 0;
+              reweigh(0, seen, sum2);
+              reweigh(1, seen, sum2);
+              tmem_wait_st();
+              tc_fence_before_sync();
+              mbar_arrive(&sfree[u]);
+              mbar_arrive(&pfull[2 * u]);
+              mbar_arrive(&pfull[2 * u + 1]);
+              break;
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&sfree[u]);
           }
           tmem_st16(tP + 32 * h, &x[32 * h]);
           tmem_st16(tP + 32 * h + 16, &x[32 * h + 16]);
@@ -1117,24 +1181,32 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
             for (int c = 0; c < TC_HALF; c += 16)
               if (seen + least_t < TC_HALF * h + c + 15) hide(y + c, seen + own_t - TC_HALF * h - c);
           }
-          // (an opaque truth value: folded into the selection below, `m_used == -inf ? max(m_used, x) : m_used` has
-          // come out as max(m_used, x))
-          int none = m_used == -INFINITY;
-          use_here(none);
-          if (__any_sync(kFullMask, none)) {  // a row's first scores
-            float e[4];
+          float bias = C::MID - rounded_up(t_used * a);
+          bool wide = is_wide(bias);
+          if (__any_sync(kFullMask, wide)) {
+            // (an opaque truth value: folded into the selection below, `t_used == hidden ? max(t_used, x) : t_used` has
+            // come out as max(t_used, x))
+            int none = t_used == hidden;
+            use_here(none);
+            if (__any_sync(kFullMask, none)) {  // a row's first scores
+              float e[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(y[c]);
+              for (int c = 0; c < 4; ++c) e[c] = __uint_as_float(y[c]);
 #pragma unroll
-            for (int i = 4; i < TC_HALF; i += 4)
+              for (int i = 4; i < TC_HALF; i += 4)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                e[c] = neg ? fminf(e[c], __uint_as_float(y[i + c])) : fmaxf(e[c], __uint_as_float(y[i + c]));
-            const float top = neg ? fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
-            // (a row that sees no key here stays without: its maximum is NaN)
-            if (none) m_used = fmaxf(m_used, rounded_up(top * a));
+                for (int c = 0; c < 4; ++c)
+                  e[c] = neg ? fminf(e[c], __uint_as_float(y[i + c])) : fmaxf(e[c], __uint_as_float(y[i + c]));
+              const float top = neg ? fminf(fminf(e[0], e[1]), fminf(e[2], e[3])) : fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+              // (a row that sees no key here stays without)
+              if (none) t_used = further(t_used, top);
+              bias = C::MID - rounded_up(t_used * a);
+              none = t_used == hidden;
+            }
+            if (none) bias = 0.f;  // (no key seen yet)
+            wide = is_wide(bias);
           }
-          const uint64_t b2 = pack_f32x2(m_used == -INFINITY ? 0.f : C::MID - m_used);  // (0: a row that has seen no key yet)
+          const uint64_t b2 = pack_f32x2(bias);
           uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < TC_HALF / 2; ++i) {
@@ -1145,7 +1217,7 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
           }
           const float2 s2 = unpack_f32x2(add_f32x2(sum2[0], sum2[1]));
           float sum = s2.x + s2.y;
-          if (__any_sync(kFullMask, sum > C::LIMIT)) {
+          if (__any_sync(kFullMask, wide || sum > C::LIMIT)) {
             sum = again(h, sum > C::LIMIT, seen);
           } else {  // P in the half's 32 columns, over scores that are in registers
             tmem_st16(tP + 32 * h, &y[0]);

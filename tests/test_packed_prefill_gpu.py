@@ -537,3 +537,95 @@ def test_requests_from_prompt_to_compaction(dtype, H, Hk, d, B):
     flat[:, int((counts != 0).sum()):] = float("nan")  # what was given back
     assert int(num) > 0
     decode_all()
+
+
+# ------------------------------------------------------------- scores of any size
+def exact_scores(p, sizes, key_exp, falling=False):
+    """Scores without an error: q is one power of two a row (`sizes`, log 2 of its magnitude; every third row is
+    negative), a key one number of 8 significant bits, growing from key to key.  Sums of d products stay below 2^24 of
+    their smallest step, so float32 holds them."""
+    n = p.rows
+    step = torch.arange(n) * 127 // max(1, n - 1)
+    k = (128 + (127 - step if falling else step)).double() * 2.0 ** (key_exp - 7)
+    p.k[:] = k.to(p.dtype)[:, None, None]
+    e = torch.tensor([sizes[i % len(sizes)] for i in range(n)])
+    sign = torch.where(torch.arange(n) % 3 == 2, -1.0, 1.0).double()
+    p.q[:] = (sign * 2.0 ** e.double()).to(p.dtype)[:, None, None]
+    p.q[:, 1::2] *= 0.5  # heads of another size
+    assert torch.isfinite(p.q.float()).all() and torch.isfinite(p.k.float()).all()
+    return p
+
+
+def check_exact_scores(p):
+    """The tolerance without the scores' own error.  What is left of it: a difference of two scores is exact and is
+    multiplied by a factor off by half a step, by an operation off by half a step: 2^-23 of itself, where a weight
+    2^-g has g 2^-g <= 0.54; up to |m| = 2^16 (log 2 units) a row's offsets m are rounded, by 2^-24 |m| at most in
+    each of three places for every block half at which they move."""
+    torch.cuda.synchronize()
+    got = to_np(p.out)
+    q, k, v = to_np(p.q), to_np(p.k), to_np(p.v)
+    with np.errstate(all="ignore"):
+        want, A, _ = so.attention(q, k, v, p.starts, p.scale, p.max_len)
+        n = max(p.lens)
+        sums = 2.0 ** -22 + (n / 8 + 16) * 2.0 ** -24
+        m = (np.abs(q[..., 0]) * np.abs(np.where(np.isfinite(k), k, 0)).max() * p.d * abs(p.scale) * 1.4427)[..., None]
+        moved = np.minimum(m, 2.0 ** 16) * 3 * 2.0 ** -24 * (n / 64 + 1)
+        tiny = n * 2.0 ** -32 * np.abs(v).max() + 2.0 ** -25 if p.dtype == F16 else 2.0 ** -100
+        tol = HALF_STEP[p.dtype] * (A + np.abs(want)) + 2 * A * (sums + 2.0 ** -23 + moved) + tiny
+        err = np.abs(got - want)
+    assert np.isfinite(got).all() and (err <= tol).all(), \
+        (np.argwhere(~(err <= tol))[:4].tolist(), float(np.nanmax(err / tol)))
+    p.check_pools(np.ones(p.rows, bool))
+
+
+# log 2 of the largest q and key of each type: products to 2^30 and 2^118, scores to 2^37 and 2^125
+LARGEST = {F16: (15, 14), BF16: (59, 58)}
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, -1.0, 0.088])
+@pytest.mark.parametrize("size", [0, 7, 8, 9, 11, 13, 15, "largest"])
+def test_equal_scores_of_any_size(size, scale, d, dtype):
+    """A row of equal scores is the mean of its values; with one key, the value itself."""
+    p = Prompts([1, 2, 70, 300], 2, 1, d, dtype, 40)
+    a, b = LARGEST[dtype] if size == "largest" else (size, min(size, 14))
+    p.q.fill_(2.0 ** a), p.k.fill_(2.0 ** b)
+    p.scale = float(np.float32(scale))
+    p.start().run()
+    check_exact_scores(p)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+@pytest.mark.parametrize("sizes,key_exp", [([-3], 0), ([3], 4), ([5, 6], 5), ([9], 7), ([12], 10), ([15], 14),
+                                           ([-6, 0, 4, 8, 12, 15], 6), ([15, -9, -9, 2], 14), ([-14, 3, 15], 0)])
+def test_growing_and_falling_scores_of_any_size(sizes, key_exp, scale, falling, d, dtype):
+    """Rows of small and of large scores side by side; maxima that move far at every block, or stay at the first key."""
+    p = exact_scores(Prompts([3, 400], 2, 1, d, dtype, 41), sizes, key_exp, falling)
+    p.scale = scale
+    p.start().run()
+    check_exact_scores(p)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, -1.0, 4096.0])  # the last: past float32 when multiplied by log2(e) and the scale
+def test_the_largest_scores_of_bfloat16(scale, d):
+    for falling in (False, True):
+        p = exact_scores(Prompts([2, 300], 4, 2, d, BF16, 42), [59, -30, 59, 40], 58, falling)
+        p.scale = scale
+        p.start().run()
+        check_exact_scores(p)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_scores_beside_keys_of_minus_infinity(d, dtype):
+    p = exact_scores(Prompts([400], 2, 1, d, dtype, 43), [15, 3, 12], 13)
+    p.q = p.q.abs()
+    p.k[1::5] = -float("inf")
+    p.k[130:260] = -float("inf")
+    p.start().run()
+    check_exact_scores(p)
