@@ -1383,18 +1383,6 @@ cudaError_t make_pool_map(CUtensorMap* map, const void* pool, int num_kv_heads, 
   return err;
 }
 
-template <typename Kernel>
-cudaError_t ensure_smem(Kernel k, int bytes, std::atomic<uint64_t>& done_mask) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (bit && (done_mask.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && bit) done_mask.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
-
 #ifndef PA_DECODE_WARPS
 #define PA_DECODE_WARPS 4
 #endif

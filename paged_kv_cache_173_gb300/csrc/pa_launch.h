@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace pa {
 
 struct ReshapeArgs {
@@ -316,6 +318,19 @@ cudaError_t launch_copy_layers(const CopyLayerArgs& a, cudaStream_t stream);
 // o [S][H][P][d], then m [S][H][P], then l [S][H][P], float32.
 inline size_t ws_rows(int num_seqs, int num_heads, int max_num_partitions) {
   return static_cast<size_t>(num_seqs) * num_heads * max_num_partitions;
+}
+
+// Raise a kernel's limit of dynamic shared memory, once per device: `bytes` is the largest size of any launch.
+template <typename Kernel>
+cudaError_t ensure_smem(Kernel k, int bytes, std::atomic<uint64_t>& done_mask) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit && (done_mask.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && bit) done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
 }
 
 }  // namespace pa

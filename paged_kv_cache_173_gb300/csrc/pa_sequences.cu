@@ -651,6 +651,10 @@ SequenceParams sequence_params(const SequenceArgs& a, const int32_t* what) {
 
 constexpr int kCluster = 8;
 constexpr int kSmallPool = 16384;  // blocks that one CTA plans for
+constexpr int kMaxSeqs = 65535;    // of a call
+
+// Dynamic shared memory of an extend CTA of `rows` sequences that keeps a list of `listed` blocks.
+constexpr size_t extend_smem(int rows, int listed) { return sizeof(int) * (5 * static_cast<size_t>(rows) + 1 + listed); }
 
 }  // namespace
 
@@ -663,6 +667,9 @@ cudaError_t launch_fork(const SequenceArgs& a, const int32_t* fork_from, cudaStr
 }
 
 cudaError_t launch_extend(const ExtendArgs& e, cudaStream_t stream) {
+  // The kernels' limits are set once per device, to the largest size of any call: they belong to the kernel, and a
+  // call that lowered them would have another thread's launch refused.
+  static std::atomic<uint64_t> smem_set[2];
   const SequenceArgs& a = e.a;
   ExtendParams p{a.block_tables, a.context_lens, a.ref_counts, e.query_start_loc, e.slot_mapping, e.block_copies, e.left,
                  static_cast<int32_t*>(e.workspace), a.num_seqs, a.max_blocks_per_seq, a.num_blocks, e.num_tokens,
@@ -672,21 +679,16 @@ cudaError_t launch_extend(const ExtendArgs& e, cudaStream_t stream) {
   // as eight CTAs do, but not those of many prompts (65536 tokens: 46.6 against 11.5 us).
   if (a.num_seqs <= kThreads && a.num_blocks <= kSmallPool && e.num_tokens <= 4 * kThreads) {
     p.rows = a.num_seqs;
-    const size_t smem = sizeof(int) * (5 * static_cast<size_t>(p.rows) + 1 + a.num_blocks);
-    if (smem > 40 * 1024) {
-      const cudaError_t err = cudaFuncSetAttribute(extend_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-      if (err != cudaSuccess) return err;
-    }
+    const size_t smem = extend_smem(p.rows, a.num_blocks);
+    const cudaError_t err = ensure_smem(extend_kernel<1>, static_cast<int>(extend_smem(kThreads, kSmallPool)), smem_set[0]);
+    if (err != cudaSuccess) return err;
     return launch(extend_kernel<1>, dim3(1), kThreads, smem, 1, p, stream);
   }
   p.rows = (a.num_seqs + kCluster - 1) / kCluster;
-  const size_t smem = sizeof(int) * (5 * static_cast<size_t>(p.rows) + 1);
-  if (smem > 40 * 1024) {  // over 16,000 sequences
-    const cudaError_t err = cudaFuncSetAttribute(extend_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-  }
+  const size_t smem = extend_smem(p.rows, 0);
+  const cudaError_t err = ensure_smem(extend_kernel<kCluster>, static_cast<int>(extend_smem((kMaxSeqs + kCluster - 1) / kCluster, 0)),
+                                      smem_set[1]);
+  if (err != cudaSuccess) return err;
   return launch(extend_kernel<kCluster>, dim3(kCluster), kThreads, smem, kCluster, p, stream);
 }
 

@@ -492,3 +492,34 @@ def test_starts_near_the_ends_of_32_bits(starts, S):
     if (np.diff(starts) >= 0).all():
         assert np.array_equal(slots.cpu().numpy(), want_slots)
     assert bool((room[:64] == 77).all()) and bool((room[64 + T:] == 77).all())
+
+
+@pytest.mark.parametrize("sizes", [((1024, 16384), (10, 11000)), ((65535, 20000), (20000, 16400))])  # one CTA, several
+def test_two_threads_with_pools_of_different_size(sizes):
+    """Launches of one kernel with much and with less shared memory, from two threads at once: none is refused."""
+    import threading
+
+    from paged_kv_cache_173_gb300 import _lib
+    L, refused = _lib.lib(), []
+
+    def work(S, N):
+        i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        tables, lens, counts, starts, left = i32(S, 2), i32(S), i32(N), i32(S + 1), i32(2)
+        copies, ws, stream = torch.zeros((S, 2), dtype=torch.int64, device="cuda"), api.alloc_sequence_workspace(N, "cuda"), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(2000):
+            status = L.pa_extend_sequences(tables.data_ptr(), 2, lens.data_ptr(), counts.data_ptr(), starts.data_ptr(), None,
+                                           copies.data_ptr(), left.data_ptr(), S, 0, N, 16, ws.data_ptr(), 4 * ws.numel(),
+                                           stream.cuda_stream)
+            if status != _lib.PA_OK:
+                refused.append((S, N, _lib.last_error()))
+        stream.synchronize()
+        if left.tolist() != [N, 0]:
+            refused.append((S, N, left.tolist()))
+
+    threads = [threading.Thread(target=work, args=x) for x in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert refused == []
