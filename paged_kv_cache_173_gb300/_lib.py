@@ -126,6 +126,7 @@ def fast():
                 address = lambda n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value  # noqa: E731
                 m.bind(*map(address, FAST_ENTRIES))
                 m.bind_sequences(*map(address, FAST_SEQUENCE_ENTRIES))
+                m.bind_check(check)
                 _fast = m
     return _fast
 

@@ -5,9 +5,11 @@
 // and calling through ctypes takes 7 to 10 us, the kernels 3 to 5.  Each function
 // here reads the tensors of one call in C++, makes the call when everything is as
 // the call wants it, and returns True.  Whatever is not (a type, a shape, a
-// stride, another device, a status) makes it return False with nothing launched;
-// api.py then takes its own way, which names what is wrong.  So api.py defines the
-// checks and the errors, and this file holds no message.
+// stride, another device, an argument that the entry point refuses) makes it return
+// False with nothing launched; api.py then takes its own way, which names what is
+// wrong.  A launch that fails is raised here, by api.py's own check of a status: a
+// call of several launches has perhaps changed its tensors and is not made again.
+// So api.py defines the checks and the errors, and this file holds no message.
 //
 // Arguments after the tensors and numbers of the call: the current device and the
 // stream's handle.
@@ -34,6 +36,8 @@ decltype(&pa_truncate_sequences) g_truncate;
 decltype(&pa_fork_sequences) g_fork;
 decltype(&pa_compact_blocks) g_compact;
 decltype(&pa_copy_layer_blocks) g_copy_layers;
+
+PyObject* g_check;  // check(name, status): raises
 
 constexpr int64_t kIntMax = 0x7fffffff;
 
@@ -120,12 +124,17 @@ PyObject* answer(bool done) { return PyBool_FromLong(done ? 1 : 0); }
 
 // One entry point's call, the interpreter free for other threads meanwhile.
 template <class F, class... A>
-PyObject* launch(F f, A... a) {
+PyObject* launch(const char* name, F f, A... a) {
   int status;
   Py_BEGIN_ALLOW_THREADS;
   status = f(a...);
   Py_END_ALLOW_THREADS;
-  return answer(status == PA_OK);
+  if (status == PA_OK || status == PA_ERR_INVALID_ARG || status == PA_ERR_UNSUPPORTED) return answer(status == PA_OK);
+  if (g_check == nullptr) {
+    PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, status);
+    return nullptr;
+  }
+  return PyObject_CallFunction(g_check, "si", name, status);  // (raises)
 }
 
 // key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping
@@ -140,8 +149,8 @@ PA_FAST(write) {
   void* ks = x.typed(4, at::kFloat, {N, Hk}); void* vs = x.typed(5, at::kFloat, {N, Hk});
   void* sm = x.typed(6, at::kLong, {T}); void* st = x.stream(8);
   if (!x.ok || code < 0 || !fits({T, N, B, Hk, d})) return answer(false);
-  return launch(g_write, k, v, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs), static_cast<int64_t*>(sm), T, N,
-                        B, Hk, d, code, st);
+  return launch("pa_reshape_and_cache_fp8_block", g_write, k, v, kc, vc, static_cast<float*>(ks),
+                static_cast<float*>(vs), static_cast<int64_t*>(sm), T, N, B, Hk, d, code, st);
 } PA_GUARD
 
 // key, key_bounds, bound_exps, slot_mapping, block_size
@@ -155,8 +164,8 @@ PA_FAST(bounds) {
   void* e = x.typed(2, at::kInt, {N, Hk}); void* sm = x.typed(3, at::kLong, {T});
   const long B = x.integer(4); void* st = x.stream(6);
   if (!x.ok || code < 0 || !fits({T, N, B, Hk, d})) return answer(false);
-  return launch(g_bounds, k, static_cast<int8_t*>(b), static_cast<int32_t*>(e), static_cast<int64_t*>(sm), T, N, B, Hk, d,
-                         code, st);
+  return launch("pa_update_key_bounds", g_bounds, k, static_cast<int8_t*>(b), static_cast<int32_t*>(e),
+                static_cast<int64_t*>(sm), T, N, B, Hk, d, code, st);
 } PA_GUARD
 
 // out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale
@@ -172,8 +181,8 @@ PA_FAST(decode) {
   void* tp = x.typed(6, at::kInt, {S, M}); void* cl = x.typed(7, at::kInt, {S});
   const float scale = x.real(8); void* st = x.stream(10);
   if (!x.ok || code < 0 || pool->size(3) != d || !fits({S, H, d, N, B, Hk, M})) return answer(false);
-  return launch(g_decode, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs), static_cast<int32_t*>(tp), M,
-                         static_cast<int32_t*>(cl), S, H, Hk, d, B, N, scale, code, st);
+  return launch("pa_decode_fp8_block", g_decode, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs),
+                static_cast<int32_t*>(tp), M, static_cast<int32_t*>(cl), S, H, Hk, d, B, N, scale, code, st);
 } PA_GUARD
 
 // as decode, then partition_size, max_num_partitions, workspace
@@ -190,9 +199,9 @@ PA_FAST(splitk) {
   void* tp = x.typed(6, at::kInt, {S, M}); void* cl = x.typed(7, at::kInt, {S});
   const float scale = x.real(8); const long ps = x.integer(9), P = x.integer(10); void* st = x.stream(13);
   if (!x.ok || code < 0 || pool->size(3) != d || !fits({S, H, d, N, B, Hk, M, ps, P})) return answer(false);
-  return launch(g_splitk, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs), static_cast<int32_t*>(tp), M,
-                         static_cast<int32_t*>(cl), S, H, Hk, d, B, N, scale, code, ps, P, ws->data_ptr(), ws->nbytes(),
-                         st);
+  return launch("pa_decode_splitk_fp8_block", g_splitk, o, qp, kc, vc, static_cast<float*>(ks),
+                static_cast<float*>(vs), static_cast<int32_t*>(tp), M, static_cast<int32_t*>(cl), S, H, Hk, d, B, N,
+                scale, code, ps, P, ws->data_ptr(), ws->nbytes(), st);
 } PA_GUARD
 
 // out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, query_start_loc, max_query_len, scale
@@ -209,9 +218,9 @@ PA_FAST(prefill) {
   void* tp = x.typed(6, at::kInt, {S, M}); void* cl = x.typed(7, at::kInt, {S}); void* qs = x.typed(8, at::kInt, {S + 1});
   const long maxq = x.integer(9); const float scale = x.real(10); void* st = x.stream(12);
   if (!x.ok || code < 0 || pool->size(3) != d || !fits({R, S, H, d, N, B, Hk, M, maxq})) return answer(false);
-  return launch(g_prefill, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs), static_cast<int32_t*>(tp), M,
-                          static_cast<int32_t*>(cl), static_cast<int32_t*>(qs), S, R, maxq, H, Hk, d, B, N, scale, code,
-                          st);
+  return launch("pa_prefill_fp8_block", g_prefill, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs),
+                static_cast<int32_t*>(tp), M, static_cast<int32_t*>(cl), static_cast<int32_t*>(qs), S, R, maxq, H, Hk,
+                d, B, N, scale, code, st);
 } PA_GUARD
 
 // sel_tables, sel_lens, q, key_bounds, bound_exps, block_tables, context_lens, block_size, num_first, num_last, workspace
@@ -227,9 +236,9 @@ PA_FAST(select) {
   void* e = x.typed(4, at::kInt, {N, Hk}); void* tp = x.typed(5, at::kInt, {S, M}); void* cl = x.typed(6, at::kInt, {S});
   const long B = x.integer(7), first = x.integer(8), last = x.integer(9); void* st = x.stream(12);
   if (!x.ok || code < 0 || !fits({S, H, d, Hk, K, N, M, B, first, last})) return answer(false);
-  return launch(g_select, static_cast<int32_t*>(tab), static_cast<int32_t*>(len), qp, static_cast<int8_t*>(b),
-                         static_cast<int32_t*>(e), static_cast<int32_t*>(tp), M, static_cast<int32_t*>(cl), S, H, Hk, d,
-                         B, N, K, first, last, code, ws->data_ptr(), ws->nbytes(), st);
+  return launch("pa_select_blocks", g_select, static_cast<int32_t*>(tab), static_cast<int32_t*>(len), qp,
+                static_cast<int8_t*>(b), static_cast<int32_t*>(e), static_cast<int32_t*>(tp), M,
+                static_cast<int32_t*>(cl), S, H, Hk, d, B, N, K, first, last, code, ws->data_ptr(), ws->nbytes(), st);
 } PA_GUARD
 
 // out, q, k_cache, v_cache, sel_tables, sel_lens, scale, k_scales or None, v_scales or None
@@ -254,8 +263,8 @@ PA_FAST(sparse) {
     kv = PA_FP8_E4M3;
   }
   if (!x.ok || code < 0 || pool->size(3) != d || !fits({S, H, d, N, B, Hk, K})) return answer(false);
-  return launch(g_sparse, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs), static_cast<int32_t*>(tab), K,
-                         static_cast<int32_t*>(len), S, H, Hk, d, B, N, scale, code, kv, st);
+  return launch("pa_decode_sparse", g_sparse, o, qp, kc, vc, static_cast<float*>(ks), static_cast<float*>(vs),
+                static_cast<int32_t*>(tab), K, static_cast<int32_t*>(len), S, H, Hk, d, B, N, scale, code, kv, st);
 } PA_GUARD
 
 // out, q, key, value, query_start_loc, max_query_len, scale, k_cache or None, v_cache or None, slot_mapping or None
@@ -279,8 +288,8 @@ PA_FAST(packed) {
     kc = x.typed(7, dt, {N, B, Hk, d}); vc = x.typed(8, dt, {N, B, Hk, d}); sm = x.typed(9, at::kLong, {R});
   }
   if (!x.ok || code < 0 || !fits({R, H, d, Hk, S, N, B, maxq})) return answer(false);
-  return launch(g_packed, o, q, qs, k, ks, v, vs, kc, vc, static_cast<int64_t*>(sm), static_cast<int32_t*>(st), S, R, maxq,
-                H, Hk, d, B, N, scale, code, stream);
+  return launch("pa_prefill_packed", g_packed, o, q, qs, k, ks, v, vs, kc, vc, static_cast<int64_t*>(sm),
+                static_cast<int32_t*>(st), S, R, maxq, H, Hk, d, B, N, scale, code, stream);
 } PA_GUARD
 
 // The tables, lengths and counts that begin a call on the sequences' blocks.
@@ -314,22 +323,23 @@ PA_FAST(extend) {
   void* bc = x.typed(5, at::kLong, {q.S, 2}); void* left = x.typed(6, at::kInt, {2});
   const long B = x.integer(7); void* stream = x.stream(10);
   if (!x.ok || !fits({T, B})) return answer(false);
-  return launch(g_extend, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(st), static_cast<int64_t*>(sm),
-                static_cast<int64_t*>(bc), static_cast<int32_t*>(left), q.S, T, q.N, B, ws->data_ptr(), ws->nbytes(), stream);
+  return launch("pa_extend_sequences", g_extend, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(st),
+                static_cast<int64_t*>(sm), static_cast<int64_t*>(bc), static_cast<int32_t*>(left), q.S, T, q.N, B,
+                ws->data_ptr(), ws->nbytes(), stream);
 } PA_GUARD
 
 // block_tables, context_lens, ref_counts, new_lens (fork: fork_from), block_size
 template <class F>
-PyObject* per_sequence(F f, PyObject* const* args, Py_ssize_t n) {
+PyObject* per_sequence(const char* name, F f, PyObject* const* args, Py_ssize_t n) {
   Args x(args, n, 7);
   const Sequences q(x, 0);
   void* what = x.ok ? x.typed(3, at::kInt, {q.S}) : nullptr;
   const long B = x.integer(4); void* stream = x.stream(6);
   if (!x.ok || !fits({B})) return answer(false);
-  return launch(f, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(what), q.S, q.N, B, stream);
+  return launch(name, f, q.tables, q.M, q.lens, q.counts, static_cast<int32_t*>(what), q.S, q.N, B, stream);
 }
-PA_FAST(truncate) { return per_sequence(g_truncate, args, n); } PA_GUARD
-PA_FAST(fork) { return per_sequence(g_fork, args, n); } PA_GUARD
+PA_FAST(truncate) { return per_sequence("pa_truncate_sequences", g_truncate, args, n); } PA_GUARD
+PA_FAST(fork) { return per_sequence("pa_fork_sequences", g_fork, args, n); } PA_GUARD
 
 // moves, num_moves, block_tables, context_lens, ref_counts, tables_out, counts_out, block_size, workspace
 PA_FAST(compact) {
@@ -341,8 +351,9 @@ PA_FAST(compact) {
   void* to = x.typed(5, at::kInt, {q.S, q.M}); void* co = x.typed(6, at::kInt, {q.N});
   const long B = x.integer(7); void* stream = x.stream(10);
   if (!x.ok || !fits({K, B})) return answer(false);
-  return launch(g_compact, static_cast<int64_t*>(m), K, static_cast<int32_t*>(num), q.tables, q.M, q.lens, q.counts,
-                static_cast<int32_t*>(to), static_cast<int32_t*>(co), q.S, q.N, B, ws->data_ptr(), ws->nbytes(), stream);
+  return launch("pa_compact_blocks", g_compact, static_cast<int64_t*>(m), K, static_cast<int32_t*>(num), q.tables,
+                q.M, q.lens, q.counts, static_cast<int32_t*>(to), static_cast<int32_t*>(co), q.S, q.N, B,
+                ws->data_ptr(), ws->nbytes(), stream);
 } PA_GUARD
 
 // pools [L, N, ...], block_mapping
@@ -361,8 +372,8 @@ PA_FAST(copy_layers) {
   }
   const int64_t L = pools.size(0), N = pools.size(1), width = pools.element_size();
   if (!fits({L, N, pairs})) return answer(false);
-  return launch(g_copy_layers, pools.data_ptr(), pools.stride(0) * width, L, inner / N * width, static_cast<int64_t*>(m),
-                pairs, N, stream);
+  return launch("pa_copy_layer_blocks", g_copy_layers, pools.data_ptr(), pools.stride(0) * width, L,
+                inner / N * width, static_cast<int64_t*>(m), pairs, N, stream);
 } PA_GUARD
 
 // bind_sequences(packed, extend, truncate, fork, compact, copy_layers): the entry points' addresses
@@ -385,6 +396,17 @@ PyObject* bind_sequences_(PyObject*, PyObject* const* args, Py_ssize_t n) noexce
   g_fork = reinterpret_cast<decltype(g_fork)>(p[3]);
   g_compact = reinterpret_cast<decltype(g_compact)>(p[4]);
   g_copy_layers = reinterpret_cast<decltype(g_copy_layers)>(p[5]);
+  Py_RETURN_NONE;
+}
+
+// bind_check(check): the function that raises a failed launch's status
+PyObject* bind_check_(PyObject*, PyObject* const* args, Py_ssize_t n) noexcept {
+  if (n != 1 || !PyCallable_Check(args[0])) {
+    PyErr_SetString(PyExc_TypeError, "bind_check takes a function");
+    return nullptr;
+  }
+  Py_INCREF(args[0]);
+  Py_XSETREF(g_check, args[0]);
   Py_RETURN_NONE;
 }
 
@@ -415,7 +437,7 @@ PyObject* bind_(PyObject*, PyObject* const* args, Py_ssize_t n) noexcept {
 #define PA_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name##_)), METH_FASTCALL, nullptr }
 PyMethodDef g_methods[] = {PA_METHOD(bind),    PA_METHOD(write),  PA_METHOD(bounds), PA_METHOD(decode), PA_METHOD(splitk),
-                           PA_METHOD(prefill), PA_METHOD(select), PA_METHOD(sparse), PA_METHOD(bind_sequences),
+                           PA_METHOD(prefill), PA_METHOD(select), PA_METHOD(sparse), PA_METHOD(bind_sequences), PA_METHOD(bind_check),
                            PA_METHOD(packed),  PA_METHOD(extend), PA_METHOD(truncate), PA_METHOD(fork), PA_METHOD(compact),
                            PA_METHOD(copy_layers), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -523,3 +523,40 @@ def test_two_threads_with_pools_of_different_size(sizes):
     for t in threads:
         t.join()
     assert refused == []
+
+
+@pytest.mark.parametrize("name", ["pa_compact_blocks", "pa_extend_sequences"])
+def test_a_launch_that_fails_is_raised_and_not_made_again(name, monkeypatch):
+    """The entry point is replaced by one that says that a launch failed: its tensors may have changed by then."""
+    import ctypes
+
+    from paged_kv_cache_173_gb300 import _lib
+    s, L, fast, made = Server(4, 3, 20, 16), _lib.lib(), _lib.fast(), []
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    i64 = lambda *n: torch.zeros(n, dtype=torch.int64, device="cuda")  # noqa: E731
+    state = (s.tables, s.lens, s.counts)
+    call = dict(pa_compact_blocks=lambda b: api.pa_compact_blocks(i64(4, 2), i32(1), *state, s.tables, s.counts, b, s.ws),
+                pa_extend_sequences=lambda b: api.pa_extend_sequences(*state, i32(5), i64(3), i64(4, 2), i32(2), b, s.ws))[name]
+    status = [_lib.PA_ERR_CUDA]
+    res, args = _lib.SIGNATURES[name]
+    fake = ctypes.CFUNCTYPE(res, *args)(lambda *a: made.append("short") or status[0])
+    monkeypatch.setattr(L, name, lambda *a: made.append("own") or status[0])
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    fast.bind_sequences(*[address(fake if n == name else getattr(L, n)) for n in _lib.FAST_SEQUENCE_ENTRIES])
+    try:
+        with pytest.raises(api.PagedAttnError) as e:
+            call(16)
+        assert e.value.status == _lib.PA_ERR_CUDA and name in str(e.value) and made == ["short"]
+        for status[0] in (_lib.PA_ERR_INVALID_ARG, _lib.PA_ERR_UNSUPPORTED):  # nothing was launched: api.py's own way names it
+            made.clear()
+            with pytest.raises(api.PagedAttnError) as e:
+                call(16)
+            assert e.value.status == status[0] and made == ["short", "own"]
+    finally:
+        monkeypatch.undo()
+        fast.bind_sequences(*[address(getattr(L, n)) for n in _lib.FAST_SEQUENCE_ENTRIES])
+    call(16)
+    s.same()
+    with pytest.raises(api.PagedAttnError) as e:
+        call(20)
+    assert e.value.status == _lib.PA_ERR_UNSUPPORTED

@@ -185,3 +185,10 @@ def test_the_short_way_declines_what_it_does_not_know(L):
         fast.bind_sequences(1, 2)
     with pytest.raises(ValueError):
         fast.bind_sequences(*[0] * 6)
+
+
+def test_the_short_way_takes_one_function_for_failed_launches(L):
+    fast = _lib.fast()
+    for args in ((), (1,), (print, print)):
+        with pytest.raises(TypeError):
+            fast.bind_check(*args)
