@@ -841,7 +841,8 @@ size_t pa_sequence_workspace_bytes(int num_blocks);
  * Refused, and left as they were, are: the first sequence whose blocks are not there and
  * every later one that needs a block; a sequence that would outgrow its table; one whose
  * partly filled last block lies outside the pool; one whose range of tokens is reversed or
- * leaves [0, num_tokens].
+ * leaves [0, num_tokens].  A sequence that brings no tokens is never refused: it is left as
+ * it was, whatever its length and its (empty) range are, and does not count in left[1].
  */
 int pa_extend_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* context_lens,
                         int32_t* ref_counts, const int32_t* query_start_loc, int64_t* slot_mapping,

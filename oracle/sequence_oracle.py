@@ -83,12 +83,14 @@ def extend(tables, lens, counts, starts, num_tokens, block):
     for s in range(S):
         a, b, n0 = int(starts[s]), int(starts[s + 1]), int(lens[s])
         n = b - a
+        if n == 0:
+            continue
         if a < 0 or b < a or b > num_tokens or n0 < 0 or n0 + n > M * block:
             refused += 1
             continue
         had, want = up(n0, block), up(n0 + n, block)
         need, copy = want - had, False
-        if n > 0 and n0 % block:
+        if n0 % block:
             last = int(tables[s, had - 1])
             if not inside(last, N):
                 refused += 1

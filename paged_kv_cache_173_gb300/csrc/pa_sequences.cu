@@ -236,10 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int len = p.context_lens[s];
       const int64_t after = static_cast<int64_t>(len) + to - from;
       int flags = 0;
-      if (from < 0 || to < from || to > p.num_tokens || len < 0 ||
-          after > (static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_b)) {
+      const bool asks = to != from;  // (who brings nothing is left alone, whatever its length and its range)
+      if (asks && (from < 0 || to < from || to > p.num_tokens || len < 0 ||
+                   after > (static_cast<int64_t>(p.max_blocks_per_seq) << p.log2_b))) {
         flags = kRefused;
-      } else if (to > from) {
+      } else if (asks) {
         want = blocks_of(static_cast<int>(after), p.log2_b) - blocks_of(len, p.log2_b);
         if (len & (bsize - 1)) {
           id = p.block_tables[static_cast<size_t>(s) * p.max_blocks_per_seq + (len >> p.log2_b)];
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     const size_t s = first + i;
     const int x = need[i];
     if (!(x & kCopy)) p.block_copies[2 * s] = p.block_copies[2 * s + 1] = -1;
-    if (!(x & kRefused)) p.context_lens[s] = lens[i] + starts[i + 1] - starts[i];
+    if (!(x & kRefused) && starts[i + 1] != starts[i]) p.context_lens[s] = lens[i] + starts[i + 1] - starts[i];
   }
 
   // the tokens' slots: in the last block, or in those that were handed out

@@ -560,3 +560,26 @@ def test_a_launch_that_fails_is_raised_and_not_made_again(name, monkeypatch):
     with pytest.raises(api.PagedAttnError) as e:
         call(20)
     assert e.value.status == _lib.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("S", [3, 1500])
+def test_sequences_without_new_tokens_are_not_refused(S):
+    """left[1] counts who asked for tokens and got none: not those of bad lengths, bad blocks or empty ranges outside
+    the tokens that bring nothing."""
+    s = Server(S, 3, 40 + 2 * S, 16)
+    first = np.zeros(S, np.int64)
+    first[:3] = 20
+    s.extend(first)
+    tables, lens, counts = (x.copy() for x in s.host)
+    lens[0], lens[1], tables[2, 1] = -3, 49, 10 ** 9
+    s.set(tables, lens, counts)
+    _, copies, left = s.extend(np.zeros(S, np.int64))
+    assert left[1] == 0 and (copies == -1).all()
+    # one sequence asks for more tokens than there are slots; those behind it have empty ranges past the last token
+    starts = np.full(S + 1, 100, np.int64)
+    starts[0] = 0
+    slots = torch.full((50,), 77, dtype=torch.int64, device="cuda")
+    copies, left = torch.empty((S, 2), dtype=torch.int64, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    api.pa_extend_sequences(s.tables, s.lens, s.counts, dev(starts.astype(np.int32)), slots, copies, left, 16, s.ws)
+    s.same()
+    assert left.tolist() == [int((counts == 0).sum()), 1] and bool((slots == -1).all()) and bool((copies == -1).all())
