@@ -629,3 +629,105 @@ def test_large_scores_beside_keys_of_minus_infinity(d, dtype):
     p.k[130:260] = -float("inf")
     p.start().run()
     check_exact_scores(p)
+
+
+# ----------------------------------------------------- bad starts, and what is not finite at head_dim 128
+def with_margins(x, rows, value):
+    """x as a view with `rows` rows of `value` before and behind it, and a function that says whether those stand."""
+    room = torch.full((x.shape[0] + 2 * rows,) + tuple(x.shape[1:]), value, dtype=x.dtype, device=x.device)
+    view = room[rows:rows + x.shape[0]]
+    view.copy_(x)
+    return view, lambda: bool((room[:rows] == value).all()) and bool((room[rows + x.shape[0]:] == value).all())
+
+
+def check_inside(p, starts):
+    """Run p with these starts: nothing is written around out and the pools, and what is written is what belongs there."""
+    p.start()
+    p.dst = torch.as_tensor(starts, dtype=torch.int32).cuda()
+    p.out, out_ok = with_margins(p.out, 300, 7.0)
+    p.kc, k_ok = with_margins(p.kc, 20, 3.0)
+    p.vc, v_ok = with_margins(p.vc, 20, 5.0)
+    p.run()
+    torch.cuda.synchronize()
+    assert out_ok() and k_ok() and v_ok()
+    assert bool(torch.isfinite(p.out.float()).all())
+    for pool, new, empty in ((p.kc, p.k, 3.0), (p.vc, p.v, 5.0)):
+        rows = pool.flatten(0, 1).cpu()
+        there = rows[p.slots]
+        written = (there == new).flatten(1).all(1)
+        assert bool((written | (there == empty).flatten(1).all(1)).all())
+        rows[p.slots] = empty
+        assert bool((rows == empty).all())
+    return p
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top", [3000, 100])  # the list of all pairs, and the grid
+def test_starts_in_no_order_write_nothing_outside(top, d):
+    rng = np.random.default_rng(32)
+    for _ in range(3):
+        check_inside(Prompts([3000], 4, 2, d, F16, 31), rng.integers(-100, top + 100, 201))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("starts", [[0, 60, 40, 100], [0, 50, 120, 100], [2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31, 100], [-2 ** 31, 2 ** 31 - 1, 0, 50],
+                                    [-300, -200, -100, 0], [100, 200, 300, 400], [0, 0, 0, 1000], [-1000, 100, 100, 100]])
+def test_bad_starts_write_nothing_outside(starts, d):
+    p = Prompts([30, 30, 40], 4, 2, d, F16, 13)
+    p.max_len = 120
+    check_inside(p, starts)
+    if starts[2:] == [0, 1000] or starts[0] == -1000:  # one prompt of all rows
+        p.starts, p.lens = np.array([0, 100]), [100]
+        p.check()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 63, 64, 127, 128, 200, 259])
+@pytest.mark.parametrize("G", [1, 4, 7])
+def test_what_is_not_finite_at_head_dim_128(dtype, bad, at, G):
+    lens, others = [260, 150], [c for c in range(128) if c != 77]
+    prompts = lambda: Prompts(lens, 2 * G, 2, 128, dtype, at, pad=2)  # noqa: E731
+
+    def value(p):
+        p.v[at, 0, 77] = bad
+
+    clean, got = finite_elsewhere(prompts(), value)
+    assert torch.equal(got[:at], clean[:at]) and torch.equal(got[260:], clean[260:])
+    assert torch.equal(got[at:260, G:], clean[at:260, G:])
+    seen = got[at:260, :G]
+    assert not torch.isfinite(seen[..., 77]).any()
+    assert torch.equal(seen[..., others], clean[at:260, :G][..., others])
+
+    def key(p):
+        p.k[at, 0, 77] = bad
+
+    p = prompts()
+    clean, got = finite_elsewhere(p, key)
+    assert torch.equal(got[:at], clean[:at]) and torch.equal(got[260:], clean[260:])
+    assert torch.equal(got[at:260, G:], clean[at:260, G:])
+    # a score of +inf or NaN makes the row NaN, one of -inf weighs nothing
+    # The tolerance at the head of this file: A is that of the weights there are (one with key `at` at a score of 0, not of
+    # -inf, gives its value a weight that it does not have, and so an A below sum w |v|: a row of two keys has twice that);
+    # S is that of the other keys, a score of -inf having no error.
+    q, k, v = to_np(p.q), to_np(p.k), to_np(p.v)
+    with np.errstate(all="ignore"):
+        want, A, _ = (x[at:260, :G] for x in so.attention(q, k, v, p.starts, p.scale))
+        S = so.attention(q, np.where(np.isfinite(k), k, 0), v, p.starts, p.scale)[2][at:260, :G]
+        n, top = max(lens), np.abs(v).max()
+        tiny = n * 2.0 ** -32 * top + 2.0 ** -25 if dtype == F16 else 2.0 ** -100
+        tol = HALF_STEP[dtype] * (A + np.abs(want)) + tiny + A * (
+            2 * (p.d + 4) * 2.0 ** -24 * S[..., None] + 2 * (2.0 ** -22 + (n / 8 + 16) * 2.0 ** -24))
+    seen = got[at:260, :G].double().numpy()
+    assert np.array_equal(np.isnan(seen), np.isnan(want))
+    fine = ~np.isnan(want)
+    assert (np.abs(seen - want)[fine] <= tol[fine]).all(), float((np.abs(seen - want) / tol)[fine].max())
+
+    def query(p):
+        p.q[at, 1] = bad
+
+    clean, got = finite_elsewhere(prompts(), query)
+    assert got[at, 1].isnan().all()
+    mask = torch.ones(got.shape[:2], dtype=torch.bool)
+    mask[at, 1] = False
+    assert torch.equal(got[mask], clean[mask])
