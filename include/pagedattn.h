@@ -819,8 +819,10 @@ size_t pa_sequence_workspace_bytes(int num_blocks);
  *   ceil((len + n) / B) - ceil(len / B)  new ones behind their last, and before these
  *   one in the place of a last block that is partly filled and has a count above 1: the
  *   sequence leaves the shared block (its count falls by 1) and the pair (old, new) is
- *   asked for in block_copies.  (Where all holders of a block leave it in one call,
- *   it is free afterwards.)
+ *   asked for in block_copies.  The count is that at the start of the call, so where all
+ *   holders of a block grow in one call, each takes a copy, the last one too, and the block
+ *   is free afterwards: a prompt's row and its n samples that all grow at once need n + 1
+ *   blocks for it (the samples first and the row in a second call: n).
  *
  * Then context_lens[s] += n, and the tokens' slots are written.  Blocks that the call
  * itself frees are not handed out by it, so that their contents are there for the copies.
@@ -895,6 +897,9 @@ int pa_fork_sequences(int32_t* block_tables, int max_blocks_per_seq, int32_t* co
  *               not overlap it.  Entries past a context are copied as they are; a length past the
  *               table's capacity counts as all of the table.
  *   workspace   as pa_extend_sequences
+ *
+ * Two launches.  PA_ERR_CUDA may mean that the first one was made: moves, num_moves and
+ * counts_out are written then, tables_out is not.
  */
 int pa_compact_blocks(int64_t* moves, int max_moves, int32_t* num_moves, const int32_t* block_tables,
                       int max_blocks_per_seq, const int32_t* context_lens, const int32_t* ref_counts,

@@ -13,7 +13,7 @@
 //
 // The bound is the tensor cores: 4 x 128 x 128 x d multiply-adds per pair and 128 keys, 2062
 // cycles at d = 128; at d = 64 the softmax, whose 256 x 128 scores take the four schedulers
-// 1530 cycles (1024 of them the exponentials).  Long prompts take 2700 and 2500 cycles.  What
+// 1530 cycles (1024 of them the exponentials).  Long prompts take 2700 and 2490 cycles.  What
 // stands against the rest:
 //  - A tile's chain (scores, weights, P V, next scores) is longer than its MMAs.  Two tiles
 //    alternate; the weights leave in halves; the offset of the exponent is taken from the block
@@ -31,12 +31,17 @@
 // spill: 233 us for the 201 below); Q K^T in halves of 64 keys (an MMA of N = 64 from shared
 // memory takes 48 cycles, one of N = 128 64); items in groups whose keys fit L2 (ragged
 // prompts 175 -> 187 us).
-// Measured through graph replays, cache write included (2.07 GHz, tensor pipe active 64%):
-// fp16, 32/8 heads of 128: 8 prompts of 2048 tokens 201 us (1.37 PFLOP/s), one of 61 6.3 us;
-// bf16, 16 prompts of 1 to 2048 164 us; 64/8 heads, 6000 + 8192 tokens 1.01 ms (1.56 PFLOP/s);
-// 28/4 heads of 64, 12 of 200 to 1500 69 us; 8 of 2048 at 32/8 heads of 64 167 us.
+// Measured, cache write included, call behind call through the binding on changing inputs (what
+// a server sees: inputs from DRAM, the clock lowered by the power limit) and, second, replays of a
+// graph on one set of inputs (2.07 GHz, tensor pipe active 64%):
+//   fp16, 32/8 heads of 128, 8 prompts of 2048 tokens   231 us (1.19 PFLOP/s), 200 us (1.37)
+//   the same, one prompt of 61                          6.4 us, 6.4 us
+//   bf16, 16 prompts of 1 to 2048                       173 us, 165 us
+//   fp16, 64/8 heads, 6000 + 8192 tokens                1.06 ms (1.49 PFLOP/s), 1.02 ms (1.55)
+//   bf16, 28/4 heads of 64, 12 of 200 to 1500           72 us, 71 us
+//   fp16, 32/8 heads of 64, 8 of 2048                   164 us in replays
 // Registers: 168 / 96 / 80 by role, no spills (a spilled register makes every arrival wait for
-// local memory: 208 -> 228 us) but 24 bytes of the items' warp at d = 64 in ragged batches, beside
+// local memory: 208 -> 228 us) but 20 bytes of the items' warp at d = 64 in ragged batches, beside
 // the search (batches that hardly search, 64 sequences: 29.5 us with them, 29.7 without).
 //
 // The method: causal multi-query attention ("in-depth reading", section 5.1, item 5;

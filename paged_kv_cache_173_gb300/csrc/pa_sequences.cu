@@ -16,7 +16,7 @@
 // shared by several sequences and copied on write; "PagedAttention: when the KV
 // cache meets OS paging", section 4.3: forks share the prompt's blocks.
 //
-// The bytes are few (0.7 MB for a step of 256 sequences over 200,000 blocks, 0.1 us): what bounds all but the copies
+// The bytes are few (0.8 MB of counts for a step of 256 sequences over 200,000 blocks, 0.1 us): what bounds all but the copies
 // is the chain of round trips to L2 (lengths, table entry, count, list) and the launches.  So every call is one
 // launch (compact two), starts while the one before ends, and reads the counts once, 4 to 32 of them per thread,
 // while the sequences' own chain is under way.  Measured one after the other (truncate, then extend): 8 sequences
