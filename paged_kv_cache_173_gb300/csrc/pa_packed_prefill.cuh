@@ -28,7 +28,7 @@
 //    7.0 us for one short prompt).
 //  - Items are taken longest first, by CTAs that come to the end of their last one.
 // Tried and dropped: two softmax threads per row (both share one MUFU, and their 80 registers
-// spill: 233 us for the 201 below); Q K^T in halves of 64 keys (an MMA of N = 64 from shared
+// spill: 233 us for the 200 below); Q K^T in halves of 64 keys (an MMA of N = 64 from shared
 // memory takes 48 cycles, one of N = 128 64); items in groups whose keys fit L2 (ragged
 // prompts 175 -> 187 us).
 // Measured, cache write included, call behind call through the binding on changing inputs (what
@@ -1071,7 +1071,8 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
       tc_fence_after_sync();
       if constexpr (C::EARLY) {
         // All scores at once.  Their place is free for the next block's when the first half's weights are done: until then
-        // a warp may have to weigh them once more.  (Given free as they are loaded, 8 x 2048 tokens take 171 us, so 164.)
+        // a warp may have to weigh them once more.  (Given free as soon as they were loaded, before there was such a
+        // case, 8 x 2048 tokens took 168 us; now 164.)
         load_half(0);
         load_half(1);
         if (seen + least_t < TC_KEYS - 1) {  // a key here may lie past some row of the warp
