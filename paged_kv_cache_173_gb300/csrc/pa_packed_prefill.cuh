@@ -413,9 +413,13 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     tma_prefetch_map(&p.tmap_k);
     tma_prefetch_map(&p.tmap_v);
   }
-  if (warp == 0) tmem_alloc(tslot, C::TMEM_COLS);
   grid_dependency_wait();
-  allow_dependent_launch();
+  // Tensor memory after the wait, and the next kernel only after that: a CTA that held it and waited for a kernel whose
+  // CTAs still want theirs on the same SM would never end, nor would they.
+  if (warp == 0) {
+    tmem_alloc(tslot, C::TMEM_COLS);
+    allow_dependent_launch();
+  }
 
   PackedItem it;
   ListPlace known;

@@ -731,3 +731,23 @@ def test_what_is_not_finite_at_head_dim_128(dtype, bad, at, G):
     mask = torch.ones(got.shape[:2], dtype=torch.bool)
     mask[at, 1] = False
     assert torch.equal(got[mask], clean[mask])
+
+
+def test_beside_library_products_on_its_stream_and_another():
+    """Matrix products whose kernels use tensor memory too run before and behind the prompts in their stream, and on
+    another stream at the same time."""
+    p = Prompts([300, 77, 200], 8, 2, 64, BF16, 44).start()
+    a = torch.randn((1024, 1024), device="cuda").bfloat16()
+    want = (a @ a).clone()
+    torch.cuda.synchronize()
+    here, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(30):
+        with torch.cuda.stream(other):
+            x = a @ a
+        with torch.cuda.stream(here):
+            y = a @ a
+            p.run()
+            z = a @ a
+    torch.cuda.synchronize()
+    p.check()
+    assert all(torch.equal(t, want) for t in (x, y, z))
