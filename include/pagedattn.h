@@ -765,6 +765,7 @@ int pa_decode_sparse(void* out, const void* q, const void* k_cache, const void* 
  *                     row, pools of dtype and of any block size; the written rows are
  *                     bit-exact copies
  *   head_dim          64 or 128; num_heads / num_kv_heads <= 16, any whole number
+ *   scale             any number whose product with log2(e) float32 holds
  *
  * Scores, softmax and accumulation are float32, for scores of any size that float32
  * holds.  The weights enter P.V rounded to the values' type, each off by half a step of

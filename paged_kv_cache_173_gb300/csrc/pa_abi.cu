@@ -850,6 +850,8 @@ int pa_prefill_packed(void* out, const void* q, int64_t q_stride, const void* ke
   if (num_seqs > 65535) return fail(PA_ERR_UNSUPPORTED, "num_seqs %d exceeds 65535", num_seqs);
   if (num_rows > INT32_MAX - 1024) return fail(PA_ERR_UNSUPPORTED, "num_rows %d exceeds 2^31 - 1025", num_rows);
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+  if (!std::isfinite(scale * 1.4426950408889634f))  // (the weights are powers of 2)
+    return fail(PA_ERR_UNSUPPORTED, "scale * log2(e) exceeds float32");
   const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
   const int64_t most = int64_t{1} << 38;  // a tensor map's strides end at 2^40 bytes
   if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)

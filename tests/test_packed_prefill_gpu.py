@@ -751,3 +751,15 @@ def test_beside_library_products_on_its_stream_and_another():
     torch.cuda.synchronize()
     p.check()
     assert all(torch.equal(t, want) for t in (x, y, z))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_the_largest_scale(sign, d, dtype):
+    """Tiny elements and a large scale (bf16: 2^127, products from 2^-121 on), which are ordinary scores."""
+    sizes, key_exp = ([-12, -10, -11], -5) if dtype == F16 else ([-30, -28, -29], -90)
+    p = exact_scores(Prompts([3, 200], 2, 1, d, dtype, 45), sizes, key_exp)
+    p.scale = sign * (2.0 ** 14 if dtype == F16 else 2.0 ** 127)
+    p.start().run()
+    check_exact_scores(p)

@@ -192,3 +192,9 @@ def test_the_short_way_takes_one_function_for_failed_launches(L):
     for args in ((), (1,), (print, print)):
         with pytest.raises(TypeError):
             fast.bind_check(*args)
+
+
+@pytest.mark.parametrize("scale,status", [(2.3e38, OK), (-2.3e38, OK), (3e38, UNSUPPORTED), (-2.4e38, UNSUPPORTED), (3.4028234e38, UNSUPPORTED),
+                                          (float("nan"), INVALID), (-float("inf"), INVALID)])
+def test_packed_prefill_takes_scales_whose_powers_of_two_exist(L, scale, status):
+    assert call(L, "pa_prefill_packed", PACKED, scale=scale, R=0) == status  # (no rows: nothing is launched)
