@@ -413,6 +413,13 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     tma_prefetch_map(&p.tmap_k);
     tma_prefetch_map(&p.tmap_v);
   }
+  // Rows of the tiles that a group leaves over are no query's: zeros, whose scores need no care.
+  if (tt * G < TC_ROWS) {
+#pragma unroll 1
+    for (int i = tt * G * 8 + static_cast<int>(threadIdx.x); i < TC_ROWS * 8; i += C::THREADS)
+      for (int b = 0; b < TC_TILES * C::DBOX; ++b) *reinterpret_cast<uint4*>(sm + b * C::QATOM + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   grid_dependency_wait();
   // Tensor memory after the wait, and the next kernel only after that: a CTA that held it and waited for a kernel whose
   // CTAs still want theirs on the same SM would never end, nor would they.
@@ -464,10 +471,6 @@ packed_prefill_tc_kernel(const __grid_constant__ PackedParams p) {
     publish(it, 0);
     if (it.blocks(tt) <= C::ASK_AT_ONCE) ask_for_cta(sm + C::RESP_OFF, cbar);
   }
-  // Rows of the tiles that a group leaves over are no query's: zeros, whose scores need no care.
-  for (int i = tt * G * 8 + static_cast<int>(threadIdx.x); i < TC_ROWS * 8; i += C::THREADS)
-    for (int b = 0; b < TC_TILES * C::DBOX; ++b) *reinterpret_cast<uint4*>(sm + b * C::QATOM + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-  if (tt * G < TC_ROWS) fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
